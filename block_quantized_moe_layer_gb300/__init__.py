@@ -24,7 +24,9 @@ EXPORTS = (
     "mtp_verify_accept", "mtp_verify_accept_noalloc", "moe_forward_residual", "moe_lm_head_create",
     "moe_lm_head_forward", "moe_lm_head_destroy", "mtp_round_workspace_bytes", "mtp_round", "moe_last_error",
     "moe_layer_timeline", "moe_layer_inject_timeout", "moe_lm_head_status", "moe_forward_f32",
-    "mtp_round_hidden", "moe_forward_resnorm",
+    "mtp_round_hidden", "moe_forward_resnorm", "moe_attn_page_bytes", "moe_attn_create", "moe_attn_append",
+    "moe_attn_read", "moe_attn_forward", "moe_attn_status", "moe_attn_workspace_bytes", "moe_attn_destroy",
+    "moe_token_logprobs",
 )
 
 # event names of moe_layer_timeline, in order
@@ -46,6 +48,13 @@ class MoeLayerDesc(_c.Structure):
                 ("gate", _c.POINTER(MoeTensor)), ("up", _c.POINTER(MoeTensor)),
                 ("down", _c.POINTER(MoeTensor)), ("sh_gate", MoeTensor), ("sh_up", MoeTensor),
                 ("sh_down", MoeTensor), ("expert_begin", _c.c_int32), ("expert_count", _c.c_int32)]
+
+
+class MoeAttnDesc(_c.Structure):
+    _fields_ = [(n, _c.c_int32) for n in ("n_q_heads", "n_kv_heads", "head_dim", "page_tokens", "n_pages", "rot_dim",
+                                          "interleaved", "window", "act_dtype", "T_max", "S_max", "len_max")] + [
+        ("eps", _c.c_float), ("scale", _c.c_float), ("rope_base", _c.c_double), ("freq", _c.POINTER(_c.c_double)),
+        ("q_norm", _c.c_void_p), ("k_norm", _c.c_void_p)]
 
 
 class MoEError(RuntimeError):
@@ -92,6 +101,15 @@ def lib():
             "moe_layer_inject_timeout": (_c.c_int, [vp, i32]),
             "mtp_round_hidden": (_c.c_int, [vp, sz, i32, i32, i32, i32, i32, vp, vp]),
             "moe_forward_resnorm": (_c.c_int, [vp, vp, i32, vp, vp, vp, _c.c_float, vp]),
+            "moe_attn_page_bytes": (sz, [i32, i32, i32]),
+            "moe_attn_create": (_c.c_int, [_c.POINTER(MoeAttnDesc), vp, _c.POINTER(vp)]),
+            "moe_attn_append": (_c.c_int, [vp, vp, vp, vp, i32, _c.POINTER(i64), vp, vp, i32, vp, vp, vp]),
+            "moe_attn_read": (_c.c_int, [vp, vp, vp, i32, vp, vp, vp]),
+            "moe_attn_forward": (_c.c_int, [vp, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
+            "moe_attn_status": (_c.c_int, [vp, vp]),
+            "moe_attn_workspace_bytes": (sz, [vp]),
+            "moe_attn_destroy": (None, [vp]),
+            "moe_token_logprobs": (_c.c_int, [vp, i32, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -388,3 +406,192 @@ def round_hidden(workspace, lm, k, n_target, stream=None):
     h = torch.empty(k + 1, lm.H, dtype=torch.float32, device=workspace.device)
     _check(lib().mtp_round_hidden(wp, wn, lm.H, k, lm.V, lm.act, n_target, h.data_ptr(), _stream(stream)))
     return h
+
+
+# --------------------------------------------------------------------------
+# Attention over a 4-bit paged cache, token scores
+# --------------------------------------------------------------------------
+
+
+def kv_page_bytes(n_kv_heads, head_dim, page_tokens):
+    """Bytes of one page of the 4-bit key/value cache (``moe_attn_page_bytes``)."""
+    n = lib().moe_attn_page_bytes(n_kv_heads, head_dim, page_tokens)
+    if n == 0:
+        raise MoEError(MOE_EINVAL, f"no page of {n_kv_heads} heads, {head_dim} channels, {page_tokens} tokens")
+    return n
+
+
+class Attention:
+    """One layer's attention over a 4-bit paged cache, on the current CUDA
+    device (``moe_attn_create``; the page format is in ``moe_layer.h``).
+
+    The cache itself is the caller's: ``pages()`` makes a zeroed uint8 tensor
+    of ``n_pages`` pages.  ``q_norm`` / ``k_norm``: fp32 weights [head_dim] of
+    the per-head RMS norms, or None; ``rot_dim`` channels are rotated
+    (default: all), in pairs (i, i + rot_dim/2) or, ``interleaved``, (2i,
+    2i + 1), by ``freq`` (rot_dim/2 numbers) or rope_base^(-2i/rot_dim) a
+    token; ``window``: how many tokens a query sees (0: all earlier ones).
+    """
+
+    def __init__(self, n_q_heads, n_kv_heads, head_dim, page_tokens, n_pages, T_max, S_max, len_max, act=ACT_BF16,
+                 rot_dim=None, interleaved=False, rope_base=10000.0, freq=None, q_norm=None, k_norm=None, eps=1e-6,
+                 window=0, scale=0.0, stream=None):
+        import torch
+        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self.page_tokens, self.n_pages, self.act = page_tokens, n_pages, act
+        self.handle = None
+        self.dtype = torch.bfloat16 if act == ACT_BF16 else torch.float32
+        rot = head_dim if rot_dim is None else rot_dim
+        d = MoeAttnDesc(n_q_heads, n_kv_heads, head_dim, page_tokens, n_pages, rot, int(interleaved), window, act,
+                        T_max, S_max, len_max, eps, scale, rope_base)
+        if freq is not None:
+            f = [float(v) for v in freq]
+            _require(len(f) == rot // 2, f"Attention: {len(f)} frequencies for rot_dim {rot}")
+            d.freq = (_c.c_double * len(f))(*f)
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None:
+                _require(w.dtype == torch.float32 and w.is_contiguous() and tuple(w.shape) == (head_dim,),
+                         f"Attention: {name} must be a contiguous fp32 [head_dim] tensor")
+                setattr(d, name, w.data_ptr())
+        h = _c.c_void_p()
+        _check(lib().moe_attn_create(_c.byref(d), _stream(stream), _c.byref(h)))
+        self.handle = h
+        self.page_bytes = kv_page_bytes(n_kv_heads, head_dim, page_tokens)
+
+    @property
+    def workspace_bytes(self):
+        return lib().moe_attn_workspace_bytes(self.handle)
+
+    def pages(self, device="cuda"):
+        """A zeroed page buffer [n_pages, page_bytes] uint8 (every row 0)."""
+        import torch
+        return torch.zeros(self.n_pages, self.page_bytes, dtype=torch.uint8, device=device)
+
+    def _rows(self, t, heads, name):
+        _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == self.head_dim and t.is_cuda
+                 and (t.stride(2) == 1 or t.shape[0] == 0),
+                 f"Attention: {name} must be a CUDA tensor [tokens, {heads}, {self.head_dim}] with contiguous channels")
+
+    def _cache(self, pages):
+        _require(pages.is_cuda and pages.is_contiguous() and pages.element_size() == 1
+                 and pages.numel() >= self.n_pages * self.page_bytes,
+                 f"Attention: pages must be {self.n_pages} x {self.page_bytes} contiguous bytes on the GPU")
+
+    def append(self, q, k, v, positions, slots, pages, q_out=None, stream=None):
+        """Norms and rotates q and k, stores k and v in the cache rows
+        ``slots`` (int64, page * page_tokens + place; negative: none) and
+        returns the queries [T, n_q_heads, head_dim] in the act dtype
+        (``moe_attn_append``).  q, k, v: bf16 or fp32, any token and head
+        strides that are multiples of 16 bytes; positions int32 [T]."""
+        import torch
+        self._rows(q, self.n_q_heads, "q")
+        self._rows(k, self.n_kv_heads, "k")
+        self._rows(v, self.n_kv_heads, "v")
+        T = q.shape[0]
+        _require(k.shape[0] == T and v.shape[0] == T, "append: q, k and v must have the same tokens")
+        _require(q.dtype == k.dtype == v.dtype and q.dtype in (torch.bfloat16, torch.float32),
+                 "append: q, k and v must all be bf16 or all fp32")
+        _require(positions.dtype == torch.int32 and positions.is_cuda and positions.is_contiguous()
+                 and positions.numel() == T, "append: positions must be contiguous int32 [T] on the GPU")
+        _require(slots.dtype == torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.numel() == T,
+                 "append: slots must be contiguous int64 [T] on the GPU")
+        self._cache(pages)
+        if q_out is None:
+            q_out = torch.empty(T, self.n_q_heads, self.head_dim, dtype=self.dtype, device=q.device)
+        else:
+            _require(q_out.shape == q.shape and q_out.dtype == self.dtype and q_out.is_cuda and q_out.is_contiguous(),
+                     "append: q_out must be contiguous [T, n_q_heads, head_dim] in the act dtype")
+        st = (_c.c_int64 * 6)(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+        _check(lib().moe_attn_append(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                     ACT_BF16 if q.dtype == torch.bfloat16 else ACT_F32, st, positions.data_ptr(),
+                                     slots.data_ptr(), T, pages.data_ptr(), q_out.data_ptr(), _stream(stream)))
+        return q_out
+
+    def read(self, slots, pages, stream=None):
+        """The cached (keys, values) of ``slots``, bf16 [n, n_kv_heads,
+        head_dim] each, exact (``moe_attn_read``)."""
+        import torch
+        _require(slots.dtype == torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.dim() == 1,
+                 "read: slots must be contiguous int64 [n] on the GPU")
+        self._cache(pages)
+        n = slots.numel()
+        out = torch.empty(2, n, self.n_kv_heads, self.head_dim, dtype=torch.bfloat16, device=slots.device)
+        k, v = out[0], out[1]
+        _check(lib().moe_attn_read(self.handle, pages.data_ptr(), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                   _stream(stream)))
+        return k, v
+
+    def forward(self, q, pages, starts, lens, table, max_q, max_len, out=None, lse=None, stream=None):
+        """Causal attention of each sequence's last tokens over the cache
+        (``moe_attn_forward``): q [T, n_q_heads, head_dim] in the act dtype,
+        sequence b's query tokens starts[b]..starts[b+1]-1, its cached tokens
+        lens[b] in the pages table[b].  max_q and max_len (host integers) bound
+        the query tokens and lengths.  ``lse``: optional fp32 [T, n_q_heads]."""
+        import torch
+        self._rows(q, self.n_q_heads, "q")
+        _require(q.dtype == self.dtype, "forward: q must be in the act dtype")
+        i32 = torch.int32
+        _require(table.dim() == 2 and table.dtype == i32 and table.is_cuda and table.stride(1) == 1,
+                 "forward: table must be int32 [sequences, pages] on the GPU")
+        n = table.shape[0]
+        _require(starts.dtype == i32 and starts.is_cuda and starts.is_contiguous() and starts.numel() == n + 1,
+                 "forward: starts must be contiguous int32 [sequences + 1] on the GPU")
+        _require(lens.dtype == i32 and lens.is_cuda and lens.is_contiguous() and lens.numel() == n,
+                 "forward: lens must be contiguous int32 [sequences] on the GPU")
+        _require(max_len <= table.shape[1] * self.page_tokens, "forward: the table holds fewer than max_len tokens")
+        self._cache(pages)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _require(out.shape == q.shape and out.dtype == q.dtype and out.is_cuda and out.is_contiguous(),
+                     "forward: out must be contiguous, of q's shape and type")
+        if lse is not None:
+            _require(tuple(lse.shape) == (q.shape[0], self.n_q_heads) and lse.dtype == torch.float32 and lse.is_cuda
+                     and lse.is_contiguous(), "forward: lse must be contiguous fp32 [T, n_q_heads] on the GPU")
+        _check(lib().moe_attn_forward(self.handle, q.data_ptr(), q.stride(0), q.stride(1), pages.data_ptr(),
+                                      starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
+                                      table.stride(0) if n > 1 else table.shape[1], n,
+                                      q.shape[0], max_q, max_len, out.data_ptr(),
+                                      None if lse is None else lse.data_ptr(), _stream(stream)))
+        return out
+
+    def status(self, stream=None):
+        """Raises MoEError if an earlier call met a slot, position, table
+        entry or length out of range, or a bounded wait gave up."""
+        _check(lib().moe_attn_status(self.handle, _stream(stream)))
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().moe_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def token_logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
+    """Scores of the rows of ``logits`` ([n, V] fp32 or bf16, rows contiguous;
+    ``moe_token_logprobs``): a dict of logprob [n] of ``tokens`` (int32 [n],
+    or None), entropy [n], top_ids [n, n_top] int32 and top_logprobs."""
+    import torch
+    _require(logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16)
+             and (logits.stride(1) == 1 or logits.shape[1] == 1),
+             "token_logprobs: logits must be fp32 or bf16 [n, V] on the GPU with contiguous rows")
+    n, V = logits.shape
+    _require(tokens is None or (tokens.dtype == torch.int32 and tokens.is_cuda and tokens.is_contiguous()
+                                and tokens.numel() == n), "token_logprobs: tokens must be contiguous int32 [n] on the GPU")
+    _require(0 <= n_top <= min(32, V), f"token_logprobs: n_top={n_top} outside 0..{min(32, V)}")
+    f32 = torch.float32
+    dev = logits.device
+    lp = None if tokens is None else torch.empty(n, dtype=f32, device=dev)
+    en = torch.empty(n, dtype=f32, device=dev) if entropy else None
+    ids = torch.empty(n, n_top, dtype=torch.int32, device=dev)
+    top = torch.empty(n, n_top, dtype=f32, device=dev)
+    _check(lib().moe_token_logprobs(logits.data_ptr(), ACT_F32 if logits.dtype == f32 else ACT_BF16, logits.stride(0), n,
+                                    V, None if tokens is None else tokens.data_ptr(), n_top,
+                                    None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(),
+                                    ids.data_ptr(), top.data_ptr(), _stream(stream)))
+    return dict(logprob=lp, entropy=en, top_ids=ids, top_logprobs=top)

@@ -368,6 +368,130 @@ int mtp_round(moe_layer* const* target_layers, int32_t n_target, moe_layer* cons
 int mtp_round_hidden(const void* workspace, size_t workspace_bytes, int32_t H, int32_t k, int32_t V, int32_t act_dtype,
                      int32_t n_target, float* h_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder block over a 4-bit paged cache, and the
+ * scores of its tokens.
+ * ------------------------------------------------------------------------ */
+
+/* Page format.  The cache's pages are one caller-owned device buffer of
+ * n_pages * moe_attn_page_bytes(...) bytes.  A page holds P = page_tokens
+ * tokens; for each key/value head in turn it holds key codes [P][D/2], key
+ * scales [P][D/16], value codes [P][D/2] and value scales [P][D/16] (D =
+ * head_dim).  16 consecutive channels share a scale byte b, the top eight
+ * bits below the sign of a half-precision number: d = fp16(b << 7), b <= 198
+ * (d <= 896).  A channel is (c - 8) d for its code c in 0..15; channel e of
+ * each eight consecutive ones is nibble e/2 + 4 (e%2) of their little-endian
+ * 32-bit word.  Storing takes d = max|x| / 7 rounded to the nearest scale
+ * (ties to the even byte) and c = 8 + x/d rounded half to even and clamped;
+ * a NaN is stored as 0 (code 8), what is beyond -8 d..7 d saturates.  4.5
+ * bits a channel, D * 9/8 bytes a token and key/value head.
+ *   slot = page * P + place in the page names a token's rows. */
+typedef struct {
+  int32_t n_q_heads;   /* 1..1024, a multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;    /* 64, 128, 192 or 256 */
+  int32_t page_tokens; /* 16, 32, 64 or 128 */
+  int32_t n_pages;     /* pages in the caller's buffer */
+  int32_t rot_dim;     /* channels rotated (the first ones): 0..head_dim, multiple of 16 */
+  int32_t interleaved; /* rotated pairs: 0 = (i, i + rot_dim/2), 1 = (2i, 2i + 1) */
+  int32_t window;      /* 0 = all earlier tokens, else each query sees its last `window` tokens (itself among them) */
+  int32_t act_dtype;   /* moe_act: type of queries and outputs of moe_attn_forward and of moe_attn_append's q_out.
+                          MOE_ACT_F32 is the check mode: fp32 throughout, slower */
+  int32_t T_max;       /* most query tokens of a call, 1..2^20 */
+  int32_t S_max;       /* most sequences of a call, 1..65535 */
+  int32_t len_max;     /* longest sequence; positions are 0..len_max-1 */
+  float eps;           /* of the norms */
+  float scale;         /* of the scores; 0 = 1/sqrt(head_dim) */
+  double rope_base;    /* 0 = 10000 */
+  const double* freq;  /* HOST array [rot_dim/2] of angles a token, or NULL: rope_base^(-2i/rot_dim) */
+  const float* q_norm; /* [head_dim] (host or device), or NULL: queries are not normalised */
+  const float* k_norm; /* [head_dim] (host or device), or NULL: keys are not normalised */
+} moe_attn_desc;
+
+typedef struct moe_attn moe_attn;
+
+/* Bytes of one page; 0 where the format has no such page. */
+size_t moe_attn_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_tokens);
+
+/* Copies the norm weights, computes the rotation table (fp64 angles, rounded
+ * once) and allocates the workspace, on the current device; synchronises
+ * `stream`.  Errors: MOE_EINVAL, MOE_ENOMEM, MOE_ECUDA; *out is set only on
+ * success. */
+int moe_attn_create(const moe_attn_desc* desc, void* stream, moe_attn** out);
+
+/* The step before attention, for T tokens of any sequences:
+ *   y = x / sqrt(mean(x^2) + eps) * w   (each query / key head, where the handle has the weights)
+ *   the pairs (a, b) of its first rot_dim channels turn by position * freq:
+ *   a' = a cos - b sin, b' = b cos + a sin;
+ * queries are rounded once to act_dtype and written to q_out [T, n_q_heads,
+ * head_dim]; keys, and values as they are, go to the rows of `slots` in the
+ * page format.  The stored codes are those of the exact result (fp64 decides
+ * where fp32 could not).
+ *   q [T, n_q_heads, D], k and v [T, n_kv_heads, D] of in_dtype (moe_act),
+ * channels contiguous; strides: HOST int64 [6], token and head strides in
+ * elements of q, k and v (e.g. slices of one projection), multiples of 16
+ * bytes, the pointers 16-byte aligned.  q_out may be q itself (contiguous).
+ *   positions int32 [T], slots int64 [T] on the device.  A negative slot
+ * stores nothing (padding).  A slot beyond the pages, or a position outside
+ * 0..len_max-1, stores nothing and is reported by moe_attn_status; the
+ * queries of such a position are 0.  Tokens of one call with the same slot
+ * leave either's rows there.  Asynchronous, no allocation. */
+int moe_attn_append(moe_attn* h, const void* q, const void* k, const void* v, int32_t in_dtype, const int64_t* strides,
+                    const int32_t* positions, const int64_t* slots, int32_t T, void* pages, void* q_out, void* stream);
+
+/* The cached rows of n slots as bf16 values (exact): k_out, v_out [n,
+ * n_kv_heads, D], either may be NULL.  A negative slot gives zeros, one
+ * beyond the pages zeros and a report by moe_attn_status. */
+int moe_attn_read(moe_attn* h, const void* pages, const int64_t* slots, int32_t n, void* k_out, void* v_out,
+                  void* stream);
+
+/* Causal attention of the last tokens of n_seqs sequences over the cache:
+ *   out[i, hq] = sum_j softmax_j(scale q[i, hq] . k_j) v_j
+ * Sequence b has lens[b] cached tokens, token j in page table[b][j / P], and
+ * the query tokens starts[b]..starts[b+1]-1 of q, which are its last ones:
+ * query i stands at position lens[b] - (starts[b+1] - starts[b]) + i -
+ * starts[b] and sees the keys 0..position (with a window, its last `window`).
+ * A query that sees none (its position is negative) is 0, its lse -inf.
+ *   q [T, n_q_heads, D] (act_dtype; strides in elements, multiples of 16
+ * bytes), out [T, n_q_heads, D] contiguous (not overlapping q), lse fp32 [T,
+ * n_q_heads] or NULL: the natural logarithm of the softmax's denominator.
+ * Rows of out that belong to no sequence are not written.
+ *   starts int32 [n_seqs + 1], lens int32 [n_seqs], table int32 [n_seqs]
+ * [table_stride], on the device.  max_q and max_len: at least the largest
+ * number of query tokens and the largest length; they size the launch, and
+ * tokens beyond them are left out and reported by moe_attn_status, as are
+ * table entries beyond the pages (their tokens are treated as masked).
+ * Pages' contents past lens[b] are not used, whatever they hold.
+ *   bf16: scores from exact products in fp32; the softmax's weights are
+ * rounded to fp16 for their product with the values, sums are fp32.
+ *   Calls on one handle must not run concurrently (they share its
+ * workspace).  Asynchronous, no allocation. */
+int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
+                     const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride,
+                     int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out, float* lse, void* stream);
+
+/* Synchronises `stream` and reports what earlier calls met: MOE_EINVAL with
+ * the kinds of bad slots, positions, table entries or lengths, MOE_ETIMEOUT
+ * where a bounded device-side wait gave up, MOE_OK otherwise.  The word is
+ * then cleared. */
+int moe_attn_status(moe_attn* h, void* stream);
+size_t moe_attn_workspace_bytes(const moe_attn* h);
+void moe_attn_destroy(moe_attn* h);
+
+/* Scores of n rows of V logits (dtype: moe_act; row_stride in elements):
+ *   logprob[i] = log softmax(row i)[tokens[i]], entropy[i] = -sum p ln p,
+ *   top_ids / top_logprobs [n][n_top]: the n_top most probable tokens,
+ *   descending, ties to the lower id.
+ * fp32 outputs, natural logarithms.  0 <= n_top <= min(32, V); logprob and
+ * entropy may be NULL (tokens too, without logprob).  A token outside
+ * 0..V-1 has logprob NaN.  Logits of -inf have probability 0; a row without
+ * any logit above -inf has entropy 0 and log probabilities -inf.  A NaN or
+ * +inf logit makes the row's sums NaN; NaN logits are never among the top
+ * (missing ids are -1).  Asynchronous, no allocation, no workspace. */
+int moe_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, int32_t n, int32_t V,
+                       const int32_t* tokens, int32_t n_top, float* logprob, float* entropy, int32_t* top_ids,
+                       float* top_logprobs, void* stream);
+
 /* Message for the last error on the calling thread; valid until the next
  * call on that thread.  Never NULL. */
 const char* moe_last_error(void);

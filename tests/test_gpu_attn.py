@@ -1,0 +1,474 @@
+"""The attention operators against the fp64 oracle.
+
+Tolerances, derived before the first run:
+  * Stored codes and scales, ids, and everything read back: equal.
+  * A rounding to type t is off by at most eps(t)/2 of the value (bf16 2^-8,
+    fp16 2^-11, fp32 2^-24).
+  * Queries after norm and rotation: fp32 leaves 2^-19 (|a cos| + |b sin|)
+    (see the kernel), then one rounding to the output type.
+  * Attention.  Scores are sums of D exact products in fp32: off by at most
+    (D + 4) 2^-24 sum|q k| scale (the accumulation, the scaling and the
+    subtraction of the maximum), called e; a weight is then off by a factor
+    e^(2e), plus 2^-21 of the exponential, plus 2^-11 where it is rounded to
+    fp16, plus an absolute 2^-25 of the largest weight there (fp16's smallest
+    step; the largest weight is at least 2^-8 after lazy rescaling, so 2^-17
+    of it); weighted sums over n keys in fp32 add n 2^-24.  All of these scale
+    the softmax-weighted |v| (mag); the output's rounding comes on top.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_moe_layer_gb300 as pkg
+from oracle import attn as oa
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(64, 4, 192, 64), (32, 8, 128, 128), (16, 16, 64, 32), (6, 2, 256, 64), (5, 1, 64, 0), (3, 3, 128, 16)]
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _norms(rng, D):
+    return [torch.tensor(1 + 0.1 * rng.normal(size=D), dtype=torch.float32, device="cuda") for _ in range(2)]
+
+
+def _slots(rng, n_pages, P, T):
+    return torch.tensor(rng.permutation(n_pages * P)[:T].astype(np.int64), device="cuda")
+
+
+def _append_check(rng, hq, hk, D, rot, T, P, in_dtype, act, norm=True, interleaved=False, far=100_000, positions=None,
+                  x=None, skip=None):
+    n_pages = -(-T // P) + 2
+    qw, kw = _norms(rng, D) if norm else (None, None)
+    at = pkg.Attention(hq, hk, D, P, n_pages, T, 1, far, act=act, rot_dim=rot, interleaved=interleaved, q_norm=qw, k_norm=kw)
+    if x is None:
+        x = rng.normal(size=(T, hq + 2 * hk, D)) * np.exp(rng.normal(size=(T, 1, 1)))
+    x = torch.tensor(x, device="cuda").to(in_dtype)
+    q, k, v = x.split([hq, hk, hk], 1)
+    pos = rng.integers(0, far, T) if positions is None else np.asarray(positions)
+    slots = _slots(rng, n_pages, P, T)
+    if skip is not None:
+        slots[skip] = -1
+    pages = at.pages()
+    pages.fill_(0xAB)
+    before = pages.clone()
+    p32 = torch.tensor(pos.astype(np.int32), device="cuda")
+    out = at.append(q, k, v, p32, slots, pages)
+    keys, values = at.read(slots, pages)
+    at.status()
+    f = oa.frequencies(rot)
+    want = oa.prepared(_np(q), None if qw is None else _np(qw), pos, rot, f, interleaved)
+    plain = oa.prepared(_np(q), None if qw is None else _np(qw), pos, 0, f)
+    # |a cos| + |b sin| <= |a| + |b|
+    m = np.abs(plain)
+    if rot:
+        i, j = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+        s = m[..., i] + m[..., j]
+        m[..., i], m[..., j] = s, s
+    tol = 2.0 ** -19 * m + np.abs(want) * (2.0 ** -8 if act == pkg.ACT_BF16 else 2.0 ** -24) * (1 + 2.0 ** -10)
+    assert (np.abs(_np(out) - want) <= tol).all()
+    kc, ks = oa.quantise(oa.prepared(_np(k), None if kw is None else _np(kw), pos, rot, f, interleaved))
+    vc, vs = oa.quantise(_np(v))
+    arrays = oa.page_arrays(pages.cpu().numpy(), hk, P, D)
+    sl = slots.cpu().numpy()
+    keep = sl >= 0
+    for (codes, scales), (gc, gs) in (((kc, ks), arrays[:2]), ((vc, vs), arrays[2:])):
+        got_c = oa.unpack(gc[sl[keep] // P, :, sl[keep] % P])
+        got_s = gs[sl[keep] // P, :, sl[keep] % P]
+        assert np.array_equal(got_s, scales[keep]), (got_s != scales[keep]).sum()
+        assert np.array_equal(got_c, codes[keep]), (got_c != codes[keep]).sum()
+    assert np.array_equal(_np(keys)[keep], oa.dequantise(kc, ks)[keep])
+    assert np.array_equal(_np(values)[keep], oa.dequantise(vc, vs)[keep])
+    assert (_np(keys)[~keep] == 0).all()
+    # nothing else is touched
+    untouched = np.ones((n_pages, P), bool)
+    untouched[sl[keep] // P, sl[keep] % P] = False
+    for g, b in zip(arrays, oa.page_arrays(before.cpu().numpy(), hk, P, D)):
+        assert np.array_equal(g.transpose(0, 2, 1, 3)[untouched], b.transpose(0, 2, 1, 3)[untouched])
+    at.close()
+
+
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS)
+@pytest.mark.parametrize("T,P", [(1, 16), (4, 64), (67, 32), (300, 128)])
+def test_append(hq, hk, D, rot, T, P):
+    rng = np.random.default_rng(T * 1000 + D + hq)
+    _append_check(rng, hq, hk, D, rot, T, P, torch.bfloat16, pkg.ACT_BF16)
+
+
+@pytest.mark.parametrize("in_dtype,act", [(torch.float32, pkg.ACT_BF16), (torch.bfloat16, pkg.ACT_F32), (torch.float32, pkg.ACT_F32)])
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS[:4])
+def test_append_types(hq, hk, D, rot, in_dtype, act):
+    _append_check(np.random.default_rng(D), hq, hk, D, rot, 37, 32, in_dtype, act)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_pairs_and_no_norm(norm, interleaved):
+    for hq, hk, D, rot in HEADS:
+        _append_check(np.random.default_rng(D + rot), hq, hk, D, rot, 50, 64, torch.bfloat16, pkg.ACT_BF16, norm, interleaved)
+
+
+def test_append_borders():
+    """Rows full of values on and next to the borders of codes and scales, at position 0 and far out."""
+    rng = np.random.default_rng(5)
+    hq, hk, D, T = 4, 2, 128, 64
+    x = rng.integers(-14, 15, (T, hq + 2 * hk, D)) / 2.0  # halves: exact ties once amax is 7
+    x[:, :, ::16] = 7.0
+    x[1::4] *= np.exp2(rng.integers(-20, 8, (T // 4, 1, 1)).astype(float))
+    x[2::4] = np.where(rng.random((T // 4, hq + 2 * hk, D)) < 0.5, 0.0, x[2::4] * (1 + 2.0 ** -7))
+    x[3::4] = 0
+    for norm in (False, True):
+        for pos in (np.zeros(T), np.full(T, 99_999), np.arange(T)):
+            for t in (torch.bfloat16, torch.float32):
+                _append_check(rng, hq, hk, D, 64, T, 16, t, pkg.ACT_BF16, norm, positions=pos.astype(np.int64), x=x)
+    # fp32 neighbours of exact ties
+    x = x * (1 + rng.integers(-1, 2, x.shape) * 2.0 ** -23)
+    _append_check(rng, hq, hk, D, 64, T, 16, torch.float32, pkg.ACT_F32, False, positions=np.zeros(T, np.int64), x=x)
+
+
+def test_append_many_rows_codes_are_exact():
+    _append_check(np.random.default_rng(6), 8, 8, 128, 128, 4096, 64, torch.bfloat16, pkg.ACT_BF16)
+
+
+def test_append_padding_strides_and_in_place():
+    rng = np.random.default_rng(7)
+    _append_check(rng, 8, 2, 64, 64, 33, 16, torch.bfloat16, pkg.ACT_BF16, skip=[0, 5, 32])
+    # a fused projection with room after each token, head-major keys, and q_out = q
+    hq, hk, D, T, P = 8, 2, 64, 19, 16
+    at = pkg.Attention(hq, hk, D, P, 4, T, 1, 1000, rot_dim=64)
+    big = torch.tensor(rng.normal(size=(T, (hq + hk) * D + 40)), device="cuda").to(torch.bfloat16)
+    q = big[:, :hq * D].unflatten(1, (hq, D))
+    v = big[:, hq * D:(hq + hk) * D].unflatten(1, (hk, D))
+    k = torch.tensor(rng.normal(size=(hk, T, D)), device="cuda").to(torch.bfloat16).transpose(0, 1)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = _slots(rng, 4, P, T)
+    a, b = at.pages(), at.pages()
+    one = at.append(q, k, v, pos, slots, a)
+    qc = q.contiguous()
+    two = at.append(qc, k.contiguous(), v.contiguous(), pos, slots, b, q_out=qc)
+    assert two is qc and torch.equal(one, two) and torch.equal(a, b)
+
+
+def test_append_special_values():
+    hq, hk, D, P = 2, 1, 64, 16
+    at = pkg.Attention(hq, hk, D, P, 2, 8, 1, 100, rot_dim=0)
+    x = torch.randn(3, hq + 2 * hk, D, device="cuda").to(torch.bfloat16)
+    x[0, 2:, 3] = float("inf")
+    x[0, 2:, 4] = float("-inf")
+    x[1, 2:, 5] = float("nan")
+    x[2, 2:, :16] = 3.0e38
+    slots = torch.tensor([0, 17, 31], device="cuda")
+    pages = at.pages()
+    at.append(x[:, :2], x[:, 2:3], x[:, 3:], torch.zeros(3, dtype=torch.int32, device="cuda"), slots, pages)
+    keys, values = at.read(slots, pages)
+    c, s = oa.quantise(_np(x[:, 2:3]))
+    assert np.array_equal(_np(keys), oa.dequantise(c, s)) and np.array_equal(_np(values), oa.dequantise(*oa.quantise(_np(x[:, 3:]))))
+    assert keys[0, 0, 3] == 7 * 896 and keys[0, 0, 4] == -8 * 896 and keys[1, 0, 5] == 0
+
+
+# ---------------------------------------------------------------- attention
+
+
+def _cache(rng, lens, hk, D, P, spare=3, wild=1.0):
+    """Random pages: valid codes and scales everywhere, rows past a sequence's end full of the format's infinities."""
+    tables = [-(-n // P) for n in lens]
+    n_pages = sum(tables) + spare
+    pages = np.full((n_pages, hk * P * D * 9 // 8), 0xFF, np.uint8)
+    arrays = oa.page_arrays(pages, hk, P, D)
+    order = rng.permutation(n_pages)
+    width = max(max(tables), 1) + 2
+    table = rng.integers(0, n_pages, (len(lens), width)).astype(np.int32)
+    keys, values, used = [], [], 0
+    for b, n in enumerate(lens):
+        mine = order[used:used + tables[b]]
+        used += tables[b]
+        table[b, :tables[b]] = mine
+        both = []
+        for i in (0, 2):
+            x = rng.normal(size=(n, hk, D)) * wild
+            c, s = oa.quantise(x)
+            j = np.arange(n)
+            if n:
+                arrays[i][mine[j // P], :, j % P] = oa.pack(c)
+                arrays[i + 1][mine[j // P], :, j % P] = s
+            both.append(oa.dequantise(c, s))
+        keys.append(both[0])
+        values.append(both[1])
+    return torch.tensor(pages, device="cuda"), torch.tensor(table, device="cuda"), keys, values, n_pages
+
+
+def _forward_check(rng, hq, hk, D, lens, news, P, act=None, window=0, scale=0.0, q_scale=1.5, wild=1.0, stream=None,
+                   pad_q=0, extra=0):
+    act = pkg.ACT_BF16 if act is None else act
+    bf = act == pkg.ACT_BF16
+    pages, table, keys, values, n_pages = _cache(rng, lens, hk, D, P, wild=wild)
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    T = int(starts[-1])
+    max_len = max(max(lens), 1) + extra
+    if max_len > table.shape[1] * P:
+        table = torch.nn.functional.pad(table, (0, -(-max_len // P) - table.shape[1]))
+    at = pkg.Attention(hq, hk, D, P, n_pages, T, len(lens), max_len, act=act, rot_dim=0, window=window, scale=scale)
+    dt = torch.bfloat16 if bf else torch.float32
+    big = torch.tensor(rng.normal(size=(T, hq, D + pad_q)) * q_scale, device="cuda").to(dt)
+    q = big[..., :D]
+    lse = torch.full((T, hq), 7.0, device="cuda")
+    out = torch.full((T, hq, D), 7.0, dtype=dt, device="cuda")
+    args = (q, pages, torch.tensor(starts, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda"), table,
+            max(max(news), 1) + (extra > 0 and max(news) < T), max_len)
+    at.forward(*args, out=out, lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    at.status()
+    again = at.forward(*args)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)  # the same bits, with and without lse
+    got, got_lse, qn = _np(out), _np(lse), _np(q)
+    sc = D ** -0.5 if scale == 0.0 else scale
+    worst = 0.0
+    for b, (n, t) in enumerate(zip(lens, news)):
+        sl = slice(starts[b], starts[b + 1])
+        want, wl, mag = oa.attention(qn[sl], keys[b], values[b], t, window, sc)
+        if t == 0:
+            continue
+        if n == 0:
+            assert (got[sl] == 0).all() and np.isneginf(got_lse[sl]).all()
+            continue
+        s_abs = sc * np.abs(qn[sl]).max() * np.abs(keys[b]).sum(-1).max()
+        e = (D + 4) * 2.0 ** -24 * s_abs
+        n_vis = min(n, window) if window else n
+        rel = np.expm1(2 * e) + 2.0 ** -20 + n_vis * 2.0 ** -24
+        tol = mag * (rel + (2.0 ** -11 if bf else 0)) + np.abs(want) * (2.0 ** -8 if bf else 2.0 ** -23)
+        if bf:
+            tol += n_vis * 2.0 ** -17 * 2.0 ** -8 * np.abs(values[b]).max()
+        err = np.abs(got[sl] - want)
+        assert np.isfinite(got[sl]).all()
+        assert (err <= tol).all(), (b, float((err - tol).max()), float((err / tol.clip(1e-30)).max()))
+        worst = max(worst, float((err / tol.clip(1e-30)).max()))
+        seen = np.isfinite(wl)
+        assert np.array_equal(np.isneginf(got_lse[sl]), ~seen)
+        assert (np.abs(got_lse[sl][seen] - wl[seen]) <= rel + (2.0 ** -11 if bf else 0) + 2.0 ** -22 * (1 + np.abs(wl[seen]))).all()
+    at.close()
+    return worst
+
+
+@pytest.mark.parametrize("act", [pkg.ACT_F32, pkg.ACT_BF16])
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS)
+def test_forward_single_tokens(hq, hk, D, rot, act):
+    rng = np.random.default_rng(D + hq)
+    for lens, P in [([1], 16), ([2, 15, 16, 17], 16), ([257, 64, 63, 65, 1], 64), ([130, 0, 128, 127, 129], 128), ([1000], 32)]:
+        _forward_check(rng, hq, hk, D, lens, [1] * len(lens), P, act)
+
+
+@pytest.mark.parametrize("act", [pkg.ACT_F32, pkg.ACT_BF16])
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS)
+def test_forward_verify_batches(hq, hk, D, rot, act):
+    rng = np.random.default_rng(D + hq + 1)
+    # ragged query counts; a sequence shorter than its queries leaves rows empty
+    _forward_check(rng, hq, hk, D, [4, 300, 2, 129], [4, 3, 4, 8], 16, act)
+    _forward_check(rng, hq, hk, D, [777, 5, 0], [4, 0, 2], 64, act)
+
+
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS)
+@pytest.mark.parametrize("window", [1, 7, 128, 500])
+def test_forward_window(hq, hk, D, rot, window):
+    rng = np.random.default_rng(window)
+    _forward_check(rng, hq, hk, D, [900, 3, 130], [4, 1, 6], 32, window=window)
+    _forward_check(rng, hq, hk, D, [400, 700], [150, 300], 64, window=window)
+
+
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS)
+def test_forward_prompts(hq, hk, D, rot):
+    rng = np.random.default_rng(D + hq + 2)
+    for lens, news, P in [([200], [200], 64), ([513], [300], 16), ([128, 300, 90], [128, 257, 33], 128), ([260, 1, 40], [129, 1, 40], 32)]:
+        _forward_check(rng, hq, hk, D, lens, news, P)
+
+
+def test_forward_long_and_split():
+    rng = np.random.default_rng(11)
+    _forward_check(rng, 16, 1, 192, [9001], [4], 64)
+    _forward_check(rng, 4, 4, 128, [12345], [1], 16)
+    _forward_check(rng, 8, 1, 64, [7000, 20], [40, 20], 32)
+
+
+def test_forward_mixed_prompt_and_single_tokens():
+    rng = np.random.default_rng(12)
+    _forward_check(rng, 16, 2, 128, [500, 1, 77, 300], [200, 1, 1, 9], 64)
+
+
+def test_forward_strides_scale_and_loose_bounds():
+    rng = np.random.default_rng(13)
+    _forward_check(rng, 8, 2, 64, [100, 33], [2, 2], 16, scale=0.3, pad_q=8)
+    _forward_check(rng, 16, 1, 128, [300, 40], [30, 9], 16, scale=0.02, pad_q=24, extra=700)
+    _forward_check(rng, 16, 1, 192, [300, 40], [3, 2], 64, extra=1500)
+
+
+def test_forward_peaked_and_flat_scores():
+    rng = np.random.default_rng(14)
+    for news in ([1], [4], [150]):
+        _forward_check(rng, 16, 2, 128, [600], news, 64, q_scale=30.0)  # one key takes nearly all
+        _forward_check(rng, 16, 2, 128, [600], news, 64, q_scale=0.0)  # all the same
+        _forward_check(rng, 16, 2, 192, [600], news, 64, wild=60.0, q_scale=0.02)  # large cached values
+
+
+def test_forward_on_another_stream():
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        _forward_check(np.random.default_rng(15), 16, 2, 64, [300, 50], [4, 4], 16)
+        _forward_check(np.random.default_rng(15), 16, 2, 64, [300, 250], [100, 4], 16)
+
+
+def test_forward_rows_of_no_sequence_are_left_alone():
+    rng = np.random.default_rng(16)
+    pages, table, keys, values, n_pages = _cache(rng, [40, 60], 2, 64, 16)
+    at = pkg.Attention(8, 2, 64, 16, n_pages, 10, 2, 64, rot_dim=0)
+    q = torch.randn(10, 8, 64, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 5.0)
+    at.forward(q, pages, torch.tensor([2, 4, 7], **i32), torch.tensor([40, 60], **i32), table, 3, 60, out=out)
+    at.status()
+    assert (out[:2] == 5).all() and (out[7:] == 5).all()
+    want, _, mag = oa.attention(_np(q[4:7]), keys[1], values[1], 3)
+    assert (np.abs(_np(out[4:7]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag).all()
+
+
+def test_forward_captured_in_a_graph_follows_its_inputs():
+    rng = np.random.default_rng(17)
+    pages, table, keys, values, n_pages = _cache(rng, [500, 300], 2, 128, 64)
+    at = pkg.Attention(16, 2, 128, 64, n_pages, 8, 2, 512, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(8, 16, 128, device="cuda").to(torch.bfloat16)
+    starts, lens = torch.tensor([0, 4, 8], **i32), torch.tensor([500, 300], **i32)
+    out = torch.empty_like(q)
+    at.forward(q, pages, starts, lens, table, 4, 512, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        at.forward(q, pages, starts, lens, table, 4, 512, out=out)
+    lens.copy_(torch.tensor([123, 64], **i32))
+    q.copy_(torch.randn(8, 16, 128, device="cuda"))
+    g.replay()
+    got = out.clone()
+    assert torch.equal(got, at.forward(q, pages, starts, lens, table, 4, 512))
+    for b, n in enumerate((123, 64)):
+        want, _, mag = oa.attention(_np(q[4 * b:4 * b + 4]), keys[b][:n], values[b][:n], 4)
+        assert (np.abs(_np(got[4 * b:4 * b + 4]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag).all()
+
+
+# ---------------------------------------------------------------- refusals and reports
+
+
+def test_refusals():
+    at = pkg.Attention(8, 2, 64, 16, 4, 10, 2, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.randn(4, 12, 64, device="cuda").to(torch.bfloat16)
+    q, k, v = x.split([8, 2, 2], 1)
+    pos, slots, pages = torch.arange(4, **i32), torch.arange(4, device="cuda"), at.pages()
+    starts, lens, table = torch.tensor([0, 4], **i32), torch.tensor([4], **i32), torch.zeros(1, 4, **i32)
+    odd = torch.randn(4 * 12 * 64 + 1, device="cuda").to(torch.bfloat16)[1:].view(4, 12, 64)
+    bad = [
+        lambda: at.append(q.float(), k, v, pos, slots, pages),
+        lambda: at.append(q, k[:3], v, pos, slots, pages),
+        lambda: at.append(q[:, :4], k, v, pos, slots, pages),
+        lambda: at.append(q, k, v, pos.long(), slots, pages),
+        lambda: at.append(q, k, v, pos, slots.int(), pages),
+        lambda: at.append(q, k, v, pos, slots, pages[:2]),
+        lambda: at.append(odd[:, :8], k, v, pos, slots, pages),  # 2 bytes off a 16-byte boundary
+        lambda: at.append(x.transpose(1, 2).contiguous().transpose(1, 2)[:, :8], k, v, pos, slots, pages),
+        lambda: at.append(torch.cat([q] * 3), torch.cat([k] * 3), torch.cat([v] * 3), pos.repeat(3), slots.repeat(3), pages),
+        lambda: at.forward(q.float(), pages, starts, lens, table, 4, 4),
+        lambda: at.forward(q, pages, starts, lens, table, 5, 4),
+        lambda: at.forward(q, pages, starts, lens, table, 4, 65),
+        lambda: at.forward(q, pages, starts[:1], lens, table, 4, 4),
+        lambda: at.forward(q, pages, starts, lens, table[:, :1], 4, 17),
+        lambda: at.forward(q, pages, torch.zeros(4, **i32), lens.repeat(3), table.repeat(3, 1), 4, 4),
+        lambda: at.forward(q.cpu(), pages, starts, lens, table, 4, 4),
+        lambda: at.forward(q, pages, starts, lens, table, 4, 4, out=torch.empty(4, 8, 64, device="cuda")),
+        lambda: at.read(slots.int(), pages),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(pkg.MoEError) as e:
+            f()
+        assert e.value.code == pkg.MOE_EINVAL, i
+    at.status()  # none of them reached the GPU
+    # empty calls launch nothing
+    at.append(q[:0], k[:0], v[:0], pos[:0], slots[:0], pages)
+    at.forward(q[:0], pages, starts, lens, table, 0, 4)
+    assert at.read(slots[:0], pages)[0].shape == (0, 2, 64)
+
+
+def test_out_of_range_inputs_are_reported_and_skipped():
+    rng = np.random.default_rng(18)
+    hq, hk, D, P = 8, 2, 64, 16
+    at = pkg.Attention(hq, hk, D, P, 4, 400, 2, 640)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.randn(4, hq + 2 * hk, D, device="cuda").to(torch.bfloat16)
+    q, k, v = x.split([hq, hk, hk], 1)
+    pages = at.pages()
+    ok = dict(positions=torch.arange(4, **i32), slots=torch.arange(4, device="cuda"))
+
+    def reports(word):
+        with pytest.raises(pkg.MoEError) as e:
+            at.status()
+        assert word in str(e.value) and e.value.code == pkg.MOE_EINVAL
+        at.status()  # cleared
+
+    at.append(q, k, v, ok["positions"], torch.tensor([0, 64, 1 << 40, 2], device="cuda"), pages)
+    reports("slot")
+    assert (at.read(torch.tensor([1], device="cuda"), pages)[0] == 0).all()
+    out = at.append(q, k, v, torch.tensor([0, 640, -1, 3], **i32), ok["slots"], pages)
+    reports("position")
+    assert (out[1:3] == 0).all() and (out[0] != 0).any()
+    assert (at.read(torch.tensor([70], device="cuda"), pages)[1] == 0).all()
+    reports("slot")
+    # a table entry beyond the pages: its tokens are masked
+    pages, table, keys, values, n_pages = _cache(rng, [40], hk, D, P, spare=0)
+    at2 = pkg.Attention(hq, hk, D, P, n_pages, 400, 2, 640, rot_dim=0)
+    for bad in (-1, n_pages, 1 << 30):
+        for news in (1, 4, 40):
+            t2 = table.clone()
+            t2[0, 1] = bad
+            qq = torch.randn(news, hq, D, device="cuda").to(torch.bfloat16)
+            out = at2.forward(qq, pages, torch.tensor([0, news], **i32), torch.tensor([40], **i32), t2, news, 40)
+            with pytest.raises(pkg.MoEError, match="block-table"):
+                at2.status()
+            gone = np.r_[0:16, 32:40]
+            if news <= 8:
+                want, _, mag = oa.attention(_np(qq[-1:]), keys[0][gone], values[0][gone], 1)
+                assert (np.abs(_np(out[-1:]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag).all()
+    # lengths and starts beyond what the call said
+    qq = torch.randn(4, hq, D, device="cuda").to(torch.bfloat16)
+    for starts, lens in (([0, 9], [40]), ([3, 1], [40]), ([-2, 4], [40]), ([0, 4], [1 << 30]), ([0, 4], [-5])):
+        at2.forward(qq, pages, torch.tensor(starts, **i32), torch.tensor(lens, **i32), table, 4, 40)
+        with pytest.raises(pkg.MoEError, match="lengths"):
+            at2.status()
+
+
+def test_offsets_past_32_bits():
+    """The last of 40,000 pages of 147 KB each lies past 2^32 bytes."""
+    hq, hk, D, P = 16, 4, 256, 128
+    n_pages = 40_000
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    at = pkg.Attention(hq, hk, D, P, n_pages, 300, 1, 4096, rot_dim=64)
+    assert n_pages * at.page_bytes > 1 << 32
+    pages = torch.empty(n_pages, at.page_bytes, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(19)
+    T = 300
+    x = torch.tensor(rng.normal(size=(T, hq + 2 * hk, D)), device="cuda").to(torch.bfloat16)
+    q, k, v = x.split([hq, hk, hk], 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.tensor([[n_pages - 1, 5, n_pages - 2]], **i32)
+    j = torch.arange(T, device="cuda")
+    slots = table[0][j // P].long() * P + j % P
+    qr = at.append(q, k, v, j.int(), slots, pages)
+    keys, values = (_np(t) for t in at.read(slots, pages))
+    c, s = oa.quantise(oa.prepared(_np(k), None, np.arange(T), 64, oa.frequencies(64)))
+    assert np.array_equal(keys, oa.dequantise(c, s))
+    for n in (1, 4, 300):
+        out = at.forward(qr[T - n:], pages, torch.tensor([0, n], **i32), torch.tensor([T], **i32), table, n, T)
+        at.status()
+        want, _, mag = oa.attention(_np(qr[T - n:]), keys, values, n)
+        assert (np.abs(_np(out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag + 1e-6).all()
