@@ -15,7 +15,9 @@ cudaError_t append_launch(const moe_attn* h, const void* q, const void* k, const
 cudaError_t read_launch(const moe_attn* h, const void* pages, const int64_t* slots, int n, void* k_out, void* v_out,
                         cudaStream_t st);
 cudaError_t rope_launch(const moe_attn* h, cudaStream_t st);
-cudaError_t check_launch(const AttnParams& p, bool f32, cudaStream_t st);
+cudaError_t check_launch(const AttnParams& p, cudaStream_t st);
+cudaError_t small_configure();
+cudaError_t small_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
 }  // namespace attn
 }  // namespace moe
 
@@ -138,6 +140,12 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
     if (h->k_norm)
       CKA(cudaMemcpyAsync(h->norm_w + h->D, d->k_norm, h->D * sizeof(float), cudaMemcpyDefault, st), "copy key norm");
   }
+  if (h->act == MOE_ACT_BF16) {
+    h->part_rows = (size_t)128 * h->num_sms;
+    h->ws_bytes = h->part_rows * (h->D * sizeof(float) + sizeof(float2));
+    CKA(cudaMalloc(&h->ws, h->ws_bytes), "alloc workspace");
+    CKA(attn::small_configure(), "configure the attention kernels");
+  }
   CKA(cudaStreamSynchronize(st), "create sync");
   guard.keep = true;
   *out = h;
@@ -215,7 +223,13 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
   p.out = out; p.lse = lse;
   p.status = h->status;
   p.timeout_ns = 2000000000ull;
-  CKA(attn::check_launch(p, h->act == MOE_ACT_F32, st), "moe_attn_forward launch");
+  if (h->act == MOE_ACT_F32) {
+    CKA(attn::check_launch(p, st), "moe_attn_forward launch (fp32)");
+    return MOE_OK;
+  }
+  p.part_o = reinterpret_cast<float*>(h->ws);
+  p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
+  CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch");
   return MOE_OK;
 }
 

@@ -20,12 +20,7 @@ namespace {
 
 constexpr int kCheckWarps = 8;
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kWords = D / 8;  // words of a row: lanes that own channels
   __shared__ float sq[D];
@@ -39,7 +34,7 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
   if (t >= s.nq) return;
   const int tok = s.start + t;
   for (int i = threadIdx.x; i < D; i += blockDim.x)
-    sq[i] = to_f32(static_cast<const T*>(p.q)[tok * p.q_tok + h * p.q_head + i]) * p.scale_log2;
+    sq[i] = static_cast<const float*>(p.q)[tok * p.q_tok + h * p.q_head + i] * p.scale_log2;
   __syncthreads();
   const int pos = s.len - s.nq + t;
   const int lo = key_lo(p, pos);
@@ -111,7 +106,7 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
 #pragma unroll
     for (int w = 0; w < kCheckWarps; ++w) v += sm[w] == -INFINITY ? 0.f : so[w][i] * exp2f(sm[w] - mx);
     // a row that sees no key is 0
-    put(static_cast<T*>(p.out) + ((int64_t)tok * p.hq + h) * D + i, lt > 0.f ? v / lt : 0.f);
+    static_cast<float*>(p.out)[((int64_t)tok * p.hq + h) * D + i] = lt > 0.f ? v / lt : 0.f;
   }
   if (p.lse && threadIdx.x == 0)
     p.lse[(int64_t)tok * p.hq + h] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
@@ -119,19 +114,14 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
 
 }  // namespace
 
-template <typename T>
-static cudaError_t check_launch_t(const AttnParams& p, cudaStream_t st) {
+cudaError_t check_launch(const AttnParams& p, cudaStream_t st) {
   const dim3 grid((unsigned)(p.max_q * p.hq), p.n_seqs);
   switch (p.D) {
-    case 64: return launch_pdl(check_kernel<64, T>, grid, kCheckWarps * 32, 0, st, p);
-    case 128: return launch_pdl(check_kernel<128, T>, grid, kCheckWarps * 32, 0, st, p);
-    case 192: return launch_pdl(check_kernel<192, T>, grid, kCheckWarps * 32, 0, st, p);
-    default: return launch_pdl(check_kernel<256, T>, grid, kCheckWarps * 32, 0, st, p);
+    case 64: return launch_pdl(check_kernel<64>, grid, kCheckWarps * 32, 0, st, p);
+    case 128: return launch_pdl(check_kernel<128>, grid, kCheckWarps * 32, 0, st, p);
+    case 192: return launch_pdl(check_kernel<192>, grid, kCheckWarps * 32, 0, st, p);
+    default: return launch_pdl(check_kernel<256>, grid, kCheckWarps * 32, 0, st, p);
   }
-}
-
-cudaError_t check_launch(const AttnParams& p, bool f32, cudaStream_t st) {
-  return f32 ? check_launch_t<float>(p, st) : check_launch_t<__nv_bfloat16>(p, st);
 }
 
 }  // namespace attn
