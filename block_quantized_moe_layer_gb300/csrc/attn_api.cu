@@ -1,5 +1,6 @@
 // attn_api.cu -- the extern "C" entry points of the attention operators
 // (include/moe_layer.h): the handle, append, read, forward.
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -18,6 +19,9 @@ cudaError_t rope_launch(const moe_attn* h, cudaStream_t st);
 cudaError_t check_launch(const AttnParams& p, cudaStream_t st);
 cudaError_t small_configure();
 cudaError_t small_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
+size_t prompt_ws_bytes(int D, int tile_cap);
+cudaError_t prompt_configure();
+cudaError_t prompt_launch(const AttnParams& p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st);
 }  // namespace attn
 }  // namespace moe
 
@@ -33,6 +37,10 @@ int cuda_fail(cudaError_t e, const char* what) {
     cudaError_t e_ = (call);                         \
     if (e_ != cudaSuccess) return cuda_fail(e_, what); \
   } while (0)
+
+// Rows (query tokens times query heads of a key/value head) up to which a
+// call runs on the small-row kernel.
+constexpr int kSmallCallRows = 64;
 
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 bool page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
@@ -143,6 +151,17 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
   if (h->act == MOE_ACT_BF16) {
     h->part_rows = (size_t)128 * h->num_sms;
     h->ws_bytes = h->part_rows * (h->D * sizeof(float) + sizeof(float2));
+    if ((int64_t)h->T_max * (h->hq / h->hk) > kSmallCallRows) {
+      // dequantised tiles of one longest sequence at least, of more while they stay within 256 MB
+      const int64_t one = (int64_t)h->hk * ((h->len_max + attn::kTileTokens - 1) / attn::kTileTokens);
+      const int64_t room = (256LL << 20) / (4LL * attn::kTileTokens * h->D);
+      const int64_t cap = one * std::max<int64_t>(1, std::min<int64_t>(h->S_max, room / one));
+      if (cap > (1 << 28)) return set_error(MOE_EINVAL, "moe_attn_create: len_max=%d with %d heads is too long", h->len_max, h->hk);
+      h->tile_cap = (int)cap;
+      h->tile_off = (h->ws_bytes + 255) / 256 * 256;
+      h->ws_bytes = h->tile_off + attn::prompt_ws_bytes(h->D, h->tile_cap);
+      CKA(attn::prompt_configure(), "configure the prompt kernel");
+    }
     CKA(cudaMalloc(&h->ws, h->ws_bytes), "alloc workspace");
     CKA(attn::small_configure(), "configure the attention kernels");
   }
@@ -229,7 +248,11 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
   }
   p.part_o = reinterpret_cast<float*>(h->ws);
   p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
-  CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch");
+  if ((int64_t)max_q * p.g <= kSmallCallRows)
+    CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch");
+  else
+    CKA(attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st),
+        "moe_attn_forward launch (prompt)");
   return MOE_OK;
 }
 

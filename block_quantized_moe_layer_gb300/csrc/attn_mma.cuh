@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 
 // A wait on an mbarrier phase that gives up after the call's limit (the
 // status word then says where) or once another thread of the block has.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit,
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit,
                                        int site) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {

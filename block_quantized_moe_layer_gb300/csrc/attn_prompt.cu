@@ -1,0 +1,503 @@
+// attn_prompt.cu -- attention of many query rows (prompt chunks) over the
+// 4-bit paged cache, on the tcgen05 tensor cores.
+//
+// Two kernels.  expand_kernel dequantises the visible tiles of 128 keys of
+// each (sequence, key/value head) once into 16-bit operand images in the
+// workspace (exact: see attn_mma.cuh); prompt_kernel reads them with one bulk
+// copy a tile.  Dequantising inside prompt_kernel instead would repeat it for
+// every 128 query rows (T g / 128 times), and its instructions and
+// shared-memory writes would not fit beside the softmax; the extra pass writes
+// 4 D bytes a key and head once, some 1% of the time of a prompt chunk.
+//
+// prompt_kernel: a block owns 128 rows (query token, query head of one
+// key/value head) and walks over the visible 128-key tiles j:
+//   S_j = Q K_j^T   (bf16, M = 128, N = 128, both operands in shared memory)
+//   P_j = 2^(scale S_j - m), rounded to fp16 into the columns of S_j
+//   O  += P_j V_j   (fp16, P from tensor memory, N = D)
+// One thread issues all MMAs; S is double-buffered, so S_{j+1} runs while the
+// softmax of S_j does.  Eight softmax warps: thread (half, row) takes 64 of a
+// row's 128 scores; the halves exchange their maxima through shared memory.
+// The reference m moves only when the maximum passes it by more than 8 (a
+// weight of 2^8 is harmless in fp16 and fp32), which keeps the rescaling of
+// the output in tensor memory rare; l and O stay consistent with m either way.
+//   TMEM columns: S at 0 and 128, O at 256.
+//
+// Operand images (no swizzle, K-major, 8x8 core matrices of 128 contiguous
+// bytes): rows x channels as [channels/8][rows][8]; values as
+// [keys/8][D][8 keys], so that the contraction index is innermost in both.
+#include "attn_mma.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace attn {
+
+// Joins the parts of split rows (attn_small.cu).
+cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st);
+
+namespace {
+
+constexpr int kRowsP = 128;
+constexpr int kSoftWarps = 8;
+constexpr int kPromptThreads = (kSoftWarps + 2) * 32;
+constexpr int kMaxRing = 8;
+constexpr float kLazy = 8.f;  // log2 units
+
+template <int D>
+struct PromptPlan {
+  static constexpr int kImage = kTileTokens * D * 2;  // bytes of one operand image
+  static constexpr int kRing = D == 64 ? 8 : (D == 128 ? 5 : (D == 192 ? 3 : 2));
+  static constexpr int kQ = 0;
+  static constexpr int kStages = kImage;  // (a query image has the same size)
+  static constexpr int kMax = kStages + kRing * kImage;              // float [2 buffers][2 halves][128]
+  static constexpr int kBars = kMax + 2 * 2 * kRowsP * 4;
+  static constexpr int kNumBars = 2 * kMaxRing + 2 + 1 + 1 + 2 + 1;
+  static constexpr int kMisc = kBars + kNumBars * 8;
+  static constexpr int kTotal = kMisc + 16 + 128;
+  static_assert(kTotal <= 232448, "shared memory plan");
+};
+
+// D[tmem] (+)= A[smem] B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// What the two kernels share about the images of a launch.
+struct Images {
+  uint8_t* base;    // [sequence][kv head][tile]{keys, values}
+  uint4* valid;     // [sequence][tile]: a bit for each key that exists
+  int tiles;        // tiles of a sequence
+};
+
+// Tiles of a sequence that any of its queries sees: [first, last).
+__device__ __forceinline__ void seq_tiles(const AttnParams& p, const Seq& s, int& first, int& last) {
+  const int lo = key_lo(p, max(0, s.len - s.nq));
+  first = lo / kTileTokens;
+  last = s.nq > 0 ? (s.len + kTileTokens - 1) / kTileTokens : first;
+}
+
+__global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Images im) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const Seq s = load_seq(p, b);
+  int first, last;
+  seq_tiles(p, s, first, last);
+  const int tile = first + blockIdx.x;
+  if (tile >= last) return;
+  __shared__ int page[kTileTokens / 16];
+  const int ppt = kTileTokens >> p.pshift, tid = threadIdx.x, D = p.D;
+  if (tid < ppt) {
+    const int i = tile * ppt + tid;
+    page[tid] = (i << p.pshift) < s.len ? load_page(p, b, i) : -1;
+  }
+  __syncthreads();
+  const int n_keys = min(kTileTokens, s.len - tile * kTileTokens);
+  if (kvh == 0 && tid < 4) {
+    uint32_t m = 0;
+    for (int i = 0; i < 32; ++i) {
+      const int k = 32 * tid + i;
+      if (k < n_keys && page[k >> p.pshift] >= 0) m |= 1u << i;
+    }
+    reinterpret_cast<uint32_t*>(im.valid + (int64_t)b * im.tiles + blockIdx.x)[tid] = m;
+  }
+  const int64_t image = (int64_t)kTileTokens * D * 2;
+  uint8_t* kd = im.base + (((int64_t)b * p.hk + kvh) * im.tiles + blockIdx.x) * 2 * image;
+  uint8_t* vd = kd + image;
+  const int words = D / 8, code_b = p.P * (D / 2);
+  // keys: a thread takes a word of 8 channels; a warp 32 keys of the same word
+  for (int u = tid; u < kTileTokens * words; u += 256) {
+    const int k = u & (kTileTokens - 1), w = u / kTileTokens;
+    const int pg = page[k >> p.pshift];
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (k < n_keys && pg >= 0) {
+      const uint8_t* base = p.pages + pg * p.page_bytes + kvh * p.head_bytes;
+      const int at = k & (p.P - 1);
+      const uint32_t sb = base[code_b + at * (D / 16) + (w >> 1)];
+      uint32_t x[4];
+      key_pairs(*reinterpret_cast<const uint32_t*>(base + at * (D / 2) + 4 * w), key_scale(sb | (sb << 16)), x);
+      o = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    *reinterpret_cast<uint4*>(kd + ((int64_t)w * kTileTokens + k) * 16) = o;
+  }
+  // values: a thread takes 8 keys of a word, and turns them to 8 channels of 8 keys
+  for (int u = tid; u < (kTileTokens / 8) * words; u += 256) {
+    const int w = u % words, k0 = 8 * (u / words);
+    const int pg = page[k0 >> p.pshift];
+    uint32_t x[4][8];  // [pair of keys][channel]
+    const uint8_t* base = p.pages + (pg < 0 ? 0 : pg) * p.page_bytes + kvh * p.head_bytes + p.head_bytes / 2;
+    const int at = k0 & (p.P - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w0 = 0, w1 = 0, s0 = 0, s1 = 0;
+      if (pg >= 0 && k0 + 2 * i < n_keys) {
+        w0 = *reinterpret_cast<const uint32_t*>(base + (at + 2 * i) * (D / 2) + 4 * w);
+        s0 = base[code_b + (at + 2 * i) * (D / 16) + (w >> 1)];
+      }
+      if (pg >= 0 && k0 + 2 * i + 1 < n_keys) {
+        w1 = *reinterpret_cast<const uint32_t*>(base + (at + 2 * i + 1) * (D / 2) + 4 * w);
+        s1 = base[code_b + (at + 2 * i + 1) * (D / 16) + (w >> 1)];
+      }
+      const ValueScale d = value_scale(s0 | (s1 << 16));
+      value_quads(__byte_perm(w0, w1, 0x5410), d, x[i][0], x[i][2], x[i][4], x[i][6]);
+      value_quads(__byte_perm(w0, w1, 0x7632), d, x[i][1], x[i][3], x[i][5], x[i][7]);
+    }
+    uint4* o = reinterpret_cast<uint4*>(vd + ((int64_t)(k0 / 8) * D + 8 * w) * 16);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = make_uint4(x[0][c], x[1][c], x[2][c], x[3][c]);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Images im, int n_rt, int chunk) {
+  using L = PromptPlan<D>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  float* smax = reinterpret_cast<float*>(sm + L::kMax);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);  // ring: copy landed
+  uint64_t* empty = full + kMaxRing;                             // ring: MMAs that read it done
+  uint64_t* sfull = empty + kMaxRing;                            // [2] scores ready
+  uint64_t* pfull = sfull + 2;                                   // weights stored
+  uint64_t* odone = pfull + 1;                                   // output product done
+  uint64_t* xbar = odone + 1;                                    // [2] maxima exchanged
+  uint64_t* fin = xbar + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
+  volatile int never = 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&xbar[i], kSoftWarps);
+    }
+    mbar_init(pfull, kSoftWarps);
+    mbar_init(odone, 1);
+    mbar_init(fin, 1);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  griddep_wait();
+
+  const int b = blockIdx.z, split = blockIdx.x % p.n_split;
+  // rows with the longest key ranges first
+  const int kvh = blockIdx.y, rt = n_rt - 1 - blockIdx.x / p.n_split;
+  const Seq s = load_seq(p, b);
+  const int row0 = rt * kRowsP, n_rows = min(kRowsP, s.nq * p.g - row0);
+  if (n_rows <= 0) return;
+  const int p0 = s.len - s.nq;
+  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + n_rows - 1) / p.g;
+  const int lo = key_lo(p, max(0, pos_min)), hi = pos_max + 1, lo_max = key_lo(p, pos_max);
+  int seq_first, seq_last;
+  seq_tiles(p, s, seq_first, seq_last);
+  const int tile_a = lo / kTileTokens + split * chunk;
+  const int n_tiles = hi > lo ? max(0, min(tile_a + chunk, (hi + kTileTokens - 1) / kTileTokens) - tile_a) : 0;
+  const uint8_t* images = im.base + (((int64_t)b * p.hk + kvh) * im.tiles + (tile_a - seq_first)) * 2 * (int64_t)L::kImage;
+  const uint4* valid = im.valid + (int64_t)b * im.tiles + (tile_a - seq_first);
+
+  if (warp == kSoftWarps + 1) tc::alloc_512(tslot);
+  // queries: thread (half, row) lays half of its row's channels into the image
+  const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // of the softmax threads
+  int tq = 0, hq = 0, hi_r = 0, lo_r = 0;
+  const bool has_row = warp < kSoftWarps && row < n_rows;
+  if (has_row) {
+    tq = (row0 + row) / p.g;
+    hq = kvh * p.g + (row0 + row) % p.g;
+    hi_r = p0 + tq + 1;
+    lo_r = key_lo(p, p0 + tq);
+  }
+  if (warp < kSoftWarps && n_tiles > 0) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
+#pragma unroll 4
+    for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
+      *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsP + row) * 16) = v;
+    }
+    tc::fence_async_smem();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tbase = *tslot;
+
+  float m = -INFINITY, l = 0.f;
+  if (warp == kSoftWarps) {
+    // ------------------------------------------------------------ copies: K0, then K(j+1), V(j)
+    if (lane == 0) {
+      const int n = 2 * n_tiles;
+      bool ok = true;
+      int i = 0;
+      for (; i < n; ++i) {
+        const int st = i % L::kRing;
+        if (i >= L::kRing)
+          ok = wait_bar(&empty[st], (uint32_t)((i / L::kRing - 1) & 1), abort, p.status, p.timeout_ns, 11);
+        if (!ok) break;
+        // order of use: K0, K1, V0, K2, V1, ..., V(n-1)
+        const bool key = i == 0 || ((i & 1) && i != n - 1);
+        const int j = key ? (i + 1) / 2 : (i - 1) / 2;
+        mbar_arrive_expect_tx(&full[st], L::kImage);
+        bulk_g2s(sm + L::kStages + st * L::kImage, images + ((int64_t)2 * j + (key ? 0 : 1)) * L::kImage, L::kImage, &full[st]);
+      }
+      for (int k = max(0, i - L::kRing); k < i; ++k)
+        wait_bar(&full[k % L::kRing], (uint32_t)((k / L::kRing) & 1), &never, p.status, p.timeout_ns, 12);
+    }
+  } else if (warp == kSoftWarps + 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0 && n_tiles > 0) {
+      constexpr uint32_t kIdescS = tc::idesc_f16(128, kTileTokens) | (1u << 7) | (1u << 10);  // bf16 operands
+      constexpr uint32_t kIdescO = tc::idesc_f16(128, D);
+      const uint64_t qd = tc::smem_desc(smem_u32(sm + L::kQ), kRowsP * 16, 128);
+      bool ok = true;
+      int i = 0;  // images used
+      auto use = [&]() {
+        const int st = i % L::kRing;
+        ok = ok && wait_bar(&full[st], (uint32_t)((i / L::kRing) & 1), abort, p.status, p.timeout_ns, 13);
+        return st;
+      };
+      auto scores = [&](int j) {
+        const int st = use();
+        if (!ok) return;
+        tc::fence_after();
+        const uint64_t kd = tc::smem_desc(smem_u32(sm + L::kStages + st * L::kImage), kTileTokens * 16, 128);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tbase + 128 * (j & 1), qd + k * (2 * kRowsP * 16 / 16), kd + k * (2 * kTileTokens * 16 / 16), kIdescS, k > 0);
+        tc::commit(&empty[st]);
+        tc::commit(&sfull[j & 1]);
+        ++i;
+      };
+      scores(0);
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        if (j + 1 < n_tiles) scores(j + 1);
+        if (!ok) break;
+        const int st = use();
+        ok = ok && wait_bar(pfull, (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 14);
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kStages + st * L::kImage), D * 16, 128);
+#pragma unroll
+        for (int k = 0; k < kTileTokens / 16; ++k)
+          tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * D * 16 / 16), kIdescO, j > 0 || k > 0);
+        tc::commit(&empty[st]);
+        tc::commit(odone);
+        ++i;
+      }
+      // all MMAs issued are complete before the block frees anything
+      tc::commit(fin);
+      wait_bar(fin, 0, &never, p.status, p.timeout_ns, 15);
+    }
+  } else if (n_tiles > 0) {
+    // ------------------------------------------------------------ softmax
+    const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+      ok = wait_bar(&sfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 16);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after();
+      uint32_t sv[4][16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::ld_32x32b_x16(tl + 128 * (j & 1) + 64 * half + 16 * c, sv[c]);
+      tc::wait_ld();
+      float x[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
+      const int c0 = (tile_a + j) * kTileTokens;
+      uint2 vm = make_uint2(0xffffffffu, 0xffffffffu);
+      {
+        const uint4 v4 = __ldcg(valid + j);
+        vm = half ? make_uint2(v4.z, v4.w) : make_uint2(v4.x, v4.y);
+      }
+      if (c0 + kTileTokens > pos_min + 1 || c0 < lo_max || (vm.x & vm.y) != 0xffffffffu) {
+        // bit c: key c0 + 64 half + c is visible to this row
+        uint64_t vis = ((uint64_t)vm.y << 32) | vm.x;
+        const int a = lo_r - (c0 + 64 * half), e = hi_r - (c0 + 64 * half);
+        vis &= e >= 64 ? ~0ull : (e <= 0 ? 0ull : (1ull << e) - 1);
+        vis &= a <= 0 ? ~0ull : (a >= 64 ? 0ull : ~((1ull << a) - 1));
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (!((vis >> c) & 1)) x[c] = -INFINITY;
+      }
+      float mx = x[0];
+#pragma unroll
+      for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
+      // the row's other half
+      float* ex = smax + (j & 1) * 2 * kRowsP;
+      ex[half * kRowsP + row] = mx;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&xbar[j & 1]);
+      ok = wait_bar(&xbar[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 17);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      mx = fmaxf(mx, ex[(half ^ 1) * kRowsP + row]) * p.scale_log2;
+      const bool move = mx > m + kLazy;  // (also the first visible keys: m = -inf)
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - mx)) : 1.f;
+        if (move) m = mx;
+        l *= f;
+        if (j > 0) {
+          ok = wait_bar(odone, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 18);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll 1
+          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+            uint32_t o[16];
+            tc::ld_32x32b_x16(tl + 256 + c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc::st_32x32b_x16(tl + 256 + c, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      uint32_t pk[2][16];
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float u = exp2_approx(fmaf(x[2 * c], p.scale_log2, -ref));
+        const float v = exp2_approx(fmaf(x[2 * c + 1], p.scale_log2, -ref));
+        l0 += u;
+        l1 += v;
+        pk[c >> 4][c & 15] = pack_h2(u, v);
+      }
+      l += l0 + l1;
+      tc::st_32x32b_x16(tl + 128 * (j & 1) + 32 * half, pk[0]);
+      tc::st_32x32b_x16(tl + 128 * (j & 1) + 32 * half + 16, pk[1]);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull);
+    }
+    if (ok) {
+      ok = wait_bar(odone, (uint32_t)((n_tiles - 1) & 1), abort, p.status, p.timeout_ns, 19);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after();
+    }
+  }
+  // the halves' sums (the maxima's last readers are past their barrier: every
+  // softmax warp has waited for the last output product, and for all of them)
+  __syncthreads();
+  if (warp < kSoftWarps) smax[half * kRowsP + row] = l;
+  __syncthreads();
+  if (warp < kSoftWarps) {
+    l += smax[(half ^ 1) * kRowsP + row];
+    const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
+    const int64_t orow = (int64_t)(s.start + tq) * p.hq + hq;
+    const int64_t part = ((int64_t)((b * p.hk + kvh) * n_rt + rt) * p.n_split + split) * kRowsP + row;
+    const float inv = p.n_split > 1 ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
+#pragma unroll 1
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+      uint32_t o[16];
+      __syncwarp();
+      if (n_tiles > 0) {
+        tc::ld_32x32b_x16(tl + 256 + c, o);
+        tc::wait_ld();
+      }
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+      if (!has_row) continue;
+      if (p.n_split > 1) {
+        float4* d = reinterpret_cast<float4*>(p.part_o + part * D + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + c);
+        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+    if (has_row && half == 0) {
+      if (p.n_split > 1) p.part_ml[part] = make_float2(m, l);
+      else if (p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kSoftWarps + 1) tc::dealloc_512(tbase);
+}
+
+template <int D>
+cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st) {
+  const int n_rt = (int)(((int64_t)p.max_q * p.g + kRowsP - 1) / kRowsP);
+  int64_t span = p.max_len;
+  if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + 2 * kTileTokens);
+  Images im;
+  im.tiles = (int)((span + kTileTokens - 1) / kTileTokens);
+  const int at_once = std::max(1, std::min(p.n_seqs, tile_cap / (p.hk * im.tiles)));
+  im.base = ws;
+  im.valid = reinterpret_cast<uint4*>(ws + (size_t)tile_cap * 2 * PromptPlan<D>::kImage);
+  // tiles of one row tile's keys: its window's, or all
+  int64_t rspan = p.max_len;
+  if (p.window > 0) rspan = std::min<int64_t>(rspan, (int64_t)p.window + kRowsP + kTileTokens);
+  const int rtiles = (int)((rspan + kTileTokens - 1) / kTileTokens);
+  const int all = p.n_seqs;
+  for (int b0 = 0; b0 < all; b0 += at_once) {
+    AttnParams g = p;
+    g.n_seqs = std::min(at_once, all - b0);
+    g.starts += b0;
+    g.lens += b0;
+    g.table += (int64_t)b0 * p.table_stride;
+    const int64_t base = (int64_t)p.hk * n_rt * g.n_seqs;
+    // keys are split only where the row tiles leave half of the GPU idle
+    int64_t want = std::max<int64_t>(1, num_sms / base);
+    want = std::min<int64_t>(want, std::max<int64_t>(1, (int64_t)(part_rows / kRowsP) / base));
+    const int chunk = (int)std::max<int64_t>(std::min(rtiles, 2), (rtiles + want - 1) / want);
+    g.n_split = (rtiles + chunk - 1) / chunk;
+    cudaError_t e = launch_pdl(expand_kernel, dim3(im.tiles, p.hk, g.n_seqs), 256, 0, st, g, im);
+    if (e == cudaSuccess)
+      e = launch_pdl(prompt_kernel<D>, dim3((unsigned)(n_rt * g.n_split), p.hk, g.n_seqs), kPromptThreads, PromptPlan<D>::kTotal,
+                     st, g, im, n_rt, chunk);
+    if (e == cudaSuccess && g.n_split > 1) e = join_launch(g, kRowsP, n_rt, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t prompt_ws_bytes(int D, int tile_cap) {
+  return (size_t)tile_cap * ((size_t)2 * kTileTokens * D * 2 + sizeof(uint4));
+}
+
+cudaError_t prompt_configure() {
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<64>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<128>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prompt_kernel<192>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<192>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prompt_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<256>::kTotal);
+  return e;
+}
+
+cudaError_t prompt_launch(const AttnParams& p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st) {
+  switch (p.D) {
+    case 64: return prompt_launch_d<64>(p, num_sms, part_rows, ws, tile_cap, st);
+    case 128: return prompt_launch_d<128>(p, num_sms, part_rows, ws, tile_cap, st);
+    case 192: return prompt_launch_d<192>(p, num_sms, part_rows, ws, tile_cap, st);
+    default: return prompt_launch_d<256>(p, num_sms, part_rows, ws, tile_cap, st);
+  }
+}
+
+}  // namespace attn
+}  // namespace moe

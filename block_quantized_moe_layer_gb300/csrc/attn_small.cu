@@ -381,6 +381,20 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ AttnPar
   if (p.lse && threadIdx.x == 0) p.lse[o] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
+}  // namespace
+
+cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st) {
+  const dim3 grid((unsigned)(p.max_q * p.hq), p.n_seqs);
+  switch (p.D) {
+    case 64: return launch_pdl(join_kernel<64>, grid, 64, 0, st, p, rows_per_tile, n_rt);
+    case 128: return launch_pdl(join_kernel<128>, grid, 128, 0, st, p, rows_per_tile, n_rt);
+    case 192: return launch_pdl(join_kernel<192>, grid, 192, 0, st, p, rows_per_tile, n_rt);
+    default: return launch_pdl(join_kernel<256>, grid, 256, 0, st, p, rows_per_tile, n_rt);
+  }
+}
+
+namespace {
+
 template <int D>
 cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStream_t st) {
   const int n_rt = (p.max_q * p.g + kSmallRows - 1) / kSmallRows;
@@ -399,7 +413,7 @@ cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStre
   cudaError_t e = launch_pdl(small_kernel<D>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads,
                              SmallPlan<D>::kTotal, st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
-  return launch_pdl(join_kernel<D>, dim3((unsigned)(p.max_q * p.hq), p.n_seqs), D, 0, st, p, kSmallRows, n_rt);
+  return join_launch(p, kSmallRows, n_rt, st);
 }
 
 }  // namespace
