@@ -137,6 +137,14 @@ def _stream(stream):
     return s.cuda_stream
 
 
+def _raw_stream(stream, t):
+    """The stream handle of ``stream``, or of the current stream on tensor t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def quantized_bytes(fmt, rows, cols):
     return lib().moe_quantized_bytes(fmt, rows, cols)
 
@@ -413,6 +421,9 @@ def round_hidden(workspace, lm, k, n_target, stream=None):
 # --------------------------------------------------------------------------
 
 
+_I64x6 = _c.c_int64 * 6
+
+
 def kv_page_bytes(n_kv_heads, head_dim, page_tokens):
     """Bytes of one page of the 4-bit key/value cache (``moe_attn_page_bytes``)."""
     n = lib().moe_attn_page_bytes(n_kv_heads, head_dim, page_tokens)
@@ -457,6 +468,8 @@ class Attention:
         _check(lib().moe_attn_create(_c.byref(d), _stream(stream), _c.byref(h)))
         self.handle = h
         self.page_bytes = kv_page_bytes(n_kv_heads, head_dim, page_tokens)
+        self._cache_bytes = n_pages * self.page_bytes
+        self._lib = lib()
 
     @property
     def workspace_bytes(self):
@@ -467,15 +480,21 @@ class Attention:
         import torch
         return torch.zeros(self.n_pages, self.page_bytes, dtype=torch.uint8, device=device)
 
-    def _rows(self, t, heads, name):
-        _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == self.head_dim and t.is_cuda
-                 and (t.stride(2) == 1 or t.shape[0] == 0),
-                 f"Attention: {name} must be a CUDA tensor [tokens, {heads}, {self.head_dim}] with contiguous channels")
+    def _cache_ok(self, pages):
+        return (pages.is_cuda and pages.is_contiguous() and pages.element_size() == 1
+                and pages.numel() >= self._cache_bytes)
 
-    def _cache(self, pages):
-        _require(pages.is_cuda and pages.is_contiguous() and pages.element_size() == 1
-                 and pages.numel() >= self.n_pages * self.page_bytes,
-                 f"Attention: pages must be {self.n_pages} x {self.page_bytes} contiguous bytes on the GPU")
+    # The calls below are on a decode step's critical path: each tests its
+    # arguments in one expression and spells out what is wrong only on failure.
+    def _rows_error(self, call, name, t, heads, dtypes):
+        want = f"a CUDA tensor [tokens, {heads}, {self.head_dim}] with contiguous channels"
+        _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == self.head_dim and t.is_cuda
+                 and t.stride(2) == 1, f"{call}: {name} must be {want}")
+        _require(t.dtype in dtypes, f"{call}: {name} must be of type {' or '.join(map(str, dtypes))}")
+
+    def _cache_error(self, call, pages):
+        _require(self._cache_ok(pages),
+                 f"{call}: pages must be {self.n_pages} x {self.page_bytes} contiguous bytes on the GPU")
 
     def append(self, q, k, v, positions, slots, pages, q_out=None, stream=None):
         """Norms and rotates q and k, stores k and v in the cache rows
@@ -484,41 +503,56 @@ class Attention:
         (``moe_attn_append``).  q, k, v: bf16 or fp32, any token and head
         strides that are multiples of 16 bytes; positions int32 [T]."""
         import torch
-        self._rows(q, self.n_q_heads, "q")
-        self._rows(k, self.n_kv_heads, "k")
-        self._rows(v, self.n_kv_heads, "v")
+        hk, D, dt = self.n_kv_heads, self.head_dim, q.dtype
+        qs, ks, vs = q.stride(), k.stride(), v.stride()
         T = q.shape[0]
-        _require(k.shape[0] == T and v.shape[0] == T, "append: q, k and v must have the same tokens")
-        _require(q.dtype == k.dtype == v.dtype and q.dtype in (torch.bfloat16, torch.float32),
-                 "append: q, k and v must all be bf16 or all fp32")
-        _require(positions.dtype == torch.int32 and positions.is_cuda and positions.is_contiguous()
-                 and positions.numel() == T, "append: positions must be contiguous int32 [T] on the GPU")
-        _require(slots.dtype == torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.numel() == T,
-                 "append: slots must be contiguous int64 [T] on the GPU")
-        self._cache(pages)
+        kv = (T, hk, D)
+        if not (q.shape == (T, self.n_q_heads, D) and k.shape == kv and v.shape == kv
+                and qs[2] == 1 and ks[2] == 1 and vs[2] == 1 and q.is_cuda and k.is_cuda and v.is_cuda
+                and (dt is torch.bfloat16 or dt is torch.float32) and k.dtype is dt and v.dtype is dt
+                and positions.shape == (T,) and positions.dtype is torch.int32 and positions.is_cuda
+                and positions.is_contiguous() and slots.shape == (T,) and slots.dtype is torch.int64 and slots.is_cuda
+                and slots.is_contiguous() and self._cache_ok(pages)):
+            both = (torch.bfloat16, torch.float32)
+            for name, x, n in (("q", q, self.n_q_heads), ("k", k, hk), ("v", v, hk)):
+                self._rows_error("append", name, x, n, both)
+            _require(k.shape[0] == T and v.shape[0] == T, "append: q, k and v must have the same tokens")
+            _require(k.dtype is dt and v.dtype is dt, "append: q, k and v must all be bf16 or all fp32")
+            _require(positions.dtype is torch.int32 and positions.is_cuda and positions.is_contiguous()
+                     and positions.shape == (T,), "append: positions must be contiguous int32 [T] on the GPU")
+            _require(slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.shape == (T,),
+                     "append: slots must be contiguous int64 [T] on the GPU")
+            self._cache_error("append", pages)
         if q_out is None:
-            q_out = torch.empty(T, self.n_q_heads, self.head_dim, dtype=self.dtype, device=q.device)
+            q_out = torch.empty((T, self.n_q_heads, D), dtype=self.dtype, device=q.device)
         else:
-            _require(q_out.shape == q.shape and q_out.dtype == self.dtype and q_out.is_cuda and q_out.is_contiguous(),
+            _require(q_out.shape == q.shape and q_out.dtype is self.dtype and q_out.is_cuda and q_out.is_contiguous(),
                      "append: q_out must be contiguous [T, n_q_heads, head_dim] in the act dtype")
-        st = (_c.c_int64 * 6)(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-        _check(lib().moe_attn_append(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                     ACT_BF16 if q.dtype == torch.bfloat16 else ACT_F32, st, positions.data_ptr(),
-                                     slots.data_ptr(), T, pages.data_ptr(), q_out.data_ptr(), _stream(stream)))
+        rc = self._lib.moe_attn_append(
+            self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), ACT_BF16 if dt is torch.bfloat16 else ACT_F32,
+            _I64x6(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]), positions.data_ptr(), slots.data_ptr(), T,
+            pages.data_ptr(), q_out.data_ptr(), _raw_stream(stream, q))
+        if rc:
+            _check(rc)
         return q_out
 
     def read(self, slots, pages, stream=None):
         """The cached (keys, values) of ``slots``, bf16 [n, n_kv_heads,
         head_dim] each, exact (``moe_attn_read``)."""
         import torch
-        _require(slots.dtype == torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.dim() == 1,
-                 "read: slots must be contiguous int64 [n] on the GPU")
-        self._cache(pages)
-        n = slots.numel()
-        out = torch.empty(2, n, self.n_kv_heads, self.head_dim, dtype=torch.bfloat16, device=slots.device)
-        k, v = out[0], out[1]
-        _check(lib().moe_attn_read(self.handle, pages.data_ptr(), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                   _stream(stream)))
+        if not (slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.dim() == 1
+                and self._cache_ok(pages)):
+            _require(slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous() and slots.dim() == 1,
+                     "read: slots must be contiguous int64 [n] on the GPU")
+            self._cache_error("read", pages)
+        n = slots.shape[0]
+        shape = (n, self.n_kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+        rc = self._lib.moe_attn_read(self.handle, pages.data_ptr(), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                     _raw_stream(stream, slots))
+        if rc:
+            _check(rc)
         return k, v
 
     def forward(self, q, pages, starts, lens, table, max_q, max_len, out=None, lse=None, stream=None):
@@ -528,31 +562,38 @@ class Attention:
         lens[b] in the pages table[b].  max_q and max_len (host integers) bound
         the query tokens and lengths.  ``lse``: optional fp32 [T, n_q_heads]."""
         import torch
-        self._rows(q, self.n_q_heads, "q")
-        _require(q.dtype == self.dtype, "forward: q must be in the act dtype")
-        i32 = torch.int32
-        _require(table.dim() == 2 and table.dtype == i32 and table.is_cuda and table.stride(1) == 1,
-                 "forward: table must be int32 [sequences, pages] on the GPU")
+        i32, D = torch.int32, self.head_dim
+        qs, ts = q.stride(), table.stride()
+        T = q.shape[0]
         n = table.shape[0]
-        _require(starts.dtype == i32 and starts.is_cuda and starts.is_contiguous() and starts.numel() == n + 1,
-                 "forward: starts must be contiguous int32 [sequences + 1] on the GPU")
-        _require(lens.dtype == i32 and lens.is_cuda and lens.is_contiguous() and lens.numel() == n,
-                 "forward: lens must be contiguous int32 [sequences] on the GPU")
-        _require(max_len <= table.shape[1] * self.page_tokens, "forward: the table holds fewer than max_len tokens")
-        self._cache(pages)
+        if not (q.shape == (T, self.n_q_heads, D) and qs[2] == 1 and q.dtype is self.dtype and q.is_cuda
+                and len(ts) == 2 and ts[1] == 1 and table.dtype is i32 and table.is_cuda
+                and starts.shape == (n + 1,) and starts.dtype is i32 and starts.is_cuda and starts.is_contiguous()
+                and lens.shape == (n,) and lens.dtype is i32 and lens.is_cuda and lens.is_contiguous()
+                and max_len <= table.shape[1] * self.page_tokens and self._cache_ok(pages)):
+            self._rows_error("forward", "q", q, self.n_q_heads, (self.dtype,))
+            _require(table.dim() == 2 and table.dtype is i32 and table.is_cuda and ts[1] == 1,
+                     "forward: table must be int32 [sequences, pages] on the GPU")
+            _require(starts.dtype is i32 and starts.is_cuda and starts.is_contiguous() and starts.shape == (n + 1,),
+                     "forward: starts must be contiguous int32 [sequences + 1] on the GPU")
+            _require(lens.dtype is i32 and lens.is_cuda and lens.is_contiguous() and lens.shape == (n,),
+                     "forward: lens must be contiguous int32 [sequences] on the GPU")
+            _require(max_len <= table.shape[1] * self.page_tokens, "forward: the table holds fewer than max_len tokens")
+            self._cache_error("forward", pages)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty((T, self.n_q_heads, D), dtype=self.dtype, device=q.device)
         else:
-            _require(out.shape == q.shape and out.dtype == q.dtype and out.is_cuda and out.is_contiguous(),
+            _require(out.shape == q.shape and out.dtype is q.dtype and out.is_cuda and out.is_contiguous(),
                      "forward: out must be contiguous, of q's shape and type")
         if lse is not None:
-            _require(tuple(lse.shape) == (q.shape[0], self.n_q_heads) and lse.dtype == torch.float32 and lse.is_cuda
+            _require(lse.shape == (T, self.n_q_heads) and lse.dtype is torch.float32 and lse.is_cuda
                      and lse.is_contiguous(), "forward: lse must be contiguous fp32 [T, n_q_heads] on the GPU")
-        _check(lib().moe_attn_forward(self.handle, q.data_ptr(), q.stride(0), q.stride(1), pages.data_ptr(),
-                                      starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
-                                      table.stride(0) if n > 1 else table.shape[1], n,
-                                      q.shape[0], max_q, max_len, out.data_ptr(),
-                                      None if lse is None else lse.data_ptr(), _stream(stream)))
+        rc = self._lib.moe_attn_forward(
+            self.handle, q.data_ptr(), qs[0], qs[1], pages.data_ptr(), starts.data_ptr(), lens.data_ptr(),
+            table.data_ptr(), ts[0] if n > 1 else table.shape[1], n, T, max_q, max_len, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), _raw_stream(stream, q))
+        if rc:
+            _check(rc)
         return out
 
     def status(self, stream=None):
@@ -577,21 +618,26 @@ def token_logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     ``moe_token_logprobs``): a dict of logprob [n] of ``tokens`` (int32 [n],
     or None), entropy [n], top_ids [n, n_top] int32 and top_logprobs."""
     import torch
-    _require(logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16)
-             and (logits.stride(1) == 1 or logits.shape[1] == 1),
-             "token_logprobs: logits must be fp32 or bf16 [n, V] on the GPU with contiguous rows")
+    f32, i32, dt = torch.float32, torch.int32, logits.dtype
+    if not (logits.dim() == 2 and logits.is_cuda and (dt is f32 or dt is torch.bfloat16)):
+        raise MoEError(MOE_EINVAL, "token_logprobs: logits must be fp32 or bf16 [n, V] on the GPU")
     n, V = logits.shape
-    _require(tokens is None or (tokens.dtype == torch.int32 and tokens.is_cuda and tokens.is_contiguous()
-                                and tokens.numel() == n), "token_logprobs: tokens must be contiguous int32 [n] on the GPU")
-    _require(0 <= n_top <= min(32, V), f"token_logprobs: n_top={n_top} outside 0..{min(32, V)}")
-    f32 = torch.float32
-    dev = logits.device
-    lp = None if tokens is None else torch.empty(n, dtype=f32, device=dev)
-    en = torch.empty(n, dtype=f32, device=dev) if entropy else None
-    ids = torch.empty(n, n_top, dtype=torch.int32, device=dev)
-    top = torch.empty(n, n_top, dtype=f32, device=dev)
-    _check(lib().moe_token_logprobs(logits.data_ptr(), ACT_F32 if logits.dtype == f32 else ACT_BF16, logits.stride(0), n,
-                                    V, None if tokens is None else tokens.data_ptr(), n_top,
-                                    None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(),
-                                    ids.data_ptr(), top.data_ptr(), _stream(stream)))
+    stride, dev = logits.stride(), logits.device
+    _require(stride[1] == 1 or V == 1, "token_logprobs: each row of logits must be contiguous")
+    _require(0 <= n_top <= 32 and n_top <= V, "token_logprobs: n_top outside 0..min(32, V)")
+    lp = en = None
+    if tokens is not None:
+        _require(tokens.shape == (n,) and tokens.dtype is i32 and tokens.is_cuda and tokens.is_contiguous(),
+                 "token_logprobs: tokens must be contiguous int32 [n] on the GPU")
+        lp = torch.empty(n, dtype=f32, device=dev)
+    if entropy:
+        en = torch.empty(n, dtype=f32, device=dev)
+    ids = torch.empty((n, n_top), dtype=i32, device=dev)
+    top = torch.empty((n, n_top), dtype=f32, device=dev)
+    rc = lib().moe_token_logprobs(logits.data_ptr(), ACT_F32 if dt is f32 else ACT_BF16, stride[0], n, V,
+                                  None if tokens is None else tokens.data_ptr(), n_top,
+                                  None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(),
+                                  ids.data_ptr(), top.data_ptr(), _raw_stream(stream, logits))
+    if rc:
+        _check(rc)
     return dict(logprob=lp, entropy=en, top_ids=ids, top_logprobs=top)

@@ -95,7 +95,7 @@ struct moe_attn {
   int hq = 0, hk = 0, D = 0, P = 0, n_pages = 0, rot = 0, interleaved = 0, window = 0, act = 0;
   int T_max = 0, S_max = 0, len_max = 0;
   float eps = 0.f, scale = 0.f;
-  float* rope = nullptr;       // [len_max][2][rot/2]: cos, sin
+  float* rope = nullptr;       // [2: rounded, rest][len_max][2: cos, sin][rot/2]
   double* freq = nullptr;      // [rot/2]
   float* norm_w = nullptr;     // [2][D]: query and key weights (ones where there are none)
   bool q_norm = false, k_norm = false;

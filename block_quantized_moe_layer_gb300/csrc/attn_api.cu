@@ -16,6 +16,7 @@ cudaError_t append_launch(const moe_attn* h, const void* q, const void* k, const
 cudaError_t read_launch(const moe_attn* h, const void* pages, const int64_t* slots, int n, void* k_out, void* v_out,
                         cudaStream_t st);
 cudaError_t rope_launch(const moe_attn* h, cudaStream_t st);
+cudaError_t append_configure(const moe_attn* h);
 cudaError_t check_launch(const AttnParams& p, cudaStream_t st);
 cudaError_t small_configure();
 cudaError_t small_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
@@ -137,7 +138,7 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
       if (!(std::fabs(f[i]) <= 1e30)) return set_error(MOE_EINVAL, "moe_attn_create: freq[%d] is not finite", i);
     }
     CKA(cudaMalloc(&h->freq, half * sizeof(double)), "alloc frequencies");
-    CKA(cudaMalloc(&h->rope, (size_t)h->len_max * h->rot * sizeof(float)), "alloc rotation table");
+    CKA(cudaMalloc(&h->rope, (size_t)2 * h->len_max * h->rot * sizeof(float)), "alloc rotation table");
     CKA(cudaMemcpy(h->freq, f, half * sizeof(double), cudaMemcpyHostToDevice), "copy frequencies");
     CKA(attn::rope_launch(h, st), "rotation table");
   }
@@ -148,6 +149,7 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
     if (h->k_norm)
       CKA(cudaMemcpyAsync(h->norm_w + h->D, d->k_norm, h->D * sizeof(float), cudaMemcpyDefault, st), "copy key norm");
   }
+  CKA(attn::append_configure(h), "configure the append kernels");
   if (h->act == MOE_ACT_BF16) {
     h->part_rows = (size_t)128 * h->num_sms;
     h->ws_bytes = h->part_rows * (h->D * sizeof(float) + sizeof(float2));

@@ -9,27 +9,29 @@
 // the even fraction), c = 8 + round-half-even(y / d), clamped to 0..15; NaN is
 // stored as 0 and larger values saturate.
 //
-// Work: one row (token, head) is D/8 lanes of 8 channels, one 16-byte load a
-// lane (two for fp32); the sum of squares and the partner channels of a
-// rotation travel by shuffles, so a row is read once and written once.  The
+// Work: one row (token, head) is D/16 lanes of 16 channels, which is a scale's
+// block, two 16-byte loads a lane (four for fp32); the sum of squares (and the
+// partners of a key's rotation) travel by shuffles, so a row is read once and
+// written once.  With 16 channels a lane rather than 8, a warp's fixed costs
+// (sums, roots, addresses, the search for a scale) serve twice the rows.  The
 // bound is HBM: D (2 + 2) bytes of a query row, D (2 + 9/16) of a key or value
-// row.  The angles' cosines and sines come from the handle's table (fp32,
-// computed in fp64: far positions lose nothing), kept in registers while a
-// warp walks over heads of one token.
+// row.  A group of lanes takes up to 2 query heads of one token, which share
+// the angles' cosines and sines (from the handle's fp32 table, computed in
+// fp64: far positions lose nothing).
 //
 // Codes are those of the exact result.  fp32 leaves each y' within
 // 2^-19 (|y_a cos| + |y_b sin|) of it (a sum of squares in at most 13
-// additions, one division and square root, four products and a sum, each
-// within 2^-24); a row in which that error could change a scale or a code
-// (about one in 500) is computed again in fp64.  Values are exact already:
-// their codes are decided by exact fp32 residuals.
+// additions, its scaling, a reciprocal square root within 2 units, four
+// products and a sum); a row in which that error could change a scale or a
+// code (about one in 500) is computed again in fp64.  Values are exact
+// already: their codes are decided by exact fp32 residuals.
 #include "attn.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 struct AppendParams {
   const void *q, *k, *v;
@@ -38,11 +40,11 @@ struct AppendParams {
   const int64_t* slots;
   uint8_t* pages;
   void* q_out;  // [T][hq][D]
-  int T, hq, hk, P, pshift, n_pages, rot, interleaved, max_pos, passes;
+  int T, hq, hk, P, pshift, n_pages, rot, interleaved, max_pos;
   bool q_norm, k_norm;
-  float eps;
+  float eps, inv_d;
   const float* rope;
-  const double* freq;
+  const float* rope_lo;
   const float* norm_w;
   int64_t head_bytes, page_bytes;
   int* status;
@@ -57,260 +59,641 @@ __device__ __forceinline__ int scale_byte(T amax) {
   b = min(max(b - 1, 0), kKvMaxScale);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const T mid = (T)(3.5f * (scale_value(b) + scale_value(b + 1)));
-    b += (amax > mid || (amax == mid && (b & 1))) ? 1 : 0;
+    // next below the midpoint where a tie goes up
+    const float mid = __int_as_float(__float_as_int(3.5f * (scale_value(b) + scale_value(b + 1))) - (b & 1));
+    b += amax > (T)mid ? 1 : 0;
   }
   return min(b, kKvMaxScale);
 }
 
-// The code of x for scale d: round half even of the exact x / d, clamped.  The
-// quotient rounds; the residual x - q d does not (both are multiples of the
-// smaller unit and |x - q d| <= |x|), so comparing it with d/2 settles q.
-__device__ __forceinline__ int code_of(float x, float d) {
-  if (!(d > 0.f) || x != x) return 8;
-  float q = rintf(fminf(fmaxf(x / d, -9.f), 8.f));
-  const float r = fmaf(-q, d, x);
-  if (r > d * 0.5f) q += 1.f;
-  else if (r < d * -0.5f) q -= 1.f;
-  return (int)fminf(fmaxf(q, -8.f), 7.f) + 8;
+// The code of x for scale d (rd = 1/d rounded), plus 8388608 * 1.5 as a float:
+// its low bits are the code.  Round half even of the exact x / d, clamped: x
+// times rd picks a candidate q at most one off; the residual x - q d does not
+// round (both are multiples of the smaller unit and it is below 1.5 d), so
+// comparing it with d/2 settles q.  unsure gets the bit where an x off by err
+// could have another code (err < 0: x is exact).  Branch-free: the branches of an if form took
+// 1100 instructions a row, this takes about 300.
+constexpr float kRound = 12582912.f;  // 1.5 2^23: adding it rounds to an integer
+__device__ __forceinline__ uint32_t code_bits(float x, float d, float rd, float err, uint32_t bit, uint32_t& unsure) {
+  const float u = fminf(fmaxf(x * rd, -9.f), 8.f) + kRound;
+  float q = u - kRound;
+  const float r = fmaf(-q, d, x), h = 0.5f * d;
+  const float edge = __int_as_float(__float_as_int(h) - (__float_as_int(u) & 1));  // an odd q gives way on a tie
+  q += r > edge ? 1.f : 0.f;
+  q -= r < -edge ? 1.f : 0.f;
+  unsure |= fabsf(fabsf(r) - h) <= err ? bit : 0u;
+  return __float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + (kRound + 8.f));
 }
-__device__ __forceinline__ int code_of(double x, double d) {
-  if (!(d > 0.0) || x != x) return 8;
-  return (int)rint(fmin(fmax(x / d, -8.0), 7.0)) + 8;
+// The same for an fp64 x.
+__device__ __forceinline__ uint32_t code_bits(double x, float d, float rd) {
+  const float u = fminf(fmaxf((float)x * rd, -9.f), 8.f) + kRound;
+  float q = u - kRound;
+  const double r = fma(-(double)q, (double)d, x), h = 0.5 * d;
+  const bool odd = __float_as_int(u) & 1;
+  q += (odd ? r >= h : r > h) ? 1.f : 0.f;
+  q -= (odd ? r <= -h : r < -h) ? 1.f : 0.f;
+  return __float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + (kRound + 8.f));
 }
-
-// Nibble of channel e of eight.
-__device__ __forceinline__ uint32_t nibble(int c, int e) { return (uint32_t)c << (4 * ((e >> 1) + 4 * (e & 1))); }
-
-template <typename In>
-__device__ __forceinline__ void load8(const In* p, float (&x)[8]) {
-  if constexpr (sizeof(In) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A word of 8 codes: channel e is nibble e/2 + 4 (e%2).
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t* c) {
+  uint32_t w = 0, k = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  for (int e = 0; e < 8; ++e) {
+    const int s = 4 * ((e >> 1) + 4 * (e & 1));
+    w += c[e] << s;
+    k += 0x4B400000u << s;
   }
+  return w - k;  // without the float's exponent bits
 }
 
-template <typename Out>
-__device__ __forceinline__ void store8(Out* p, const float (&x)[8]) {
-  if constexpr (sizeof(Out) == 2) {
-    uint32_t w[4];
+// The partners of a rotation in halves (i, i + rot/2): a lane's channels 8 b
+// .. 8 b + 7 (b = 0, 1) have theirs in lane src[b], in its half b ^ odd.
+struct Partner {
+  int src[2];
+  bool rotated[2], first[2], odd;
+};
+__device__ __forceinline__ Partner partner_of(int L, int rot) {
+  Partner a;
+  const int lane = threadIdx.x & 31;
+  a.odd = (rot >> 4) & 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  for (int b = 0; b < 2; ++b) {
+    const int c = 16 * L + 8 * b;
+    a.rotated[b] = c < rot;
+    a.first[b] = c < (rot >> 1);
+    const int q = a.rotated[b] ? (a.first[b] ? c + (rot >> 1) : c - (rot >> 1)) : c;
+    a.src[b] = lane - L + (q >> 4);
   }
+  return a;
 }
 
-// A key row in fp64 (the whole warp calls it): this lane's word of codes and
-// its block's scale byte.
+// The angle index of a lane's channel i (of the first half, or its partner's).
+__device__ __forceinline__ int angle_of(int L, int i, int rot, bool interleaved) {
+  const int c = 16 * L + i;
+  return interleaved ? c >> 1 : (c < (rot >> 1) ? c : c - (rot >> 1));
+}
+
+// A key row in fp64 (the whole warp calls it): this lane's two words of codes
+// and its scale byte.  The angles' cosines and sines are the sums of two fp32
+// tables (2^-49 off; fp64 sincos of a far position costs 10 us here).
 template <int G>
-__device__ __noinline__ uint32_t key_codes_f64(const float (&x)[8], const float* w, bool norm, double eps, int D, int L,
-                                               int rot, bool interleaved, const double* freq, int pos, int& sbyte) {
-  double y[8];
+__device__ __noinline__ uint2 key_codes_f64(const float (&x)[16], const float* w, double eps, int D, int L, int rot,
+                                            bool interleaved, const float* hi, const float* lo, int& sbyte) {
+  double y[16];
   double ss = 0.0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     y[i] = x[i];
     ss = fma(y[i], y[i], ss);
   }
 #pragma unroll
   for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (norm) {
-    const double inv = 1.0 / sqrt(ss / D + eps);
+  if (w && 16 * L < D) {
+    // a reciprocal square root by two Newton steps from the fp32 one (2^-22, 2^-43, 2^-53)
+    const double v = fma(ss, 1.0 / D, eps);
+    double inv = (double)rsqrtf((float)v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * (double)w[i];
+    for (int i = 0; i < 2; ++i) inv = fma(inv * 0.5, fma(-v * inv, inv, 1.0), inv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = y[i] * inv * (double)w[16 * L + i];
   }
-  const int half = rot >> 4;  // lanes of half the rotated channels
   if (interleaved) {
-    if (8 * L < rot) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        double s, c;
-        sincos(pos * freq[4 * L + i], &s, &c);
+    for (int i = 0; i < 8; ++i)
+      if (16 * L + 2 * i < rot) {
+        const int f = 8 * L + i, g = (rot >> 1) + f;
+        const double c = (double)hi[f] + lo[f], s = (double)hi[g] + lo[g];
         const double a = y[2 * i], b = y[2 * i + 1];
         y[2 * i] = a * c - b * s;
         y[2 * i + 1] = b * c + a * s;
       }
-    }
-  } else {
-    const int lane = threadIdx.x & 31;
-    const bool first = L < half;
-    const int src = (8 * L < rot) ? lane + (first ? half : -half) : lane;
+  } else if (rot) {
+    const Partner pa = partner_of(L, rot);
+    double o[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double o = __shfl_sync(0xffffffffu, y[i], src);
-      if (8 * L < rot) {
-        double s, c;
-        sincos(pos * freq[8 * (first ? L : L - half) + i], &s, &c);
-        y[i] = first ? y[i] * c - o * s : y[i] * c + o * s;
+    for (int i = 0; i < 16; ++i) o[i] = __shfl_sync(0xffffffffu, pa.odd ? y[i ^ 8] : y[i], pa.src[i >> 3]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (pa.rotated[i >> 3]) {
+        const int f = angle_of(L, i, rot, false), g = (rot >> 1) + f;
+        const double c = (double)hi[f] + lo[f], s = (double)hi[g] + lo[g];
+        y[i] = pa.first[i >> 3] ? y[i] * c - o[i] * s : y[i] * c + o[i] * s;
       }
-    }
   }
   double amax = 0.0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmax(amax, fabs(y[i]));
-  amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  for (int i = 0; i < 16; ++i) {
+    if (y[i] != y[i]) y[i] = 0.0;
+    amax = fmax(amax, fabs(y[i]));
+  }
   sbyte = scale_byte<double>(amax);
-  const double d = (double)scale_value(sbyte);
-  uint32_t word = 0;
+  const float d = scale_value(sbyte);
+  if (!(d > 0.f)) return make_uint2(0x88888888u, 0x88888888u);
+  const float rd = 1.f / d;
+  uint32_t c[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) word |= nibble(code_of(y[i], d), i);
-  return word;
+  for (int i = 0; i < 16; ++i) c[i] = code_bits(y[i], d, rd);
+  return make_uint2(pack_codes(c), pack_codes(c + 8));
 }
 
-// G lanes a row: 8 (D = 64), 16 (128) or 32 (192: 24 of them hold channels; 256).
-template <int G, typename In, typename Out>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p, int D) {
-  griddep_launch_dependents();
+// x_hi + x_lo: the sum of squares of a lane's channels, each step's rounding
+// error kept (two-sum; the square's own by an fma).
+__device__ __forceinline__ double square_sum(const float (&x)[16]) {
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float sq = x[i] * x[i], e = fmaf(x[i], x[i], -sq);
+    const float s = hi + sq, b = s - hi;
+    lo += ((hi - (s - b)) + (sq - b)) + e;
+    hi = s;
+  }
+  return (double)hi + (double)lo;
+}
+
+__device__ __forceinline__ float pick(const float (&x)[16], int i) {
+  float v = x[0];
+#pragma unroll
+  for (int k = 1; k < 16; ++k) v = i == k ? x[k] : v;
+  return v;
+}
+
+// Decides the codes marked in each lane's `mask` in fp64 (the whole warp calls
+// it), one channel a turn: the row's sum, that channel and its partner.  A row
+// with one channel at a border pays some 25 dependent fp64 instructions
+// instead of the 400 of key_codes_f64, whose 10 us would be most of a small call.
+template <int G>
+__device__ __noinline__ void settle_codes(const float (&x)[16], const float* w, double eps, int D, int L, int rot,
+                                          bool interleaved, const float* hi, const float* lo, float d, uint32_t mask, uint2& words) {
   const int lane = threadIdx.x & 31;
-  const int L = lane & (G - 1);  // lane of the row
-  const int t = blockIdx.x;
-  constexpr int kRows = kAppendThreads / G;  // rows of a pass
-  const bool holds = 8 * L < D;
-  const int half = p.rot >> 4;
-  const bool rotated = 8 * L < p.rot;
-  const bool first = L < half;
-  griddep_wait();  // the projections and positions may come from the previous kernel
-  const int pos = p.positions[t];
-  const int64_t slot = p.slots[t];
-  const bool pos_ok = pos >= 0 && pos < p.max_pos;
-  const bool slot_ok = slot >= 0 && slot < ((int64_t)p.n_pages << p.pshift);
-  if (threadIdx.x == 0 && blockIdx.y == 0) {
-    if (!pos_ok) atomicOr(p.status, kBadPosition);
-    if (slot >= 0 && !slot_ok) atomicOr(p.status, kBadSlot);
-  }
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  if (rotated && pos_ok) {
-    const float* r = p.rope + (int64_t)pos * p.rot;
-    if (p.interleaved) {  // four angles
-      const float4 c4 = *reinterpret_cast<const float4*>(r + 4 * L);
-      const float4 s4 = *reinterpret_cast<const float4*>(r + (p.rot >> 1) + 4 * L);
-      cs[0] = c4.x; cs[1] = c4.y; cs[2] = c4.z; cs[3] = c4.w;
-      sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
-    } else {
-      const int f = 8 * (first ? L : L - half);
-      load8<float>(r + f, cs);
-      load8<float>(r + (p.rot >> 1) + f, sn);
-    }
-  }
-  const int heads = p.hq + 2 * p.hk;
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int h = (blockIdx.y * p.passes + pass) * kRows + threadIdx.x / G;
-    if (((blockIdx.y * p.passes + pass) * kRows + (threadIdx.x & ~31) / G) >= heads) break;  // the whole warp is past the heads
-    const bool valid = h < heads;
-    const int kind = h < p.hq ? 0 : (h < p.hq + p.hk ? 1 : 2);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (valid && holds) {
-      const In* src;
-      if (kind == 0) src = static_cast<const In*>(p.q) + t * p.q_tok + h * p.q_head;
-      else if (kind == 1) src = static_cast<const In*>(p.k) + t * p.k_tok + (h - p.hq) * p.k_head;
-      else src = static_cast<const In*>(p.v) + t * p.v_tok + (h - p.hq - p.hk) * p.v_head;
-      load8<In>(src + 8 * L, x);
-    }
-    const bool norm = kind == 0 ? p.q_norm : (kind == 1 ? p.k_norm : false);
-    float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    if (norm && holds) load8<float>(p.norm_w + (kind == 1 ? D : 0) + 8 * L, w);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+  double inv = 1.0;
+  if (w) {
+    double ss = square_sum(x);
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    float y[8];
-    const float inv = norm ? 1.f / sqrtf(ss / (float)D + p.eps) : 1.f;
+    const double v = fma(ss, 1.0 / D, eps);
+    inv = (double)rsqrtf((float)v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = norm ? x[i] * inv * w[i] : x[i];
-    // rotation (values stay): err bounds what fp32 lost of each channel
-    float z[8], mag[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = y[i], mag[i] = norm ? fabsf(y[i]) : 0.f;
-    if (p.interleaved) {
-      if (rotated && kind != 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = y[2 * i], b = y[2 * i + 1];
-          z[2 * i] = a * cs[i] - b * sn[i];
-          z[2 * i + 1] = b * cs[i] + a * sn[i];
-          mag[2 * i] = fabsf(a * cs[i]) + fabsf(b * sn[i]);
-          mag[2 * i + 1] = fabsf(b * cs[i]) + fabsf(a * sn[i]);
-        }
-      }
-    } else {
-      const int src = rotated ? lane + (first ? half : -half) : lane;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xffffffffu, y[i], src);
-        if (rotated && kind != 2) {
-          z[i] = first ? y[i] * cs[i] - o * sn[i] : y[i] * cs[i] + o * sn[i];
-          mag[i] = fabsf(y[i] * cs[i]) + fabsf(o * sn[i]);
-        }
-      }
+    for (int i = 0; i < 2; ++i) inv = fma(inv * 0.5, fma(-v * inv, inv, 1.0), inv);
+  }
+  for (uint32_t any; (any = __ballot_sync(0xffffffffu, mask != 0)) != 0;) {
+    const int who = __ffs(any) - 1, Lw = who & (G - 1);
+    const int i = __shfl_sync(0xffffffffu, __ffs(mask) - 1, who);
+    const int c = 16 * Lw + i;
+    const bool rotated = c < rot;
+    const bool first = interleaved ? !(c & 1) : c < (rot >> 1);
+    const int q = !rotated ? c : (interleaved ? c ^ 1 : (first ? c + (rot >> 1) : c - (rot >> 1)));
+    double y = __shfl_sync(0xffffffffu, pick(x, i), who);
+    double z = __shfl_sync(0xffffffffu, pick(x, q & 15), who - Lw + (q >> 4));
+    const double iw = __shfl_sync(0xffffffffu, inv, who);
+    if (w) {
+      y = y * iw * (double)w[c];
+      z = z * iw * (double)w[q];
     }
-    if (kind == 0) {
-      if (valid && holds) {
-        if (!pos_ok) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = 0.f;
-        }
-        store8<Out>(static_cast<Out*>(p.q_out) + ((int64_t)t * p.hq + h) * D + 8 * L, z);
-      }
+    if (rotated) {
+      const int f = interleaved ? c >> 1 : (first ? c : q), g = (rot >> 1) + f;
+      const double cs = (double)hi[f] + lo[f], sn = (double)hi[g] + lo[g];
+      y = first ? y * cs - z * sn : y * cs + z * sn;
     }
-    const bool stores = valid && kind != 0 && slot_ok && pos_ok;
-    if (!__any_sync(0xffffffffu, stores)) continue;
-    float amax = 0.f, emax = 0.f;
-    // position 0 turns nothing, and a row without a norm is exact there
-    const bool inexact = norm || pos != 0;
-    float err[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      err[i] = inexact ? mag[i] * 0x1p-19f : 0.f;
-      amax = fmaxf(amax, fabsf(z[i]));
-      emax = fmaxf(emax, err[i]);
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, 1));
-    int sb = scale_byte<float>(amax);
-    bool unsure = false;
-    if (emax > 0.f) unsure = scale_byte<float>(amax - emax) != sb || scale_byte<float>(amax + emax) != sb;
-    const float d = scale_value(sb);
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = code_of(z[i], d);
-      if (err[i] > 0.f) unsure |= code_of(z[i] - err[i], d) != c || code_of(z[i] + err[i], d) != c;
-      word |= nibble(c, i);
-    }
-    unsure = unsure && kind == 1 && stores;
-    if (__any_sync(0xffffffffu, unsure)) {
-      int sb2;
-      const uint32_t word2 = key_codes_f64<G>(x, w, norm, (double)p.eps, D, L, p.rot, p.interleaved != 0, p.freq, pos, sb2);
-      if (kind == 1) word = word2, sb = sb2;
-    }
-    if (stores && holds) {
-      const int pg = (int)(slot >> p.pshift), at = (int)(slot & (p.P - 1));
-      const int hh = kind == 1 ? h - p.hq : h - p.hq - p.hk;
-      uint8_t* base = p.pages + pg * p.page_bytes + hh * p.head_bytes + (kind == 2 ? p.head_bytes / 2 : 0);
-      *reinterpret_cast<uint32_t*>(base + at * (D / 2) + 4 * L) = word;
-      if (!(L & 1)) base[p.P * (D / 2) + at * (D / 16) + (L >> 1)] = (uint8_t)sb;
+    if (lane == who) {
+      const uint32_t code = code_bits(y, d, 1.f / d) & 15u;
+      const int e = i & 7, s = 4 * ((e >> 1) + 4 * (e & 1));
+      uint32_t& word = i < 8 ? words.x : words.y;
+      word = (word & ~(15u << s)) | (code << s);
+      mask &= mask - 1;
     }
   }
+}
+
+// Two floats in a register pair: the packed fp32 instructions halve the
+// arithmetic of a row, which is what bounds it after HBM.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_get(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void copy16(void* smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's 16-byte pieces of the rows it works on: kAhead tokens are on
+// their way in shared memory while one is worked on.  Each thread reads only
+// what it copied itself; a warp shares its token's angles.
+constexpr int kAhead = 3;
+constexpr int kRing = kAhead + 1;
+
+// Eight channels from a thread's pieces, as four pairs.
+__device__ __forceinline__ void pairs8(const uint4* s, uint64_t* a, __nv_bfloat16*) {
+  const uint4 u = *s;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void pairs8(const uint4* s, uint64_t* a, float*) {
+  const uint4 u = s[0], v = s[kAppendThreads];
+  a[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+  a[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+  a[2] = f2(__uint_as_float(v.x), __uint_as_float(v.y));
+  a[3] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename In>
+__device__ __forceinline__ void copy8(uint4* s, const In* p) {
+  copy16(s, p);
+  if (sizeof(In) == 4) copy16(s + kAppendThreads, p + 4);
+}
+// A warp's copy of the angles of a position: cos [rot/2], sin [rot/2].
+__device__ __forceinline__ void copy_angles(float* s, const AppendParams& p, int pos) {
+  if (pos < 0 || pos >= p.max_pos) return;
+  const float* r = p.rope + (int64_t)pos * p.rot;
+  for (int i = 4 * (threadIdx.x & 31); i < p.rot; i += 128) copy16(s + i, r + i);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint64_t* a) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x, y;
+    f2_get(a[i], x, y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const uint64_t* a) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_get(a[i], x[2 * i], x[2 * i + 1]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// The query heads [h0, h0 + NB) of tokens t, t + step, ..., by the G lanes of
+// a group.  Of the rotated channels a lane takes 8 and their 8 partners, so
+// that a rotation needs no exchange; of the others 16 neighbours.
+template <int G, int NB, typename In, typename Out>
+__device__ __forceinline__ void query_heads(const AppendParams& p, int D, int t, int step, int h0, int L, const float* w_sm,
+                                            uint4* ring, float* rope_sm) {
+  const int rows = min(NB, p.hq - h0);
+  const bool holds = 16 * L < D && rows > 0, rotated = 16 * L < p.rot, pairs = rotated && !p.interleaved;
+  const int c0 = pairs ? 8 * L : 16 * L, c1 = pairs ? (p.rot >> 1) + 8 * L : 16 * L + 8;
+  constexpr int kPieces = NB * 2 * (sizeof(In) / 2);
+  const In* q = static_cast<const In*>(p.q) + t * p.q_tok + h0 * p.q_head;
+  Out* out = static_cast<Out*>(p.q_out) + ((int64_t)t * p.hq + h0) * D;
+  const int64_t q_step = step * p.q_tok, o_step = (int64_t)step * p.hq * D;
+  uint4* mine = ring + threadIdx.x;
+  auto issue = [&](int slot, int at, int pos) {  // token `at` into a slot
+    if (at < p.T) {
+      if (holds) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          if (i < rows) {
+            uint4* s = mine + (slot * kPieces + i * (kPieces / NB)) * kAppendThreads;
+            copy8(s, q + i * p.q_head + c0);
+            copy8(s + kPieces / NB / 2 * kAppendThreads, q + i * p.q_head + c1);
+          }
+      }
+      copy_angles(rope_sm + slot * p.rot, p, pos);
+    }
+    copies_commit();
+    q += q_step;
+  };
+  auto position = [&](int at) { return at < p.T ? p.positions[at] : -1; };
+  int pq[kRing];  // positions of tokens t, t + step, ...
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) pq[i] = position(t + i * step);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) issue(i, t + i * step, pq[i]);
+  for (int slot = 0; t < p.T; t += step, slot = slot + 1 == kRing ? 0 : slot + 1) {
+    const int after = position(t + kRing * step);
+    issue(slot == 0 ? kRing - 1 : slot - 1, t + kAhead * step, pq[kAhead]);
+    copies_wait<kAhead>();
+    __syncwarp();
+    const bool pos_ok = pq[0] >= 0 && pq[0] < p.max_pos;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) pq[i] = pq[i + 1];
+    pq[kAhead] = after;
+    uint64_t x[NB][8];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const uint4* s = mine + (slot * kPieces + i * (kPieces / NB)) * kAppendThreads;
+      pairs8(s, x[i], (In*)nullptr);
+      pairs8(s + kPieces / NB / 2 * kAppendThreads, x[i] + 4, (In*)nullptr);
+      if (!holds) {  // lanes past the channels add nothing to the sum
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] = 0;
+      }
+    }
+    uint64_t cs[4], sn[4];
+    if (rotated) {
+      const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(rope_sm + slot * p.rot + 8 * L);
+      const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(rope_sm + slot * p.rot + (p.rot >> 1) + 8 * L);
+      cs[0] = c2[0].x; cs[1] = c2[0].y; cs[2] = c2[1].x; cs[3] = c2[1].y;
+      sn[0] = s2[0].x; sn[1] = s2[0].y; sn[2] = s2[1].x; sn[3] = s2[1].y;
+    }
+    __syncwarp();  // the warp has its angles before the slot is filled again
+    if (p.q_norm) {
+      float ss[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        uint64_t s2 = f2_mul(x[i][0], x[i][0]);
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s2 = f2_fma(x[i][k], x[i][k], s2);
+        float s1;
+        f2_get(s2, ss[i], s1);
+        ss[i] += s1;
+      }
+#pragma unroll
+      for (int o = G / 2; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+      uint64_t i2[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const float inv = rsqrtf(fmaf(ss[i], p.inv_d, p.eps));
+        i2[i] = f2(inv, inv);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(w_sm + (k < 2 ? c0 + 4 * k : c1 + 4 * (k - 2)));
+        const uint64_t w0 = f2(v.x, v.y), w1 = f2(v.z, v.w);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          x[i][2 * k] = f2_mul(x[i][2 * k], f2_mul(i2[i], w0));
+          x[i][2 * k + 1] = f2_mul(x[i][2 * k + 1], f2_mul(i2[i], w1));
+        }
+      }
+    }
+    if (rotated) {
+      if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // pairs 2k, 2k + 1: (x0 x1) (x2 x3) -> (x0 x2) (x1 x3)
+            float a, b, c, d;
+            f2_get(x[i][2 * k], a, b);
+            f2_get(x[i][2 * k + 1], c, d);
+            const uint64_t u = f2(a, c), v = f2(b, d);
+            const uint64_t nv = f2(-b, -d);
+            f2_get(f2_fma(nv, sn[k], f2_mul(u, cs[k])), a, c);
+            f2_get(f2_fma(u, sn[k], f2_mul(v, cs[k])), b, d);
+            x[i][2 * k] = f2(a, b);
+            x[i][2 * k + 1] = f2(c, d);
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float s0, s1;
+          f2_get(sn[k], s0, s1);
+          const uint64_t ns = f2(-s0, -s1);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint64_t u = x[i][k], v = x[i][4 + k];
+            x[i][k] = f2_fma(v, ns, f2_mul(u, cs[k]));
+            x[i][4 + k] = f2_fma(u, sn[k], f2_mul(v, cs[k]));
+          }
+        }
+      }
+    }
+    if (!pos_ok) {  // a position outside the table: zeros
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] = 0;
+    }
+    if (holds) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        if (i < rows) {
+          store8(out + i * D + c0, x[i]);
+          store8(out + i * D + c1, x[i] + 4);
+        }
+    }
+    out += o_step;
+  }
+}
+
+// The key head h < hk or value head h - hk of tokens t, t + step, ..., a lane
+// a scale's 16 channels.
+template <int G, typename In>
+__device__ __forceinline__ void cache_heads(const AppendParams& p, int D, int t, int step, int h, int L, const float* w_sm,
+                                            uint4* ring, float* rope_sm) {
+  const bool key = h < p.hk, valid = h < 2 * p.hk, holds = valid && 16 * L < D;
+  const In* src = key ? static_cast<const In*>(p.k) + t * p.k_tok + h * p.k_head
+                      : static_cast<const In*>(p.v) + t * p.v_tok + (h - p.hk) * p.v_head;
+  const int64_t src_step = step * (key ? p.k_tok : p.v_tok);
+  const bool keys = __any_sync(0xffffffffu, key);
+  const int64_t head = (key ? h : h - p.hk) * p.head_bytes + (key ? 0 : p.head_bytes / 2);
+  constexpr int kPieces = 2 * (sizeof(In) / 2);
+  uint4* mine = ring + threadIdx.x;
+  auto issue = [&](int slot, int at, int pos) {
+    if (at < p.T) {
+      if (holds) {
+        copy8(mine + slot * kPieces * kAppendThreads, src + 16 * L);
+        copy8(mine + (slot * kPieces + kPieces / 2) * kAppendThreads, src + 16 * L + 8);
+      }
+      if (keys) copy_angles(rope_sm + slot * p.rot, p, pos);
+    }
+    copies_commit();
+    src += src_step;
+  };
+  auto position = [&](int at) { return at < p.T ? p.positions[at] : -1; };
+  int pq[kRing];  // positions of tokens t, t + step, ...
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) pq[i] = position(t + i * step);
+  int64_t slot_n = p.slots[t];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) issue(i, t + i * step, pq[i]);
+  for (int at = 0; t < p.T; t += step, at = at + 1 == kRing ? 0 : at + 1) {
+    const int after = position(t + kRing * step);
+    issue(at == 0 ? kRing - 1 : at - 1, t + kAhead * step, pq[kAhead]);
+    const int64_t my_slot = slot_n;
+    if (t + step < p.T) slot_n = p.slots[t + step];
+    copies_wait<kAhead>();
+    __syncwarp();
+    const int my_pos = pq[0];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) pq[i] = pq[i + 1];
+    pq[kAhead] = after;
+    float x[16], y[16], err[16];
+    {
+      uint64_t u[8];
+      pairs8(mine + at * kPieces * kAppendThreads, u, (In*)nullptr);
+      pairs8(mine + (at * kPieces + kPieces / 2) * kAppendThreads, u + 4, (In*)nullptr);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f2_get(u[i], x[2 * i], x[2 * i + 1]);
+        x[2 * i] = holds ? x[2 * i] : 0.f;
+        x[2 * i + 1] = holds ? x[2 * i + 1] : 0.f;
+      }
+    }
+    const float* rope = rope_sm + at * p.rot;
+    const bool pos_ok = my_pos >= 0 && my_pos < p.max_pos;
+    const bool slot_ok = my_slot >= 0 && my_slot < ((int64_t)p.n_pages << p.pshift);
+    if (h == 0 && L == 0) {
+      if (!pos_ok) atomicOr(p.status, kBadPosition);
+      if (my_slot >= 0 && !slot_ok) atomicOr(p.status, kBadSlot);
+    }
+    if (!slot_ok || !pos_ok) {  // (all lanes)
+      __syncwarp();
+      continue;
+    }
+    float emax = -1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = x[i], err[i] = -1.f;
+    if (keys) {
+      float mag[16];
+      const bool norm = p.k_norm && holds;
+      if (p.k_norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        if (norm) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 w = *reinterpret_cast<const float4*>(w_sm + 16 * L + 4 * k);
+            y[4 * k] *= inv * w.x;
+            y[4 * k + 1] *= inv * w.y;
+            y[4 * k + 2] *= inv * w.z;
+            y[4 * k + 3] *= inv * w.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mag[i] = norm ? fabsf(y[i]) : 0.f;
+      if (p.interleaved) {
+        if (16 * L < p.rot) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float c = rope[8 * L + i], s = rope[(p.rot >> 1) + 8 * L + i];
+            const float a = y[2 * i], b = y[2 * i + 1];
+            y[2 * i] = a * c - b * s;
+            y[2 * i + 1] = b * c + a * s;
+            mag[2 * i] = fabsf(a * c) + fabsf(b * s);
+            mag[2 * i + 1] = fabsf(b * c) + fabsf(a * s);
+          }
+        }
+      } else if (p.rot) {
+        const Partner pa = partner_of(L, p.rot);
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __shfl_sync(0xffffffffu, pa.odd ? y[i ^ 8] : y[i], pa.src[i >> 3]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (pa.rotated[b]) {
+            const float4* cr = reinterpret_cast<const float4*>(rope + angle_of(L, 8 * b, p.rot, false));
+            const float4* sr = reinterpret_cast<const float4*>(rope + (p.rot >> 1) + angle_of(L, 8 * b, p.rot, false));
+            const float4 c4[2] = {cr[0], cr[1]}, s4[2] = {sr[0], sr[1]};
+            const float c[8] = {c4[0].x, c4[0].y, c4[0].z, c4[0].w, c4[1].x, c4[1].y, c4[1].z, c4[1].w};
+            const float s[8] = {s4[0].x, s4[0].y, s4[0].z, s4[0].w, s4[1].x, s4[1].y, s4[1].z, s4[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float u = y[8 * b + i] * c[i], v = o[8 * b + i] * s[i];
+              y[8 * b + i] = pa.first[b] ? u - v : u + v;
+              mag[8 * b + i] = fabsf(u) + fabsf(v);
+            }
+          }
+      }
+      // exact: values, zeros, and without a norm what position 0 turns by nothing
+      const bool inexact = key && (norm || my_pos != 0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        y[i] = key ? y[i] : x[i];
+        err[i] = inexact && mag[i] > 0.f ? mag[i] * 0x1p-19f : -1.f;
+        emax = fmaxf(emax, err[i]);
+      }
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      y[i] = y[i] == y[i] ? y[i] : 0.f;
+      amax = fmaxf(amax, fabsf(y[i]));
+    }
+    int sb = scale_byte<float>(amax);
+    const float d = scale_value(sb);
+    bool border = fabsf(amax - 3.5f * (d + scale_value(sb + 1))) <= emax;
+    border |= fabsf(amax - 3.5f * (d + scale_value(max(sb - 1, 0)))) <= emax;
+    border &= emax > 0.f;  // (a row of zeros is exact)
+    const float rd = 1.f / fmaxf(d, 0x1p-17f);
+    uint32_t c[16], unsure = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[i] = code_bits(y[i], d, rd, err[i], 1u << i, unsure);
+    uint2 words = d > 0.f ? make_uint2(pack_codes(c), pack_codes(c + 8)) : make_uint2(0x88888888u, 0x88888888u);
+    if (!(d > 0.f)) unsure = 0;
+    if (keys && __any_sync(0xffffffffu, border || unsure)) {
+      const float* hi = p.rope + (int64_t)my_pos * p.rot;
+      const float* lo = p.rope_lo + (int64_t)my_pos * p.rot;
+      const float* w = p.k_norm ? w_sm : nullptr;
+      if (__any_sync(0xffffffffu, border)) {
+        int sb2;
+        const uint2 words2 = key_codes_f64<G>(x, w, (double)p.eps, D, L, p.rot, p.interleaved != 0, hi, lo, sb2);
+        if (key) words = words2, sb = sb2;
+      } else {
+        settle_codes<G>(x, w, (double)p.eps, D, L, p.rot, p.interleaved != 0, hi, lo, d, unsure, words);
+      }
+    }
+    __syncwarp();  // the warp has its angles before the slot is filled again
+    if (holds) {
+      const int64_t pg = my_slot >> p.pshift;
+      const int at = (int)(my_slot & (p.P - 1));
+      uint8_t* base = p.pages + pg * p.page_bytes + head;
+      *reinterpret_cast<uint2*>(base + at * (D / 2) + 8 * L) = words;
+      base[p.P * (D / 2) + at * (D / 16) + L] = (uint8_t)sb;
+    }
+  }
+}
+
+template <int NB, typename In>
+__host__ __device__ constexpr int append_pieces() {
+  return NB * 2 * (int)(sizeof(In) / 2);
+}
+
+// G lanes a row: 4 (D = 64), 8 (128) or 16 (192: 12 of them hold channels;
+// 256).  A block takes one part of the heads (NB query heads a group, or a key
+// or value head a group) of every step-th token: its next rows
+// and // angles are on their way while it works on a token (a block a token and part
+// instead spent 3 us on each, waiting for its position, then its angles).
+template <int G, int NB, typename In, typename Out>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p, int D, int q_parts, int q_tokens,
+                                                                int kv_parts, int kv_tokens) {
+  extern __shared__ __align__(16) uint4 ring[];  // [slot][piece][thread], then the warps' angles [warp][slot][rot]
+  __shared__ __align__(16) float w_sm[256];
+  griddep_launch_dependents();
+  constexpr int kRows = kAppendThreads / G;  // groups of the block
+  const int L = threadIdx.x & (G - 1), group = threadIdx.x / G;
+  // blocks of keys and values come first: theirs is the longer work
+  const int b = (int)blockIdx.x - kv_parts * kv_tokens;
+  const bool queries = b >= 0;
+  const int part = queries ? b % q_parts : (int)blockIdx.x % kv_parts;
+  const int t = queries ? b / q_parts : (int)blockIdx.x / kv_parts, step = queries ? q_tokens : kv_tokens;
+  if (queries ? p.q_norm : p.k_norm)
+    for (int i = threadIdx.x; i < D; i += kAppendThreads) w_sm[i] = p.norm_w[(queries ? 0 : D) + i];
+  __syncthreads();
+  griddep_wait();  // the projections and positions may come from the previous kernel
+  float* rope_sm = reinterpret_cast<float*>(ring + kRing * append_pieces<NB, In>() * kAppendThreads) +
+                   (threadIdx.x >> 5) * kRing * p.rot;
+  if (queries) query_heads<G, NB, In, Out>(p, D, t, step, (part * kRows + group) * NB, L, w_sm, ring, rope_sm);
+  else cache_heads<G, In>(p, D, t, step, part * kRows + group, L, w_sm, ring, rope_sm);
 }
 
 // Rows of the cache as bf16 values: one thread a word of 8 channels.
@@ -350,27 +733,66 @@ __global__ void __launch_bounds__(256) read_kernel(const uint8_t* __restrict__ p
   }
 }
 
-// cos and sin of position times frequency, in fp64, rounded once to fp32.
-__global__ void rope_kernel(const double* __restrict__ freq, int half, int n, float* __restrict__ rope) {
+// cos and sin of position times frequency, in fp64: rounded to fp32, and the
+// rest (for the rows that are decided in fp64).
+__global__ void rope_kernel(const double* __restrict__ freq, int half, int n, float* __restrict__ hi, float* __restrict__ lo) {
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)n * half;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t pos = i / half;
-    const int f = (int)(i % half);
+    const int64_t at = i / half * 2 * half + i % half;
     double s, c;
-    sincos((double)pos * freq[f], &s, &c);
-    rope[pos * 2 * half + f] = (float)c;
-    rope[pos * 2 * half + half + f] = (float)s;
+    sincos((double)(i / half) * freq[i % half], &s, &c);
+    hi[at] = (float)c;
+    lo[at] = (float)(c - (double)(float)c);
+    hi[at + half] = (float)s;
+    lo[at + half] = (float)(s - (double)(float)s);
   }
 }
 
-template <int G, typename In>
-cudaError_t append_out(const AppendParams& p, int D, bool out_f32, dim3 grid, cudaStream_t st) {
-  if (out_f32) return launch_pdl(append_kernel<G, In, float>, grid, kAppendThreads, 0, st, p, D);
-  return launch_pdl(append_kernel<G, In, __nv_bfloat16>, grid, kAppendThreads, 0, st, p, D);
+constexpr int kAppendBlocks = 5;  // resident on a multiprocessor (96 registers a thread)
+
+template <int NB, typename In>
+size_t append_smem(int rot) {
+  return (size_t)kRing * append_pieces<NB, In>() * kAppendThreads * 16 + (size_t)(kAppendThreads / 32) * kRing * rot * sizeof(float);
+}
+template <int G, typename In, typename Out>
+cudaError_t append_rows(const AppendParams* p, int D, int num_sms, cudaStream_t st) {
+  if (!p) {  // configure
+    cudaError_t e = cudaFuncSetAttribute(append_kernel<G, 2, In, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)append_smem<2, In>(256));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(append_kernel<G, 1, In, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)append_smem<1, In>(256));
+  }
+  constexpr int kRows = kAppendThreads / G;
+  const int kv_parts = (2 * p->hk + kRows - 1) / kRows;
+  const int q_two = (p->hq + 2 * kRows - 1) / (2 * kRows), q_one = (p->hq + kRows - 1) / kRows;
+  // two query rows a group once their blocks still fill the GPU
+  const int64_t places = (int64_t)kAppendBlocks * num_sms;
+  const bool two = (int64_t)p->T * (q_two + kv_parts) >= places;
+  const int q_parts = two ? q_two : q_one;
+  // tokens worked on at once: a token of keys and values takes a block about
+  // twice the time of two query rows a group (3.5 against 1.6 us, both bound by
+  // their instructions' latency), so they get twice the blocks
+  const int64_t q_tokens = std::min<int64_t>(p->T, std::max<int64_t>(1, places / (q_parts + 2 * kv_parts)));
+  const int64_t kv_tokens = std::min<int64_t>(p->T, std::max<int64_t>(1, (places - q_parts * q_tokens) / kv_parts));
+  const dim3 grid((unsigned)(q_tokens * q_parts + kv_tokens * kv_parts));
+  if (two)
+    return launch_pdl(append_kernel<G, 2, In, Out>, grid, kAppendThreads, append_smem<2, In>(p->rot), st, *p, D, q_parts,
+                      (int)q_tokens, kv_parts, (int)kv_tokens);
+  return launch_pdl(append_kernel<G, 1, In, Out>, grid, kAppendThreads, append_smem<1, In>(p->rot), st, *p, D, q_parts,
+                    (int)q_tokens, kv_parts, (int)kv_tokens);
 }
 template <int G>
-cudaError_t append_in(const AppendParams& p, int D, bool in_f32, bool out_f32, dim3 grid, cudaStream_t st) {
-  return in_f32 ? append_out<G, float>(p, D, out_f32, grid, st) : append_out<G, __nv_bfloat16>(p, D, out_f32, grid, st);
+cudaError_t append_types(const AppendParams* p, int D, bool in_f32, bool out_f32, int num_sms, cudaStream_t st) {
+  if (in_f32)
+    return out_f32 ? append_rows<G, float, float>(p, D, num_sms, st) : append_rows<G, float, __nv_bfloat16>(p, D, num_sms, st);
+  return out_f32 ? append_rows<G, __nv_bfloat16, float>(p, D, num_sms, st)
+                 : append_rows<G, __nv_bfloat16, __nv_bfloat16>(p, D, num_sms, st);
+}
+cudaError_t append_any(const AppendParams* p, int D, bool in_f32, bool out_f32, int num_sms, cudaStream_t st) {
+  if (D == 64) return append_types<4>(p, D, in_f32, out_f32, num_sms, st);
+  if (D == 128) return append_types<8>(p, D, in_f32, out_f32, num_sms, st);
+  return append_types<16>(p, D, in_f32, out_f32, num_sms, st);
 }
 
 }  // namespace
@@ -390,21 +812,17 @@ cudaError_t append_launch(const moe_attn* h, const void* q, const void* k, const
   p.pshift = 31 - __builtin_clz((unsigned)h->P);
   p.rot = h->rot; p.interleaved = h->interleaved; p.max_pos = h->len_max;
   p.q_norm = h->q_norm; p.k_norm = h->k_norm; p.eps = h->eps;
-  p.rope = h->rope; p.freq = h->freq; p.norm_w = h->norm_w;
+  p.inv_d = 1.f / (float)h->D;
+  p.rope = h->rope; p.rope_lo = h->rope + (int64_t)h->len_max * h->rot; p.norm_w = h->norm_w;
   p.head_bytes = h->head_bytes; p.page_bytes = h->page_bytes;
   p.status = h->status;
-  const int G = h->D == 64 ? 8 : (h->D == 128 ? 16 : 32);
-  const int rows = kAppendThreads / G, heads = h->hq + 2 * h->hk;
-  const int all = (heads + rows - 1) / rows;
-  // passes of a block over a token's heads: one while the blocks do not fill
-  // the GPU, more where that keeps the angles in registers
-  p.passes = 1;
-  while (p.passes < all && (int64_t)T * ((all + 2 * p.passes - 1) / (2 * p.passes)) >= 16LL * h->num_sms) p.passes *= 2;
-  const dim3 grid(T, (all + p.passes - 1) / p.passes);
-  const bool out_f32 = h->act == MOE_ACT_F32;
-  if (G == 8) return append_in<8>(p, h->D, in_f32, out_f32, grid, st);
-  if (G == 16) return append_in<16>(p, h->D, in_f32, out_f32, grid, st);
-  return append_in<32>(p, h->D, in_f32, out_f32, grid, st);
+  return append_any(&p, h->D, in_f32, h->act == MOE_ACT_F32, h->num_sms, st);
+}
+
+// Lets the kernels of a handle use their shared memory.
+cudaError_t append_configure(const moe_attn* h) {
+  const cudaError_t e = append_any(nullptr, h->D, false, h->act == MOE_ACT_F32, 0, nullptr);
+  return e != cudaSuccess ? e : append_any(nullptr, h->D, true, h->act == MOE_ACT_F32, 0, nullptr);
 }
 
 cudaError_t read_launch(const moe_attn* h, const void* pages, const int64_t* slots, int n, void* k_out, void* v_out,
@@ -419,7 +837,7 @@ cudaError_t read_launch(const moe_attn* h, const void* pages, const int64_t* slo
 cudaError_t rope_launch(const moe_attn* h, cudaStream_t st) {
   if (!h->rot) return cudaSuccess;
   rope_kernel<<<(unsigned)std::min<int64_t>(((int64_t)h->len_max * h->rot / 2 + 255) / 256, 4096), 256, 0, st>>>(
-      h->freq, h->rot / 2, h->len_max, h->rope);
+      h->freq, h->rot / 2, h->len_max, h->rope, h->rope + (int64_t)h->len_max * h->rot);
   return cudaGetLastError();
 }
 
