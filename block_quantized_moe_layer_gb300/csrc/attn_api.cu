@@ -20,6 +20,8 @@ cudaError_t append_configure(const moe_attn* h);
 cudaError_t check_launch(const AttnParams& p, cudaStream_t st);
 cudaError_t small_configure();
 cudaError_t small_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
+cudaError_t verify_configure(int D);
+cudaError_t verify_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
 size_t prompt_ws_bytes(int D, int tile_cap);
 cudaError_t prompt_configure();
 cudaError_t prompt_launch(const AttnParams& p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st);
@@ -39,9 +41,9 @@ int cuda_fail(cudaError_t e, const char* what) {
     if (e_ != cudaSuccess) return cuda_fail(e_, what); \
   } while (0)
 
-// Rows (query tokens times query heads of a key/value head) up to which a
-// call runs on the small-row kernel.
-constexpr int kSmallCallRows = 64;
+// Rows (query tokens times query heads of a key/value head) of a sequence up
+// to which a call runs on the small-row kernel, and on the verify kernel.
+constexpr int kSmallCallRows = 16, kVerifyCallRows = 128;
 
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 bool page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
@@ -153,7 +155,9 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
   if (h->act == MOE_ACT_BF16) {
     h->part_rows = (size_t)128 * h->num_sms;
     h->ws_bytes = h->part_rows * (h->D * sizeof(float) + sizeof(float2));
-    if ((int64_t)h->T_max * (h->hq / h->hk) > kSmallCallRows) {
+    const int64_t most_rows = (int64_t)h->T_max * (h->hq / h->hk);
+    if (most_rows > kSmallCallRows) CKA(attn::verify_configure(h->D), "configure the verify kernel");
+    if (most_rows > kVerifyCallRows) {
       // dequantised tiles of one longest sequence at least, of more while they stay within 256 MB
       const int64_t one = (int64_t)h->hk * ((h->len_max + attn::kTileTokens - 1) / attn::kTileTokens);
       const int64_t room = (256LL << 20) / (4LL * attn::kTileTokens * h->D);
@@ -250,8 +254,11 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
   }
   p.part_o = reinterpret_cast<float*>(h->ws);
   p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
-  if ((int64_t)max_q * p.g <= kSmallCallRows)
+  const int64_t rows = (int64_t)max_q * p.g;
+  if (rows <= kSmallCallRows)
     CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch");
+  else if (rows <= kVerifyCallRows)
+    CKA(attn::verify_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch (verify)");
   else
     CKA(attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st),
         "moe_attn_forward launch (prompt)");

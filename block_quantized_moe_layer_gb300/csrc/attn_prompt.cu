@@ -25,8 +25,7 @@
 // Operand images (no swizzle, K-major, 8x8 core matrices of 128 contiguous
 // bytes): rows x channels as [channels/8][rows][8]; values as
 // [keys/8][D][8 keys], so that the contraction index is innermost in both.
-#include "attn_mma.cuh"
-#include "tc.cuh"
+#include "attn_tc.cuh"
 
 namespace moe {
 namespace attn {
@@ -40,7 +39,6 @@ constexpr int kRowsP = 128;
 constexpr int kSoftWarps = 8;
 constexpr int kPromptThreads = (kSoftWarps + 2) * 32;
 constexpr int kMaxRing = 8;
-constexpr float kLazy = 8.f;  // log2 units
 
 template <int D>
 struct PromptPlan {
@@ -50,21 +48,11 @@ struct PromptPlan {
   static constexpr int kStages = kImage;  // (a query image has the same size)
   static constexpr int kMax = kStages + kRing * kImage;              // float [2 buffers][2 halves][128]
   static constexpr int kBars = kMax + 2 * 2 * kRowsP * 4;
-  static constexpr int kNumBars = 2 * kMaxRing + 2 + 1 + 1 + 2 + 1;
+  static constexpr int kNumBars = 2 * kMaxRing + 2 + 2 + 1 + 2 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16 + 128;
   static_assert(kTotal <= 232448, "shared memory plan");
 };
-
-// D[tmem] (+)= A[smem] B[smem]^T
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 // What the two kernels share about the images of a launch.
 struct Images {
@@ -162,8 +150,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);  // ring: copy landed
   uint64_t* empty = full + kMaxRing;                             // ring: MMAs that read it done
   uint64_t* sfull = empty + kMaxRing;                            // [2] scores ready
-  uint64_t* pfull = sfull + 2;                                   // weights stored
-  uint64_t* odone = pfull + 1;                                   // output product done
+  uint64_t* pfull = sfull + 2;                                   // [2] weights stored (the softmax may be a tile ahead)
+  uint64_t* odone = pfull + 2;                                   // output product done
   uint64_t* xbar = odone + 1;                                    // [2] maxima exchanged
   uint64_t* fin = xbar + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
@@ -178,9 +166,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], kSoftWarps);
       mbar_init(&xbar[i], kSoftWarps);
     }
-    mbar_init(pfull, kSoftWarps);
     mbar_init(odone, 1);
     mbar_init(fin, 1);
     *abort = 0;
@@ -281,7 +269,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (j + 1 < n_tiles) scores(j + 1);
         if (!ok) break;
         const int st = use();
-        ok = ok && wait_bar(pfull, (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 14);
+        ok = ok && wait_bar(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 14);
         if (!ok) break;
         tc::fence_after();
         const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kStages + st * L::kImage), D * 16, 128);
@@ -378,7 +366,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pfull);
+      if (lane == 0) mbar_arrive(&pfull[j & 1]);
     }
     if (ok) {
       ok = wait_bar(odone, (uint32_t)((n_tiles - 1) & 1), abort, p.status, p.timeout_ns, 19);
@@ -405,25 +393,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc::ld_32x32b_x16(tl + 256 + c, o);
         tc::wait_ld();
       }
-      float v[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
-      if (!has_row) continue;
-      if (p.n_split > 1) {
-        float4* d = reinterpret_cast<float4*>(p.part_o + part * D + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-      } else {
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-          w[e] = *reinterpret_cast<const uint32_t*>(&h2);
-        }
-        uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + c);
-        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+      store_out16(p, o, l, inv, has_row, part, orow, c, D);
     }
     if (has_row && half == 0) {
       if (p.n_split > 1) p.part_ml[part] = make_float2(m, l);

@@ -1,0 +1,462 @@
+// attn_verify.cu -- attention of verify batches over the 4-bit paged cache: up
+// to 64 rows (query token, query head) of a key/value head a block, on the
+// tcgen05 tensor cores, the cache read once and dequantised in the block.
+//
+// At 4 tokens of 16 query heads a key/value head the cache's bytes and the
+// products are nearly in balance (227 flops a byte), so warp-level MMAs
+// (attn_small.cu) run out at 0.38 of the memory's rate before anything else;
+// and an expansion to 16 bits in memory (attn_prompt.cu) would move 8 times the
+// bytes.  Here a block's roles run beside each other, tile by tile of KT keys:
+//   warp 16      copies (page, head) blocks into a ring of raw stages;
+//   8 warps      (index % 4 >= 2) dequantise keys into a bf16 and values into
+//                an fp16 operand image in shared memory (exact);
+//   warp 17      issues S = Q K^T and O += P V (M = 128 of which 64 rows are
+//                used: the tensor memory lanes that warps of index % 4 < 2 read);
+//   8 warps      (index % 4 < 2) softmax, a quarter of the tile's keys each.
+// The images are single: keys j + 1 are dequantised while O += P_j V_j runs,
+// values j while S_{j+1} does.  Keys are split over blocks and joined.
+//
+// Values' image: 8x8 core matrices 144 bytes apart instead of 128, so that the
+// 8 lanes of a store phase (8 channels apart) meet all banks.
+#include "attn_tc.cuh"
+
+namespace moe {
+namespace attn {
+
+cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st);
+
+namespace {
+
+constexpr int kRowsV = 64;
+constexpr int kWarpsV = 18;
+constexpr int kThreadsV = kWarpsV * 32;
+constexpr int kMaxRaw = 8;
+// page masks kept: the softmax may be a raw ring and a tile behind the copies
+constexpr int kMasks = 16;
+constexpr int kCoreV = 144;  // bytes from one 8-channel group of the value image to the next
+
+template <int D>
+struct VerifyPlan {
+  static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile
+  static constexpr int kRawStage = KT * D * 9 / 8;
+  static constexpr int kRaw = D == 64 ? 8 : (D == 128 ? 5 : 3);
+  // queries [D/8][64 rows][8]: the MMA's rows 64..127 run into the next slab
+  // (and past the last one into the keys' image): read, never used
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + D / 8 * kRowsV * 16;
+  static constexpr int kV = kK + D / 8 * KT * 16;
+  static constexpr int kRawAt = (kV + KT / 8 * (D / 8) * kCoreV + 127) / 128 * 128;
+  static constexpr int kMax = kRawAt + kRaw * kRawStage;  // float [2][4][64]
+  static constexpr int kBars = kMax + 2 * 4 * kRowsV * 4;
+  static constexpr int kNumBars = 2 * kMaxRaw + 4 + 2 + 2 + 2 + 1;
+  static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory slot, abort, page masks
+  static constexpr int kTotal = kMisc + 16 + kMasks * 4 + 128;
+  static_assert(kTotal <= 232448, "shared memory plan");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_constant__ AttnParams p, int n_rt, int chunk) {
+  using L = VerifyPlan<D>;
+  constexpr int KT = L::KT, QC = KT / 4;  // keys of a softmax thread
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  float* smax = reinterpret_cast<float*>(sm + L::kMax);
+  uint64_t* rfull = reinterpret_cast<uint64_t*>(sm + L::kBars);  // raw ring: copies landed
+  uint64_t* rempty = rfull + kMaxRaw;                             // raw ring: keys and values dequantised
+  uint64_t* kfull = rempty + kMaxRaw;                             // key image written
+  uint64_t* kempty = kfull + 1;                                   // scores computed from it
+  uint64_t* vfull = kempty + 1;                                   // value image written
+  uint64_t* odone = vfull + 1;                                    // output product done (value image free)
+  uint64_t* sfull = odone + 1;                                    // [2] scores ready
+  uint64_t* pfull = sfull + 2;                                    // [2] weights stored (the softmax may be a tile ahead)
+  uint64_t* xbar = pfull + 2;                                     // [2] maxima exchanged
+  uint64_t* fin = xbar + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
+  volatile uint32_t* pmask = reinterpret_cast<volatile uint32_t*>(sm + L::kMisc + 16);  // pages present of tile j, at j % kMasks
+  volatile int never = 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 8);
+    }
+    mbar_init(kfull, 8);
+    mbar_init(kempty, 1);
+    mbar_init(vfull, 8);
+    mbar_init(odone, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 8);
+      mbar_init(&xbar[i], 8);
+    }
+    mbar_init(fin, 1);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  griddep_wait();
+
+  const int split = blockIdx.x, b = blockIdx.z;
+  const int kvh = blockIdx.y / n_rt, rt = blockIdx.y % n_rt;
+  const Seq s = load_seq(p, b);
+  const int row0 = rt * kRowsV, n_rows = min(kRowsV, s.nq * p.g - row0);
+  if (n_rows <= 0) return;
+  const int p0 = s.len - s.nq;
+  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + n_rows - 1) / p.g;
+  const int lo = key_lo(p, max(0, pos_min)), hi = pos_max + 1, lo_max = key_lo(p, pos_max);
+  const int tile_a = lo / KT + split * chunk;
+  const int n_tiles = hi > lo ? max(0, min(tile_a + chunk, (hi + KT - 1) / KT) - tile_a) : 0;
+  const int ppt = KT >= p.P ? KT >> p.pshift : 1;  // pages of a tile (a tile of half a page copies the page's head whole)
+
+  if (warp == 17) tc::alloc_512(tslot);
+  const bool soft = warp < 16 && (warp & 3) < 2;
+  const int row = (warp & 1) * 32 + lane, quarter = warp >> 2;  // of the softmax threads
+  int tq = 0, hq = 0, hi_r = 0, lo_r = 0;
+  const bool has_row = soft && row < n_rows;
+  if (has_row) {
+    tq = (row0 + row) / p.g;
+    hq = kvh * p.g + (row0 + row) % p.g;
+    hi_r = p0 + tq + 1;
+    lo_r = key_lo(p, p0 + tq);
+  }
+  if (soft && n_tiles > 0) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
+#pragma unroll
+    for (int c = quarter * (D / 32); c < (quarter + 1) * (D / 32); ++c) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
+      *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsV + row) * 16) = v;
+    }
+    tc::fence_async_smem();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tbase = *tslot;
+
+  float m = -INFINITY, l = 0.f;
+  if (warp == 16) {
+    // ------------------------------------------------------------ raw copies
+    const uint64_t pol = l2_evict_first_policy();
+    auto page_of = [&](int i) {  // lane: page of the tile; -1 where nothing of it is seen
+      const int j0 = (tile_a + i) * KT + (lane << p.pshift);
+      return lane < ppt && i < n_tiles && j0 < hi && j0 + min(p.P, KT) > lo ? load_page(p, b, j0 >> p.pshift) : -1;
+    };
+    bool ok = true;
+    int pg = page_of(0), i = 0;
+    for (; i < n_tiles; ++i) {
+      const int next = page_of(i + 1), st = i % L::kRaw;
+      if (i >= L::kRaw)
+        ok = wait_bar(&rempty[st], (uint32_t)((i / L::kRaw - 1) & 1), abort, p.status, p.timeout_ns, 21);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0);
+      const int keys = min(p.P, KT);                    // of a page in this tile
+      const int at = ((tile_a + i) * KT) & (p.P - 1);   // the tile's first key in its page
+      if (lane == 0) {
+        pmask[i % kMasks] = mask;
+        mbar_arrive_expect_tx(&rfull[st], (uint32_t)(__popc(mask) * keys * (D * 9 / 8)));
+      }
+      __syncwarp();
+      if (pg >= 0) {
+        const uint8_t* src = p.pages + pg * p.page_bytes + kvh * p.head_bytes;
+        uint8_t* dst = sm + L::kRawAt + st * L::kRawStage + lane * keys * (D * 9 / 8);
+        if (keys == p.P) {
+          bulk_g2s_hint(dst, src, (uint32_t)p.head_bytes, &rfull[st], pol);
+        } else {  // part of a page: its four arrays
+          const int64_t half = p.head_bytes / 2;
+          bulk_g2s_hint(dst, src + at * (D / 2), keys * (D / 2), &rfull[st], pol);
+          bulk_g2s_hint(dst + keys * (D / 2), src + p.P * (D / 2) + at * (D / 16), keys * (D / 16), &rfull[st], pol);
+          bulk_g2s_hint(dst + keys * (D * 9 / 16), src + half + at * (D / 2), keys * (D / 2), &rfull[st], pol);
+          bulk_g2s_hint(dst + keys * (D * 9 / 16) + keys * (D / 2), src + half + p.P * (D / 2) + at * (D / 16), keys * (D / 16),
+                        &rfull[st], pol);
+        }
+      }
+      pg = next;
+    }
+    for (int k = max(0, i - L::kRaw); k < i; ++k)
+      wait_bar(&rfull[k % L::kRaw], (uint32_t)((k / L::kRaw) & 1), &never, p.status, p.timeout_ns, 22);
+  } else if (warp == 17) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0 && n_tiles > 0) {
+      constexpr uint32_t kIdescS = tc::idesc_f16(128, KT) | (1u << 7) | (1u << 10);  // bf16 operands
+      constexpr uint32_t kIdescO = tc::idesc_f16(128, D);
+      const uint64_t qd = tc::smem_desc(smem_u32(sm + L::kQ), kRowsV * 16, 128);
+      const uint64_t kd = tc::smem_desc(smem_u32(sm + L::kK), KT * 16, 128);
+      constexpr uint32_t kLboV = D / 8 * kCoreV;
+      const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kV), kLboV, kCoreV);
+      bool ok = true;
+      auto scores = [&](int j) {
+        ok = wait_bar(kfull, (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 23);
+        if (!ok) return;
+        tc::fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tbase + 128 * (j & 1), qd + k * (2 * kRowsV * 16 / 16), kd + k * (2 * KT * 16 / 16), kIdescS, k > 0);
+        tc::commit(kempty);
+        tc::commit(&sfull[j & 1]);
+      };
+      scores(0);
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        if (j + 1 < n_tiles) scores(j + 1);
+        ok = ok && wait_bar(vfull, (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 24);
+        ok = ok && wait_bar(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 25);
+        if (!ok) break;
+        tc::fence_after();
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * kLboV / 16), kIdescO, j > 0 || k > 0);
+        tc::commit(odone);
+      }
+      // all MMAs issued are complete before the block frees anything
+      tc::commit(fin);
+      wait_bar(fin, 0, &never, p.status, p.timeout_ns, 26);
+    }
+  } else if (!soft && n_tiles > 0) {
+    // ------------------------------------------------------------ dequantisation
+    const int dt = ((warp >> 2) * 2 + (warp & 1)) * 32 + lane;  // 0..255
+    const int keys = min(p.P, KT);                              // of a page's part in a raw stage
+    const int kshift = 31 - __clz(keys);
+    const int part = keys * (D * 9 / 8), codes = keys * (D / 2), half = keys * (D * 9 / 16);
+    bool ok = true;
+    auto keys_image = [&](int j) {
+      const int st = j % L::kRaw;
+      ok = wait_bar(&rfull[st], (uint32_t)((j / L::kRaw) & 1), abort, p.status, p.timeout_ns, 27);
+      if (j > 0) ok = ok && wait_bar(kempty, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 28);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const uint8_t* raw = sm + L::kRawAt + st * L::kRawStage;
+      // a warp takes 8 keys of 64 channels: each 8 lanes 8 keys (their stores
+      // meet all banks), the 16-channel group turned by a pattern in which 16
+      // lanes' loads do too (at 192 and 64 channels)
+      const int k8 = lane & 7, q = lane >> 3;
+      const int c4 = (2 * (q & 1) + (k8 >> 2)) ^ (q >> 1);
+      for (int u = dt >> 5; u < KT / 8 * (D / 64); u += 8) {
+        const int key = 8 * (u % (KT / 8)) + k8, c = 4 * (u / (KT / 8)) + c4;
+        const uint8_t* base = raw + (key >> kshift) * part;
+        const int at = key & (keys - 1);
+        const uint2 w = *reinterpret_cast<const uint2*>(base + at * (D / 2) + 8 * c);
+        const uint32_t sb = base[codes + at * (D / 16) + c];
+        const KeyScale d = key_scale(sb | (sb << 16));
+        uint32_t x[8];
+        key_pairs(w.x, d, x);
+        key_pairs(w.y, d, x + 4);
+        uint4* o = reinterpret_cast<uint4*>(sm + L::kK + (2 * c * KT + key) * 16);
+        o[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        o[KT] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kfull);
+    };
+    auto values_image = [&](int j) {
+      const int st = j % L::kRaw;
+      if (j > 0) ok = wait_bar(odone, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 29);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const uint8_t* raw = sm + L::kRawAt + st * L::kRawStage;
+      const uint32_t mask = pmask[j % kMasks];
+      const int j0 = (tile_a + j) * KT;
+      const bool whole = mask == (ppt == 32 ? 0xffffffffu : (1u << ppt) - 1u) && j0 + KT <= s.len;
+      for (int u = dt; u < KT / 8 * (D / 8); u += 256) {
+        const int w = u % (D / 8), k0 = 8 * (u / (D / 8));
+        const uint8_t* base = raw + (k0 >> kshift) * part + half;
+        const int at = k0 & (keys - 1);
+        const uint8_t* vc = base + at * (D / 2) + 4 * w;
+        const uint8_t* vs = base + codes + at * (D / 16) + (w >> 1);
+        // keys past the end or on absent pages: scale 0, whatever lies there
+        const int n = whole ? 8 : (((mask >> (k0 >> kshift)) & 1) ? min(8, s.len - j0 - k0) : 0);
+        uint32_t x[4][8];  // [pair of keys][channel]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vc + 2 * i * (D / 2));
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vc + (2 * i + 1) * (D / 2));
+          uint32_t s0 = vs[2 * i * (D / 16)], s1 = vs[(2 * i + 1) * (D / 16)];
+          s0 = 2 * i < n ? s0 : 0;
+          s1 = 2 * i + 1 < n ? s1 : 0;
+          const ValueScale d = value_scale(s0 | (s1 << 16));
+          value_quads(__byte_perm(w0, w1, 0x5410), d, x[i][0], x[i][2], x[i][4], x[i][6]);
+          value_quads(__byte_perm(w0, w1, 0x7632), d, x[i][1], x[i][3], x[i][5], x[i][7]);
+        }
+        uint8_t* o = sm + L::kV + (k0 / 8) * (D / 8 * kCoreV) + w * kCoreV;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(o + 16 * c) = make_uint4(x[0][c], x[1][c], x[2][c], x[3][c]);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(vfull);
+        mbar_arrive(&rempty[st]);
+      }
+    };
+    keys_image(0);
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      if (j + 1 < n_tiles) keys_image(j + 1);
+      if (ok) values_image(j);
+    }
+  } else if (soft && n_tiles > 0) {
+    // ------------------------------------------------------------ softmax
+    const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+      ok = wait_bar(&sfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 30);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after();
+      uint32_t sv[QC / 16][16];
+#pragma unroll
+      for (int c = 0; c < QC / 16; ++c) tc::ld_32x32b_x16(tl + 128 * (j & 1) + QC * quarter + 16 * c, sv[c]);
+      tc::wait_ld();
+      float x[QC];
+#pragma unroll
+      for (int c = 0; c < QC; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
+      const int c0 = (tile_a + j) * KT;
+      const uint32_t mask = pmask[j % kMasks];
+      if (c0 + KT > pos_min + 1 || c0 < lo_max || mask != (1u << ppt) - 1u) {
+        // bit c: key c0 + QC quarter + c is visible to this row
+        const int k0 = c0 + QC * quarter;
+        uint32_t vis = 0xffffffffu;
+        const int a = lo_r - k0, e = hi_r - k0;
+        vis &= e >= 32 ? ~0u : (e <= 0 ? 0u : (1u << e) - 1);
+        vis &= a <= 0 ? ~0u : (a >= 32 ? 0u : ~((1u << a) - 1));
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+          const bool page = p.P >= KT ? mask != 0 : (mask >> ((QC * quarter + c) >> p.pshift)) & 1;
+          if (!((vis >> c) & 1) || !page) x[c] = -INFINITY;
+        }
+      }
+      float mx = x[0];
+#pragma unroll
+      for (int c = 1; c < QC; ++c) mx = fmaxf(mx, x[c]);
+      // the row's other quarters
+      float* ex = smax + (j & 1) * 4 * kRowsV;
+      ex[quarter * kRowsV + row] = mx;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&xbar[j & 1]);
+      ok = wait_bar(&xbar[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 31);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, ex[i * kRowsV + row]);
+      mx *= p.scale_log2;
+      const bool move = mx > m + kLazy;  // (also the first visible keys: m = -inf)
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - mx)) : 1.f;
+        if (move) m = mx;
+        l *= f;
+        if (j > 0) {
+          ok = wait_bar(odone, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 32);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll 1
+          for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+            uint32_t o[16];
+            tc::ld_32x32b_x16(tl + 256 + c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc::st_32x32b_x16(tl + 256 + c, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      uint32_t pk[QC / 2];
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < QC / 2; ++c) {
+        const float u = exp2_approx(fmaf(x[2 * c], p.scale_log2, -ref));
+        const float v = exp2_approx(fmaf(x[2 * c + 1], p.scale_log2, -ref));
+        l0 += u;
+        l1 += v;
+        pk[c] = pack_h2(u, v);
+      }
+      l += l0 + l1;
+      st_cols<QC / 2>(tl + 128 * (j & 1) + QC / 2 * quarter, pk);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[j & 1]);
+    }
+    if (ok) {
+      ok = wait_bar(odone, (uint32_t)((n_tiles - 1) & 1), abort, p.status, p.timeout_ns, 33);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after();
+    }
+  }
+  // the quarters' sums
+  __syncthreads();
+  if (soft) smax[quarter * kRowsV + row] = l;
+  __syncthreads();
+  if (soft) {
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l += smax[i * kRowsV + row];
+    const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
+    const int64_t orow = (int64_t)(s.start + tq) * p.hq + hq;
+    const int64_t part = ((int64_t)(b * p.hk * n_rt + blockIdx.y) * p.n_split + split) * kRowsV + row;
+    const float inv = p.n_split > 1 ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
+#pragma unroll 1
+    for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+      uint32_t o[16];
+      __syncwarp();
+      if (n_tiles > 0) {
+        tc::ld_32x32b_x16(tl + 256 + c, o);
+        tc::wait_ld();
+      }
+      store_out16(p, o, l, inv, has_row, part, orow, c, D);
+    }
+    if (has_row && quarter == 0) {
+      if (p.n_split > 1) p.part_ml[part] = make_float2(m, l);
+      else if (p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 17) tc::dealloc_512(tbase);
+}
+
+template <int D>
+cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStream_t st) {
+  constexpr int KT = VerifyPlan<D>::KT;
+  const int n_rt = (p.max_q * p.g + kRowsV - 1) / kRowsV;
+  const int64_t base = (int64_t)p.hk * n_rt * p.n_seqs;
+  int64_t span = p.max_len;  // keys a row tile can see: the window's, or all
+  if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + KT);
+  const int tiles = (int)((span + KT - 1) / KT);
+  // one block a multiprocessor; at least two tiles a block
+  int64_t want = std::max<int64_t>(1, num_sms / base);
+  want = std::min<int64_t>(want, std::max<int64_t>(1, (int64_t)(part_rows / kRowsV) / base));
+  const int chunk = (int)std::max<int64_t>(std::min(tiles, 2), (tiles + want - 1) / want);
+  p.n_split = (tiles + chunk - 1) / chunk;
+  cudaError_t e = launch_pdl(verify_kernel<D>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
+                             VerifyPlan<D>::kTotal, st, p, n_rt, chunk);
+  if (e != cudaSuccess || p.n_split == 1) return e;
+  return join_launch(p, kRowsV, n_rt, st);
+}
+
+}  // namespace
+
+cudaError_t verify_configure(int D) {
+  const auto set = [](const void* f, int bytes) { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); };
+  switch (D) {
+    case 64: return set((const void*)verify_kernel<64>, VerifyPlan<64>::kTotal);
+    case 128: return set((const void*)verify_kernel<128>, VerifyPlan<128>::kTotal);
+    case 192: return set((const void*)verify_kernel<192>, VerifyPlan<192>::kTotal);
+    default: return set((const void*)verify_kernel<256>, VerifyPlan<256>::kTotal);
+  }
+}
+
+cudaError_t verify_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st) {
+  switch (p.D) {
+    case 64: return verify_launch_d<64>(p, num_sms, part_rows, st);
+    case 128: return verify_launch_d<128>(p, num_sms, part_rows, st);
+    case 192: return verify_launch_d<192>(p, num_sms, part_rows, st);
+    default: return verify_launch_d<256>(p, num_sms, part_rows, st);
+  }
+}
+
+}  // namespace attn
+}  // namespace moe
