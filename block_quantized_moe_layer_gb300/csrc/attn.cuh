@@ -35,6 +35,7 @@ enum : int {
 
 // Dequantised key/value tiles of one pass of the prompt path.
 constexpr int kTileTokens = 128;
+constexpr int kMaxSplit = 1024;  // most parts of a row's keys
 
 struct AttnParams {
   int hq, hk, g, D, P, pshift, n_pages, window;

@@ -18,7 +18,7 @@ cudaError_t read_launch(const moe_attn* h, const void* pages, const int64_t* slo
 cudaError_t rope_launch(const moe_attn* h, cudaStream_t st);
 cudaError_t append_configure(const moe_attn* h);
 cudaError_t check_launch(const AttnParams& p, cudaStream_t st);
-cudaError_t small_configure();
+cudaError_t small_configure(int D);
 cudaError_t small_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
 cudaError_t verify_configure(int D);
 cudaError_t verify_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
@@ -169,7 +169,7 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
       CKA(attn::prompt_configure(), "configure the prompt kernel");
     }
     CKA(cudaMalloc(&h->ws, h->ws_bytes), "alloc workspace");
-    CKA(attn::small_configure(), "configure the attention kernels");
+    CKA(attn::small_configure(h->D), "configure the attention kernels");
   }
   CKA(cudaStreamSynchronize(st), "create sync");
   guard.keep = true;

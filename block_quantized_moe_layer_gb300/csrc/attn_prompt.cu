@@ -430,7 +430,7 @@ cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t
     const int64_t base = (int64_t)p.hk * n_rt * g.n_seqs;
     // keys are split only where the row tiles leave half of the GPU idle
     int64_t want = std::max<int64_t>(1, num_sms / base);
-    want = std::min<int64_t>(want, std::max<int64_t>(1, (int64_t)(part_rows / kRowsP) / base));
+    want = std::min<int64_t>(std::min<int64_t>(want, kMaxSplit), std::max<int64_t>(1, (int64_t)(part_rows / kRowsP) / base));
     const int chunk = (int)std::max<int64_t>(std::min(rtiles, 2), (rtiles + want - 1) / want);
     g.n_split = (rtiles + chunk - 1) / chunk;
     cudaError_t e = launch_pdl(expand_kernel, dim3(im.tiles, p.hk, g.n_seqs), 256, 0, st, g, im);

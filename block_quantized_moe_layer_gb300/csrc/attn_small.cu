@@ -4,26 +4,26 @@
 //
 //   o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),  s_j = log2(e) scale q.k_j,
 // in one pass over the keys with a running maximum m, sum l and output, split
-// over blocks along the keys and over the 4 compute warps inside a block (32
-// keys of each 128-key tile a warp); the parts are joined by their m and l.
+// over blocks along the keys and over the 4 warps of a block (32 keys of each
+// 128-key tile a warp); the parts are joined by their m and l.
 //
 // Whole (page, head) blocks (codes and scales of keys and values lie
 // together, one bulk copy each) are copied into a ring of 128-key stages.
 // The warps dequantise straight into the operand registers of m16n8k16 MMAs
-// (no shared-memory round trip for 16-bit values), exactly:
-//   scores: A = 16 query rows (held in registers), B = keys.  The channel
-//     order inside an MMA's k is free as long as both operands agree: lane
-//     (n, t) of the 8x4 grid takes channels 64 j + 16 t .. + 15 of key n,
-//     two words that share one scale.
-//   output: A = weights (the score accumulators as they lie, rounded to
-//     fp16), B = values; lane (n, t) takes word n of 64 channels of the keys
-//     at k = 2t, 2t+1, 2t+8, 2t+9, and two words interleave to pairs of keys
-//     before dequantisation.
+// (no shared-memory round trip for 16-bit values), exactly.  Keys and values
+// are the wide operand (M = 16), the query rows the narrow one (N = 8, or two
+// of them): with the rows as M a single token of 4 query heads would waste
+// three quarters of the products, the weights and the accumulators' registers.
+//   scores: A = 16 keys, B = query rows (in registers).  The channel order
+//     inside an MMA's k is free as long as both operands agree: lane (n, t) of
+//     the 8x4 grid takes channels 64 j + 16 t .. + 15 of key n, two words that
+//     share one scale.
+//   output: A = 16 channels of 16 keys' values, B = weights, rounded to fp16
+//     and transposed in registers.  Lane (n, t) takes word n of 64 channels of
+//     the keys at k = 2t, 2t+1, 2t+8, 2t+9; two words interleave to pairs of
+//     keys before dequantisation.
 // Slot n of 8 keys is key kKey(n) = 0,6,1,7,2,4,3,5: then both access patterns
 // meet all banks at 192 and 64 channels.
-//
-// Per 128 keys of D = 192 a block issues ~3900 instructions and 768 MMAs,
-// against 27.6 KB of HBM: both near the memory's time.
 #include "attn_mma.cuh"
 
 namespace moe {
@@ -32,23 +32,36 @@ namespace {
 
 constexpr int kSmallWarps = 4;
 constexpr int kSmallThreads = kSmallWarps * 32;
-constexpr int kSmallRows = 16;
 constexpr int kSmallTile = 128;
 constexpr int kSmallMaxStages = 8;
 
-template <int D>
+// NT: 8-row groups of a block.  Blocks a multiprocessor by the registers that
+// the accumulators and queries take (24 D NT / 64 of them); stages by what
+// those blocks leave of the shared memory.
+template <int D, int NT>
 struct SmallPlan {
+  static constexpr int kBlocks = D * NT <= 128 ? 4 : (D * NT <= 256 ? 3 : 2);
   static constexpr int kStage = kSmallTile * D * 9 / 8;
-  static constexpr int kStages = D == 64 ? 8 : (D == 128 ? 5 : 3);
+  static constexpr int kFit = (227 * 1024 / kBlocks - 2048) / kStage;
+  static constexpr int kStages = kFit > kSmallMaxStages ? kSmallMaxStages : kFit;
+  static_assert(kStages >= 2, "a stage in flight while one is worked on");
+  static constexpr int kRows = 8 * NT;
   static constexpr int kBars = kStages * kStage;
-  static constexpr int kTotal = kBars + 2 * kSmallMaxStages * 8 + kSmallMaxStages * 4 + 16 + kSmallWarps * kSmallRows * 8;
-  static_assert(kSmallWarps * kSmallRows * D * 4 <= kBars, "the warps' outputs reuse the ring");
+  static constexpr int kTotal = kBars + 2 * kSmallMaxStages * 8 + kSmallMaxStages * 4 + 16 + kSmallWarps * kRows * 8;
+  static_assert(kSmallWarps * kRows * D * 4 <= kBars, "the warps' outputs reuse the ring");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kSmallThreads, 2) small_kernel(const __grid_constant__ AttnParams p, int n_rt, int chunk) {
-  using L = SmallPlan<D>;
-  constexpr int kJ = D / 64;
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8x8 fragment of 16-bit elements
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
+    small_kernel(const __grid_constant__ AttnParams p, int n_rt, int chunk) {
+  using L = SmallPlan<D, NT>;
+  constexpr int kJ = D / 64, kRows = L::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + kSmallMaxStages;
@@ -72,7 +85,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_kernel(const __grid_co
   const int split = blockIdx.x, b = blockIdx.z;
   const int kvh = blockIdx.y / n_rt, rt = blockIdx.y % n_rt;
   const Seq s = load_seq(p, b);
-  const int row0 = rt * kSmallRows, n_rows = min(kSmallRows, s.nq * p.g - row0);
+  const int row0 = rt * kRows, n_rows = min(kRows, s.nq * p.g - row0);
   if (n_rows <= 0) return;  // (the whole block; every thread has passed its dependency wait)
   // keys that some row sees, and this block's tiles of them
   const int p0 = s.len - s.nq;  // position of the first query
@@ -82,6 +95,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_kernel(const __grid_co
   const int tile_b = min(tile_a + chunk, (max(hi, 0) + kSmallTile - 1) / kSmallTile);
   const int n_tiles = hi > lo ? max(0, tile_b - tile_a) : 0;
   const int ppt = kSmallTile >> p.pshift;  // pages of a tile
+  const int head_bytes = (int)p.head_bytes;
 
   // Warp 0 issues the copies too (a fifth warp would cost the compute warps a
   // third of their registers): lane i takes page i of a tile.
@@ -95,12 +109,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_kernel(const __grid_co
     const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0);
     if (lane == 0) {
       pmask[st] = mask;
-      mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * p.head_bytes));
+      mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * head_bytes));
     }
     __syncwarp();
     if (pg >= 0)
-      bulk_g2s_hint(smem + st * L::kStage + lane * p.head_bytes, p.pages + pg * p.page_bytes + kvh * p.head_bytes,
-                    (uint32_t)p.head_bytes, &full[st], pol);
+      bulk_g2s_hint(smem + st * L::kStage + lane * head_bytes, p.pages + pg * p.page_bytes + (int64_t)kvh * head_bytes,
+                    (uint32_t)head_bytes, &full[st], pol);
   };
   int issued = 0, next_pg = -1;
   if (warp == 0) {
@@ -112,225 +126,244 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_kernel(const __grid_co
     for (int i = 0; i < L::kStages - 1; ++i)
       if (i < n_tiles) issue(i, pg[i]), ++issued;
   }
-  {
-    // ------------------------------------------------------------ compute
-    const int n = lane >> 2, t = lane & 3;
-    const int key_n = (n >> 1) + ((n & 1) ? (((n >> 1) + 2) & 3) + 4 - (n >> 1) : 0);  // kKey(n)
-    const int key_e = t, key_o = 4 + ((t + 2) & 3);                                     // kKey(2t), kKey(2t + 1)
-    // query rows n and n + 8, channels 64 j + 16 t .. + 15
-    uint32_t aq[4 * kJ][4];
-    int hi_r[2], lo_r[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = row0 + n + 8 * r;
-      const bool valid = n + 8 * r < n_rows;
-      const int tq = valid ? row / p.g : 0, h = kvh * p.g + (valid ? row % p.g : 0);
-      hi_r[r] = valid ? p0 + tq + 1 : 0;
-      lo_r[r] = valid ? key_lo(p, p0 + tq) : 0;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + h * p.q_head;
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        uint4 x = make_uint4(0, 0, 0, 0), y = x;
-        if (valid) {
-          x = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * t);
-          y = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * t + 8);
-        }
-        aq[4 * j][r] = x.x; aq[4 * j][2 + r] = x.y;
-        aq[4 * j + 1][r] = x.z; aq[4 * j + 1][2 + r] = x.w;
-        aq[4 * j + 2][r] = y.x; aq[4 * j + 2][2 + r] = y.y;
-        aq[4 * j + 3][r] = y.z; aq[4 * j + 3][2 + r] = y.w;
-      }
-    }
-    const int lo_max = key_lo(p, pos_max);
-    float o[8 * kJ][4];
-#pragma unroll
-    for (int i = 0; i < 8 * kJ; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    const int code_b = p.P * (D / 2), half_b = (int)(p.head_bytes / 2);
 
-    for (int i = 0; i < n_tiles; ++i) {
-      const int st = i % L::kStages;
-      bool ok = true;
-      if (warp == 0 && issued < n_tiles) {  // the stage of tile i - 1 is free once every warp is past it
-        const int pg = next_pg;
-        next_pg = page_of(issued + 1);
-        if (issued >= L::kStages)
-          ok = wait_bar(&empty[issued % L::kStages], (uint32_t)((issued / L::kStages - 1) & 1), abort, p.status,
-                        p.timeout_ns, 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        issue(issued, pg);
-        ++issued;
+  const int n = lane >> 2, t = lane & 3;
+  const int key_n = (n & 1) ? 4 + (((n >> 1) + 2) & 3) : n >> 1;  // kKey(n)
+  const int key_e = t, key_o = 4 + ((t + 2) & 3);                  // kKey(2t), kKey(2t + 1)
+  // query rows 8 i + n as B operands (channels 64 j + 16 t .. + 15), and what
+  // the rows 8 i + 2t, 8 i + 2t + 1 of the accumulators see
+  uint32_t bq[NT][8 * kJ];
+  int hi_r[2 * NT], lo_r[2 * NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = 8 * i + n, tq = (row0 + r) / p.g, h = kvh * p.g + (row0 + r) % p.g;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + h * p.q_head;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      if (r < n_rows) {
+        x = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * t);
+        y = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * t + 8);
       }
-      ok = wait_bar(&full[st], (uint32_t)((i / L::kStages) & 1), abort, p.status, p.timeout_ns, 2);
+      bq[i][8 * j] = x.x; bq[i][8 * j + 1] = x.y; bq[i][8 * j + 2] = x.z; bq[i][8 * j + 3] = x.w;
+      bq[i][8 * j + 4] = y.x; bq[i][8 * j + 5] = y.y; bq[i][8 * j + 6] = y.z; bq[i][8 * j + 7] = y.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = 8 * i + 2 * t + e, pos = p0 + (row0 + rr) / p.g;
+      hi_r[2 * i + e] = rr < n_rows ? pos + 1 : 0;
+      lo_r[2 * i + e] = key_lo(p, pos);
+    }
+  }
+  const int lo_max = key_lo(p, pos_max);
+  float o[NT][4 * kJ][4];  // [.][4 j + e]: channels 64 j + 8 n + 2 e (+1), rows 8 i + 2 t (+1)
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int k = 0; k < 4 * kJ; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][k][e] = 0.f;
+  float m[2 * NT], l[2 * NT];
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  const int code_b = p.P * (D / 2), half_b = head_bytes / 2;
+
+  for (int i = 0; i < n_tiles; ++i) {
+    const int st = i % L::kStages;
+    bool ok = true;
+    if (warp == 0 && issued < n_tiles) {  // the stage of tile i - 1 is free once every warp is past it
+      const int pg = next_pg;
+      next_pg = page_of(issued + 1);
+      if (issued >= L::kStages)
+        ok = wait_bar(&empty[issued % L::kStages], (uint32_t)((issued / L::kStages - 1) & 1), abort, p.status, p.timeout_ns, 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t mask = pmask[st];
-      const int c0 = (tile_a + i) * kSmallTile + warp * 32;  // this warp's first key
-      if (c0 < hi && c0 + 32 > lo) {
-        const uint8_t* ring = smem + st * L::kStage;
-        // the 8-key group at key k of the tile lies in one page
-        auto group = [&](int k, int& at) {
-          at = k & (p.P - 1);
-          return ring + (k >> p.pshift) * p.head_bytes;
-        };
-        float sc[4][4];
+      issue(issued, pg);
+      ++issued;
+    }
+    ok = wait_bar(&full[st], (uint32_t)((i / L::kStages) & 1), abort, p.status, p.timeout_ns, 2);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const uint32_t mask = pmask[st];
+    const int c0 = (tile_a + i) * kSmallTile + warp * 32;  // this warp's first key
+    if (c0 < hi && c0 + 32 > lo) {
+      // 16 keys lie in one page
+      const uint8_t* base[2];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
+      for (int a = 0; a < 2; ++a) {
+        const int k = warp * 32 + 16 * a;
+        base[a] = smem + st * L::kStage + (k >> p.pshift) * head_bytes + (k & (p.P - 1)) * (D / 2);
+      }
+      // from a key's codes to its scales: (P - at) rows of codes on, then at rows of scales
+      float sc[NT][2][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[a][e] = 0.f;
-          int at;
-          const uint8_t* base = group(warp * 32 + 8 * a, at);
-          const uint8_t* kc = base + (at + key_n) * (D / 2) + 8 * t;
-          const uint8_t* ks = base + code_b + (at + key_n) * (D / 16);
+      for (int a = 0; a < 2; ++a) {
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + 32 * j);
-            const uint32_t sw = *reinterpret_cast<const uint32_t*>(ks + 4 * j);
-            const KeyScale d = key_scale(__byte_perm(sw, 0, 0x4040 + t * 0x0101));
-            uint32_t k[8];
-            key_pairs(w.x, d, k);
-            key_pairs(w.y, d, k + 4);
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mma_bf16(sc[a], aq[4 * j + c], k[2 * c], k[2 * c + 1]);
+          for (int e = 0; e < 4; ++e) sc[u][a][e] = 0.f;
+        const int at = (warp * 32 + 16 * a) & (p.P - 1);
+        const uint8_t* kc = base[a] + key_n * (D / 2) + 8 * t;
+        const uint8_t* ks = base[a] - at * (D / 2) + code_b + (at + key_n) * (D / 16);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          uint32_t k0[8], k1[8];  // keys n and n + 8
+          const uint2 w0 = *reinterpret_cast<const uint2*>(kc + 32 * j);
+          const uint2 w1 = *reinterpret_cast<const uint2*>(kc + 8 * (D / 2) + 32 * j);
+          const uint32_t s0 = *reinterpret_cast<const uint32_t*>(ks + 4 * j);
+          const uint32_t s1 = *reinterpret_cast<const uint32_t*>(ks + 8 * (D / 16) + 4 * j);
+          const KeyScale d0 = key_scale(__byte_perm(s0, 0, 0x4040 + t * 0x0101));
+          const KeyScale d1 = key_scale(__byte_perm(s1, 0, 0x4040 + t * 0x0101));
+          key_pairs(w0.x, d0, k0);
+          key_pairs(w0.y, d0, k0 + 4);
+          key_pairs(w1.x, d1, k1);
+          key_pairs(w1.y, d1, k1 + 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t ak[4] = {k0[2 * c], k1[2 * c], k0[2 * c + 1], k1[2 * c + 1]};
+#pragma unroll
+            for (int u = 0; u < NT; ++u) mma_bf16(sc[u][a], ak, bq[u][8 * j + 2 * c], bq[u][8 * j + 2 * c + 1]);
           }
         }
-        // masks: past the last or before the first visible key, on absent pages
-        const uint32_t need = ppt == 32 ? 0xffffffffu : (1u << ppt) - 1u;
-        const bool partial = c0 + 32 > pos_min + 1 || c0 < lo_max || mask != need;
+      }
+      // masks: past the last or before the first visible key, on absent pages
+      const bool partial = c0 + 32 > pos_min + 1 || c0 < lo_max || mask != (1u << ppt) - 1u;
+      if (partial) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const bool page = (mask >> ((warp * 32 + 16 * a) >> p.pshift)) & 1;
+          const int j0 = c0 + 16 * a + key_n, j1 = j0 + 8;
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (!page || j0 >= hi_r[2 * u + e] || j0 < lo_r[2 * u + e]) sc[u][a][e] = -INFINITY;
+              if (!page || j1 >= hi_r[2 * u + e] || j1 < lo_r[2 * u + e]) sc[u][a][2 + e] = -INFINITY;
+            }
+        }
+      }
+      float mn[2 * NT];
+      bool grows = false;
+#pragma unroll
+      for (int r = 0; r < 2 * NT; ++r) {
+        const int u = r >> 1, e = r & 1;
+        float x = fmaxf(fmaxf(sc[u][0][e], sc[u][0][2 + e]), fmaxf(sc[u][1][e], sc[u][1][2 + e]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        mn[r] = fmaxf(m[r], x * p.scale_log2);
+        grows |= mn[r] > m[r];
+      }
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int r = 0; r < 2 * NT; ++r) {
+          const float f = m[r] == -INFINITY ? 0.f : exp2_approx(m[r] - mn[r]);
+          m[r] = mn[r];
+          l[r] *= f;
+#pragma unroll
+          for (int k = 0; k < 4 * kJ; ++k) {
+            o[r >> 1][k][r & 1] *= f;
+            o[r >> 1][k][2 + (r & 1)] *= f;
+          }
+        }
+      }
+      uint32_t bp[NT][2][2];  // weights as B operands
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        // a row that has seen nothing: all weights 0
+        const float r0 = m[2 * u] == -INFINITY ? 0.f : m[2 * u], r1 = m[2 * u + 1] == -INFINITY ? 0.f : m[2 * u + 1];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = exp2_approx(fmaf(sc[u][a][e], p.scale_log2, (e & 1) ? -r1 : -r0));
+          l[2 * u] += w[0] + w[2];
+          l[2 * u + 1] += w[1] + w[3];
+          bp[u][a][0] = transpose8(pack_h2(w[0], w[1]));
+          bp[u][a][1] = transpose8(pack_h2(w[2], w[3]));
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int at = (warp * 32 + 16 * a) & (p.P - 1);
+        const uint8_t* vc = base[a] + half_b + 4 * n;
+        const uint8_t* vs = base[a] - at * (D / 2) + half_b + code_b + at * (D / 16);
+        // scales of keys past the end or on absent pages are 0: whatever lies there stays finite
+        bool z[4] = {false, false, false, false};
         if (partial) {
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const bool page = (mask >> ((warp * 32 + 8 * a) >> p.pshift)) & 1;
-            const int j0 = c0 + 8 * a + key_e, j1 = c0 + 8 * a + key_o;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if (!page || j0 >= hi_r[r] || j0 < lo_r[r]) sc[a][2 * r] = -INFINITY;
-              if (!page || j1 >= hi_r[r] || j1 < lo_r[r]) sc[a][2 * r + 1] = -INFINITY;
-            }
-          }
-        }
-        float mn[2];
-        bool grows = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x = fmaxf(sc[0][2 * r], sc[0][2 * r + 1]);
-#pragma unroll
-          for (int a = 1; a < 4; ++a) x = fmaxf(x, fmaxf(sc[a][2 * r], sc[a][2 * r + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mn[r] = fmaxf(m[r], x * p.scale_log2);
-          grows |= mn[r] > m[r];
-        }
-        if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float f = m[r] == -INFINITY ? 0.f : exp2_approx(m[r] - mn[r]);
-            m[r] = mn[r];
-            l[r] *= f;
-#pragma unroll
-            for (int k = 0; k < 8 * kJ; ++k) {
-              o[k][2 * r] *= f;
-              o[k][2 * r + 1] *= f;
-            }
-          }
-        }
-        uint32_t pr[4][2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float ref = m[r] == -INFINITY ? 0.f : m[r];  // a row that has seen nothing: all weights 0
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const float x = exp2_approx(fmaf(sc[a][2 * r], p.scale_log2, -ref));
-            const float y = exp2_approx(fmaf(sc[a][2 * r + 1], p.scale_log2, -ref));
-            l[r] += x + y;
-            pr[a][r] = pack_h2(x, y);
-          }
+          const bool page = (mask >> ((warp * 32 + 16 * a) >> p.pshift)) & 1;
+          const int j = c0 + 16 * a;
+          z[0] = !page || j + key_e >= s.len;
+          z[1] = !page || j + key_o >= s.len;
+          z[2] = !page || j + 8 + key_e >= s.len;
+          z[3] = !page || j + 8 + key_o >= s.len;
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const uint32_t ap[4] = {pr[2 * kk][0], pr[2 * kk][1], pr[2 * kk + 1][0], pr[2 * kk + 1][1]};
-          int at;
-          const uint8_t* base = group(warp * 32 + 16 * kk, at) + half_b;  // 16 keys lie in one page
-          const uint8_t* vc = base + at * (D / 2) + 4 * n;
-          const uint8_t* vs = base + code_b + at * (D / 16);
-          // scales of keys past the end or on absent pages are 0: whatever lies there stays finite
-          bool z[4] = {false, false, false, false};
-          if (partial) {
-            const bool page = (mask >> ((warp * 32 + 16 * kk) >> p.pshift)) & 1;
-            const int j = c0 + 16 * kk;
-            z[0] = !page || j + key_e >= s.len;
-            z[1] = !page || j + key_o >= s.len;
-            z[2] = !page || j + 8 + key_e >= s.len;
-            z[3] = !page || j + 8 + key_o >= s.len;
+        for (int j = 0; j < kJ; ++j) {
+          uint32_t bb[2][8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int ke = 8 * u + key_e, ko = 8 * u + key_o;
+            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vc + ke * (D / 2) + 32 * j);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vc + ko * (D / 2) + 32 * j);
+            uint32_t s0 = *reinterpret_cast<const uint32_t*>(vs + ke * (D / 16) + 4 * j);
+            uint32_t s1 = *reinterpret_cast<const uint32_t*>(vs + ko * (D / 16) + 4 * j);
+            if (z[2 * u]) s0 = 0;
+            if (z[2 * u + 1]) s1 = 0;
+            const uint32_t h = n >> 1;
+            const ValueScale d = value_scale(__byte_perm(s0, s1, h | ((4 + h) << 8)) & 0x00FF00FFu);
+            value_quads(__byte_perm(w0, w1, 0x5410), d, bb[u][0], bb[u][2], bb[u][4], bb[u][6]);
+            value_quads(__byte_perm(w0, w1, 0x7632), d, bb[u][1], bb[u][3], bb[u][5], bb[u][7]);
           }
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            uint32_t bb[2][8];
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t av[4] = {bb[0][2 * e], bb[0][2 * e + 1], bb[1][2 * e], bb[1][2 * e + 1]};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int ke = 8 * u + key_e, ko = 8 * u + key_o;
-              const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vc + ke * (D / 2) + 32 * j);
-              const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vc + ko * (D / 2) + 32 * j);
-              uint32_t s0 = *reinterpret_cast<const uint32_t*>(vs + ke * (D / 16) + 4 * j);
-              uint32_t s1 = *reinterpret_cast<const uint32_t*>(vs + ko * (D / 16) + 4 * j);
-              if (z[2 * u]) s0 = 0;
-              if (z[2 * u + 1]) s1 = 0;
-              const uint32_t h = n >> 1;
-              const ValueScale d = value_scale(__byte_perm(s0, s1, h | ((4 + h) << 8)) & 0x00FF00FFu);
-              value_quads(__byte_perm(w0, w1, 0x5410), d, bb[u][0], bb[u][2], bb[u][4], bb[u][6]);
-              value_quads(__byte_perm(w0, w1, 0x7632), d, bb[u][1], bb[u][3], bb[u][5], bb[u][7]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mma_f16(o[8 * j + e], ap, bb[0][e], bb[1][e]);
+            for (int u = 0; u < NT; ++u) mma_f16(o[u][4 * j + e], av, bp[u][a][0], bp[u][a][1]);
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
     }
-    // this warp's part
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t == 0) ml[warp * kSmallRows + n + 8 * r] = make_float2(m[r], l[r]);
-    }
-    // every copy issued has landed before the ring is reused (they all have, unless a wait gave up)
-    if (warp == 0)
-      for (int j = max(0, issued - L::kStages); j < issued; ++j)
-        wait_bar(&full[j % L::kStages], (uint32_t)((j / L::kStages) & 1), &never, p.status, p.timeout_ns, 3);
-    __syncthreads();  // every warp has read its last stage
-    float* ob = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        float* d = ob + (warp * kSmallRows + n + 8 * r) * D + 64 * j + 16 * t;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[e] = o[8 * j + e][2 * r];
-          d[8 + e] = o[8 * j + e][2 * r + 1];
-        }
-      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
   }
+  // this warp's part
+#pragma unroll
+  for (int r = 0; r < 2 * NT; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 4);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+    if (n == 0) ml[warp * kRows + 8 * (r >> 1) + 2 * t + (r & 1)] = make_float2(m[r], l[r]);
+  }
+  // every copy issued has landed before the ring is reused (they all have, unless a wait gave up)
+  if (warp == 0)
+    for (int j = max(0, issued - L::kStages); j < issued; ++j)
+      wait_bar(&full[j % L::kStages], (uint32_t)((j / L::kStages) & 1), &never, p.status, p.timeout_ns, 3);
+  __syncthreads();  // every warp has read its last stage
+  float* ob = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int u = 0; u < NT; ++u)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float* d = ob + (warp * kRows + 8 * u + 2 * t + e) * D + 8 * n;
+#pragma unroll
+      for (int k = 0; k < 4 * kJ; ++k)
+        *reinterpret_cast<float2*>(d + 64 * (k >> 2) + 2 * (k & 3)) = make_float2(o[u][k][e], o[u][k][2 + e]);
+    }
   __syncthreads();
   // join the warps' parts
-  const int64_t part = ((int64_t)(b * p.hk * n_rt + blockIdx.y) * p.n_split + split) * kSmallRows;
-  const float* ob = reinterpret_cast<const float*>(smem);
+  const int64_t part = ((int64_t)(b * p.hk * n_rt + blockIdx.y) * p.n_split + split) * kRows;
   for (int i = tid; i < n_rows * (D / 4); i += kSmallThreads) {
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, ml[w * kSmallRows + r].x);
+    for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, ml[w * kRows + r].x);
     float lt = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kSmallWarps; ++w) {
-      const float2 a = ml[w * kSmallRows + r];
+      const float2 a = ml[w * kRows + r];
       const float f = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mx);
-      const float4 v = *reinterpret_cast<const float4*>(ob + (w * kSmallRows + r) * D + c);
+      const float4 v = *reinterpret_cast<const float4*>(ob + (w * kRows + r) * D + c);
       lt = fmaf(a.y, f, lt);
       x[0] = fmaf(v.x, f, x[0]);
       x[1] = fmaf(v.y, f, x[1]);
@@ -354,31 +387,96 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_kernel(const __grid_co
   }
 }
 
-// Joins the parts of a row's keys: one block a (query token, query head).
+// Joins the parts of a row's keys: one block a (query token, query head), a
+// group of D/4 threads every kJoinGroups-th part.  (A thread a channel walking
+// over all parts took 21 us for 37 of them: a chain of loads each.)
+constexpr int kJoinGroups = 8;
 template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt) {
+__global__ void __launch_bounds__(kJoinGroups * D / 4) join_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt) {
+  __shared__ float wt[1024];                 // a part's weight 2^(m - max)
+  __shared__ float4 sum[kJoinGroups][D / 4];
+  __shared__ float2 red[32];
   griddep_launch_dependents();
-  griddep_wait();
   const int t = blockIdx.x / p.hq, h = blockIdx.x % p.hq, b = blockIdx.y;
+  constexpr int kThreads = kJoinGroups * D / 4, kWarps = kThreads / 32;
+  const int tid = threadIdx.x, g = tid / (D / 4), c = tid % (D / 4);
+  griddep_wait();
   const Seq s = load_seq(p, b);
   if (t >= s.nq) return;
   const int kvh = h / p.g, row = t * p.g + h % p.g;
   const int64_t tile = (int64_t)(b * p.hk + kvh) * n_rt + row / rows_per_tile;
   const int64_t first = tile * p.n_split * rows_per_tile + row % rows_per_tile;
-  float mx = -INFINITY;
-  for (int i = 0; i < p.n_split; ++i) mx = fmaxf(mx, p.part_ml[first + (int64_t)i * rows_per_tile].x);
-  float lt = 0.f, x = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < p.n_split; ++i) {
-    const float2 a = p.part_ml[first + (int64_t)i * rows_per_tile];
-    const float v = p.part_o[(first + (int64_t)i * rows_per_tile) * D + threadIdx.x];
-    const float f = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mx);
-    lt = fmaf(a.y, f, lt);
-    x = fmaf(v, f, x);
+  const float4* po = reinterpret_cast<const float4*>(p.part_o) + first * (D / 4) + c;
+  const int64_t step = (int64_t)rows_per_tile * (D / 4);
+  // the first parts are on their way while the weights are found
+  constexpr int kBatch = 4;
+  float4 v[kBatch];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int i = g + k * kJoinGroups;
+    v[k] = i < p.n_split ? po[i * step] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float mx = -INFINITY;
+  for (int i = tid; i < p.n_split; i += kThreads) mx = fmaxf(mx, p.part_ml[first + (int64_t)i * rows_per_tile].x);
+  mx = warp_max(mx);
+  if ((tid & 31) == 0) red[tid >> 5].x = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w].x);
+  float lt = 0.f;
+  for (int i = tid; i < p.n_split; i += kThreads) {
+    const float2 a = p.part_ml[first + (int64_t)i * rows_per_tile];
+    const float f = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mx);
+    wt[i] = f;
+    lt = fmaf(a.y, f, lt);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+  if ((tid & 31) == 0) red[tid >> 5].y = lt;
+  __syncthreads();
+  lt = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) lt += red[w].y;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = g; i0 < p.n_split; i0 += kBatch * kJoinGroups) {
+    if (i0 != g) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kJoinGroups;
+        v[k] = i < p.n_split ? po[i * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kJoinGroups;
+      const float f = i < p.n_split ? wt[i] : 0.f;
+      x.x = fmaf(v[k].x, f, x.x);
+      x.y = fmaf(v[k].y, f, x.y);
+      x.z = fmaf(v[k].z, f, x.z);
+      x.w = fmaf(v[k].w, f, x.w);
+    }
+  }
+  sum[g][c] = x;
+  __syncthreads();
   const int64_t o = (int64_t)(s.start + t) * p.hq + h;
-  static_cast<__nv_bfloat16*>(p.out)[o * D + threadIdx.x] = __float2bfloat16_rn(lt > 0.f ? x * kValueUnscale / lt : 0.f);
-  if (p.lse && threadIdx.x == 0) p.lse[o] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+  if (g == 0) {
+    x = sum[0][c];
+#pragma unroll
+    for (int k = 1; k < kJoinGroups; ++k) {
+      const float4 y = sum[k][c];
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+    const float inv = lt > 0.f ? kValueUnscale / lt : 0.f;
+    const __nv_bfloat162 u = __floats2bfloat162_rn(x.x * inv, x.y * inv), w = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+    uint2 r;
+    r.x = *reinterpret_cast<const uint32_t*>(&u);
+    r.y = *reinterpret_cast<const uint32_t*>(&w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 4 * c) = r;
+  }
+  if (p.lse && tid == 0) p.lse[o] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
@@ -386,55 +484,66 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ AttnPar
 cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st) {
   const dim3 grid((unsigned)(p.max_q * p.hq), p.n_seqs);
   switch (p.D) {
-    case 64: return launch_pdl(join_kernel<64>, grid, 64, 0, st, p, rows_per_tile, n_rt);
-    case 128: return launch_pdl(join_kernel<128>, grid, 128, 0, st, p, rows_per_tile, n_rt);
-    case 192: return launch_pdl(join_kernel<192>, grid, 192, 0, st, p, rows_per_tile, n_rt);
-    default: return launch_pdl(join_kernel<256>, grid, 256, 0, st, p, rows_per_tile, n_rt);
+    case 64: return launch_pdl(join_kernel<64>, grid, kJoinGroups * 64 / 4, 0, st, p, rows_per_tile, n_rt);
+    case 128: return launch_pdl(join_kernel<128>, grid, kJoinGroups * 128 / 4, 0, st, p, rows_per_tile, n_rt);
+    case 192: return launch_pdl(join_kernel<192>, grid, kJoinGroups * 192 / 4, 0, st, p, rows_per_tile, n_rt);
+    default: return launch_pdl(join_kernel<256>, grid, kJoinGroups * 256 / 4, 0, st, p, rows_per_tile, n_rt);
   }
 }
 
 namespace {
 
-template <int D>
+template <int D, int NT>
 cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStream_t st) {
-  const int n_rt = (p.max_q * p.g + kSmallRows - 1) / kSmallRows;
+  using L = SmallPlan<D, NT>;
+  const int n_rt = (p.max_q * p.g + L::kRows - 1) / L::kRows;
   const int64_t base = (int64_t)p.hk * n_rt * p.n_seqs;
   // tiles that a row can see: the window's, or all
   int64_t span = p.max_len;
   if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + kSmallTile);
   const int tiles = (int)((span + kSmallTile - 1) / kSmallTile);
-  // keys are split until there are four blocks for each place on the GPU (two
-  // a multiprocessor), so that ragged lengths even out
-  const int64_t want = std::max<int64_t>(1, 8LL * num_sms / base);
+  // keys are split until there are two blocks for each place on the GPU, so
+  // that ragged lengths even out
+  const int64_t want = std::max<int64_t>(1, 2LL * L::kBlocks * num_sms / base);
   int chunk = (int)std::max<int64_t>(1, (tiles + want - 1) / want);
-  const int64_t fit = std::max<int64_t>(1, (int64_t)(part_rows / kSmallRows) / base);
+  const int64_t fit = std::min<int64_t>(kMaxSplit, std::max<int64_t>(1, (int64_t)(part_rows / L::kRows) / base));
   chunk = std::max<int>(chunk, (int)((tiles + fit - 1) / fit));
   p.n_split = (tiles + chunk - 1) / chunk;
-  cudaError_t e = launch_pdl(small_kernel<D>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads,
-                             SmallPlan<D>::kTotal, st, p, n_rt, chunk);
+  cudaError_t e = launch_pdl(small_kernel<D, NT>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads, L::kTotal,
+                             st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
-  return join_launch(p, kSmallRows, n_rt, st);
+  return join_launch(p, L::kRows, n_rt, st);
+}
+
+template <int D>
+cudaError_t small_configure_d() {
+  cudaError_t e = cudaFuncSetAttribute(small_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<D, 1>::kTotal);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(small_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<D, 2>::kTotal);
+}
+
+template <int D>
+cudaError_t small_launch_nt(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st) {
+  return p.max_q * p.g <= 8 ? small_launch_d<D, 1>(p, num_sms, part_rows, st) : small_launch_d<D, 2>(p, num_sms, part_rows, st);
 }
 
 }  // namespace
 
-cudaError_t small_configure() {
-  cudaError_t e = cudaFuncSetAttribute(small_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<64>::kTotal);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(small_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<128>::kTotal);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(small_kernel<192>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<192>::kTotal);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(small_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<256>::kTotal);
-  return e;
+cudaError_t small_configure(int D) {
+  switch (D) {
+    case 64: return small_configure_d<64>();
+    case 128: return small_configure_d<128>();
+    case 192: return small_configure_d<192>();
+    default: return small_configure_d<256>();
+  }
 }
 
 cudaError_t small_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st) {
   switch (p.D) {
-    case 64: return small_launch_d<64>(p, num_sms, part_rows, st);
-    case 128: return small_launch_d<128>(p, num_sms, part_rows, st);
-    case 192: return small_launch_d<192>(p, num_sms, part_rows, st);
-    default: return small_launch_d<256>(p, num_sms, part_rows, st);
+    case 64: return small_launch_nt<64>(p, num_sms, part_rows, st);
+    case 128: return small_launch_nt<128>(p, num_sms, part_rows, st);
+    case 192: return small_launch_nt<192>(p, num_sms, part_rows, st);
+    default: return small_launch_nt<256>(p, num_sms, part_rows, st);
   }
 }
 

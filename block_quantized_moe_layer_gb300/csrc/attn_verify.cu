@@ -428,7 +428,7 @@ cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStr
   const int tiles = (int)((span + KT - 1) / KT);
   // one block a multiprocessor; at least two tiles a block
   int64_t want = std::max<int64_t>(1, num_sms / base);
-  want = std::min<int64_t>(want, std::max<int64_t>(1, (int64_t)(part_rows / kRowsV) / base));
+  want = std::min<int64_t>(std::min<int64_t>(want, kMaxSplit), std::max<int64_t>(1, (int64_t)(part_rows / kRowsV) / base));
   const int chunk = (int)std::max<int64_t>(std::min(tiles, 2), (tiles + want - 1) / want);
   p.n_split = (tiles + chunk - 1) / chunk;
   cudaError_t e = launch_pdl(verify_kernel<D>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
