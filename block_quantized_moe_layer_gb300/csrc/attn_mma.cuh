@@ -89,6 +89,17 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return r;
 }
 
+// Channels 4 c .. 4 c + 3 of an output row, and its logarithm.
+__device__ __forceinline__ void store_joined(const AttnParams& p, int64_t o, int c, int D, float4 x, float lt, float mx) {
+  const float inv = lt > 0.f ? kValueUnscale / lt : 0.f;
+  const __nv_bfloat162 u = __floats2bfloat162_rn(x.x * inv, x.y * inv), w = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+  uint2 r;
+  r.x = *reinterpret_cast<const uint32_t*>(&u);
+  r.y = *reinterpret_cast<const uint32_t*>(&w);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 4 * c) = r;
+  if (p.lse && c == 0) p.lse[o] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+}
+
 // A wait on an mbarrier phase that gives up after the call's limit (the
 // status word then says where) or once another thread of the block has.
 static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit,
@@ -104,9 +115,19 @@ static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, vo
   }
   return true;
 }
+// SPINS: tests before the suspending wait, whose sleeper takes a few hundred
+// cycles to resume.  For the one thread that issues MMAs, not for the many
+// that compute: their spinning takes the issue slots of the others.
+template <int SPINS = 0>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit,
                                          int site) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if constexpr (SPINS == 0) {
+    if (mbar_try_wait(bar, parity)) return true;
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < SPINS; ++i)
+      if (mbar_test_wait(bar, parity)) return true;
+  }
   return wait_slow(bar, parity, abort, status, limit, site);
 }
 

@@ -387,6 +387,46 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   }
 }
 
+// Joins up to kJoinFew parts of a row's keys: a thread 4 channels of a row,
+// all its loads at once.
+constexpr int kJoinFew = 8;
+template <int D>
+__global__ void __launch_bounds__(256) join_few_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int b = blockIdx.y;
+  const Seq s = load_seq(p, b);
+  const int i = blockIdx.x * 256 + threadIdx.x, c = i % (D / 4), th = i / (D / 4);
+  const int t = th / p.hq, h = th % p.hq;
+  if (t >= s.nq) return;
+  const int kvh = h / p.g, row = t * p.g + h % p.g;
+  const int64_t tile = (int64_t)(b * p.hk + kvh) * n_rt + row / rows_per_tile;
+  const int64_t first = tile * p.n_split * rows_per_tile + row % rows_per_tile;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o) + first * (D / 4) + c;
+  float2 ml[kJoinFew];
+  float4 v[kJoinFew];
+#pragma unroll
+  for (int k = 0; k < kJoinFew; ++k) {
+    const bool has = k < p.n_split;
+    ml[k] = has ? p.part_ml[first + (int64_t)k * rows_per_tile] : make_float2(-INFINITY, 0.f);
+    v[k] = has ? po[(int64_t)k * rows_per_tile * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinFew; ++k) mx = fmaxf(mx, ml[k].x);
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kJoinFew; ++k) {
+    const float f = ml[k].x == -INFINITY ? 0.f : exp2_approx(ml[k].x - mx);
+    lt = fmaf(ml[k].y, f, lt);
+    x.x = fmaf(v[k].x, f, x.x);
+    x.y = fmaf(v[k].y, f, x.y);
+    x.z = fmaf(v[k].z, f, x.z);
+    x.w = fmaf(v[k].w, f, x.w);
+  }
+  store_joined(p, (int64_t)(s.start + t) * p.hq + h, c, D, x, lt, mx);
+}
+
 // Joins the parts of a row's keys: one block a (query token, query head), a
 // group of D/4 threads every kJoinGroups-th part.  (A thread a channel walking
 // over all parts took 21 us for 37 of them: a chain of loads each.)
@@ -469,25 +509,27 @@ __global__ void __launch_bounds__(kJoinGroups * D / 4) join_kernel(const __grid_
       x.z += y.z;
       x.w += y.w;
     }
-    const float inv = lt > 0.f ? kValueUnscale / lt : 0.f;
-    const __nv_bfloat162 u = __floats2bfloat162_rn(x.x * inv, x.y * inv), w = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-    uint2 r;
-    r.x = *reinterpret_cast<const uint32_t*>(&u);
-    r.y = *reinterpret_cast<const uint32_t*>(&w);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 4 * c) = r;
+    store_joined(p, o, c, D, x, lt, mx);
   }
-  if (p.lse && tid == 0) p.lse[o] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
 
+template <int D>
+static cudaError_t join_launch_d(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st) {
+  const unsigned rows = (unsigned)(p.max_q * p.hq);
+  if (p.n_split <= kJoinFew)
+    return launch_pdl(join_few_kernel<D>, dim3((unsigned)(((int64_t)rows * (D / 4) + 255) / 256), p.n_seqs), 256, 0, st, p,
+                      rows_per_tile, n_rt);
+  return launch_pdl(join_kernel<D>, dim3(rows, p.n_seqs), kJoinGroups * D / 4, 0, st, p, rows_per_tile, n_rt);
+}
+
 cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st) {
-  const dim3 grid((unsigned)(p.max_q * p.hq), p.n_seqs);
   switch (p.D) {
-    case 64: return launch_pdl(join_kernel<64>, grid, kJoinGroups * 64 / 4, 0, st, p, rows_per_tile, n_rt);
-    case 128: return launch_pdl(join_kernel<128>, grid, kJoinGroups * 128 / 4, 0, st, p, rows_per_tile, n_rt);
-    case 192: return launch_pdl(join_kernel<192>, grid, kJoinGroups * 192 / 4, 0, st, p, rows_per_tile, n_rt);
-    default: return launch_pdl(join_kernel<256>, grid, kJoinGroups * 256 / 4, 0, st, p, rows_per_tile, n_rt);
+    case 64: return join_launch_d<64>(p, rows_per_tile, n_rt, st);
+    case 128: return join_launch_d<128>(p, rows_per_tile, n_rt, st);
+    case 192: return join_launch_d<192>(p, rows_per_tile, n_rt, st);
+    default: return join_launch_d<256>(p, rows_per_tile, n_rt, st);
   }
 }
 

@@ -7,17 +7,23 @@
 // (attn_small.cu) run out at 0.38 of the memory's rate before anything else;
 // and an expansion to 16 bits in memory (attn_prompt.cu) would move 8 times the
 // bytes.  Here a block's roles run beside each other, tile by tile of KT keys:
-//   warp 16      copies (page, head) blocks into a ring of raw stages;
-//   8 warps      (index % 4 >= 2) dequantise keys into a bf16 and values into
-//                an fp16 operand image in shared memory (exact);
-//   warp 17      issues S = Q K^T and O += P V (M = 128 of which 64 rows are
-//                used: the tensor memory lanes that warps of index % 4 < 2 read);
-//   8 warps      (index % 4 < 2) softmax, a quarter of the tile's keys each.
-// The images are single: keys j + 1 are dequantised while O += P_j V_j runs,
-// values j while S_{j+1} does.  Keys are split over blocks and joined.
+//   warps 0-15   index % 4 < 2: softmax, a quarter of the tile's keys each (the
+//                MMA's M is 128, of which 64 rows are used: the tensor memory
+//                lanes that these warps read); the others: keys to a bf16
+//                operand image in shared memory (exact);
+//   warps 16-23  values to an fp16 image (exact);
+//   warp 24      copies (page, head) blocks into a ring of raw stages;
+//   warp 25      issues S = Q K^T and O += P V.
+// Both images are [channels/8][keys][8 channels]: for the keys that is K-major
+// (the contraction runs over channels), for the values MN-major, so neither is
+// transposed.  Keys are split over blocks and joined.
 //
-// Values' image: 8x8 core matrices 144 bytes apart instead of 128, so that the
-// 8 lanes of a store phase (8 channels apart) meet all banks.
+// What a tile of 128 keys at D = 192 costs (cycles of a multiprocessor): shared
+// memory moves 300 KB for it, 2350 at 128 bytes a cycle, before the MMAs'
+// 1540, the memory's 1180 and 1500 of instructions.  Measured steps: one group
+// of 8 warps for both images took 4100 a tile (1450 for the keys, 1820 for the
+// values, one after the other, and values transposed into cores 144 bytes
+// apart made O += P V 1850 instead of 800).
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -28,12 +34,12 @@ cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaSt
 namespace {
 
 constexpr int kRowsV = 64;
-constexpr int kWarpsV = 18;
+constexpr int kWarpsV = 26;
+constexpr int kCopyWarp = 24, kMmaWarp = 25;
 constexpr int kThreadsV = kWarpsV * 32;
 constexpr int kMaxRaw = 8;
 // page masks kept: the softmax may be a raw ring and a tile behind the copies
 constexpr int kMasks = 16;
-constexpr int kCoreV = 144;  // bytes from one 8-channel group of the value image to the next
 
 template <int D>
 struct VerifyPlan {
@@ -45,13 +51,15 @@ struct VerifyPlan {
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + D / 8 * kRowsV * 16;
   static constexpr int kV = kK + D / 8 * KT * 16;
-  static constexpr int kRawAt = (kV + KT / 8 * (D / 8) * kCoreV + 127) / 128 * 128;
+  static constexpr int kRawAt = kV + D / 8 * KT * 16;
   static constexpr int kMax = kRawAt + kRaw * kRawStage;  // float [2][4][64]
-  static constexpr int kBars = kMax + 2 * 4 * kRowsV * 4;
-  static constexpr int kNumBars = 2 * kMaxRaw + 4 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = kMax + 2 * 4 * kRowsV * 4;  // (the sums and references need 5 x 64 of them)
+  static constexpr int kNumBars = 2 * kMaxRaw + 12 + 2 + 2 + 2 + 2;
   static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory slot, abort, page masks
   static constexpr int kTotal = kMisc + 16 + kMasks * 4 + 128;
   static_assert(kTotal <= 232448, "shared memory plan");
+  static constexpr int kPitch = D * 4 + 16;  // of an output row on its way out, over the images
+  static_assert(kRowsV * kPitch <= kRawAt, "the output fits the images' room");
 };
 
 template <int D>
@@ -63,14 +71,16 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   float* smax = reinterpret_cast<float*>(sm + L::kMax);
   uint64_t* rfull = reinterpret_cast<uint64_t*>(sm + L::kBars);  // raw ring: copies landed
   uint64_t* rempty = rfull + kMaxRaw;                             // raw ring: keys and values dequantised
-  uint64_t* kfull = rempty + kMaxRaw;                             // key image written
-  uint64_t* kempty = kfull + 1;                                   // scores computed from it
-  uint64_t* vfull = kempty + 1;                                   // value image written
-  uint64_t* odone = vfull + 1;                                    // output product done (value image free)
-  uint64_t* sfull = odone + 1;                                    // [2] scores ready
+  uint64_t* kfull = rempty + kMaxRaw;                             // [D/64] 64 channels of the key image written
+  uint64_t* kfree = kfull + 4;                                    // [D/64] scores' products from them done
+  uint64_t* vfull = kfree + 4;                                    // [2] half of the value image's keys written
+  uint64_t* vfree = vfull + 2;                                    // [2] output products from them done
+  uint64_t* odone = vfree + 1;                                    // (the second half's ends a tile's)
+  uint64_t* sfull = vfree + 2;                                    // [2] scores ready
   uint64_t* pfull = sfull + 2;                                    // [2] weights stored (the softmax may be a tile ahead)
   uint64_t* xbar = pfull + 2;                                     // [2] maxima exchanged
-  uint64_t* fin = xbar + 2;
+  uint64_t* qfull = xbar + 2;                                     // queries written
+  uint64_t* fin = qfull + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   volatile uint32_t* pmask = reinterpret_cast<volatile uint32_t*>(sm + L::kMisc + 16);  // pages present of tile j, at j % kMasks
@@ -80,36 +90,42 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   if (tid == 0) {
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], 8);
+      mbar_init(&rempty[i], 16);
     }
-    mbar_init(kfull, 8);
-    mbar_init(kempty, 1);
-    mbar_init(vfull, 8);
-    mbar_init(odone, 1);
+    for (int i = 0; i < D / 64; ++i) {
+      mbar_init(&kfull[i], 8);
+      mbar_init(&kfree[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&vfull[i], 8);
+      mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 8);
       mbar_init(&xbar[i], 8);
     }
+    mbar_init(qfull, 8);
     mbar_init(fin, 1);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kMmaWarp) tc::alloc_512(tslot);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tbase = *tslot;
   griddep_wait();
 
   const int split = blockIdx.x, b = blockIdx.z;
   const int kvh = blockIdx.y / n_rt, rt = blockIdx.y % n_rt;
   const Seq s = load_seq(p, b);
-  const int row0 = rt * kRowsV, n_rows = min(kRowsV, s.nq * p.g - row0);
-  if (n_rows <= 0) return;
+  const int row0 = rt * kRowsV, n_rows = max(0, min(kRowsV, s.nq * p.g - row0));
   const int p0 = s.len - s.nq;
-  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + n_rows - 1) / p.g;
+  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + max(n_rows, 1) - 1) / p.g;
   const int lo = key_lo(p, max(0, pos_min)), hi = pos_max + 1, lo_max = key_lo(p, pos_max);
   const int tile_a = lo / KT + split * chunk;
-  const int n_tiles = hi > lo ? max(0, min(tile_a + chunk, (hi + KT - 1) / KT) - tile_a) : 0;
+  const int n_tiles = hi > lo && n_rows > 0 ? max(0, min(tile_a + chunk, (hi + KT - 1) / KT) - tile_a) : 0;
   const int ppt = KT >= p.P ? KT >> p.pshift : 1;  // pages of a tile (a tile of half a page copies the page's head whole)
 
-  if (warp == 17) tc::alloc_512(tslot);
   const bool soft = warp < 16 && (warp & 3) < 2;
   const int row = (warp & 1) * 32 + lane, quarter = warp >> 2;  // of the softmax threads
   int tq = 0, hq = 0, hi_r = 0, lo_r = 0;
@@ -120,23 +136,9 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     hi_r = p0 + tq + 1;
     lo_r = key_lo(p, p0 + tq);
   }
-  if (soft && n_tiles > 0) {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
-#pragma unroll
-    for (int c = quarter * (D / 32); c < (quarter + 1) * (D / 32); ++c) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
-      *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsV + row) * 16) = v;
-    }
-    tc::fence_async_smem();
-  }
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tbase = *tslot;
 
   float m = -INFINITY, l = 0.f;
-  if (warp == 16) {
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------ raw copies
     const uint64_t pol = l2_evict_first_policy();
     auto page_of = [&](int i) {  // lane: page of the tile; -1 where nothing of it is seen
@@ -177,126 +179,136 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     }
     for (int k = max(0, i - L::kRaw); k < i; ++k)
       wait_bar(&rfull[k % L::kRaw], (uint32_t)((k / L::kRaw) & 1), &never, p.status, p.timeout_ns, 22);
-  } else if (warp == 17) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     if (lane == 0 && n_tiles > 0) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, KT) | (1u << 7) | (1u << 10);  // bf16 operands
-      constexpr uint32_t kIdescO = tc::idesc_f16(128, D);
+      constexpr uint32_t kIdescO = tc::idesc_f16(128, D) | (1u << 16);  // fp16, the values MN-major
       const uint64_t qd = tc::smem_desc(smem_u32(sm + L::kQ), kRowsV * 16, 128);
       const uint64_t kd = tc::smem_desc(smem_u32(sm + L::kK), KT * 16, 128);
-      constexpr uint32_t kLboV = D / 8 * kCoreV;
-      const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kV), kLboV, kCoreV);
+      // MN-major: 8 keys of a core matrix 128 bytes on, 8 channels a slab on
+      const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kV), 128, KT * 16);
       bool ok = true;
       auto scores = [&](int j) {
-        ok = wait_bar(kfull, (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 23);
-        if (!ok) return;
-        tc::fence_after();
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tbase + 128 * (j & 1), qd + k * (2 * kRowsV * 16 / 16), kd + k * (2 * KT * 16 / 16), kIdescS, k > 0);
-        tc::commit(kempty);
+        for (int c = 0; c < D / 64; ++c) {
+          ok = ok && wait_bar<64>(&kfull[c], (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 23);
+          if (!ok) return;
+          tc::fence_after();
+#pragma unroll
+          for (int k = 4 * c; k < 4 * c + 4; ++k)
+            mma_ss(tbase + 128 * (j & 1), qd + k * (2 * kRowsV * 16 / 16), kd + k * (2 * KT * 16 / 16), kIdescS, k > 0);
+          tc::commit(&kfree[c]);
+        }
         tc::commit(&sfull[j & 1]);
       };
-      scores(0);
+      ok = wait_bar<64>(qfull, 0, abort, p.status, p.timeout_ns, 34);
+      if (ok) scores(0);
       for (int j = 0; j < n_tiles && ok; ++j) {
         if (j + 1 < n_tiles) scores(j + 1);
-        ok = ok && wait_bar(vfull, (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 24);
-        ok = ok && wait_bar(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 25);
-        if (!ok) break;
-        tc::fence_after();
+        ok = ok && wait_bar<64>(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 25);
 #pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
-          tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * kLboV / 16), kIdescO, j > 0 || k > 0);
-        tc::commit(odone);
+        for (int v = 0; v < 2; ++v) {
+          ok = ok && wait_bar<64>(&vfull[v], (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 24);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll
+          for (int k = v * (KT / 32); k < (v + 1) * (KT / 32); ++k)
+            tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * 128 / 16), kIdescO, j > 0 || k > 0);
+          tc::commit(&vfree[v]);
+        }
       }
       // all MMAs issued are complete before the block frees anything
       tc::commit(fin);
-      wait_bar(fin, 0, &never, p.status, p.timeout_ns, 26);
+      wait_bar<64>(fin, 0, &never, p.status, p.timeout_ns, 26);
     }
   } else if (!soft && n_tiles > 0) {
     // ------------------------------------------------------------ dequantisation
-    const int dt = ((warp >> 2) * 2 + (warp & 1)) * 32 + lane;  // 0..255
-    const int keys = min(p.P, KT);                              // of a page's part in a raw stage
+    const bool values = warp >= 16;
+    const int dw = values ? warp - 16 : (warp >> 2) * 2 + (warp & 1);  // 0..7
+    const int keys = min(p.P, KT);                                   // of a page's part in a raw stage
     const int kshift = 31 - __clz(keys);
-    const int part = keys * (D * 9 / 8), codes = keys * (D / 2), half = keys * (D * 9 / 16);
-    bool ok = true;
-    auto keys_image = [&](int j) {
+    const int part = keys * (D * 9 / 8), codes = keys * (D / 2), half = values ? keys * (D * 9 / 16) : 0;
+    // the images are written, and free again, in parts: 64 channels of the
+    // keys, half of the values' keys (of the whole images, each waiting for the
+    // products of the last tile, the two chains took 4200 cycles a tile)
+    constexpr int kParts = D / 64;
+    uint64_t* image_full = values ? vfull : kfull;
+    uint64_t* image_free = values ? vfree : kfree;
+    uint8_t* image = sm + (values ? L::kV : L::kK);
+    // a warp takes 8 keys of 64 channels: each 8 lanes 8 keys (their stores
+    // meet all banks), the 16-channel group turned by a pattern in which 16
+    // lanes' loads do too (at 192 and 64 channels)
+    const int k8 = lane & 7, q = lane >> 3;
+    const int c4 = (2 * (q & 1) + (k8 >> 2)) ^ (q >> 1);
+    for (int j = 0; j < n_tiles; ++j) {
       const int st = j % L::kRaw;
-      ok = wait_bar(&rfull[st], (uint32_t)((j / L::kRaw) & 1), abort, p.status, p.timeout_ns, 27);
-      if (j > 0) ok = ok && wait_bar(kempty, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 28);
+      bool ok = wait_bar(&rfull[st], (uint32_t)((j / L::kRaw) & 1), abort, p.status, p.timeout_ns, 27);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const uint8_t* raw = sm + L::kRawAt + st * L::kRawStage;
-      // a warp takes 8 keys of 64 channels: each 8 lanes 8 keys (their stores
-      // meet all banks), the 16-channel group turned by a pattern in which 16
-      // lanes' loads do too (at 192 and 64 channels)
-      const int k8 = lane & 7, q = lane >> 3;
-      const int c4 = (2 * (q & 1) + (k8 >> 2)) ^ (q >> 1);
-      for (int u = dt >> 5; u < KT / 8 * (D / 64); u += 8) {
-        const int key = 8 * (u % (KT / 8)) + k8, c = 4 * (u / (KT / 8)) + c4;
+      if (!ok) break;
+      const uint8_t* raw = sm + L::kRawAt + st * L::kRawStage + half;
+      const uint32_t mask = pmask[j % kMasks];
+      const int j0 = (tile_a + j) * KT;
+      const bool whole = mask == (1u << ppt) - 1u && j0 + KT <= s.len;
+      static_assert(KT / 8 % 8 == 0 && KT / 16 * (D / 64) % 8 == 0, "the same work for each warp");
+      auto unit = [&](int key8, int c64) {  // 8 keys of 64 channels
+        const int key = 8 * key8 + k8, c = 4 * c64 + c4;
         const uint8_t* base = raw + (key >> kshift) * part;
         const int at = key & (keys - 1);
         const uint2 w = *reinterpret_cast<const uint2*>(base + at * (D / 2) + 8 * c);
-        const uint32_t sb = base[codes + at * (D / 16) + c];
-        const KeyScale d = key_scale(sb | (sb << 16));
+        uint32_t sb = base[codes + at * (D / 16) + c];
         uint32_t x[8];
-        key_pairs(w.x, d, x);
-        key_pairs(w.y, d, x + 4);
-        uint4* o = reinterpret_cast<uint4*>(sm + L::kK + (2 * c * KT + key) * 16);
+        if (values) {
+          // a key past the end or on an absent page: scale 0, whatever lies there
+          if (!whole && (!((mask >> (key >> kshift)) & 1) || j0 + key >= s.len)) sb = 0;
+          const ValueScale d = value_scale(sb | (sb << 16));
+          value_quads(w.x, d, x[0], x[1], x[2], x[3]);
+          value_quads(w.y, d, x[4], x[5], x[6], x[7]);
+        } else {
+          const KeyScale d = key_scale(sb | (sb << 16));
+          key_pairs(w.x, d, x);
+          key_pairs(w.y, d, x + 4);
+        }
+        uint4* o = reinterpret_cast<uint4*>(image + (2 * c * KT + key) * 16);
         o[0] = make_uint4(x[0], x[1], x[2], x[3]);
         o[KT] = make_uint4(x[4], x[5], x[6], x[7]);
-      }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(kfull);
-    };
-    auto values_image = [&](int j) {
-      const int st = j % L::kRaw;
-      if (j > 0) ok = wait_bar(odone, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 29);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const uint8_t* raw = sm + L::kRawAt + st * L::kRawStage;
-      const uint32_t mask = pmask[j % kMasks];
-      const int j0 = (tile_a + j) * KT;
-      const bool whole = mask == (ppt == 32 ? 0xffffffffu : (1u << ppt) - 1u) && j0 + KT <= s.len;
-      for (int u = dt; u < KT / 8 * (D / 8); u += 256) {
-        const int w = u % (D / 8), k0 = 8 * (u / (D / 8));
-        const uint8_t* base = raw + (k0 >> kshift) * part + half;
-        const int at = k0 & (keys - 1);
-        const uint8_t* vc = base + at * (D / 2) + 4 * w;
-        const uint8_t* vs = base + codes + at * (D / 16) + (w >> 1);
-        // keys past the end or on absent pages: scale 0, whatever lies there
-        const int n = whole ? 8 : (((mask >> (k0 >> kshift)) & 1) ? min(8, s.len - j0 - k0) : 0);
-        uint32_t x[4][8];  // [pair of keys][channel]
+      };
+      const int n_parts = values ? 2 : kParts;
+      for (int i = 0; i < n_parts; ++i) {
+        if (j > 0) ok = wait_bar(&image_free[i], (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 28);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (values) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vc + 2 * i * (D / 2));
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vc + (2 * i + 1) * (D / 2));
-          uint32_t s0 = vs[2 * i * (D / 16)], s1 = vs[(2 * i + 1) * (D / 16)];
-          s0 = 2 * i < n ? s0 : 0;
-          s1 = 2 * i + 1 < n ? s1 : 0;
-          const ValueScale d = value_scale(s0 | (s1 << 16));
-          value_quads(__byte_perm(w0, w1, 0x5410), d, x[i][0], x[i][2], x[i][4], x[i][6]);
-          value_quads(__byte_perm(w0, w1, 0x7632), d, x[i][1], x[i][3], x[i][5], x[i][7]);
+          for (int v = 0; v < KT / 16 * kParts / 8; ++v) {
+            const int u = dw + 8 * v;
+            unit(i * (KT / 16) + u % (KT / 16), u / (KT / 16));
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < KT / 64; ++v) unit(dw + 8 * v, i);
         }
-        uint8_t* o = sm + L::kV + (k0 / 8) * (D / 8 * kCoreV) + w * kCoreV;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(o + 16 * c) = make_uint4(x[0][c], x[1][c], x[2][c], x[3][c]);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&image_full[i]);
       }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(vfull);
-        mbar_arrive(&rempty[st]);
-      }
-    };
-    keys_image(0);
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      if (j + 1 < n_tiles) keys_image(j + 1);
-      if (ok) values_image(j);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&rempty[st]);
     }
   } else if (soft && n_tiles > 0) {
     // ------------------------------------------------------------ softmax
+    {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
+#pragma unroll
+      for (int c = quarter * (D / 32); c < (quarter + 1) * (D / 32); ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
+        *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsV + row) * 16) = v;
+      }
+    }
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qfull);
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
@@ -385,37 +397,46 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       tc::fence_after();
     }
   }
-  // the quarters' sums
+  // the quarters' sums; the outputs go through shared memory (the images'
+  // room), since a thread's row is D apart from its neighbour's: stored from
+  // the accumulator's layout they took 5 us
+  tc::fence_before();
   __syncthreads();
+  tc::fence_after();
   if (soft) smax[quarter * kRowsV + row] = l;
-  __syncthreads();
-  if (soft) {
-    l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) l += smax[i * kRowsV + row];
+  if (soft && n_tiles > 0) {
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
-    const int64_t orow = (int64_t)(s.start + tq) * p.hq + hq;
-    const int64_t part = ((int64_t)(b * p.hk * n_rt + blockIdx.y) * p.n_split + split) * kRowsV + row;
-    const float inv = p.n_split > 1 ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
 #pragma unroll 1
     for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
       uint32_t o[16];
-      __syncwarp();
-      if (n_tiles > 0) {
-        tc::ld_32x32b_x16(tl + 256 + c, o);
-        tc::wait_ld();
-      }
-      store_out16(p, o, l, inv, has_row, part, orow, c, D);
+      tc::ld_32x32b_x16(tl + 256 + c, o);
+      tc::wait_ld();
+      uint4* d = reinterpret_cast<uint4*>(sm + row * L::kPitch + c * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
     }
-    if (has_row && quarter == 0) {
-      if (p.n_split > 1) p.part_ml[part] = make_float2(m, l);
-      else if (p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-    }
-    tc::fence_before();
+    if (quarter == 0) smax[4 * kRowsV + row] = m;
   }
+  tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 17) tc::dealloc_512(tbase);
+  if (warp == kMmaWarp) tc::dealloc_512(tbase);
+  const int64_t part0 = ((int64_t)(b * p.hk * n_rt + blockIdx.y) * p.n_split + split) * kRowsV;
+  for (int i = tid; i < n_rows * (D / 4); i += kThreadsV) {
+    const int r = i / (D / 4), c = i % (D / 4);
+    float lt = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) lt += smax[k * kRowsV + r];
+    const float mr = n_tiles > 0 ? smax[4 * kRowsV + r] : -INFINITY;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lt > 0.f) v = *reinterpret_cast<const float4*>(sm + r * L::kPitch + c * 16);
+    if (p.n_split > 1) {
+      *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + 4 * c) = v;
+      if (c == 0) p.part_ml[part0 + r] = make_float2(mr, lt);
+    } else {
+      store_joined(p, (int64_t)(s.start + (row0 + r) / p.g) * p.hq + kvh * p.g + (row0 + r) % p.g, c, D, v, lt, mr);
+    }
+  }
 }
 
 template <int D>
