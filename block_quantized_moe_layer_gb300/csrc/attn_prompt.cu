@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
   const int ppt = kTileTokens >> p.pshift, tid = threadIdx.x, D = p.D;
   if (tid < ppt) {
     const int i = tile * ppt + tid;
-    page[tid] = (i << p.pshift) < s.len ? load_page(p, b, i) : -1;
+    // (a page that no query sees is not looked at: it may have been given back)
+    const bool seen = (i << p.pshift) < s.len && ((i + 1) << p.pshift) > key_lo(p, max(0, s.len - s.nq));
+    page[tid] = seen ? load_page(p, b, i) : -1;
   }
   __syncthreads();
   const int n_keys = min(kTileTokens, s.len - tile * kTileTokens);

@@ -9,21 +9,22 @@
 // bytes.  Here a block's roles run beside each other, tile by tile of KT keys:
 //   warps 0-15   index % 4 < 2: softmax, a quarter of the tile's keys each (the
 //                MMA's M is 128, of which 64 rows are used: the tensor memory
-//                lanes that these warps read); the others: keys to a bf16
-//                operand image in shared memory (exact);
+//                lanes that these warps read); the others: keys, from the
+//                pages by way of registers (a tile ahead) to a bf16 operand
+//                image in shared memory (exact);
 //   warps 16-23  values to an fp16 image (exact);
-//   warp 24      copies (page, head) blocks into a ring of raw stages;
-//   warp 25      issues S = Q K^T and O += P V.
+//   warp 24      issues S = Q K^T and O += P V.
 // Both images are [channels/8][keys][8 channels]: for the keys that is K-major
 // (the contraction runs over channels), for the values MN-major, so neither is
-// transposed.  Keys are split over blocks and joined.
+// transposed.  There are two of each.  Keys are split over blocks and joined.
 //
-// What a tile of 128 keys at D = 192 costs (cycles of a multiprocessor): shared
-// memory moves 300 KB for it, 2350 at 128 bytes a cycle, before the MMAs'
-// 1540, the memory's 1180 and 1500 of instructions.  Measured steps: one group
-// of 8 warps for both images took 4100 a tile (1450 for the keys, 1820 for the
-// values, one after the other, and values transposed into cores 144 bytes
-// apart made O += P V 1850 instead of 800).
+// Bound: shared memory.  A tile of 128 keys at D = 192 moves 240 KB through it
+// (both images in and out, the queries), 1900 cycles at 128 bytes a cycle,
+// beside 1540 of MMAs, 1180 of the memory's time and 1500 of instructions.
+// Measured on the way, cycles a tile: 4300 with the raw pages copied to shared
+// memory first (another 54 KB) and single images, whatever the order of the
+// roles; values transposed by hand into cores 144 bytes apart made O += P V
+// 1850 instead of 800.
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -34,32 +35,29 @@ cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaSt
 namespace {
 
 constexpr int kRowsV = 64;
-constexpr int kWarpsV = 26;
-constexpr int kCopyWarp = 24, kMmaWarp = 25;
+constexpr int kWarpsV = 25;
+constexpr int kMmaWarp = 24;
 constexpr int kThreadsV = kWarpsV * 32;
-constexpr int kMaxRaw = 8;
-// page masks kept: the softmax may be a raw ring and a tile behind the copies
-constexpr int kMasks = 16;
 
 template <int D>
 struct VerifyPlan {
   static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile
-  static constexpr int kRawStage = KT * D * 9 / 8;
-  static constexpr int kRaw = D == 64 ? 8 : (D == 128 ? 5 : 3);
+  static constexpr int kImage = D / 8 * KT * 16;
   // queries [D/8][64 rows][8]: the MMA's rows 64..127 run into the next slab
   // (and past the last one into the keys' image): read, never used
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + D / 8 * kRowsV * 16;
-  static constexpr int kV = kK + D / 8 * KT * 16;
-  static constexpr int kRawAt = kV + D / 8 * KT * 16;
-  static constexpr int kMax = kRawAt + kRaw * kRawStage;  // float [2][4][64]
-  static constexpr int kBars = kMax + 2 * 4 * kRowsV * 4;  // (the sums and references need 5 x 64 of them)
-  static constexpr int kNumBars = 2 * kMaxRaw + 12 + 2 + 2 + 2 + 2;
-  static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory slot, abort, page masks
-  static constexpr int kTotal = kMisc + 16 + kMasks * 4 + 128;
+  static constexpr int kV = kK + 2 * kImage;
+  static constexpr int kMax = kV + 2 * kImage;                 // float [2][4][64] (the sums and references need 5 x 64)
+  // [8 tiles][16]: a byte for each 8 keys that exist (written up to 4 tiles before the softmax reads it)
+  static constexpr int kHere = kMax + 2 * 4 * kRowsV * 4;
+  static constexpr int kBars = kHere + 8 * 16;
+  static constexpr int kNumBars = 8 + 2 + 2 + 2 + 2;
+  static constexpr int kMisc = kBars + kNumBars * 8;           // tensor memory slot, abort
+  static constexpr int kTotal = kMisc + 16 + 128;
   static_assert(kTotal <= 232448, "shared memory plan");
   static constexpr int kPitch = D * 4 + 16;  // of an output row on its way out, over the images
-  static_assert(kRowsV * kPitch <= kRawAt, "the output fits the images' room");
+  static_assert(kRowsV * kPitch <= kMax, "the output fits the images' room");
 };
 
 template <int D>
@@ -69,13 +67,11 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   float* smax = reinterpret_cast<float*>(sm + L::kMax);
-  uint64_t* rfull = reinterpret_cast<uint64_t*>(sm + L::kBars);  // raw ring: copies landed
-  uint64_t* rempty = rfull + kMaxRaw;                             // raw ring: keys and values dequantised
-  uint64_t* kfull = rempty + kMaxRaw;                             // [D/64] 64 channels of the key image written
-  uint64_t* kfree = kfull + 4;                                    // [D/64] scores' products from them done
-  uint64_t* vfull = kfree + 4;                                    // [2] half of the value image's keys written
-  uint64_t* vfree = vfull + 2;                                    // [2] output products from them done
-  uint64_t* odone = vfree + 1;                                    // (the second half's ends a tile's)
+  uint8_t* here = sm + L::kHere;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + L::kBars);  // [2] key image written
+  uint64_t* kfree = kfull + 2;                                    // [2] scores' products from it done
+  uint64_t* vfull = kfree + 2;                                    // [2] value image written
+  uint64_t* vfree = vfull + 2;                                    // [2] output products from it done
   uint64_t* sfull = vfree + 2;                                    // [2] scores ready
   uint64_t* pfull = sfull + 2;                                    // [2] weights stored (the softmax may be a tile ahead)
   uint64_t* xbar = pfull + 2;                                     // [2] maxima exchanged
@@ -83,20 +79,13 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   uint64_t* fin = qfull + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
-  volatile uint32_t* pmask = reinterpret_cast<volatile uint32_t*>(sm + L::kMisc + 16);  // pages present of tile j, at j % kMasks
   volatile int never = 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < L::kRaw; ++i) {
-      mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], 16);
-    }
-    for (int i = 0; i < D / 64; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 8);
       mbar_init(&kfree[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(&vfull[i], 8);
       mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1);
@@ -124,7 +113,6 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   const int lo = key_lo(p, max(0, pos_min)), hi = pos_max + 1, lo_max = key_lo(p, pos_max);
   const int tile_a = lo / KT + split * chunk;
   const int n_tiles = hi > lo && n_rows > 0 ? max(0, min(tile_a + chunk, (hi + KT - 1) / KT) - tile_a) : 0;
-  const int ppt = KT >= p.P ? KT >> p.pshift : 1;  // pages of a tile (a tile of half a page copies the page's head whole)
 
   const bool soft = warp < 16 && (warp & 3) < 2;
   const int row = (warp & 1) * 32 + lane, quarter = warp >> 2;  // of the softmax threads
@@ -138,48 +126,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   }
 
   float m = -INFINITY, l = 0.f;
-  if (warp == kCopyWarp) {
-    // ------------------------------------------------------------ raw copies
-    const uint64_t pol = l2_evict_first_policy();
-    auto page_of = [&](int i) {  // lane: page of the tile; -1 where nothing of it is seen
-      const int j0 = (tile_a + i) * KT + (lane << p.pshift);
-      return lane < ppt && i < n_tiles && j0 < hi && j0 + min(p.P, KT) > lo ? load_page(p, b, j0 >> p.pshift) : -1;
-    };
-    bool ok = true;
-    int pg = page_of(0), i = 0;
-    for (; i < n_tiles; ++i) {
-      const int next = page_of(i + 1), st = i % L::kRaw;
-      if (i >= L::kRaw)
-        ok = wait_bar(&rempty[st], (uint32_t)((i / L::kRaw - 1) & 1), abort, p.status, p.timeout_ns, 21);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0);
-      const int keys = min(p.P, KT);                    // of a page in this tile
-      const int at = ((tile_a + i) * KT) & (p.P - 1);   // the tile's first key in its page
-      if (lane == 0) {
-        pmask[i % kMasks] = mask;
-        mbar_arrive_expect_tx(&rfull[st], (uint32_t)(__popc(mask) * keys * (D * 9 / 8)));
-      }
-      __syncwarp();
-      if (pg >= 0) {
-        const uint8_t* src = p.pages + pg * p.page_bytes + kvh * p.head_bytes;
-        uint8_t* dst = sm + L::kRawAt + st * L::kRawStage + lane * keys * (D * 9 / 8);
-        if (keys == p.P) {
-          bulk_g2s_hint(dst, src, (uint32_t)p.head_bytes, &rfull[st], pol);
-        } else {  // part of a page: its four arrays
-          const int64_t half = p.head_bytes / 2;
-          bulk_g2s_hint(dst, src + at * (D / 2), keys * (D / 2), &rfull[st], pol);
-          bulk_g2s_hint(dst + keys * (D / 2), src + p.P * (D / 2) + at * (D / 16), keys * (D / 16), &rfull[st], pol);
-          bulk_g2s_hint(dst + keys * (D * 9 / 16), src + half + at * (D / 2), keys * (D / 2), &rfull[st], pol);
-          bulk_g2s_hint(dst + keys * (D * 9 / 16) + keys * (D / 2), src + half + p.P * (D / 2) + at * (D / 16), keys * (D / 16),
-                        &rfull[st], pol);
-        }
-      }
-      pg = next;
-    }
-    for (int k = max(0, i - L::kRaw); k < i; ++k)
-      wait_bar(&rfull[k % L::kRaw], (uint32_t)((k / L::kRaw) & 1), &never, p.status, p.timeout_ns, 22);
-  } else if (warp == kMmaWarp) {
+  if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     if (lane == 0 && n_tiles > 0) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, KT) | (1u << 7) | (1u << 10);  // bf16 operands
@@ -190,33 +137,30 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kV), 128, KT * 16);
       bool ok = true;
       auto scores = [&](int j) {
+        const int i = j & 1;
+        ok = wait_bar<64>(&kfull[i], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 23);
+        if (!ok) return;
+        tc::fence_after();
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          ok = ok && wait_bar<64>(&kfull[c], (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 23);
-          if (!ok) return;
-          tc::fence_after();
-#pragma unroll
-          for (int k = 4 * c; k < 4 * c + 4; ++k)
-            mma_ss(tbase + 128 * (j & 1), qd + k * (2 * kRowsV * 16 / 16), kd + k * (2 * KT * 16 / 16), kIdescS, k > 0);
-          tc::commit(&kfree[c]);
-        }
-        tc::commit(&sfull[j & 1]);
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tbase + 128 * i, qd + k * (2 * kRowsV * 16 / 16), kd + i * (L::kImage / 16) + k * (2 * KT * 16 / 16), kIdescS,
+                 k > 0);
+        tc::commit(&kfree[i]);
+        tc::commit(&sfull[i]);
       };
       ok = wait_bar<64>(qfull, 0, abort, p.status, p.timeout_ns, 34);
       if (ok) scores(0);
       for (int j = 0; j < n_tiles && ok; ++j) {
+        const int i = j & 1;
         if (j + 1 < n_tiles) scores(j + 1);
-        ok = ok && wait_bar<64>(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 25);
+        ok = ok && wait_bar<64>(&vfull[i], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 24);
+        ok = ok && wait_bar<64>(&pfull[i], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 25);
+        if (!ok) break;
+        tc::fence_after();
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          ok = ok && wait_bar<64>(&vfull[v], (uint32_t)(j & 1), abort, p.status, p.timeout_ns, 24);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int k = v * (KT / 32); k < (v + 1) * (KT / 32); ++k)
-            tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * 128 / 16), kIdescO, j > 0 || k > 0);
-          tc::commit(&vfree[v]);
-        }
+        for (int k = 0; k < KT / 16; ++k)
+          tc::mma_ts(tbase + 256, tbase + 128 * i + 8 * k, vd + i * (L::kImage / 16) + k * (2 * 128 / 16), kIdescO, j > 0 || k > 0);
+        tc::commit(&vfree[i]);
       }
       // all MMAs issued are complete before the block frees anything
       tc::commit(fin);
@@ -226,74 +170,69 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     // ------------------------------------------------------------ dequantisation
     const bool values = warp >= 16;
     const int dw = values ? warp - 16 : (warp >> 2) * 2 + (warp & 1);  // 0..7
-    const int keys = min(p.P, KT);                                   // of a page's part in a raw stage
-    const int kshift = 31 - __clz(keys);
-    const int part = keys * (D * 9 / 8), codes = keys * (D / 2), half = values ? keys * (D * 9 / 16) : 0;
-    // the images are written, and free again, in parts: 64 channels of the
-    // keys, half of the values' keys (of the whole images, each waiting for the
-    // products of the last tile, the two chains took 4200 cycles a tile)
-    constexpr int kParts = D / 64;
+    const int codes = p.P * (D / 2);
     uint64_t* image_full = values ? vfull : kfull;
     uint64_t* image_free = values ? vfree : kfree;
     uint8_t* image = sm + (values ? L::kV : L::kK);
-    // a warp takes 8 keys of 64 channels: each 8 lanes 8 keys (their stores
-    // meet all banks), the 16-channel group turned by a pattern in which 16
-    // lanes' loads do too (at 192 and 64 channels)
-    const int k8 = lane & 7, q = lane >> 3;
-    const int c4 = (2 * (q & 1) + (k8 >> 2)) ^ (q >> 1);
+    // a warp takes the key groups dw, dw + 8 (of 8 keys), of 64 channels at a
+    // time: each 8 lanes 8 keys, so that their stores meet all banks
+    const int k8 = lane & 7, c4 = lane >> 3;
+    constexpr int kGroups = KT / 64, kUnits = kGroups * (D / 64);
+    uint2 code[kUnits];
+    uint32_t scale[kUnits];
+    auto fetch = [&](int j) {  // this lane's codes and scales of tile j: 0 for a key past the end or on an absent page
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int g8 = dw + 8 * g, key = (tile_a + j) * KT + 8 * g8;
+        // (a page that no row here sees is not looked at: it may have been given back)
+        const int pg = j < n_tiles && key < hi && (key | (p.P - 1)) >= lo ? load_page(p, b, key >> p.pshift) : -1;
+        const int at = (key & (p.P - 1)) + k8;
+        const uint8_t* src = p.pages + pg * p.page_bytes + (int64_t)kvh * p.head_bytes + (values ? p.head_bytes / 2 : 0);
+        const bool has = pg >= 0 && key + k8 < s.len;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          code[g * (D / 64) + c] = make_uint2(0, 0);
+          scale[g * (D / 64) + c] = 0;
+          if (has) {
+            code[g * (D / 64) + c] = __ldcg(reinterpret_cast<const uint2*>(src + at * (D / 2) + 32 * c + 8 * c4));
+            scale[g * (D / 64) + c] = __ldcg(src + codes + at * (D / 16) + 4 * c + c4);
+          }
+        }
+        if (!values && lane == 0) here[(j & 7) * 16 + g8] = pg >= 0;
+      }
+    };
+    fetch(0);
     for (int j = 0; j < n_tiles; ++j) {
-      const int st = j % L::kRaw;
-      bool ok = wait_bar(&rfull[st], (uint32_t)((j / L::kRaw) & 1), abort, p.status, p.timeout_ns, 27);
+      const int i = j & 1;
+      bool ok = true;
+      if (j > 1) ok = wait_bar(&image_free[i], (uint32_t)((j >> 1) - 1) & 1, abort, p.status, p.timeout_ns, 28);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint8_t* raw = sm + L::kRawAt + st * L::kRawStage + half;
-      const uint32_t mask = pmask[j % kMasks];
-      const int j0 = (tile_a + j) * KT;
-      const bool whole = mask == (1u << ppt) - 1u && j0 + KT <= s.len;
-      static_assert(KT / 8 % 8 == 0 && KT / 16 * (D / 64) % 8 == 0, "the same work for each warp");
-      auto unit = [&](int key8, int c64) {  // 8 keys of 64 channels
-        const int key = 8 * key8 + k8, c = 4 * c64 + c4;
-        const uint8_t* base = raw + (key >> kshift) * part;
-        const int at = key & (keys - 1);
-        const uint2 w = *reinterpret_cast<const uint2*>(base + at * (D / 2) + 8 * c);
-        uint32_t sb = base[codes + at * (D / 16) + c];
-        uint32_t x[8];
-        if (values) {
-          // a key past the end or on an absent page: scale 0, whatever lies there
-          if (!whole && (!((mask >> (key >> kshift)) & 1) || j0 + key >= s.len)) sb = 0;
-          const ValueScale d = value_scale(sb | (sb << 16));
-          value_quads(w.x, d, x[0], x[1], x[2], x[3]);
-          value_quads(w.y, d, x[4], x[5], x[6], x[7]);
-        } else {
-          const KeyScale d = key_scale(sb | (sb << 16));
-          key_pairs(w.x, d, x);
-          key_pairs(w.y, d, x + 4);
-        }
-        uint4* o = reinterpret_cast<uint4*>(image + (2 * c * KT + key) * 16);
-        o[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        o[KT] = make_uint4(x[4], x[5], x[6], x[7]);
-      };
-      const int n_parts = values ? 2 : kParts;
-      for (int i = 0; i < n_parts; ++i) {
-        if (j > 0) ok = wait_bar(&image_free[i], (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 28);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (values) {
+      uint4* o = reinterpret_cast<uint4*>(image + i * L::kImage);
 #pragma unroll
-          for (int v = 0; v < KT / 16 * kParts / 8; ++v) {
-            const int u = dw + 8 * v;
-            unit(i * (KT / 16) + u % (KT / 16), u / (KT / 16));
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint2 w = code[g * (D / 64) + c];
+          const uint32_t sb = scale[g * (D / 64) + c] * 0x00010001u;
+          uint32_t x[8];
+          if (values) {
+            const ValueScale d = value_scale(sb);
+            value_quads(w.x, d, x[0], x[1], x[2], x[3]);
+            value_quads(w.y, d, x[4], x[5], x[6], x[7]);
+          } else {
+            const KeyScale d = key_scale(sb);
+            key_pairs(w.x, d, x);
+            key_pairs(w.y, d, x + 4);
           }
-        } else {
-#pragma unroll
-          for (int v = 0; v < KT / 64; ++v) unit(dw + 8 * v, i);
+          uint4* r = o + (8 * c + 2 * c4) * KT + 8 * (dw + 8 * g) + k8;
+          r[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          r[KT] = make_uint4(x[4], x[5], x[6], x[7]);
         }
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&image_full[i]);
-      }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&rempty[st]);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&image_full[i]);
+      if (j + 1 < n_tiles) fetch(j + 1);
     }
   } else if (soft && n_tiles > 0) {
     // ------------------------------------------------------------ softmax
@@ -324,8 +263,11 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
 #pragma unroll
       for (int c = 0; c < QC; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
       const int c0 = (tile_a + j) * KT;
-      const uint32_t mask = pmask[j % kMasks];
-      if (c0 + KT > pos_min + 1 || c0 < lo_max || mask != (1u << ppt) - 1u) {
+      // the existing 8-key groups of this quarter, a byte each
+      uint32_t mask;
+      if constexpr (QC == 32) mask = *reinterpret_cast<const volatile uint32_t*>(here + (j & 7) * 16 + 4 * quarter);
+      else mask = *reinterpret_cast<const volatile uint16_t*>(here + (j & 7) * 16 + 2 * quarter);
+      if (c0 + KT > pos_min + 1 || c0 < lo_max || mask != (0x01010101u >> (32 - QC))) {
         // bit c: key c0 + QC quarter + c is visible to this row
         const int k0 = c0 + QC * quarter;
         uint32_t vis = 0xffffffffu;
@@ -334,7 +276,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
         vis &= a <= 0 ? ~0u : (a >= 32 ? 0u : ~((1u << a) - 1));
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
-          const bool page = p.P >= KT ? mask != 0 : (mask >> ((QC * quarter + c) >> p.pshift)) & 1;
+          const bool page = (mask >> (c & ~7)) & 1;
           if (!((vis >> c) & 1) || !page) x[c] = -INFINITY;
         }
       }
@@ -358,7 +300,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
         if (move) m = mx;
         l *= f;
         if (j > 0) {
-          ok = wait_bar(odone, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 32);
+          ok = wait_bar(&vfree[(j - 1) & 1], (uint32_t)(((j - 1) >> 1) & 1), abort, p.status, p.timeout_ns, 32);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after();
@@ -392,7 +334,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       if (lane == 0) mbar_arrive(&pfull[j & 1]);
     }
     if (ok) {
-      ok = wait_bar(odone, (uint32_t)((n_tiles - 1) & 1), abort, p.status, p.timeout_ns, 33);
+      ok = wait_bar(&vfree[(n_tiles - 1) & 1], (uint32_t)(((n_tiles - 1) >> 1) & 1), abort, p.status, p.timeout_ns, 33);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after();
     }

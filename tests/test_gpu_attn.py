@@ -334,6 +334,23 @@ def test_forward_rows_of_no_sequence_are_left_alone():
     assert (np.abs(_np(out[4:7]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag).all()
 
 
+@pytest.mark.parametrize("D", [64, 192, 256])
+@pytest.mark.parametrize("news", [1, 4, 40])
+def test_forward_window_with_pages_given_back(D, news):
+    """Table entries of pages wholly before every query's window are not looked at."""
+    rng = np.random.default_rng(20)
+    hq, hk, P, n, window = 16, 1, 16, 700, 100
+    pages, table, keys, values, n_pages = _cache(rng, [n], hk, D, P)
+    at = pkg.Attention(hq, hk, D, P, n_pages, news, 1, n, rot_dim=0, window=window)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(news, hq, D, device="cuda").to(torch.bfloat16)
+    args = (torch.tensor([0, news], **i32), torch.tensor([n], **i32))
+    whole = at.forward(q, pages, *args, table, news, n)
+    table[0, :(n - news - window + 1) // P] = -1
+    assert torch.equal(at.forward(q, pages, *args, table, news, n), whole)
+    at.status()
+
+
 def test_forward_captured_in_a_graph_follows_its_inputs():
     rng = np.random.default_rng(17)
     pages, table, keys, values, n_pages = _cache(rng, [500, 300], 2, 128, 64)
