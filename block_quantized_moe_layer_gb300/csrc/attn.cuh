@@ -71,14 +71,19 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   return s;
 }
 
-// The page of the tokens [i P, (i + 1) P) of sequence b, or -1 for an entry outside the pool.
+// The page of the tokens [i P, (i + 1) P) of sequence b, or -1 for an entry
+// outside the pool; in two steps where the load is to be on its way meanwhile
+// (kNoPage: nothing to look at).
+constexpr int kNoPage = -0x7fffffff;
+__device__ __forceinline__ int page_entry(const AttnParams& p, int b, int i) { return p.table[(int64_t)b * p.table_stride + i]; }
+__device__ __forceinline__ int checked_page(const AttnParams& p, int pg) {
+  if (pg >= 0 && pg < p.n_pages) return pg;
+  if (pg != kNoPage) atomicOr(p.status, kBadPage);
+  return -1;
+}
 __device__ __forceinline__ int load_page(const AttnParams& p, int b, int i) {
-  const int pg = p.table[(int64_t)b * p.table_stride + i];
-  if (pg < 0 || pg >= p.n_pages) {
-    atomicOr(p.status, kBadPage);
-    return -1;
-  }
-  return pg;
+  const int pg = page_entry(p, b, i);
+  return checked_page(p, pg == kNoPage ? -1 : pg);
 }
 
 // Keys visible to a query at position pos: [key_lo(pos), pos].

@@ -15,8 +15,9 @@
 //   P_j = 2^(scale S_j - m), rounded to fp16 into the columns of S_j
 //   O  += P_j V_j   (fp16, P from tensor memory, N = D)
 // One thread issues all MMAs; S is double-buffered, so S_{j+1} runs while the
-// softmax of S_j does.  Eight softmax warps: thread (half, row) takes 64 of a
-// row's 128 scores; the halves exchange their maxima through shared memory.
+// softmax of S_j does.  Sixteen softmax warps: thread (quarter, row) takes 32 of
+// a row's 128 scores (with eight warps and 64 scores a thread the softmax's
+// latency, 2500 cycles a tile, was the bound).
 // The reference m moves only when the maximum passes it by more than 8 (a
 // weight of 2^8 is harmless in fp16 and fp32), which keeps the rescaling of
 // the output in tensor memory rare; l and O stay consistent with m either way.
@@ -36,7 +37,7 @@ cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaSt
 namespace {
 
 constexpr int kRowsP = 128;
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 16, kCopyWarp = 16, kMmaWarp = 17;
 constexpr int kPromptThreads = (kSoftWarps + 2) * 32;
 constexpr int kMaxRing = 8;
 
@@ -46,9 +47,9 @@ struct PromptPlan {
   static constexpr int kRing = D == 64 ? 8 : (D == 128 ? 5 : (D == 192 ? 3 : 2));
   static constexpr int kQ = 0;
   static constexpr int kStages = kImage;  // (a query image has the same size)
-  static constexpr int kMax = kStages + kRing * kImage;              // float [2 buffers][2 halves][128]
-  static constexpr int kBars = kMax + 2 * 2 * kRowsP * 4;
-  static constexpr int kNumBars = 2 * kMaxRing + 2 + 2 + 1 + 2 + 1;
+  static constexpr int kMax = kStages + kRing * kImage;              // float [2][4 quarters][128]
+  static constexpr int kBars = kMax + 2 * 4 * kRowsP * 4;
+  static constexpr int kNumBars = 2 * kMaxRing + 6 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16 + 128;
   static_assert(kTotal <= 232448, "shared memory plan");
@@ -153,9 +154,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* empty = full + kMaxRing;                             // ring: MMAs that read it done
   uint64_t* sfull = empty + kMaxRing;                            // [2] scores ready
   uint64_t* pfull = sfull + 2;                                   // [2] weights stored (the softmax may be a tile ahead)
-  uint64_t* odone = pfull + 2;                                   // output product done
-  uint64_t* xbar = odone + 1;                                    // [2] maxima exchanged
-  uint64_t* fin = xbar + 2;
+  uint64_t* odone = pfull + 2;                                   // [2] output product done
+  uint64_t* fin = odone + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   volatile int never = 0;
@@ -169,9 +169,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], kSoftWarps);
-      mbar_init(&xbar[i], kSoftWarps);
+      mbar_init(&odone[i], 1);
     }
-    mbar_init(odone, 1);
     mbar_init(fin, 1);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -194,9 +193,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint8_t* images = im.base + (((int64_t)b * p.hk + kvh) * im.tiles + (tile_a - seq_first)) * 2 * (int64_t)L::kImage;
   const uint4* valid = im.valid + (int64_t)b * im.tiles + (tile_a - seq_first);
 
-  if (warp == kSoftWarps + 1) tc::alloc_512(tslot);
-  // queries: thread (half, row) lays half of its row's channels into the image
-  const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // of the softmax threads
+  if (warp == kMmaWarp) tc::alloc_512(tslot);
+  // queries: thread (quarter, row) lays a quarter of its row's channels into the image
+  const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;  // of the softmax threads
   int tq = 0, hq = 0, hi_r = 0, lo_r = 0;
   const bool has_row = warp < kSoftWarps && row < n_rows;
   if (has_row) {
@@ -207,8 +206,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   if (warp < kSoftWarps && n_tiles > 0) {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
-#pragma unroll 4
-    for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+#pragma unroll
+    for (int c = quarter * (D / 32); c < (quarter + 1) * (D / 32); ++c) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
       *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsP + row) * 16) = v;
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tbase = *tslot;
 
   float m = -INFINITY, l = 0.f;
-  if (warp == kSoftWarps) {
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------ copies: K0, then K(j+1), V(j)
     if (lane == 0) {
       const int n = 2 * n_tiles;
@@ -241,7 +240,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int k = max(0, i - L::kRing); k < i; ++k)
         wait_bar(&full[k % L::kRing], (uint32_t)((k / L::kRing) & 1), &never, p.status, p.timeout_ns, 12);
     }
-  } else if (warp == kSoftWarps + 1) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     if (lane == 0 && n_tiles > 0) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, kTileTokens) | (1u << 7) | (1u << 10);  // bf16 operands
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int k = 0; k < kTileTokens / 16; ++k)
           tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * D * 16 / 16), kIdescO, j > 0 || k > 0);
         tc::commit(&empty[st]);
-        tc::commit(odone);
+        tc::commit(&odone[j & 1]);
         ++i;
       }
       // all MMAs issued are complete before the block frees anything
@@ -289,106 +288,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (n_tiles > 0) {
     // ------------------------------------------------------------ softmax
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    bool ok = true;
-    for (int j = 0; j < n_tiles; ++j) {
-      ok = wait_bar(&sfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 16);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc::fence_after();
-      uint32_t sv[4][16];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc::ld_32x32b_x16(tl + 128 * (j & 1) + 64 * half + 16 * c, sv[c]);
-      tc::wait_ld();
-      float x[64];
-#pragma unroll
-      for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
+    softmax_tiles<D, 32>(p, n_tiles, tl, quarter, row, kRowsP, smax, sfull, pfull, odone, abort, m, l, [&](int j, uint32_t& bits) {
       const int c0 = (tile_a + j) * kTileTokens;
-      uint2 vm = make_uint2(0xffffffffu, 0xffffffffu);
-      {
-        const uint4 v4 = __ldcg(valid + j);
-        vm = half ? make_uint2(v4.z, v4.w) : make_uint2(v4.x, v4.y);
-      }
-      if (c0 + kTileTokens > pos_min + 1 || c0 < lo_max || (vm.x & vm.y) != 0xffffffffu) {
-        // bit c: key c0 + 64 half + c is visible to this row
-        uint64_t vis = ((uint64_t)vm.y << 32) | vm.x;
-        const int a = lo_r - (c0 + 64 * half), e = hi_r - (c0 + 64 * half);
-        vis &= e >= 64 ? ~0ull : (e <= 0 ? 0ull : (1ull << e) - 1);
-        vis &= a <= 0 ? ~0ull : (a >= 64 ? 0ull : ~((1ull << a) - 1));
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (!((vis >> c) & 1)) x[c] = -INFINITY;
-      }
-      float mx = x[0];
-#pragma unroll
-      for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
-      // the row's other half
-      float* ex = smax + (j & 1) * 2 * kRowsP;
-      ex[half * kRowsP + row] = mx;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&xbar[j & 1]);
-      ok = wait_bar(&xbar[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 17);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      mx = fmaxf(mx, ex[(half ^ 1) * kRowsP + row]) * p.scale_log2;
-      const bool move = mx > m + kLazy;  // (also the first visible keys: m = -inf)
-      if (__any_sync(0xffffffffu, move)) {
-        const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - mx)) : 1.f;
-        if (move) m = mx;
-        l *= f;
-        if (j > 0) {
-          ok = wait_bar(odone, (uint32_t)((j - 1) & 1), abort, p.status, p.timeout_ns, 18);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll 1
-          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-            uint32_t o[16];
-            tc::ld_32x32b_x16(tl + 256 + c, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tc::st_32x32b_x16(tl + 256 + c, o);
-          }
-        }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      uint32_t pk[2][16];
-      float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float u = exp2_approx(fmaf(x[2 * c], p.scale_log2, -ref));
-        const float v = exp2_approx(fmaf(x[2 * c + 1], p.scale_log2, -ref));
-        l0 += u;
-        l1 += v;
-        pk[c >> 4][c & 15] = pack_h2(u, v);
-      }
-      l += l0 + l1;
-      tc::st_32x32b_x16(tl + 128 * (j & 1) + 32 * half, pk[0]);
-      tc::st_32x32b_x16(tl + 128 * (j & 1) + 32 * half + 16, pk[1]);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[j & 1]);
-    }
-    if (ok) {
-      ok = wait_bar(odone, (uint32_t)((n_tiles - 1) & 1), abort, p.status, p.timeout_ns, 19);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after();
-    }
+      const uint32_t exist = __ldcg(reinterpret_cast<const uint32_t*>(valid + j) + quarter);
+      if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && exist == 0xffffffffu) return false;
+      bits = key_bits<32>(c0 + 32 * quarter, lo_r, hi_r) & exist;
+      return true;
+    });
   }
-  // the halves' sums (the maxima's last readers are past their barrier: every
-  // softmax warp has waited for the last output product, and for all of them)
+  // the quarters' sums
   __syncthreads();
-  if (warp < kSoftWarps) smax[half * kRowsP + row] = l;
+  if (warp < kSoftWarps) smax[quarter * kRowsP + row] = l;
   __syncthreads();
   if (warp < kSoftWarps) {
-    l += smax[(half ^ 1) * kRowsP + row];
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l += smax[i * kRowsP + row];
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
     const int64_t orow = (int64_t)(s.start + tq) * p.hq + hq;
     const int64_t part = ((int64_t)((b * p.hk + kvh) * n_rt + rt) * p.n_split + split) * kRowsP + row;
     const float inv = p.n_split > 1 ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
 #pragma unroll 1
-    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+    for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
       uint32_t o[16];
       __syncwarp();
       if (n_tiles > 0) {
@@ -397,7 +318,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       store_out16(p, o, l, inv, has_row, part, orow, c, D);
     }
-    if (has_row && half == 0) {
+    if (has_row && quarter == 0) {
       if (p.n_split > 1) p.part_ml[part] = make_float2(m, l);
       else if (p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
@@ -405,7 +326,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   __syncthreads();
   tc::fence_after();
-  if (warp == kSoftWarps + 1) tc::dealloc_512(tbase);
+  if (warp == kMmaWarp) tc::dealloc_512(tbase);
 }
 
 template <int D>

@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   // Warp 0 issues the copies too (a fifth warp would cost the compute warps a
   // third of their registers): lane i takes page i of a tile.
   const uint64_t pol = l2_evict_first_policy();
-  auto page_of = [&](int i) {  // -1 where nothing of the page is seen
+  auto page_of = [&](int i) {  // kNoPage where nothing of the page is seen
     const int pi = (tile_a + i) * ppt + lane, j0 = pi << p.pshift;
-    return lane < ppt && i < n_tiles && j0 < hi && j0 + p.P > lo ? load_page(p, b, pi) : -1;
+    return lane < ppt && i < n_tiles && j0 < hi && j0 + p.P > lo ? page_entry(p, b, pi) : kNoPage;
   };
-  auto issue = [&](int i, int pg) {
-    const int st = i % L::kStages;
+  auto issue = [&](int i, int entry) {
+    const int st = i % L::kStages, pg = checked_page(p, entry);
     const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0);
     if (lane == 0) {
       pmask[st] = mask;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       bulk_g2s_hint(smem + st * L::kStage + lane * head_bytes, p.pages + pg * p.page_bytes + (int64_t)kvh * head_bytes,
                     (uint32_t)head_bytes, &full[st], pol);
   };
-  int issued = 0, next_pg = -1;
+  int issued = 0, next_pg = kNoPage;
   if (warp == 0) {
     int pg[L::kStages - 1];
 #pragma unroll

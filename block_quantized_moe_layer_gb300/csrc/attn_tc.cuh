@@ -33,6 +33,112 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[N]) 
   }
 }
 
+// The softmax of a block's tiles: thread (quarter, row) takes QC keys of each
+// tile's 4 QC, reads its scores from tensor memory (columns 0 or 128 on, by
+// the tile's parity), and stores the weights as fp16 over them.  m is the
+// row's reference (log2 units), the same in its four threads, l this thread's
+// share of the row's sum.  vis(j, bits): bit c of `bits` tells whether key c of
+// the thread's is seen; false where all are.
+//   The four threads of a row exchange their maxima through shared memory,
+// behind a barrier of the row group's 4 warps; a warp whose wait gave up keeps
+// coming to that barrier, so that the others never wait for it in vain.
+template <int D, int QC, class Vis>
+__device__ __forceinline__ bool softmax_tiles(const AttnParams& p, int n_tiles, uint32_t tl, int quarter, int row, int rows, float* ex,
+                                              uint64_t* sfull, uint64_t* pfull, uint64_t* odone, volatile int* abort, float& m,
+                                              float& l, Vis vis) {
+  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) & 3;
+  bool ok = true;
+  for (int j = 0; j < n_tiles; ++j) {
+    const uint32_t tile = tl + 128 * (j & 1);
+    float x[QC];
+    if (ok) {
+      ok = wait_bar(&sfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 30);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (ok) {
+      tc::fence_after();
+      uint32_t sv[QC / 16][16];
+#pragma unroll
+      for (int c = 0; c < QC / 16; ++c) tc::ld_32x32b_x16(tile + QC * quarter + 16 * c, sv[c]);
+      tc::wait_ld();
+#pragma unroll
+      for (int c = 0; c < QC; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
+      uint32_t bits;
+      if (vis(j, bits)) {
+#pragma unroll
+        for (int c = 0; c < QC; ++c)
+          if (!((bits >> c) & 1)) x[c] = -INFINITY;
+      }
+      float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+#pragma unroll
+      for (int c = 4; c < QC; c += 4) {
+        a = fmaxf(a, fmaxf(x[c], x[c + 1]));
+        b = fmaxf(b, fmaxf(x[c + 2], x[c + 3]));
+      }
+      ex[((j & 1) * 4 + quarter) * rows + row] = fmaxf(a, b);
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+    if (!ok) continue;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, ex[((j & 1) * 4 + i) * rows + row]);
+    mx *= p.scale_log2;
+    const bool move = mx > m + kLazy;  // (also the first visible keys: m = -inf)
+    if (__any_sync(0xffffffffu, move)) {
+      const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - mx)) : 1.f;
+      if (move) m = mx;
+      l *= f;
+      if (j > 0) {
+        ok = wait_bar(&odone[(j - 1) & 1], (uint32_t)(((j - 1) >> 1) & 1), abort, p.status, p.timeout_ns, 32);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        tc::fence_after();
+#pragma unroll 1
+        for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+          uint32_t o[16];
+          tc::ld_32x32b_x16(tl + 256 + c, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tc::st_32x32b_x16(tl + 256 + c, o);
+        }
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    uint32_t pk[QC / 2];
+    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < QC / 2; ++c) {
+      const float u = exp2_approx(fmaf(x[2 * c], p.scale_log2, -ref));
+      const float v = exp2_approx(fmaf(x[2 * c + 1], p.scale_log2, -ref));
+      l0 += u;
+      l1 += v;
+      pk[c] = pack_h2(u, v);
+    }
+    l += l0 + l1;
+    st_cols<QC / 2>(tile + QC / 2 * quarter, pk);
+    tc::wait_st();
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&pfull[j & 1]);
+  }
+  if (ok) {
+    ok = wait_bar(&odone[(n_tiles - 1) & 1], (uint32_t)(((n_tiles - 1) >> 1) & 1), abort, p.status, p.timeout_ns, 33);
+    ok = __all_sync(0xffffffffu, ok);
+    tc::fence_after();
+  }
+  return ok;
+}
+
+// The bits of QC keys from k0 on that lie in [lo, hi).
+template <int QC>
+__device__ __forceinline__ uint32_t key_bits(int k0, int lo, int hi) {
+  const int a = lo - k0, e = hi - k0;
+  uint32_t v = e >= 32 ? ~0u : (e <= 0 ? 0u : (1u << e) - 1);
+  v &= a <= 0 ? ~0u : (a >= 32 ? 0u : ~((1u << a) - 1));
+  return v;
+}
+
 // 16 columns of a row's accumulator, to the output or to a part.
 __device__ __forceinline__ void store_out16(const AttnParams& p, const uint32_t (&o)[16], float l, float inv, bool has_row,
                                             int64_t part, int64_t orow, int c, int D) {

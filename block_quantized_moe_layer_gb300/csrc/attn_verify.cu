@@ -52,7 +52,7 @@ struct VerifyPlan {
   // [8 tiles][16]: a byte for each 8 keys that exist (written up to 4 tiles before the softmax reads it)
   static constexpr int kHere = kMax + 2 * 4 * kRowsV * 4;
   static constexpr int kBars = kHere + 8 * 16;
-  static constexpr int kNumBars = 8 + 2 + 2 + 2 + 2;
+  static constexpr int kNumBars = 8 + 2;
   static constexpr int kMisc = kBars + kNumBars * 8;           // tensor memory slot, abort
   static constexpr int kTotal = kMisc + 16 + 128;
   static_assert(kTotal <= 232448, "shared memory plan");
@@ -69,13 +69,10 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   float* smax = reinterpret_cast<float*>(sm + L::kMax);
   uint8_t* here = sm + L::kHere;
   uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + L::kBars);  // [2] key image written
-  uint64_t* kfree = kfull + 2;                                    // [2] scores' products from it done
-  uint64_t* vfull = kfree + 2;                                    // [2] value image written
-  uint64_t* vfree = vfull + 2;                                    // [2] output products from it done
-  uint64_t* sfull = vfree + 2;                                    // [2] scores ready
-  uint64_t* pfull = sfull + 2;                                    // [2] weights stored (the softmax may be a tile ahead)
-  uint64_t* xbar = pfull + 2;                                     // [2] maxima exchanged
-  uint64_t* qfull = xbar + 2;                                     // queries written
+  uint64_t* sfull = kfull + 2;                                    // [2] scores ready (key image free)
+  uint64_t* pvfull = sfull + 2;                                   // [2] value image and weights written
+  uint64_t* odone = pvfull + 2;                                   // [2] output product done (value image free)
+  uint64_t* qfull = odone + 2;                                    // queries written
   uint64_t* fin = qfull + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
@@ -85,12 +82,9 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 8);
-      mbar_init(&kfree[i], 1);
-      mbar_init(&vfull[i], 8);
-      mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 8);
-      mbar_init(&xbar[i], 8);
+      mbar_init(&pvfull[i], 16);
+      mbar_init(&odone[i], 1);
     }
     mbar_init(qfull, 8);
     mbar_init(fin, 1);
@@ -145,7 +139,6 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
         for (int k = 0; k < D / 16; ++k)
           mma_ss(tbase + 128 * i, qd + k * (2 * kRowsV * 16 / 16), kd + i * (L::kImage / 16) + k * (2 * KT * 16 / 16), kIdescS,
                  k > 0);
-        tc::commit(&kfree[i]);
         tc::commit(&sfull[i]);
       };
       ok = wait_bar<64>(qfull, 0, abort, p.status, p.timeout_ns, 34);
@@ -153,14 +146,13 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       for (int j = 0; j < n_tiles && ok; ++j) {
         const int i = j & 1;
         if (j + 1 < n_tiles) scores(j + 1);
-        ok = ok && wait_bar<64>(&vfull[i], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 24);
-        ok = ok && wait_bar<64>(&pfull[i], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 25);
+        ok = ok && wait_bar<64>(&pvfull[i], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 24);
         if (!ok) break;
         tc::fence_after();
 #pragma unroll
         for (int k = 0; k < KT / 16; ++k)
           tc::mma_ts(tbase + 256, tbase + 128 * i + 8 * k, vd + i * (L::kImage / 16) + k * (2 * 128 / 16), kIdescO, j > 0 || k > 0);
-        tc::commit(&vfree[i]);
+        tc::commit(&odone[i]);
       }
       // all MMAs issued are complete before the block frees anything
       tc::commit(fin);
@@ -171,68 +163,77 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     const bool values = warp >= 16;
     const int dw = values ? warp - 16 : (warp >> 2) * 2 + (warp & 1);  // 0..7
     const int codes = p.P * (D / 2);
-    uint64_t* image_full = values ? vfull : kfull;
-    uint64_t* image_free = values ? vfree : kfree;
+    uint64_t* image_full = values ? pvfull : kfull;
+    uint64_t* image_free = values ? odone : sfull;
     uint8_t* image = sm + (values ? L::kV : L::kK);
-    // a warp takes the key groups dw, dw + 8 (of 8 keys), of 64 channels at a
-    // time: each 8 lanes 8 keys, so that their stores meet all banks
-    const int k8 = lane & 7, c4 = lane >> 3;
-    constexpr int kGroups = KT / 64, kUnits = kGroups * (D / 64);
-    uint2 code[kUnits];
+    // a warp takes KT/8 neighbouring keys, which lie in one page; a lane a key
+    // and every (32 / keys)-th piece of 32 channels (one 16-byte load; 8-byte
+    // loads held the load units up for a third of a tile).  Each 8 lanes store
+    // 8 keys, so they meet all banks.
+    constexpr int kKeys = KT / 8, kStep = 32 / kKeys, kUnits = D / 32 / kStep;
+    const int kk = lane % kKeys, piece = lane / kKeys;
+    // the next tile's codes and scales are asked for once a tile is written,
+    // their page number a tile before that (a second set of registers, to ask
+    // a whole tile ahead, was slower: 24.6 against 23 us at 32765 keys)
+    uint4 code[kUnits];
     uint32_t scale[kUnits];
-    auto fetch = [&](int j) {  // this lane's codes and scales of tile j: 0 for a key past the end or on an absent page
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const int g8 = dw + 8 * g, key = (tile_a + j) * KT + 8 * g8;
-        // (a page that no row here sees is not looked at: it may have been given back)
-        const int pg = j < n_tiles && key < hi && (key | (p.P - 1)) >= lo ? load_page(p, b, key >> p.pshift) : -1;
-        const int at = (key & (p.P - 1)) + k8;
-        const uint8_t* src = p.pages + pg * p.page_bytes + (int64_t)kvh * p.head_bytes + (values ? p.head_bytes / 2 : 0);
-        const bool has = pg >= 0 && key + k8 < s.len;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          code[g * (D / 64) + c] = make_uint2(0, 0);
-          scale[g * (D / 64) + c] = 0;
-          if (has) {
-            code[g * (D / 64) + c] = __ldcg(reinterpret_cast<const uint2*>(src + at * (D / 2) + 32 * c + 8 * c4));
-            scale[g * (D / 64) + c] = __ldcg(src + codes + at * (D / 16) + 4 * c + c4);
-          }
-        }
-        if (!values && lane == 0) here[(j & 7) * 16 + g8] = pg >= 0;
-      }
+    int page = kNoPage;
+    auto look_up = [&](int j) {  // (a page that no row here sees is not looked at: it may have been given back)
+      const int key = (tile_a + j) * KT + kKeys * dw;
+      page = j < n_tiles && key < hi && (key | (p.P - 1)) >= lo ? page_entry(p, b, key >> p.pshift) : kNoPage;
     };
+    auto fetch = [&](int j) {  // this lane's codes and scales of tile j: 0 for a key past the end or on an absent page
+      const int key = (tile_a + j) * KT + kKeys * dw, at = (key & (p.P - 1)) + kk, pg = checked_page(p, page);
+      const uint8_t* src = p.pages + pg * p.page_bytes + (int64_t)kvh * p.head_bytes + (values ? p.head_bytes / 2 : 0);
+      const bool has = pg >= 0 && key + kk < s.len;
+      const uint8_t* sc = src + at * (D / 2) + 16 * piece;
+      const uint8_t* ss = src + codes + at * (D / 16) + 2 * piece;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        code[u] = make_uint4(0, 0, 0, 0);
+        scale[u] = 0;
+        if (has) {
+          code[u] = __ldcg(reinterpret_cast<const uint4*>(sc + 16 * kStep * u));
+          scale[u] = __ldcg(reinterpret_cast<const uint16_t*>(ss + 2 * kStep * u));
+        }
+      }
+      if (!values && lane < kKeys / 8 && j < n_tiles) here[(j & 7) * 16 + kKeys / 8 * dw + lane] = pg >= 0;
+    };
+    look_up(0);
     fetch(0);
+    look_up(1);
     for (int j = 0; j < n_tiles; ++j) {
       const int i = j & 1;
       bool ok = true;
       if (j > 1) ok = wait_bar(&image_free[i], (uint32_t)((j >> 1) - 1) & 1, abort, p.status, p.timeout_ns, 28);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      uint4* o = reinterpret_cast<uint4*>(image + i * L::kImage);
+      uint4* o = reinterpret_cast<uint4*>(image + i * L::kImage) + 4 * piece * KT + kKeys * dw + kk;
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
+      for (int u = 0; u < kUnits; ++u) {
+        const uint32_t w[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint2 w = code[g * (D / 64) + c];
-          const uint32_t sb = scale[g * (D / 64) + c] * 0x00010001u;
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t sb = __byte_perm(scale[u], 0, h ? 0x4141 : 0x4040);
           uint32_t x[8];
           if (values) {
             const ValueScale d = value_scale(sb);
-            value_quads(w.x, d, x[0], x[1], x[2], x[3]);
-            value_quads(w.y, d, x[4], x[5], x[6], x[7]);
+            value_quads(w[2 * h], d, x[0], x[1], x[2], x[3]);
+            value_quads(w[2 * h + 1], d, x[4], x[5], x[6], x[7]);
           } else {
             const KeyScale d = key_scale(sb);
-            key_pairs(w.x, d, x);
-            key_pairs(w.y, d, x + 4);
+            key_pairs(w[2 * h], d, x);
+            key_pairs(w[2 * h + 1], d, x + 4);
           }
-          uint4* r = o + (8 * c + 2 * c4) * KT + 8 * (dw + 8 * g) + k8;
-          r[0] = make_uint4(x[0], x[1], x[2], x[3]);
-          r[KT] = make_uint4(x[4], x[5], x[6], x[7]);
+          o[(4 * kStep * u + 2 * h) * KT] = make_uint4(x[0], x[1], x[2], x[3]);
+          o[(4 * kStep * u + 2 * h + 1) * KT] = make_uint4(x[4], x[5], x[6], x[7]);
         }
+      }
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&image_full[i]);
-      if (j + 1 < n_tiles) fetch(j + 1);
+      fetch(j + 1);
+      look_up(j + 2);
     }
   } else if (soft && n_tiles > 0) {
     // ------------------------------------------------------------ softmax
@@ -249,95 +250,16 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     __syncwarp();
     if (lane == 0) mbar_arrive(qfull);
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    bool ok = true;
-    for (int j = 0; j < n_tiles; ++j) {
-      ok = wait_bar(&sfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 30);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc::fence_after();
-      uint32_t sv[QC / 16][16];
-#pragma unroll
-      for (int c = 0; c < QC / 16; ++c) tc::ld_32x32b_x16(tl + 128 * (j & 1) + QC * quarter + 16 * c, sv[c]);
-      tc::wait_ld();
-      float x[QC];
-#pragma unroll
-      for (int c = 0; c < QC; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
+    softmax_tiles<D, QC>(p, n_tiles, tl, quarter, row, kRowsV, smax, sfull, pvfull, odone, abort, m, l, [&](int j, uint32_t& bits) {
       const int c0 = (tile_a + j) * KT;
       // the existing 8-key groups of this quarter, a byte each
       uint32_t mask;
       if constexpr (QC == 32) mask = *reinterpret_cast<const volatile uint32_t*>(here + (j & 7) * 16 + 4 * quarter);
       else mask = *reinterpret_cast<const volatile uint16_t*>(here + (j & 7) * 16 + 2 * quarter);
-      if (c0 + KT > pos_min + 1 || c0 < lo_max || mask != (0x01010101u >> (32 - QC))) {
-        // bit c: key c0 + QC quarter + c is visible to this row
-        const int k0 = c0 + QC * quarter;
-        uint32_t vis = 0xffffffffu;
-        const int a = lo_r - k0, e = hi_r - k0;
-        vis &= e >= 32 ? ~0u : (e <= 0 ? 0u : (1u << e) - 1);
-        vis &= a <= 0 ? ~0u : (a >= 32 ? 0u : ~((1u << a) - 1));
-#pragma unroll
-        for (int c = 0; c < QC; ++c) {
-          const bool page = (mask >> (c & ~7)) & 1;
-          if (!((vis >> c) & 1) || !page) x[c] = -INFINITY;
-        }
-      }
-      float mx = x[0];
-#pragma unroll
-      for (int c = 1; c < QC; ++c) mx = fmaxf(mx, x[c]);
-      // the row's other quarters
-      float* ex = smax + (j & 1) * 4 * kRowsV;
-      ex[quarter * kRowsV + row] = mx;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&xbar[j & 1]);
-      ok = wait_bar(&xbar[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 31);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, ex[i * kRowsV + row]);
-      mx *= p.scale_log2;
-      const bool move = mx > m + kLazy;  // (also the first visible keys: m = -inf)
-      if (__any_sync(0xffffffffu, move)) {
-        const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - mx)) : 1.f;
-        if (move) m = mx;
-        l *= f;
-        if (j > 0) {
-          ok = wait_bar(&vfree[(j - 1) & 1], (uint32_t)(((j - 1) >> 1) & 1), abort, p.status, p.timeout_ns, 32);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll 1
-          for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
-            uint32_t o[16];
-            tc::ld_32x32b_x16(tl + 256 + c, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tc::st_32x32b_x16(tl + 256 + c, o);
-          }
-        }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      uint32_t pk[QC / 2];
-      float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-      for (int c = 0; c < QC / 2; ++c) {
-        const float u = exp2_approx(fmaf(x[2 * c], p.scale_log2, -ref));
-        const float v = exp2_approx(fmaf(x[2 * c + 1], p.scale_log2, -ref));
-        l0 += u;
-        l1 += v;
-        pk[c] = pack_h2(u, v);
-      }
-      l += l0 + l1;
-      st_cols<QC / 2>(tl + 128 * (j & 1) + QC / 2 * quarter, pk);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[j & 1]);
-    }
-    if (ok) {
-      ok = wait_bar(&vfree[(n_tiles - 1) & 1], (uint32_t)(((n_tiles - 1) >> 1) & 1), abort, p.status, p.timeout_ns, 33);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after();
-    }
+      if (c0 + KT <= pos_min + 1 && c0 >= lo_max && mask == (0x01010101u >> (32 - QC))) return false;
+      bits = key_bits<QC>(c0 + QC * quarter, lo_r, hi_r) & (mask * 0xFFu);  // (bytes of 1 to bytes of 0xFF)
+      return true;
+    });
   }
   // the quarters' sums; the outputs go through shared memory (the images'
   // room), since a thread's row is D apart from its neighbour's: stored from
