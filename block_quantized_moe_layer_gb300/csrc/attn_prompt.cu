@@ -15,9 +15,9 @@
 //   P_j = 2^(scale S_j - m), rounded to fp16 into the columns of S_j
 //   O  += P_j V_j   (fp16, P from tensor memory, N = D)
 // One thread issues all MMAs; S is double-buffered, so S_{j+1} runs while the
-// softmax of S_j does.  Sixteen softmax warps: thread (quarter, row) takes 32 of
-// a row's 128 scores (with eight warps and 64 scores a thread the softmax's
-// latency, 2500 cycles a tile, was the bound).
+// softmax of S_j does.  Eight softmax warps: thread (half, row) takes 64 of a
+// row's 128 scores (sixteen warps with 32 each finish a tile's softmax sooner,
+// but take issue slots from the MMA thread: 351 against 328 us).
 // The reference m moves only when the maximum passes it by more than 8 (a
 // weight of 2^8 is harmless in fp16 and fp32), which keeps the rescaling of
 // the output in tensor memory rare; l and O stay consistent with m either way.
@@ -32,12 +32,14 @@ namespace moe {
 namespace attn {
 
 // Joins the parts of split rows (attn_small.cu).
-cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st);
+cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, int whole, cudaStream_t st);
 
 namespace {
 
 constexpr int kRowsP = 128;
-constexpr int kSoftWarps = 16, kCopyWarp = 16, kMmaWarp = 17;
+constexpr int kShares = 2;  // threads of a row
+constexpr int kShareKeys = kTileTokens / kShares;
+constexpr int kSoftWarps = 4 * kShares, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kPromptThreads = (kSoftWarps + 2) * 32;
 constexpr int kMaxRing = 8;
 
@@ -47,8 +49,8 @@ struct PromptPlan {
   static constexpr int kRing = D == 64 ? 8 : (D == 128 ? 5 : (D == 192 ? 3 : 2));
   static constexpr int kQ = 0;
   static constexpr int kStages = kImage;  // (a query image has the same size)
-  static constexpr int kMax = kStages + kRing * kImage;              // float [2][4 quarters][128]
-  static constexpr int kBars = kMax + 2 * 4 * kRowsP * 4;
+  static constexpr int kMax = kStages + kRing * kImage;              // float [2][shares][128]
+  static constexpr int kBars = kMax + 2 * kShares * kRowsP * 4;
   static constexpr int kNumBars = 2 * kMaxRing + 6 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16 + 128;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
 
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    prompt_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Images im, int n_rt, int chunk) {
+    prompt_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Images im, int n_rt, int whole, int chunk) {
   using L = PromptPlan<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -177,9 +179,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   griddep_wait();
 
-  const int b = blockIdx.z, split = blockIdx.x % p.n_split;
-  // rows with the longest key ranges first
-  const int kvh = blockIdx.y, rt = n_rt - 1 - blockIdx.x / p.n_split;
+  // the first `whole` blocks take a row tile each, those with the longest key
+  // ranges first; the others p.n_split parts of one
+  const bool split_tile = (int)blockIdx.x >= whole;
+  const int tile_i = split_tile ? whole + ((int)blockIdx.x - whole) / p.n_split : (int)blockIdx.x;
+  const int split = split_tile ? ((int)blockIdx.x - whole) % p.n_split : 0;
+  const int rt = n_rt - 1 - tile_i / (p.hk * p.n_seqs), b = tile_i % (p.hk * p.n_seqs) / p.hk, kvh = tile_i % p.hk;
+  const bool parts = split_tile && p.n_split > 1;
   const Seq s = load_seq(p, b);
   const int row0 = rt * kRowsP, n_rows = min(kRowsP, s.nq * p.g - row0);
   if (n_rows <= 0) return;
@@ -189,13 +195,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   int seq_first, seq_last;
   seq_tiles(p, s, seq_first, seq_last);
   const int tile_a = lo / kTileTokens + split * chunk;
-  const int n_tiles = hi > lo ? max(0, min(tile_a + chunk, (hi + kTileTokens - 1) / kTileTokens) - tile_a) : 0;
+  const int n_tiles = hi > lo ? max(0, min(split_tile ? tile_a + chunk : 0x7fffffff, (hi + kTileTokens - 1) / kTileTokens) - tile_a) : 0;
   const uint8_t* images = im.base + (((int64_t)b * p.hk + kvh) * im.tiles + (tile_a - seq_first)) * 2 * (int64_t)L::kImage;
   const uint4* valid = im.valid + (int64_t)b * im.tiles + (tile_a - seq_first);
 
   if (warp == kMmaWarp) tc::alloc_512(tslot);
-  // queries: thread (quarter, row) lays a quarter of its row's channels into the image
-  const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;  // of the softmax threads
+  // queries: thread (share, row) lays its share of the row's channels into the image
+  const int share = warp >> 2, row = (warp & 3) * 32 + lane;  // of the softmax threads
   int tq = 0, hq = 0, hi_r = 0, lo_r = 0;
   const bool has_row = warp < kSoftWarps && row < n_rows;
   if (has_row) {
@@ -206,8 +212,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   if (warp < kSoftWarps && n_tiles > 0) {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
-#pragma unroll
-    for (int c = quarter * (D / 32); c < (quarter + 1) * (D / 32); ++c) {
+#pragma unroll 4
+    for (int c = share * (D / 8 / kShares); c < (share + 1) * (D / 8 / kShares); ++c) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
       *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsP + row) * 16) = v;
@@ -288,38 +294,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (n_tiles > 0) {
     // ------------------------------------------------------------ softmax
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    softmax_tiles<D, 32>(p, n_tiles, tl, quarter, row, kRowsP, smax, sfull, pfull, odone, abort, m, l, [&](int j, uint32_t& bits) {
-      const int c0 = (tile_a + j) * kTileTokens;
-      const uint32_t exist = __ldcg(reinterpret_cast<const uint32_t*>(valid + j) + quarter);
-      if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && exist == 0xffffffffu) return false;
-      bits = key_bits<32>(c0 + 32 * quarter, lo_r, hi_r) & exist;
-      return true;
-    });
+    softmax_tiles<D, kShareKeys, kShares>(
+        p, n_tiles, tl, share, row, kRowsP, smax, sfull, pfull, odone, abort, m, l, [&](int j, KeyBits<kShareKeys>& bits) {
+          const int c0 = (tile_a + j) * kTileTokens;
+          const auto exist = __ldcg(reinterpret_cast<const KeyBits<kShareKeys>*>(valid + j) + share);
+          if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && exist == ~KeyBits<kShareKeys>(0)) return false;
+          bits = key_bits<kShareKeys>(c0 + kShareKeys * share, lo_r, hi_r) & exist;
+          return true;
+        });
   }
-  // the quarters' sums
+  // the shares' sums
   __syncthreads();
-  if (warp < kSoftWarps) smax[quarter * kRowsP + row] = l;
+  if (warp < kSoftWarps) smax[share * kRowsP + row] = l;
   __syncthreads();
   if (warp < kSoftWarps) {
     l = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) l += smax[i * kRowsP + row];
+    for (int i = 0; i < kShares; ++i) l += smax[i * kRowsP + row];
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
     const int64_t orow = (int64_t)(s.start + tq) * p.hq + hq;
-    const int64_t part = ((int64_t)((b * p.hk + kvh) * n_rt + rt) * p.n_split + split) * kRowsP + row;
-    const float inv = p.n_split > 1 ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
+    const int64_t part = ((int64_t)(tile_i - whole) * p.n_split + split) * kRowsP + row;
+    const float inv = parts ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
 #pragma unroll 1
-    for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+    for (int c = share * (D / kShares); c < (share + 1) * (D / kShares); c += 16) {
       uint32_t o[16];
       __syncwarp();
       if (n_tiles > 0) {
         tc::ld_32x32b_x16(tl + 256 + c, o);
         tc::wait_ld();
       }
-      store_out16(p, o, l, inv, has_row, part, orow, c, D);
+      store_out16(p, parts, o, l, inv, has_row, part, orow, c, D);
     }
-    if (has_row && quarter == 0) {
-      if (p.n_split > 1) p.part_ml[part] = make_float2(m, l);
+    if (has_row && share == 0) {
+      if (parts) p.part_ml[part] = make_float2(m, l);
       else if (p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
     tc::fence_before();
@@ -350,17 +357,25 @@ cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t
     g.starts += b0;
     g.lens += b0;
     g.table += (int64_t)b0 * p.table_stride;
-    const int64_t base = (int64_t)p.hk * n_rt * g.n_seqs;
-    // keys are split only where the row tiles leave half of the GPU idle
-    int64_t want = std::max<int64_t>(1, num_sms / base);
-    want = std::min<int64_t>(std::min<int64_t>(want, kMaxSplit), std::max<int64_t>(1, (int64_t)(part_rows / kRowsP) / base));
-    const int chunk = (int)std::max<int64_t>(std::min(rtiles, 2), (rtiles + want - 1) / want);
-    g.n_split = (rtiles + chunk - 1) / chunk;
+    // Row tiles that fill the GPU go whole; the keys of the rest are split, so
+    // that a last wave takes part of one's time: into the number of parts that
+    // ends first, counting a block's start and end as 4 tiles.  (512 row tiles
+    // of 60 key tiles on 152 multiprocessors: 4 waves whole, 3.5 so.)
+    const int64_t total = (int64_t)p.hk * n_rt * g.n_seqs, whole = total / num_sms * num_sms, rest = total - whole;
+    int64_t best = 0;
+    int chunk = rtiles;
+    g.n_split = 1;
+    for (int n = 1; rest > 0 && n <= std::min(kMaxSplit, std::max(1, rtiles / 2)); ++n) {
+      if (n > 1 && rest * n * kRowsP > (int64_t)part_rows) break;
+      const int c = (rtiles + n - 1) / n;
+      const int64_t cost = (rest * n + num_sms - 1) / num_sms * (c + 4) + (n > 1 ? 4 : 0);
+      if (n == 1 || cost < best) best = cost, chunk = c, g.n_split = (rtiles + c - 1) / c;
+    }
     cudaError_t e = launch_pdl(expand_kernel, dim3(im.tiles, p.hk, g.n_seqs), 256, 0, st, g, im);
     if (e == cudaSuccess)
-      e = launch_pdl(prompt_kernel<D>, dim3((unsigned)(n_rt * g.n_split), p.hk, g.n_seqs), kPromptThreads, PromptPlan<D>::kTotal,
-                     st, g, im, n_rt, chunk);
-    if (e == cudaSuccess && g.n_split > 1) e = join_launch(g, kRowsP, n_rt, st);
+      e = launch_pdl(prompt_kernel<D>, dim3((unsigned)(whole + rest * g.n_split)), kPromptThreads, PromptPlan<D>::kTotal, st, g, im,
+                     n_rt, (int)whole, chunk);
+    if (e == cudaSuccess && g.n_split > 1) e = join_launch(g, kRowsP, n_rt, (int)whole, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

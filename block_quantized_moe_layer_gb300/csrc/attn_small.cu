@@ -390,8 +390,17 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
 // Joins up to kJoinFew parts of a row's keys: a thread 4 channels of a row,
 // all its loads at once.
 constexpr int kJoinFew = 8;
+// The tile's place among the split ones (-1: it was not split).  whole < 0: all
+// were, in the order sequence, head, row tile; else the prompt kernel's order,
+// whose first `whole` went whole.
+__device__ __forceinline__ int64_t part_tile(const AttnParams& p, int b, int kvh, int rt, int n_rt, int whole) {
+  if (whole < 0) return (int64_t)(b * p.hk + kvh) * n_rt + rt;
+  const int64_t i = (int64_t)(n_rt - 1 - rt) * p.hk * p.n_seqs + b * p.hk + kvh - whole;
+  return i < 0 ? -1 : i;
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) join_few_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt) {
+__global__ void __launch_bounds__(256) join_few_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt, int whole) {
   griddep_launch_dependents();
   griddep_wait();
   const int b = blockIdx.y;
@@ -400,7 +409,8 @@ __global__ void __launch_bounds__(256) join_few_kernel(const __grid_constant__ A
   const int t = th / p.hq, h = th % p.hq;
   if (t >= s.nq) return;
   const int kvh = h / p.g, row = t * p.g + h % p.g;
-  const int64_t tile = (int64_t)(b * p.hk + kvh) * n_rt + row / rows_per_tile;
+  const int64_t tile = part_tile(p, b, kvh, row / rows_per_tile, n_rt, whole);
+  if (tile < 0) return;
   const int64_t first = tile * p.n_split * rows_per_tile + row % rows_per_tile;
   const float4* po = reinterpret_cast<const float4*>(p.part_o) + first * (D / 4) + c;
   float2 ml[kJoinFew];
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const __grid_constant__ A
 // over all parts took 21 us for 37 of them: a chain of loads each.)
 constexpr int kJoinGroups = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinGroups * D / 4) join_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt) {
+__global__ void __launch_bounds__(kJoinGroups * D / 4) join_kernel(const __grid_constant__ AttnParams p, int rows_per_tile, int n_rt, int whole) {
   __shared__ float wt[1024];                 // a part's weight 2^(m - max)
   __shared__ float4 sum[kJoinGroups][D / 4];
   __shared__ float2 red[32];
@@ -444,7 +454,8 @@ __global__ void __launch_bounds__(kJoinGroups * D / 4) join_kernel(const __grid_
   const Seq s = load_seq(p, b);
   if (t >= s.nq) return;
   const int kvh = h / p.g, row = t * p.g + h % p.g;
-  const int64_t tile = (int64_t)(b * p.hk + kvh) * n_rt + row / rows_per_tile;
+  const int64_t tile = part_tile(p, b, kvh, row / rows_per_tile, n_rt, whole);
+  if (tile < 0) return;
   const int64_t first = tile * p.n_split * rows_per_tile + row % rows_per_tile;
   const float4* po = reinterpret_cast<const float4*>(p.part_o) + first * (D / 4) + c;
   const int64_t step = (int64_t)rows_per_tile * (D / 4);
@@ -516,20 +527,23 @@ __global__ void __launch_bounds__(kJoinGroups * D / 4) join_kernel(const __grid_
 }  // namespace
 
 template <int D>
-static cudaError_t join_launch_d(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st) {
-  const unsigned rows = (unsigned)(p.max_q * p.hq);
+static cudaError_t join_launch_d(const AttnParams& p, int rows_per_tile, int n_rt, int whole, cudaStream_t st) {
+  // query tokens that may lie in a split tile
+  int64_t tokens = p.max_q;
+  if (whole >= 0) tokens = std::min<int64_t>(tokens, ((int64_t)(n_rt - whole / (p.hk * p.n_seqs)) * rows_per_tile + p.g - 1) / p.g);
+  const unsigned rows = (unsigned)(tokens * p.hq);
   if (p.n_split <= kJoinFew)
     return launch_pdl(join_few_kernel<D>, dim3((unsigned)(((int64_t)rows * (D / 4) + 255) / 256), p.n_seqs), 256, 0, st, p,
-                      rows_per_tile, n_rt);
-  return launch_pdl(join_kernel<D>, dim3(rows, p.n_seqs), kJoinGroups * D / 4, 0, st, p, rows_per_tile, n_rt);
+                      rows_per_tile, n_rt, whole);
+  return launch_pdl(join_kernel<D>, dim3(rows, p.n_seqs), kJoinGroups * D / 4, 0, st, p, rows_per_tile, n_rt, whole);
 }
 
-cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st) {
+cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, int whole, cudaStream_t st) {
   switch (p.D) {
-    case 64: return join_launch_d<64>(p, rows_per_tile, n_rt, st);
-    case 128: return join_launch_d<128>(p, rows_per_tile, n_rt, st);
-    case 192: return join_launch_d<192>(p, rows_per_tile, n_rt, st);
-    default: return join_launch_d<256>(p, rows_per_tile, n_rt, st);
+    case 64: return join_launch_d<64>(p, rows_per_tile, n_rt, whole, st);
+    case 128: return join_launch_d<128>(p, rows_per_tile, n_rt, whole, st);
+    case 192: return join_launch_d<192>(p, rows_per_tile, n_rt, whole, st);
+    default: return join_launch_d<256>(p, rows_per_tile, n_rt, whole, st);
   }
 }
 
@@ -554,7 +568,7 @@ cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStre
   cudaError_t e = launch_pdl(small_kernel<D, NT>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads, L::kTotal,
                              st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
-  return join_launch(p, L::kRows, n_rt, st);
+  return join_launch(p, L::kRows, n_rt, -1, st);
 }
 
 template <int D>

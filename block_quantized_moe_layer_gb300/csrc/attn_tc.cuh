@@ -3,6 +3,8 @@
 #include "attn_mma.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace moe {
 namespace attn {
 
@@ -27,22 +29,31 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[N]) 
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-  } else {
-    static_assert(N == 16, "8 or 16 columns");
+  } else if constexpr (N == 16) {
     tc::st_32x32b_x16(taddr, v);
+  } else {
+    static_assert(N == 32, "8, 16 or 32 columns");
+    uint32_t a[16], b[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = v[i], b[i] = v[16 + i];
+    tc::st_32x32b_x16(taddr, a);
+    tc::st_32x32b_x16(taddr + 16, b);
   }
 }
 
-// The softmax of a block's tiles: thread (quarter, row) takes QC keys of each
-// tile's 4 QC, reads its scores from tensor memory (columns 0 or 128 on, by
+// The softmax of a block's tiles: thread (share, row) takes QC keys of each
+// tile's NQ QC, reads its scores from tensor memory (columns 0 or 128 on, by
 // the tile's parity), and stores the weights as fp16 over them.  m is the
-// row's reference (log2 units), the same in its four threads, l this thread's
+// row's reference (log2 units), the same in its NQ threads, l this thread's
 // share of the row's sum.  vis(j, bits): bit c of `bits` tells whether key c of
 // the thread's is seen; false where all are.
-//   The four threads of a row exchange their maxima through shared memory,
-// behind a barrier of the row group's 4 warps; a warp whose wait gave up keeps
+//   The threads of a row exchange their maxima through shared memory,
+// behind a barrier of the row group's NQ warps; a warp whose wait gave up keeps
 // coming to that barrier, so that the others never wait for it in vain.
-template <int D, int QC, class Vis>
+template <int QC>
+using KeyBits = std::conditional_t<QC == 64, uint64_t, uint32_t>;
+
+template <int D, int QC, int NQ, class Vis>
 __device__ __forceinline__ bool softmax_tiles(const AttnParams& p, int n_tiles, uint32_t tl, int quarter, int row, int rows, float* ex,
                                               uint64_t* sfull, uint64_t* pfull, uint64_t* odone, volatile int* abort, float& m,
                                               float& l, Vis vis) {
@@ -63,7 +74,7 @@ __device__ __forceinline__ bool softmax_tiles(const AttnParams& p, int n_tiles, 
       tc::wait_ld();
 #pragma unroll
       for (int c = 0; c < QC; ++c) x[c] = __uint_as_float(sv[c >> 4][c & 15]);
-      uint32_t bits;
+      KeyBits<QC> bits;
       if (vis(j, bits)) {
 #pragma unroll
         for (int c = 0; c < QC; ++c)
@@ -75,13 +86,13 @@ __device__ __forceinline__ bool softmax_tiles(const AttnParams& p, int n_tiles, 
         a = fmaxf(a, fmaxf(x[c], x[c + 1]));
         b = fmaxf(b, fmaxf(x[c + 2], x[c + 3]));
       }
-      ex[((j & 1) * 4 + quarter) * rows + row] = fmaxf(a, b);
+      ex[((j & 1) * NQ + quarter) * rows + row] = fmaxf(a, b);
     }
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NQ * 32) : "memory");
     if (!ok) continue;
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, ex[((j & 1) * 4 + i) * rows + row]);
+    for (int i = 0; i < NQ; ++i) mx = fmaxf(mx, ex[((j & 1) * NQ + i) * rows + row]);
     mx *= p.scale_log2;
     const bool move = mx > m + kLazy;  // (also the first visible keys: m = -inf)
     if (__any_sync(0xffffffffu, move)) {
@@ -94,7 +105,7 @@ __device__ __forceinline__ bool softmax_tiles(const AttnParams& p, int n_tiles, 
         if (!ok) continue;
         tc::fence_after();
 #pragma unroll 1
-        for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+        for (int c = quarter * (D / NQ); c < (quarter + 1) * (D / NQ); c += 16) {
           uint32_t o[16];
           tc::ld_32x32b_x16(tl + 256 + c, o);
           tc::wait_ld();
@@ -132,21 +143,23 @@ __device__ __forceinline__ bool softmax_tiles(const AttnParams& p, int n_tiles, 
 
 // The bits of QC keys from k0 on that lie in [lo, hi).
 template <int QC>
-__device__ __forceinline__ uint32_t key_bits(int k0, int lo, int hi) {
+__device__ __forceinline__ KeyBits<QC> key_bits(int k0, int lo, int hi) {
+  using B = KeyBits<QC>;
+  constexpr int kBits = 8 * sizeof(B);
   const int a = lo - k0, e = hi - k0;
-  uint32_t v = e >= 32 ? ~0u : (e <= 0 ? 0u : (1u << e) - 1);
-  v &= a <= 0 ? ~0u : (a >= 32 ? 0u : ~((1u << a) - 1));
+  B v = e >= kBits ? ~B(0) : (e <= 0 ? B(0) : (B(1) << e) - 1);
+  v &= a <= 0 ? ~B(0) : (a >= kBits ? B(0) : ~((B(1) << a) - 1));
   return v;
 }
 
 // 16 columns of a row's accumulator, to the output or to a part.
-__device__ __forceinline__ void store_out16(const AttnParams& p, const uint32_t (&o)[16], float l, float inv, bool has_row,
+__device__ __forceinline__ void store_out16(const AttnParams& p, bool parts, const uint32_t (&o)[16], float l, float inv, bool has_row,
                                             int64_t part, int64_t orow, int c, int D) {
   float v[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
   if (!has_row) return;
-  if (p.n_split > 1) {
+  if (parts) {
     float4* d = reinterpret_cast<float4*>(p.part_o + part * D + c);
 #pragma unroll
     for (int e = 0; e < 4; ++e) d[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);

@@ -30,7 +30,7 @@
 namespace moe {
 namespace attn {
 
-cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, cudaStream_t st);
+cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, int whole, cudaStream_t st);
 
 namespace {
 
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     __syncwarp();
     if (lane == 0) mbar_arrive(qfull);
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    softmax_tiles<D, QC>(p, n_tiles, tl, quarter, row, kRowsV, smax, sfull, pvfull, odone, abort, m, l, [&](int j, uint32_t& bits) {
+    softmax_tiles<D, QC, 4>(p, n_tiles, tl, quarter, row, kRowsV, smax, sfull, pvfull, odone, abort, m, l, [&](int j, uint32_t& bits) {
       const int c0 = (tile_a + j) * KT;
       // the existing 8-key groups of this quarter, a byte each
       uint32_t mask;
@@ -319,7 +319,7 @@ cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStr
   cudaError_t e = launch_pdl(verify_kernel<D>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
                              VerifyPlan<D>::kTotal, st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
-  return join_launch(p, kRowsV, n_rt, st);
+  return join_launch(p, kRowsV, n_rt, -1, st);
 }
 
 }  // namespace
