@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
   __shared__ float tmax[kLpWarps][32];
   __shared__ uint64_t lists[kLpWarps][32];
   __shared__ float bound;
+  __shared__ uint8_t reachers[kLpWarps][32];  // the warp's threads that reach the bound
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,13 +242,15 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     __syncthreads();
     float thr = bound;
     uint64_t best = 0;  // lane r: the r-th best key of this warp so far, 0 for none
-    auto offer = [&](float v, int id, bool has) {
-      uint32_t set = __ballot_sync(0xffffffffu, has && v >= thr);
-      const uint64_t k = top_key(v, id);
-      while (set) {
-        const int from = __ffs(set) - 1;
-        set &= set - 1;
-        const uint64_t c = __shfl_sync(0xffffffffu, k, from);
+    // candidates: bit e of a lane's mask stands for its v[e], of id + e
+    auto offer = [&](const float (&v)[N], int id, uint32_t mask) {
+      for (uint32_t set; (set = __ballot_sync(0xffffffffu, mask != 0)) != 0;) {
+        const int from = __ffs(set) - 1, e = __ffs(mask) - 1;
+        float x = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) x = e == i ? v[i] : x;
+        const uint64_t c = __shfl_sync(0xffffffffu, top_key(x, id + e), from);
+        if (lane == from) mask &= mask - 1;
         const int at = __popc(__ballot_sync(0xffffffffu, best > c));
         const uint64_t up = __shfl_up_sync(0xffffffffu, best, 1);
         best = lane < at ? best : (lane == at ? c : up);
@@ -255,30 +258,31 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
       const uint64_t kth = __shfl_sync(0xffffffffu, best, p.n_top - 1);
       if (kth) thr = fmaxf(thr, key_value(kth));
     };
-    uint32_t todo = __ballot_sync(0xffffffffu, my_max >= thr);
-    while (todo) {
-      const int j = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int t = warp * 32 + j;  // the thread whose elements are read again
-      const int h = rank == 0 && t < head ? t : -1, e0 = rank == p.C - 1 && t < p.V - tail0 ? tail0 + t : -1;
-      if (h >= 0 || e0 >= 0) {
-        const int id = lane == 0 ? h : (lane == 1 ? e0 : -1);
-        const float v = id >= 0 ? Vec<In>::one(x + id) : 0.f;
-        offer(v, id, id >= 0);
-      }
-      for (int u0 = v0 + t; u0 < v1; u0 += 32 * kLpThreads) {
-        const int u = u0 + lane * kLpThreads;
-        float v[N];
-        if (u < v1) Vec<In>::load(xv + (int64_t)u * N, v);
-        float mx = -INFINITY;
-        if (u < v1) {
+    // the vectors of the warp's threads that reach the bound, spread over its
+    // lanes: all of them are on their way at once
+    const bool mine_too = my_max >= thr;
+    const uint32_t reach = __ballot_sync(0xffffffffu, mine_too);
+    if (mine_too) reachers[warp][__popc(reach & ((1u << lane) - 1))] = lane;
+    __syncwarp();
+    if (reach) {  // (the same in all lanes)
+      float v[N] = {};
+      if (has_head) v[0] = Vec<In>::one(x + tid);
+      offer(v, tid, has_head && mine_too && v[0] >= thr ? 1u : 0u);
+      if (has_tail) v[0] = Vec<In>::one(x + tail0 + tid);
+      offer(v, tail0 + tid, has_tail && mine_too && v[0] >= thr ? 1u : 0u);
+    }
+    const int n_u = (v1 - v0 + kLpThreads - 1) / kLpThreads, items = __popc(reach) * n_u;
+    for (int i0 = 0; i0 < items; i0 += 32) {
+      const int i = i0 + lane, r = i / max(n_u, 1);
+      const int u = i < items ? v0 + warp * 32 + reachers[warp][r] + (i - r * n_u) * kLpThreads : v1;
+      float v[N] = {};
+      uint32_t mask = 0;
+      if (u < v1) {
+        Vec<In>::load(xv + (int64_t)u * N, v);
 #pragma unroll
-          for (int e = 0; e < N; ++e) mx = fmaxf(mx, v[e]);
-        }
-        if (!__any_sync(0xffffffffu, u < v1 && mx >= thr)) continue;
-#pragma unroll
-        for (int e = 0; e < N; ++e) offer(u < v1 ? v[e] : 0.f, head + u * N + e, u < v1);
+        for (int e = 0; e < N; ++e) mask |= v[e] >= thr ? 1u << e : 0u;
       }
+      offer(v, head + u * N, mask);
     }
     lists[warp][lane] = best;
     __syncthreads();
@@ -388,8 +392,11 @@ extern "C" int moe_token_logprobs(const void* logits, int32_t dtype, int64_t row
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return set_error(MOE_ECUDA, "%s: %s", who, cudaGetErrorString(e));
   LpParams p{logits, row_stride, n, V, n_top, 1, tokens, logprob, entropy, top_ids, top_logprobs};
-  // blocks a row: more while the GPU is not full and a block keeps 1024 logits
-  while (p.C < kLpMaxCluster && (int64_t)n * p.C < 2LL * sms && V / (2 * p.C) >= 1024) p.C *= 2;
+  // blocks a row: more while they stay within 5/4 of the multiprocessors and a
+  // block keeps 1024 logits (33 rows of 151936 bf16 logits: 15.3, 10.9, 8.7 and
+  // 9.9 us with 1, 2, 4 and 8 blocks a row; 64 of 32768 fp32: 6.9, 6.2, 6.5, 7.5;
+  // 1023 of 32768: 25, 29, 34, 47)
+  while (p.C < kLpMaxCluster && 2LL * n * p.C <= 5LL * sms / 4 && V / (2 * p.C) >= 1024) p.C *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = dtype == MOE_ACT_F32 ? logprob_launch<float>(p, st) : logprob_launch<__nv_bfloat16>(p, st);
   if (e != cudaSuccess) return set_error(MOE_ECUDA, "%s launch: %s", who, cudaGetErrorString(e));
