@@ -229,6 +229,17 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       // masks: past the last or before the first visible key, on absent pages
       const bool partial = c0 + 32 > pos_min + 1 || c0 < lo_max || mask != (1u << ppt) - 1u;
       if (partial) {
+        // the values' scales of keys past the end or on absent pages become 0:
+        // whatever lies there stays finite (only this warp reads its keys)
+        const int k = warp * 32 + lane;
+        if (!((mask >> (k >> p.pshift)) & 1) || c0 + lane >= s.len) {
+          uint32_t* z = reinterpret_cast<uint32_t*>(smem + st * L::kStage + (k >> p.pshift) * head_bytes + half_b + code_b +
+                                                    (k & (p.P - 1)) * (D / 16));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) z[i] = 0;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
+        __syncwarp();
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
           const bool page = (mask >> ((warp * 32 + 16 * a) >> p.pshift)) & 1;
@@ -288,16 +299,6 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
         const int at = (warp * 32 + 16 * a) & (p.P - 1);
         const uint8_t* vc = base[a] + half_b + 4 * n;
         const uint8_t* vs = base[a] - at * (D / 2) + half_b + code_b + at * (D / 16);
-        // scales of keys past the end or on absent pages are 0: whatever lies there stays finite
-        bool z[4] = {false, false, false, false};
-        if (partial) {
-          const bool page = (mask >> ((warp * 32 + 16 * a) >> p.pshift)) & 1;
-          const int j = c0 + 16 * a;
-          z[0] = !page || j + key_e >= s.len;
-          z[1] = !page || j + key_o >= s.len;
-          z[2] = !page || j + 8 + key_e >= s.len;
-          z[3] = !page || j + 8 + key_o >= s.len;
-        }
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
           uint32_t bb[2][8];
@@ -306,10 +307,8 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
             const int ke = 8 * u + key_e, ko = 8 * u + key_o;
             const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vc + ke * (D / 2) + 32 * j);
             const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vc + ko * (D / 2) + 32 * j);
-            uint32_t s0 = *reinterpret_cast<const uint32_t*>(vs + ke * (D / 16) + 4 * j);
-            uint32_t s1 = *reinterpret_cast<const uint32_t*>(vs + ko * (D / 16) + 4 * j);
-            if (z[2 * u]) s0 = 0;
-            if (z[2 * u + 1]) s1 = 0;
+            const uint32_t s0 = *reinterpret_cast<const uint32_t*>(vs + ke * (D / 16) + 4 * j);
+            const uint32_t s1 = *reinterpret_cast<const uint32_t*>(vs + ko * (D / 16) + 4 * j);
             const uint32_t h = n >> 1;
             const ValueScale d = value_scale(__byte_perm(s0, s1, h | ((4 + h) << 8)) & 0x00FF00FFu);
             value_quads(__byte_perm(w0, w1, 0x5410), d, bb[u][0], bb[u][2], bb[u][4], bb[u][6]);
@@ -558,10 +557,14 @@ cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStre
   int64_t span = p.max_len;
   if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + kSmallTile);
   const int tiles = (int)((span + kSmallTile - 1) / kSmallTile);
-  // keys are split until there are two blocks for each place on the GPU, so
-  // that ragged lengths even out
-  const int64_t want = std::max<int64_t>(1, 2LL * L::kBlocks * num_sms / base);
+  // keys are split until there are four blocks for each place on the GPU, so
+  // that ragged lengths even out (32 sequences of 4096 to 8192 keys, 32/8 heads
+  // of 128: 104, 88, 78 and 78 us with 2, 4, 8 and 10 parts), but not into a
+  // few more parts than the quick join takes
+  const int64_t want = std::max<int64_t>(1, 4LL * L::kBlocks * num_sms / base);
   int chunk = (int)std::max<int64_t>(1, (tiles + want - 1) / want);
+  const int few = (tiles + kJoinFew - 1) / kJoinFew;
+  if (few > chunk && few <= 2 * chunk) chunk = few;
   const int64_t fit = std::min<int64_t>(kMaxSplit, std::max<int64_t>(1, (int64_t)(part_rows / L::kRows) / base));
   chunk = std::max<int>(chunk, (int)((tiles + fit - 1) / fit));
   p.n_split = (tiles + chunk - 1) / chunk;
