@@ -629,11 +629,8 @@ def token_logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     if tokens is not None:
         _require(tokens.shape == (n,) and tokens.dtype is i32 and tokens.is_cuda and tokens.is_contiguous(),
                  "token_logprobs: tokens must be contiguous int32 [n] on the GPU")
-        if entropy:
-            lp, en = torch.empty((2, n), dtype=f32, device=dev).unbind()
-        else:
-            lp = torch.empty(n, dtype=f32, device=dev)
-    elif entropy:
+        lp = torch.empty(n, dtype=f32, device=dev)
+    if entropy:
         en = torch.empty(n, dtype=f32, device=dev)
     ids = torch.empty((n, n_top), dtype=i32, device=dev)
     top = torch.empty((n, n_top), dtype=f32, device=dev)

@@ -9,7 +9,8 @@
 // One block a (query token, query head); its warps take chunks of 32 keys in
 // turn.  For the scores a lane owns a key and reads its D/2 bytes (the query
 // waits in shared memory, read as broadcasts); for the output a lane owns 8
-// channels (a 32-bit word a key).  It is for verification: it re-reads a
+// channels (a 32-bit word) of every key, or of every 2nd or 4th at 128 and 64
+// channels.  It is for verification: it re-reads a
 // key/value head for each of its query heads and is bound by the
 // dequantisation's instructions, not by HBM.
 #include "attn.cuh"
@@ -23,6 +24,7 @@ constexpr int kCheckWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kWords = D / 8;  // words of a row: lanes that own channels
+  constexpr int kPar = kWords <= 16 ? 32 / kWords : 1, kBatch = 8;
   __shared__ float sq[D];
   __shared__ float so[kCheckWarps][D];
   __shared__ float sm[kCheckWarps], sl[kCheckWarps];
@@ -39,6 +41,7 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
   const int pos = s.len - s.nq + t;
   const int lo = key_lo(p, pos);
   const int kvh = h / p.g;
+  const int word = kPar > 1 ? lane % kWords : lane, sub = kPar > 1 ? lane / kWords : 0;
   float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   // chunks of 32 keys, aligned so that a chunk lies in at most two pages (16-token pages)
   for (int c = (lo & ~31) + 32 * warp; c <= pos; c += 32 * kCheckWarps) {
@@ -52,7 +55,7 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
       const uint32_t* kw = reinterpret_cast<const uint32_t*>(base + at * (D / 2));
       const uint8_t* ks = base + p.P * (D / 2) + at * (D / 16);
       sc = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int w = 0; w < kWords; ++w) {
         const uint32_t u = kw[w];
         float a = 0.f;
@@ -73,21 +76,39 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
     l = l * f + pr;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] *= f;
-    for (int i = 0; i < 32; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, pr, i);
-      const uint64_t bi = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(base), i);
-      if (!bi || lane >= kWords) continue;
-      const uint8_t* vb = reinterpret_cast<const uint8_t*>(bi) + p.head_bytes / 2;
-      const int ai = (c + i) & (p.P - 1);
-      const uint32_t u = *reinterpret_cast<const uint32_t*>(vb + ai * (D / 2) + 4 * lane);
-      const float pd = pi * scale_value(vb[p.P * (D / 2) + ai * (D / 16) + (lane >> 1)]);
+    // kPar keys at a time, a lane 8 channels of one; their loads go out together
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[2 * e] = fmaf((float)((int)((u >> (4 * e)) & 15) - 8), pd, o[2 * e]);
-        o[2 * e + 1] = fmaf((float)((int)((u >> (4 * e + 16)) & 15) - 8), pd, o[2 * e + 1]);
+    for (int i0 = 0; i0 < 32; i0 += kPar * kBatch) {
+      uint32_t u[kBatch];
+      float pd[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + kPar * k + sub;
+        const float pi = __shfl_sync(0xffffffffu, pr, i);
+        const uint64_t bi = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(base), i);
+        u[k] = 0;
+        pd[k] = 0.f;
+        if (bi && word < kWords) {
+          const uint8_t* vb = reinterpret_cast<const uint8_t*>(bi) + p.head_bytes / 2;
+          const int ai = (c + i) & (p.P - 1);
+          u[k] = *reinterpret_cast<const uint32_t*>(vb + ai * (D / 2) + 4 * word);
+          pd[k] = pi * scale_value(vb[p.P * (D / 2) + ai * (D / 16) + (word >> 1)]);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = fmaf((float)((int)((u[k] >> (4 * e)) & 15) - 8), pd[k], o[2 * e]);
+          o[2 * e + 1] = fmaf((float)((int)((u[k] >> (4 * e + 16)) & 15) - 8), pd[k], o[2 * e + 1]);
+        }
     }
   }
+  // the keys of a lane group apart
+#pragma unroll
+  for (int x = kWords; x < 32 && kPar > 1; x <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], x);
 #pragma unroll
   for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   if (lane == 0) sm[warp] = m, sl[warp] = l;
