@@ -11,17 +11,16 @@
 //
 // prompt_kernel: a block owns 128 rows (query token, query head of one
 // key/value head) and walks over the visible 128-key tiles j:
-//   S_j = Q K_j^T   (bf16, M = 128, N = 128, both operands in shared memory)
+//   S_j = Q K_j^T   (bf16, M = 128, N = 128; Q in tensor memory as far as it fits)
 //   P_j = 2^(scale S_j - m), rounded to fp16 into the columns of S_j
 //   O  += P_j V_j   (fp16, P from tensor memory, N = D)
 // One thread issues all MMAs; S is double-buffered, so S_{j+1} runs while the
 // softmax of S_j does.  Eight softmax warps: thread (half, row) takes 64 of a
-// row's 128 scores (sixteen warps with 32 each finish a tile's softmax sooner,
-// but take issue slots from the MMA thread: 351 against 328 us).
+// row's 128 scores (sixteen warps with 32 each: 283 against 275 us).
 // The reference m moves only when the maximum passes it by more than 8 (a
 // weight of 2^8 is harmless in fp16 and fp32), which keeps the rescaling of
 // the output in tensor memory rare; l and O stay consistent with m either way.
-//   TMEM columns: S at 0 and 128, O at 256.
+//   TMEM columns: S at 0 and 128, O at 256, then Q (two channels a column).
 //
 // Operand images (no swizzle, K-major, 8x8 core matrices of 128 contiguous
 // bytes): rows x channels as [channels/8][rows][8]; values as
@@ -46,9 +45,11 @@ constexpr int kMaxRing = 8;
 template <int D>
 struct PromptPlan {
   static constexpr int kImage = kTileTokens * D * 2;  // bytes of one operand image
-  static constexpr int kRing = D == 64 ? 8 : (D == 128 ? 5 : (D == 192 ? 3 : 2));
-  static constexpr int kQ = 0;
-  static constexpr int kStages = kImage;  // (a query image has the same size)
+  // channels of the queries that fit in tensor memory beside scores and output
+  static constexpr int kTmemQ = D <= 128 ? D : (D == 192 ? 128 : 0);
+  static constexpr int kRing = D == 64 ? 8 : (D == 128 ? 6 : (D == 192 ? 4 : 2));
+  static constexpr int kQ = 0;  // the other channels
+  static constexpr int kStages = kRowsP * (D - kTmemQ) * 2;
   static constexpr int kMax = kStages + kRing * kImage;              // float [2][shares][128]
   static constexpr int kBars = kMax + 2 * kShares * kRowsP * 4;
   static constexpr int kNumBars = 2 * kMaxRing + 6 + 1;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   volatile int never = 0;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
@@ -210,20 +211,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     hi_r = p0 + tq + 1;
     lo_r = key_lo(p, p0 + tq);
   }
+  constexpr int kChunks = D / 32 / kShares;
+  uint32_t qr[kChunks][16];
   if (warp < kSoftWarps && n_tiles > 0) {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (s.start + tq) * p.q_tok + hq * p.q_head;
-#pragma unroll 4
-    for (int c = share * (D / 8 / kShares); c < (share + 1) * (D / 8 / kShares); ++c) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (has_row) v = *reinterpret_cast<const uint4*>(q + 8 * c);
-      *reinterpret_cast<uint4*>(sm + L::kQ + (c * kRowsP + row) * 16) = v;
-    }
-    tc::fence_async_smem();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (has_row) v = *reinterpret_cast<const uint4*>(q + 32 * (share * kChunks + c) + 8 * i);
+        qr[c][4 * i] = v.x, qr[c][4 * i + 1] = v.y, qr[c][4 * i + 2] = v.z, qr[c][4 * i + 3] = v.w;
+      }
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tbase = *tslot;
+  if (warp < kSoftWarps && n_tiles > 0) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int ch = 32 * (share * kChunks + c);
+      if (ch < L::kTmemQ) {
+        tc::st_32x32b_x16(tbase + ((uint32_t)(warp & 3) << 21) + 256 + D + ch / 2, qr[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(sm + L::kQ + (((ch - L::kTmemQ) / 8 + i) * kRowsP + row) * 16) =
+              make_uint4(qr[c][4 * i], qr[c][4 * i + 1], qr[c][4 * i + 2], qr[c][4 * i + 3]);
+      }
+    }
+    tc::wait_st();
+    tc::fence_async_smem();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
 
   float m = -INFINITY, l = 0.f;
   if (warp == kCopyWarp) {
@@ -248,43 +271,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && n_tiles > 0) {
+    if (n_tiles > 0 && elect_one()) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, kTileTokens) | (1u << 7) | (1u << 10);  // bf16 operands
       constexpr uint32_t kIdescO = tc::idesc_f16(128, D);
       const uint64_t qd = tc::smem_desc(smem_u32(sm + L::kQ), kRowsP * 16, 128);
       bool ok = true;
-      int i = 0;  // images used
-      auto use = [&]() {
-        const int st = i % L::kRing;
-        ok = ok && wait_bar(&full[st], (uint32_t)((i / L::kRing) & 1), abort, p.status, p.timeout_ns, 13);
-        return st;
+      auto landed = [&](int i) {
+        ok = ok && wait_bar(&full[i % L::kRing], (uint32_t)((i / L::kRing) & 1), abort, p.status, p.timeout_ns, 13);
       };
-      auto scores = [&](int j) {
-        const int st = use();
+      auto stored = [&](int j) {
+        ok = ok && wait_bar<64>(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 14);
+      };
+      auto scores = [&](int j, int i) {
+        const uint64_t kd = tc::smem_desc(smem_u32(sm + L::kStages + i % L::kRing * L::kImage), kTileTokens * 16, 128);
+        landed(i);
         if (!ok) return;
         tc::fence_after();
-        const uint64_t kd = tc::smem_desc(smem_u32(sm + L::kStages + st * L::kImage), kTileTokens * 16, 128);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tbase + 128 * (j & 1), qd + k * (2 * kRowsP * 16 / 16), kd + k * (2 * kTileTokens * 16 / 16), kIdescS, k > 0);
-        tc::commit(&empty[st]);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t kk = kd + k * (2 * kTileTokens * 16 / 16);
+          if (16 * k < L::kTmemQ) tc::mma_ts(tbase + 128 * (j & 1), tbase + 256 + D + 8 * k, kk, kIdescS, k > 0);
+          else mma_ss(tbase + 128 * (j & 1), qd + (k - L::kTmemQ / 16) * (2 * kRowsP * 16 / 16), kk, kIdescS, k > 0);
+        }
         tc::commit(&sfull[j & 1]);
-        ++i;
+        tc::commit(&empty[i % L::kRing]);
       };
-      scores(0);
+      int i = 0;  // images used
+      scores(0, i++);
       for (int j = 0; j < n_tiles && ok; ++j) {
-        if (j + 1 < n_tiles) scores(j + 1);
-        if (!ok) break;
-        const int st = use();
-        ok = ok && wait_bar(&pfull[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 14);
+        if (j + 1 < n_tiles) scores(j + 1, i++);
+        const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kStages + i % L::kRing * L::kImage), D * 16, 128);
+        landed(i);
+        stored(j);
         if (!ok) break;
         tc::fence_after();
-        const uint64_t vd = tc::smem_desc(smem_u32(sm + L::kStages + st * L::kImage), D * 16, 128);
 #pragma unroll
         for (int k = 0; k < kTileTokens / 16; ++k)
           tc::mma_ts(tbase + 256, tbase + 128 * (j & 1) + 8 * k, vd + k * (2 * D * 16 / 16), kIdescO, j > 0 || k > 0);
-        tc::commit(&empty[st]);
         tc::commit(&odone[j & 1]);
+        tc::commit(&empty[i % L::kRing]);
         ++i;
       }
       // all MMAs issued are complete before the block frees anything
@@ -294,11 +319,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (n_tiles > 0) {
     // ------------------------------------------------------------ softmax
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    using Bits = KeyBits<kShareKeys>;
+    const Bits* exist_words = reinterpret_cast<const Bits*>(valid) + share;
+    Bits ahead = __ldcg(exist_words);  // read a tile early: it waits for L2
     softmax_tiles<D, kShareKeys, kShares>(
-        p, n_tiles, tl, share, row, kRowsP, smax, sfull, pfull, odone, abort, m, l, [&](int j, KeyBits<kShareKeys>& bits) {
+        p, n_tiles, tl, share, row, kRowsP, smax, sfull, pfull, odone, abort, m, l, [&](int j, Bits& bits) {
           const int c0 = (tile_a + j) * kTileTokens;
-          const auto exist = __ldcg(reinterpret_cast<const KeyBits<kShareKeys>*>(valid + j) + share);
-          if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && exist == ~KeyBits<kShareKeys>(0)) return false;
+          const Bits exist = ahead;
+          if (j + 1 < n_tiles) ahead = __ldcg(exist_words + (j + 1) * kShares);
+          if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && exist == ~Bits(0)) return false;
           bits = key_bits<kShareKeys>(c0 + kShareKeys * share, lo_r, hi_r) & exist;
           return true;
         });

@@ -12,6 +12,18 @@ namespace attn {
 // this (log2 units): a weight of 2^8 is harmless in fp16 and fp32.
 constexpr float kLazy = 8.f;
 
+// One thread of a converged warp, the same each time.  MMAs are issued under
+// it, in a warp whose number came by a shuffle: the compiler then knows that
+// one thread of a uniform warp runs them, and an MMA takes 9 cycles to issue.
+// Under `lane == 0` it takes 45, and 70 beside busy warps, which is more than
+// the MMA itself.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 // D[tmem] (+)= A[smem] B[smem]^T
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(

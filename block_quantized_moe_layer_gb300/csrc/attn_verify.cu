@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   volatile int never = 0;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   float m = -INFINITY, l = 0.f;
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && n_tiles > 0) {
+    if (n_tiles > 0 && elect_one()) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, KT) | (1u << 7) | (1u << 10);  // bf16 operands
       constexpr uint32_t kIdescO = tc::idesc_f16(128, D) | (1u << 16);  // fp16, the values MN-major
       const uint64_t qd = tc::smem_desc(smem_u32(sm + L::kQ), kRowsV * 16, 128);
