@@ -102,8 +102,8 @@ __device__ __forceinline__ void store_joined(const AttnParams& p, int64_t o, int
 
 // A wait on an mbarrier phase that gives up after the call's limit (the
 // status word then says where) or once another thread of the block has.
-static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit,
-                                       int site) {
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*abort) return false;
@@ -114,6 +114,12 @@ static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, vo
     }
   }
   return true;
+}
+// The same as a call, where many waits share the code (a call keeps few
+// registers: not for threads that hold a row of scores).
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit,
+                                       int site) {
+  return wait_inline(bar, parity, abort, status, limit, site);
 }
 // SPINS: tests before the suspending wait, whose sleeper takes a few hundred
 // cycles to resume.  For the one thread that issues MMAs, not for the many

@@ -164,29 +164,5 @@ __device__ __forceinline__ KeyBits<QC> key_bits(int k0, int lo, int hi) {
   return v;
 }
 
-// 16 columns of a row's accumulator, to the output or to a part.
-__device__ __forceinline__ void store_out16(const AttnParams& p, bool parts, const uint32_t (&o)[16], float l, float inv, bool has_row,
-                                            int64_t part, int64_t orow, int c, int D) {
-  float v[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
-  if (!has_row) return;
-  if (parts) {
-    float4* d = reinterpret_cast<float4*>(p.part_o + part * D + c);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) d[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-      w[e] = *reinterpret_cast<const uint32_t*>(&h2);
-    }
-    uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + c);
-    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
 }  // namespace attn
 }  // namespace moe
