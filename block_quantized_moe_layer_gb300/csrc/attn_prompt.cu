@@ -28,8 +28,9 @@
 // the output in tensor memory rare; l and O stay consistent with m either way.
 //   TMEM columns: S at 0 and 128, O at 256, P from 256 + D on.
 // Bound: MMA issue and execution; 1024 query tokens of 64/4 heads of 192 behind
-// 7168 keys take 250 us (1.55 PFLOP/s, 0.80 of the cuBLAS rate measured), of
-// which expanding takes 8, joining 6 and the blocks' starts and ends some 25.
+// 7168 keys take 243 us (1.59 PFLOP/s, 0.82 of the cuBLAS rate measured): the
+// tensor pipe is active 77% of prompt_kernel; the rest are the blocks' starts
+// and ends (some 12000 cycles of 120000) and the last wave.
 //
 // Operand images (no swizzle, K-major, 8x8 core matrices of 128 contiguous
 // bytes): rows x channels as [channels/8][rows][8]; values as
@@ -89,14 +90,18 @@ __device__ __forceinline__ void seq_tiles(const AttnParams& p, const Seq& s, int
   last = s.nq > 0 ? (s.len + kTileTokens - 1) / kTileTokens : first;
 }
 
+// Four blocks a tile: the keys and the values of its first and second 64 keys
+// (one block a tile waits longer for its loads: 250 against 243 us in all for
+// the prompt chunk above).
 __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Images im) {
   griddep_launch_dependents();
   griddep_wait();
-  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int b = blockIdx.z, kvh = blockIdx.y, at_tile = blockIdx.x >> 2, k_lo = (blockIdx.x & 1) * (kTileTokens / 2);
+  const bool values = blockIdx.x & 2;
   const Seq s = load_seq(p, b);
   int first, last;
   seq_tiles(p, s, first, last);
-  const int tile = first + blockIdx.x;
+  const int tile = first + at_tile;
   if (tile >= last) return;
   __shared__ int page[kTileTokens / 16];
   const int ppt = kTileTokens >> p.pshift, tid = threadIdx.x, D = p.D;
@@ -108,21 +113,21 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
   }
   __syncthreads();
   const int n_keys = min(kTileTokens, s.len - tile * kTileTokens);
-  if (kvh == 0 && tid < 4) {
+  if (kvh == 0 && (blockIdx.x & 3) == 0 && tid < 4) {
     uint32_t m = 0;
     for (int i = 0; i < 32; ++i) {
       const int k = 32 * tid + i;
       if (k < n_keys && page[k >> p.pshift] >= 0) m |= 1u << i;
     }
-    reinterpret_cast<uint32_t*>(im.valid + (int64_t)b * im.tiles + blockIdx.x)[tid] = m;
+    reinterpret_cast<uint32_t*>(im.valid + (int64_t)b * im.tiles + at_tile)[tid] = m;
   }
   const int64_t image = (int64_t)kTileTokens * D * 2;
-  uint8_t* kd = im.base + (((int64_t)b * p.hk + kvh) * im.tiles + blockIdx.x) * 2 * image;
+  uint8_t* kd = im.base + (((int64_t)b * p.hk + kvh) * im.tiles + at_tile) * 2 * image;
   uint8_t* vd = kd + image;
   const int words = D / 8, code_b = p.P * (D / 2);
   // keys: a thread takes a word of 8 channels; a warp 32 keys of the same word
-  for (int u = tid; u < kTileTokens * words; u += 256) {
-    const int k = u & (kTileTokens - 1), w = u / kTileTokens;
+  for (int u = tid; u < (values ? 0 : kTileTokens / 2 * words); u += 256) {
+    const int k = k_lo + (u & (kTileTokens / 2 - 1)), w = u / (kTileTokens / 2);
     const int pg = page[k >> p.pshift];
     uint4 o = make_uint4(0, 0, 0, 0);
     if (k < n_keys && pg >= 0) {
@@ -136,8 +141,8 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
     *reinterpret_cast<uint4*>(kd + (k >= kTileTokens / 2 ? image / 2 : 0) + ((int64_t)w * (kTileTokens / 2) + k % (kTileTokens / 2)) * 16) = o;
   }
   // values: a thread takes 8 keys of a word, and turns them to 8 channels of 8 keys
-  for (int u = tid; u < (kTileTokens / 8) * words; u += 256) {
-    const int w = u % words, k0 = 8 * (u / words);
+  for (int u = tid; u < (values ? kTileTokens / 16 * words : 0); u += 256) {
+    const int w = u % words, k0 = k_lo + 8 * (u / words);
     const int pg = page[k0 >> p.pshift];
     uint32_t x[4][8];  // [pair of keys][channel]
     const uint8_t* base = p.pages + (pg < 0 ? 0 : pg) * p.page_bytes + kvh * p.head_bytes + p.head_bytes / 2;
@@ -640,7 +645,7 @@ cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t
       const int64_t cost = (rest * n + places - 1) / places * (c + 4) + (n > 1 ? 4 : 0);
       if (n == 1 || cost < best) best = cost, chunk = c, g.n_split = (rtiles + c - 1) / c;
     }
-    cudaError_t e = launch_pdl(expand_kernel, dim3(im.tiles, p.hk, g.n_seqs), 256, 0, st, g, im);
+    cudaError_t e = launch_pdl(expand_kernel, dim3(4 * im.tiles, p.hk, g.n_seqs), 256, 0, st, g, im);
     if (e == cudaSuccess)
       e = launch_pdl(prompt_kernel<D>, dim3((unsigned)(2 * (whole + rest * g.n_split))), kPromptThreads, PromptPlan<D>::kTotal, st, g, im,
                      n_rt, (int)whole, chunk);
