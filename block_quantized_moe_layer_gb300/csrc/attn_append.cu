@@ -23,8 +23,13 @@
 // 2^-19 (|y_a cos| + |y_b sin|) of it (a sum of squares in at most 13
 // additions, its scaling, a reciprocal square root within 2 units, four
 // products and a sum); a row in which that error could change a scale or a
-// code (about one in 500) has just those channels computed again in fp64.  Values are exact
-// already: their codes are decided by exact fp32 residuals.
+// code (about one in 500) has just those channels computed again in fp64.
+// Values are exact already: their codes are decided by exact fp32 residuals.
+//
+// Measured: 4096 tokens of 64/4 heads of 192 in 66 us, 3.5 TB/s of 6.8 (issue
+// slots 60% busy, 20 warps a multiprocessor: the chains of a row's sum, its
+// rotation and the search for its scale are what is waited for); 4 tokens in
+// 4.2 us, of which a launch alone is 2.
 #include "attn.cuh"
 
 namespace moe {

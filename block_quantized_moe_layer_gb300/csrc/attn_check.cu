@@ -12,7 +12,9 @@
 // channels (a 32-bit word) of every key, or of every 2nd or 4th at 128 and 64
 // channels.  It is for verification: it re-reads a
 // key/value head for each of its query heads and is bound by the
-// dequantisation's instructions, not by HBM.
+// dequantisation's instructions, not by HBM.  Measured: 2 sequences of 3
+// tokens over 999 keys, 16 heads of 64, in 12.4 us (one block a row, 32 chunks
+// of keys: a chain of loads, not a rate).
 #include "attn.cuh"
 
 namespace moe {

@@ -22,6 +22,10 @@
 //     and transposed in registers.  Lane (n, t) takes word n of 64 channels of
 //     the keys at k = 2t, 2t+1, 2t+8, 2t+9; two words interleave to pairs of
 //     keys before dequantisation.
+// Measured: 32 sequences of up to 8192 keys, 32/8 heads of 128, in 75 us, 3.0
+// TB/s: issue slots are 61% busy (a 32-bit word of codes takes some 10
+// instructions to 8 operands, twice for each row tile), the tensor pipe 16%.
+// One token over 257 keys takes 8.1 us: two launches and one chain of loads.
 // Slot n of 8 keys is key kKey(n) = 0,6,1,7,2,4,3,5: then both access patterns
 // meet all banks at 192 and 64 channels.
 #include "attn_mma.cuh"

@@ -19,6 +19,10 @@
 // Rows are read with 16-byte loads, four in flight a thread, and bound by HBM;
 // where there are few rows a cluster of up to 8 blocks shares one and joins
 // its parts through distributed shared memory (no workspace, one launch).
+// Measured: 1023 rows of 32768 fp32 in 28.4 us, 4.7 TB/s of 6.8 (a row is a
+// block of 256 threads, so its join and its best tokens are not covered by its
+// own loads, only by the other blocks'); 33 rows of 151936 bf16, top 20, in
+// 12.5 us; 4 rows of 32768 in 7.3 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
