@@ -42,8 +42,15 @@ int cuda_fail(cudaError_t e, const char* what) {
   } while (0)
 
 // Rows (query tokens times query heads of a key/value head) of a sequence up
-// to which a call runs on the small-row kernel, and on the verify kernel.
-constexpr int kSmallCallRows = 16, kVerifyCallRows = 128;
+// to which a call runs on the small-row kernel, and on the verify kernel.  That
+// one reads the cache again for each 64 rows, but needs no expansion: verify
+// and prompt kernel take, for one sequence of 8000 keys, 20.5 and 30.6 us at 144
+// rows (heads of 192), 27 and 36 at 256 (128), 22 and 33 (256); for 8 sequences
+// 93 and 111, 145 and 144, 92 and 90.  Heads of 64, whose products are short
+// beside their softmax, 30 and 39 us at 141 rows, 41 and 39 at 256; for 8
+// sequences 200 and 219, 265 and 221.
+constexpr int kSmallCallRows = 16;
+constexpr int verify_call_rows(int D) { return D == 64 ? 192 : 256; }
 
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 bool page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
@@ -157,7 +164,7 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
     h->ws_bytes = h->part_rows * (h->D * sizeof(float) + sizeof(float2));
     const int64_t most_rows = (int64_t)h->T_max * (h->hq / h->hk);
     if (most_rows > kSmallCallRows) CKA(attn::verify_configure(h->D), "configure the verify kernel");
-    if (most_rows > kVerifyCallRows) {
+    if (most_rows > verify_call_rows(h->D)) {
       // dequantised tiles of one longest sequence at least, of more while they stay within 256 MB
       const int64_t one = (int64_t)h->hk * ((h->len_max + attn::kTileTokens - 1) / attn::kTileTokens);
       const int64_t room = (256LL << 20) / (4LL * attn::kTileTokens * h->D);
@@ -257,7 +264,7 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
   const int64_t rows = (int64_t)max_q * p.g;
   if (rows <= kSmallCallRows)
     CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch");
-  else if (rows <= kVerifyCallRows)
+  else if (rows <= verify_call_rows(h->D))
     CKA(attn::verify_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch (verify)");
   else
     CKA(attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st),

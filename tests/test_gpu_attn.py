@@ -285,6 +285,14 @@ def test_forward_prompts(hq, hk, D, rot):
         _forward_check(rng, hq, hk, D, lens, news, P)
 
 
+@pytest.mark.parametrize("hq,hk,D,tokens", [(16, 16, 64, 192), (4, 1, 128, 64), (8, 1, 192, 32), (16, 1, 256, 16)])
+def test_forward_around_the_row_limit(hq, hk, D, tokens):
+    """The most rows of the verify kernel, and one token more."""
+    rng = np.random.default_rng(D + tokens)
+    for t in (tokens, tokens + 1):
+        _forward_check(rng, hq, hk, D, [t + 40, t, 150], [t, t // 2, 1], 32)
+
+
 def test_forward_long_and_split():
     rng = np.random.default_rng(11)
     _forward_check(rng, 16, 1, 192, [9001], [4], 64)
