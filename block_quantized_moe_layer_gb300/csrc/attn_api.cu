@@ -126,7 +126,10 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
     }
   } guard{h};
   h->hq = d->n_q_heads; h->hk = d->n_kv_heads; h->D = d->head_dim; h->P = d->page_tokens;
-  h->n_pages = d->n_pages; h->rot = d->rot_dim; h->interleaved = d->interleaved; h->window = d->window;
+  h->n_pages = d->n_pages; h->rot = d->rot_dim; h->interleaved = d->interleaved;
+  // A window that holds every sequence is none.  So position - window, with
+  // positions down to -T_max, stays within 32 bits.
+  h->window = d->window < d->len_max ? d->window : 0;
   h->act = d->act_dtype; h->T_max = d->T_max; h->S_max = d->S_max; h->len_max = d->len_max;
   h->eps = d->eps;
   h->scale = d->scale > 0.f ? d->scale : (float)(1.0 / std::sqrt((double)d->head_dim));

@@ -497,3 +497,14 @@ def test_offsets_past_32_bits():
         at.status()
         want, _, mag = oa.attention(_np(qr[T - n:]), keys, values, n)
         assert (np.abs(_np(out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag + 1e-6).all()
+
+
+@pytest.mark.parametrize("act", [pkg.ACT_F32, pkg.ACT_BF16])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30])
+def test_forward_window_beyond_every_length(window, act):
+    """Also where queries stand before the first token, at negative positions."""
+    rng = np.random.default_rng(23)
+    _forward_check(rng, 4, 2, 64, [3, 300], [8, 5], 16, act=act, window=window)
+    if act == pkg.ACT_BF16:
+        _forward_check(rng, 16, 1, 192, [2, 300], [8, 5], 16, window=window)
+        _forward_check(rng, 16, 1, 128, [30, 300], [70, 50], 16, window=window)
