@@ -233,7 +233,7 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
   if (max_len < 0 || max_len > h->len_max)
     return set_error(MOE_EINVAL, "%s: max_len=%d outside 0..%d", who, max_len, h->len_max);
   if (T == 0 || n_seqs == 0 || max_q == 0) return MOE_OK;
-  if (!pages || !starts || !lens || !table || !out) return set_error(MOE_EINVAL, "%s: NULL argument", who);
+  if (!pages || !starts || !lens || (!table && max_len > 0) || !out) return set_error(MOE_EINVAL, "%s: NULL argument", who);
   if ((int64_t)table_stride * h->P < max_len)
     return set_error(MOE_EINVAL, "%s: %d table entries a sequence hold %lld tokens, max_len is %d", who, table_stride,
                      (long long)table_stride * h->P, max_len);

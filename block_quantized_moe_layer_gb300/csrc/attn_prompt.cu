@@ -613,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
 template <int D>
 cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st) {
   const int n_rt = (int)(((int64_t)p.max_q * p.g + kPairRows - 1) / kPairRows);
-  int64_t span = p.max_len;
+  int64_t span = std::max(p.max_len, 1);
   if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + 2 * kTileTokens);
   Images im;
   im.tiles = (int)((span + kTileTokens - 1) / kTileTokens);
@@ -621,7 +621,7 @@ cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t
   im.base = ws;
   im.valid = reinterpret_cast<uint4*>(ws + (size_t)tile_cap * 2 * PromptPlan<D>::kImage);
   // tiles of one row tile's keys: its window's, or all
-  int64_t rspan = p.max_len;
+  int64_t rspan = std::max(p.max_len, 1);
   if (p.window > 0) rspan = std::min<int64_t>(rspan, (int64_t)p.window + kPairRows + kTileTokens);
   const int rtiles = (int)((rspan + kTileTokens - 1) / kTileTokens);
   const int all = p.n_seqs, places = std::max(1, num_sms / 2);

@@ -558,7 +558,7 @@ cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStre
   const int n_rt = (p.max_q * p.g + L::kRows - 1) / L::kRows;
   const int64_t base = (int64_t)p.hk * n_rt * p.n_seqs;
   // tiles that a row can see: the window's, or all
-  int64_t span = p.max_len;
+  int64_t span = std::max(p.max_len, 1);
   if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + kSmallTile);
   const int tiles = (int)((span + kSmallTile - 1) / kSmallTile);
   // keys are split until there are four blocks for each place on the GPU, so

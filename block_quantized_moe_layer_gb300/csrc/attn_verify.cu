@@ -311,7 +311,7 @@ cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStr
   constexpr int KT = VerifyPlan<D>::KT;
   const int n_rt = (p.max_q * p.g + kRowsV - 1) / kRowsV;
   const int64_t base = (int64_t)p.hk * n_rt * p.n_seqs;
-  int64_t span = p.max_len;  // keys a row tile can see: the window's, or all
+  int64_t span = std::max(p.max_len, 1);  // keys a row tile can see: the window's, or all
   if (p.window > 0) span = std::min<int64_t>(span, (int64_t)p.window + p.max_q + KT);
   const int tiles = (int)((span + KT - 1) / KT);
   // one block a multiprocessor; at least two tiles a block

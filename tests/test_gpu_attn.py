@@ -508,3 +508,27 @@ def test_forward_window_beyond_every_length(window, act):
     if act == pkg.ACT_BF16:
         _forward_check(rng, 16, 1, 192, [2, 300], [8, 5], 16, window=window)
         _forward_check(rng, 16, 1, 128, [30, 300], [70, 50], 16, window=window)
+
+
+@pytest.mark.parametrize("act", [pkg.ACT_F32, pkg.ACT_BF16])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("news", [1, 4, 40])
+def test_forward_with_no_cached_token_at_all(D, news, act):
+    """max_len = 0: no query sees a key, whichever kernel the row count takes."""
+    hq, hk, P = 16, 1, 16
+    at = pkg.Attention(hq, hk, D, P, 4, 2 * news, 2, 64, act=act, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(2 * news, hq, D, device="cuda").to(at.dtype)
+    starts, table = torch.tensor([0, news, 2 * news], **i32), torch.full((2, 1), -1, **i32)
+    out, lse = torch.full_like(q, 5.0), torch.full((2 * news, hq), 5.0, device="cuda")
+    for t in (table, table[:, :0], torch.empty(2, 0, **i32)):
+        at.forward(q, at.pages(), starts, torch.tensor([0, 0], **i32), t, news, 0, out=out, lse=lse)
+        at.status()
+        assert (out == 0).all() and torch.isneginf(lse).all()
+        out.fill_(5.0)
+        lse.fill_(5.0)
+    # a length beyond it is reported, and nothing of it is read
+    at.forward(q, at.pages(), starts, torch.tensor([0, 9], **i32), table, news, 0, out=out, lse=lse)
+    with pytest.raises(pkg.MoEError, match="lengths"):
+        at.status()
+    assert (out == 0).all() and torch.isneginf(lse).all()
