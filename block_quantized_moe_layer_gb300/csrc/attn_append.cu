@@ -65,9 +65,13 @@ __device__ __forceinline__ int scale_byte(T amax) {
   b = min(max(b - 1, 0), kKvMaxScale);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    // next below the midpoint where a tie goes up
-    const float mid = __int_as_float(__float_as_int(3.5f * (scale_value(b) + scale_value(b + 1))) - (b & 1));
-    b += amax > (T)mid ? 1 : 0;
+    const float mid = 3.5f * (scale_value(b) + scale_value(b + 1));
+    if constexpr (sizeof(T) == 4) {
+      // at an odd b a tie goes up: an fp32 amax is at the midpoint or above if it is above the fp32 number before it
+      b += amax > __int_as_float(__float_as_int(mid) - (b & 1)) ? 1 : 0;
+    } else {
+      b += ((b & 1) ? amax >= (T)mid : amax > (T)mid) ? 1 : 0;
+    }
   }
   return min(b, kKvMaxScale);
 }

@@ -532,3 +532,32 @@ def test_forward_with_no_cached_token_at_all(D, news, act):
     with pytest.raises(pkg.MoEError, match="lengths"):
         at.status()
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("angle", [2.0 ** -26, 1e-9, 2.0 ** -40])
+def test_append_scales_next_to_the_midpoint_of_two_scales(angle):
+    """A largest channel within 2^-26 of the midpoint of two neighbouring
+    scales, below and above it (a rotation by a small angle puts it there):
+    the nearer scale is stored, for every pair of scales."""
+    hq, hk, D, P = 1, 1, 64, 16
+    b = np.arange(1, oa.KV_MAX_SCALE)
+    mid = 3.5 * (oa.scale_of(b) + oa.scale_of(b + 1))  # 8 significant bits: exact in bf16
+    T = 2 * len(b)
+    k = np.zeros((T, hk, D))
+    k[:, 0, 0] = np.repeat(mid, 2)
+    k[:, 0, 8] = np.repeat(mid / 2, 2) * np.where(np.arange(T) % 2, -1, 1)  # its partner: below for +, above for -
+    k[:, 0, 16:] = np.random.default_rng(0).normal(size=(T, D - 16))
+    n_pages = -(-T // P)
+    for dtype in (torch.bfloat16, torch.float32):
+        at = pkg.Attention(hq, hk, D, P, n_pages, T, 1, 4, rot_dim=16, freq=[angle] * 8)
+        kd = torch.tensor(k, device="cuda").to(dtype)
+        pos, slots = torch.ones(T, dtype=torch.int32, device="cuda"), torch.arange(T, device="cuda")
+        pages = at.pages()
+        at.append(kd, kd, kd, pos, slots, pages)
+        at.status()
+        codes, scales = oa.quantise(oa.prepared(_np(kd), None, np.ones(T), 16, [angle] * 8))
+        assert np.array_equal(scales[:, 0, 0], np.repeat(b, 2) + np.arange(T) % 2)  # (the oracle's own choice)
+        gc, gs = oa.page_arrays(pages.cpu().numpy(), hk, P, D)[:2]
+        sl = np.arange(T)
+        assert np.array_equal(gs[sl // P, :, sl % P], scales), (gs[sl // P, :, sl % P] != scales).sum()
+        assert np.array_equal(oa.unpack(gc[sl // P, :, sl % P]), codes)
