@@ -91,6 +91,11 @@ __device__ __forceinline__ int key_lo(const AttnParams& p, int pos) {
   return p.window > 0 ? max(0, pos - p.window + 1) : 0;
 }
 
+// A row's softmax reference once it has seen a key, whatever the key's score:
+// -inf stands for no key (the row is 0), so that a row whose scores are NaN, or
+// all -inf, becomes NaN.
+constexpr float kSeen = -3.402823466e+38f;
+
 __device__ __forceinline__ float scale_value(int b) { return __half2float(__ushort_as_half((unsigned short)(b << 7))); }
 
 }  // namespace attn

@@ -69,9 +69,8 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
         sc = fmaf(a, scale_value(ks[w >> 1]), sc);
       }
     }
-    const float mc = warp_max(sc);
-    if (mc == -INFINITY) continue;
-    const float mn = fmaxf(m, mc);
+    if (!__any_sync(0xffffffffu, base != nullptr)) continue;
+    const float mn = fmaxf(m, fmaxf(warp_max(sc), kSeen));
     const float f = exp2f(m - mn);  // 0 at the first keys
     const float pr = exp2f(sc - mn);
     m = mn;
@@ -129,10 +128,10 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
 #pragma unroll
     for (int w = 0; w < kCheckWarps; ++w) v += sm[w] == -INFINITY ? 0.f : so[w][i] * exp2f(sm[w] - mx);
     // a row that sees no key is 0
-    static_cast<float*>(p.out)[((int64_t)tok * p.hq + h) * D + i] = lt > 0.f ? v / lt : 0.f;
+    static_cast<float*>(p.out)[((int64_t)tok * p.hq + h) * D + i] = mx > -INFINITY ? v / lt : 0.f;
   }
   if (p.lse && threadIdx.x == 0)
-    p.lse[(int64_t)tok * p.hq + h] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    p.lse[(int64_t)tok * p.hq + h] = mx > -INFINITY ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace

@@ -91,13 +91,13 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 
 // Channels 4 c .. 4 c + 3 of an output row, and its logarithm.
 __device__ __forceinline__ void store_joined(const AttnParams& p, int64_t o, int c, int D, float4 x, float lt, float mx) {
-  const float inv = lt > 0.f ? kValueUnscale / lt : 0.f;
+  const float inv = mx > -INFINITY ? kValueUnscale / lt : 0.f;
   const __nv_bfloat162 u = __floats2bfloat162_rn(x.x * inv, x.y * inv), w = __floats2bfloat162_rn(x.z * inv, x.w * inv);
   uint2 r;
   r.x = *reinterpret_cast<const uint32_t*>(&u);
   r.y = *reinterpret_cast<const uint32_t*>(&w);
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 4 * c) = r;
-  if (p.lse && c == 0) p.lse[o] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+  if (p.lse && c == 0) p.lse[o] = mx > -INFINITY ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 // A wait on an mbarrier phase that gives up after the call's limit (the

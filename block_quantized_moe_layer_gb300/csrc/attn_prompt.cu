@@ -533,15 +533,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
       const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
       uint4 ahead = make_uint4(0, 0, 0, 0);  // the keys that exist, read two tiles early: they wait for L2
       if (turn < n_tiles) ahead = __ldcg(valid + turn);
+      bool seen = false;
       softmax_turns<D>(p, n_tiles, tl, turn, row, smax, sfull, sread, pfull, odone, abort, m, l, [&](int j, uint64_t (&bits)[2]) {
         const int c0 = (tile_a + j) * kTileTokens;
         const uint64_t e0 = ahead.x | ((uint64_t)ahead.y << 32), e1 = ahead.z | ((uint64_t)ahead.w << 32);
         if (j + 2 < n_tiles) ahead = __ldcg(valid + j + 2);
-        if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && (e0 & e1) == ~0ull) return false;
+        if (c0 + kTileTokens <= pos_min + 1 && c0 >= lo_max && (e0 & e1) == ~0ull) {
+          seen = true;
+          return false;
+        }
         bits[0] = key_bits<64>(c0, lo_r, hi_r) & e0;
         bits[1] = key_bits<64>(c0 + 64, lo_r, hi_r) & e1;
+        seen |= (bits[0] | bits[1]) != 0;
         return true;
       });
+      if (seen) m = fmaxf(m, kSeen);
     }
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
@@ -560,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
     l += other == -INFINITY ? 0.f : smax[(2 + (turn ^ 1)) * kRowsP + row] * exp2_approx(other - mm);
     m = mm;
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
-    const float inv = parts ? 1.f : (l > 0.f ? kValueUnscale / l : 0.f);
+    const float inv = parts ? 1.f : kValueUnscale / l;  // (rows that see no key: not used)
     // the outputs go through shared memory, where queries and images were: a
     // thread's row is D apart from its neighbour's (stored from here they took
     // 6000 cycles, a part's 11000)
@@ -577,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
       for (int e = 0; e < 4; ++e) {
         const float4 v = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
                                      __uint_as_float(o[4 * e + 3]));
-        d[e] = l > 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+        d[e] = m > -INFINITY ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
     if (has_row && turn == 0) {
@@ -585,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
                                  : (int64_t)(s.start + tq) * p.hq + hq;
       *reinterpret_cast<int64_t*>(sm + row * L::kPitch + D * 4) = orow;
       if (parts) p.part_ml[orow] = make_float2(m, l);
-      else if (p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      else if (p.lse) p.lse[orow] = m > -INFINITY ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
     tc::fence_before();
   }

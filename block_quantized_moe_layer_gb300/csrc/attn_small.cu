@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   float m[2 * NT], l[2 * NT];
 #pragma unroll
   for (int i = 0; i < 2 * NT; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  uint32_t seen = 0;  // bit r: row r of m and l has seen a key
   const int code_b = p.P * (D / 2), half_b = head_bytes / 2;
 
   for (int i = 0; i < n_tiles; ++i) {
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       }
       // masks: past the last or before the first visible key, on absent pages
       const bool partial = c0 + 32 > pos_min + 1 || c0 < lo_max || mask != (1u << ppt) - 1u;
-      if (partial) {
+      if (!partial) seen = ~0u;
+      else {
         // the values' scales of keys past the end or on absent pages become 0:
         // whatever lies there stays finite (only this warp reads its keys)
         const int k = warp * 32 + lane;
@@ -252,8 +254,11 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
           for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (!page || j0 >= hi_r[2 * u + e] || j0 < lo_r[2 * u + e]) sc[u][a][e] = -INFINITY;
-              if (!page || j1 >= hi_r[2 * u + e] || j1 < lo_r[2 * u + e]) sc[u][a][2 + e] = -INFINITY;
+              const bool s0 = page && j0 < hi_r[2 * u + e] && j0 >= lo_r[2 * u + e];
+              const bool s1 = page && j1 < hi_r[2 * u + e] && j1 >= lo_r[2 * u + e];
+              if (!s0) sc[u][a][e] = -INFINITY;
+              if (!s1) sc[u][a][2 + e] = -INFINITY;
+              seen |= s0 || s1 ? 1u << (2 * u + e) : 0u;
             }
         }
       }
@@ -332,7 +337,10 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   }
   // this warp's part
 #pragma unroll
+  for (int x = 4; x < 32; x <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, x);
+#pragma unroll
   for (int r = 0; r < 2 * NT; ++r) {
+    if ((seen >> r) & 1) m[r] = fmaxf(m[r], kSeen);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 4);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       x[3] = fmaf(v.w, f, x[3]);
     }
     if (p.n_split == 1) {
-      const float inv = lt > 0.f ? kValueUnscale / lt : 0.f;
+      const float inv = mx > -INFINITY ? kValueUnscale / lt : 0.f;
       const int row = row0 + r, tok = s.start + row / p.g, h = kvh * p.g + row % p.g;
       const __nv_bfloat162 u = __floats2bfloat162_rn(x[0] * inv, x[1] * inv), v = __floats2bfloat162_rn(x[2] * inv, x[3] * inv);
       uint2 w;
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       w.y = *reinterpret_cast<const uint32_t*>(&v);
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + ((int64_t)tok * p.hq + h) * D + c) = w;
       if (p.lse && c == 0)
-        p.lse[(int64_t)tok * p.hq + h] = lt > 0.f ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+        p.lse[(int64_t)tok * p.hq + h] = mx > -INFINITY ? (mx + log2f(lt)) * 0.69314718055994531f : -INFINITY;
     } else {
       if (c == 0) p.part_ml[part + r] = make_float2(mx, lt);
       *reinterpret_cast<float4*>(p.part_o + (part + r) * D + c) = make_float4(x[0], x[1], x[2], x[3]);

@@ -51,7 +51,7 @@ struct VerifyPlan {
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + D / 8 * kRowsV * 16;
   static constexpr int kV = kK + 2 * kImage;
-  static constexpr int kMax = kV + 2 * kImage;                 // float [2][4][64] (the sums and references need 5 x 64)
+  static constexpr int kMax = kV + 2 * kImage;                 // float [2][4][64] (the sums and references take as much)
   // [8 tiles][16]: a byte for each 8 keys that exist (written up to 4 tiles before the softmax reads it)
   static constexpr int kHere = kMax + 2 * 4 * kRowsV * 4;
   static constexpr int kBars = kHere + 8 * 16;
@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   }
 
   float m = -INFINITY, l = 0.f;
+  bool seen = false;  // this thread's keys: one of them by the row
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     if (n_tiles > 0 && elect_one()) {
@@ -259,8 +260,12 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       uint32_t mask;
       if constexpr (QC == 32) mask = *reinterpret_cast<const volatile uint32_t*>(here + (j & 7) * 16 + 4 * quarter);
       else mask = *reinterpret_cast<const volatile uint16_t*>(here + (j & 7) * 16 + 2 * quarter);
-      if (c0 + KT <= pos_min + 1 && c0 >= lo_max && mask == (0x01010101u >> (32 - QC))) return false;
+      if (c0 + KT <= pos_min + 1 && c0 >= lo_max && mask == (0x01010101u >> (32 - QC))) {
+        seen = true;
+        return false;
+      }
       bits = key_bits<QC>(c0 + QC * quarter, lo_r, hi_r) & (mask * 0xFFu);  // (bytes of 1 to bytes of 0xFF)
+      seen |= bits != 0;
       return true;
     });
   }
@@ -270,7 +275,10 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (soft) smax[quarter * kRowsV + row] = l;
+  if (soft) {
+    smax[quarter * kRowsV + row] = l;
+    smax[(4 + quarter) * kRowsV + row] = seen ? fmaxf(m, kSeen) : m;
+  }
   if (soft && n_tiles > 0) {
     const uint32_t tl = tbase + ((uint32_t)(warp & 3) << 21);
 #pragma unroll 1
@@ -282,7 +290,6 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
     }
-    if (quarter == 0) smax[4 * kRowsV + row] = m;
   }
   tc::fence_before();
   __syncthreads();
@@ -294,9 +301,11 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     float lt = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) lt += smax[k * kRowsV + r];
-    const float mr = n_tiles > 0 ? smax[4 * kRowsV + r] : -INFINITY;
+    float mr = smax[4 * kRowsV + r];
+#pragma unroll
+    for (int k = 5; k < 8; ++k) mr = fmaxf(mr, smax[k * kRowsV + r]);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lt > 0.f) v = *reinterpret_cast<const float4*>(sm + r * L::kPitch + c * 16);
+    if (mr > -INFINITY) v = *reinterpret_cast<const float4*>(sm + r * L::kPitch + c * 16);
     if (p.n_split > 1) {
       *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + 4 * c) = v;
       if (c == 0) p.part_ml[part0 + r] = make_float2(mr, lt);

@@ -451,7 +451,9 @@ int moe_attn_read(moe_attn* h, const void* pages, const int64_t* slots, int32_t 
  * the query tokens starts[b]..starts[b+1]-1 of q, which are its last ones:
  * query i stands at position lens[b] - (starts[b+1] - starts[b]) + i -
  * starts[b] and sees the keys 0..position (with a window, its last `window`).
- * A query that sees none (its position is negative) is 0, its lse -inf.
+ * A query that sees none (its position is negative) is 0, its lse -inf.  A NaN
+ * or infinite query that sees a key is NaN, and so is one whose scores are all
+ * -inf (then with an lse of -inf).
  *   q [T, n_q_heads, D] (act_dtype; strides in elements, multiples of 16
  * bytes), out [T, n_q_heads, D] contiguous (not overlapping q), lse fp32 [T,
  * n_q_heads] or NULL: the natural logarithm of the softmax's denominator.

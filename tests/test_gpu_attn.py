@@ -561,3 +561,74 @@ def test_append_scales_next_to_the_midpoint_of_two_scales(angle):
         sl = np.arange(T)
         assert np.array_equal(gs[sl // P, :, sl % P], scales), (gs[sl // P, :, sl % P] != scales).sum()
         assert np.array_equal(oa.unpack(gc[sl // P, :, sl % P]), codes)
+
+
+@pytest.mark.parametrize("act,news,lens", [(pkg.ACT_F32, 4, [300, 2]), (pkg.ACT_BF16, 1, [300, 40]), (pkg.ACT_BF16, 1, [9000, 40]),
+                                           (pkg.ACT_BF16, 4, [300, 2]), (pkg.ACT_BF16, 4, [9000, 2]), (pkg.ACT_BF16, 70, [300, 50]),
+                                           (pkg.ACT_BF16, 70, [9000, 50])])
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 64), (16, 1, 64), (16, 2, 128), (16, 1, 192), (16, 1, 256)])
+def test_forward_nan_and_infinite_queries(hq, hk, D, act, news, lens):
+    """Their rows are NaN in every kernel (a row without a key stays 0), the
+    other rows keep their bits."""
+    rng = np.random.default_rng(21)
+    P = 16
+    pages, table, keys, values, n_pages = _cache(rng, lens, hk, D, P)
+    T = 2 * news
+    at = pkg.Attention(hq, hk, D, P, n_pages, T, 2, max(lens), act=act, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (pages, torch.tensor([0, news, T], **i32), torch.tensor(lens, **i32), table, news, max(lens))
+    q = torch.randn(T, hq, D, device="cuda").to(at.dtype)
+    lse, lse_bad = (torch.empty(T, hq, device="cuda") for _ in range(2))
+    good = at.forward(q, *args, lse=lse)
+    empty = torch.isneginf(lse)  # (rows before the first token of a sequence shorter than its queries)
+    bad = q.clone()
+    bad[0, 0, 3] = float("nan")
+    bad[0, 2, 5] = float("inf")
+    bad[news - 1, 1, D - 1] = float("-inf")
+    bad[news - 1, hq - 1, 7] = 3.0e38  # finite, with scores beyond fp32
+    bad[news - 1, hq - 1, 8] = -3.0e38
+    bad[news, 3] = float("nan")
+    bad[T - 1, 4, 0] = float("nan")
+    rows = torch.zeros(T, hq, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 0), (0, 2), (news - 1, 1), (news, 3), (T - 1, 4)):
+        rows[t, h] = True
+    out = at.forward(bad, *args, lse=lse_bad)
+    at.status()
+    dead = rows & ~empty
+    assert torch.isnan(out[dead]).all(), torch.isnan(out[dead]).all(1)
+    assert (out[rows & empty] == 0).all() and torch.isneginf(lse_bad[rows & empty]).all()
+    nan = dead.clone()
+    nan[0, 2] = nan[news - 1, 1] = False  # (scores of -inf alone have an lse of -inf)
+    assert torch.isnan(lse_bad[nan]).all()
+    rows[news - 1, hq - 1] = True
+    assert torch.equal(out[~rows], good[~rows]) and torch.equal(lse_bad[~rows], lse[~rows])
+
+
+@pytest.mark.parametrize("act,news", [(pkg.ACT_F32, 1), (pkg.ACT_BF16, 1), (pkg.ACT_BF16, 4), (pkg.ACT_BF16, 70)])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_forward_scores_of_minus_infinity(D, act, news):
+    """Keys whose score is -inf have weight 0 beside others; where a row sees
+    only such keys its softmax has no value and the row is NaN."""
+    hq, hk, P, n = 16, 1, 16, 90
+    at = pkg.Attention(hq, hk, D, P, 6, news, 1, 96, act=act, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.ones(n, hk, D, device="cuda")
+    k[40:, :, :16] = 0  # (the later keys do not meet the query's infinity: 0 codes would make NaN of it, so it is finite)
+    pages, j = at.pages(), torch.arange(n, device="cuda")
+    tmp = pkg.Attention(1, hk, D, P, 6, n, 1, 96, rot_dim=0)
+    tmp.append(k[:, :1], k, torch.randn_like(k), j.int(), j, pages)
+    v = tmp.read(j, pages)[1].float()
+    q = torch.zeros(news, hq, D, device="cuda")
+    q[:, 0, :16] = -3.0e38  # 16 of them times a key of 1 is beyond fp32
+    table = torch.arange(6, **i32)[None]
+    args = lambda m: (pages, torch.tensor([0, news], **i32), torch.tensor([m], **i32), table, news, m)
+    out = at.forward(q.to(at.dtype), *args(n)).float()
+    if news <= 50:  # keys 40.. have score 0: the mean of their values
+        want = torch.stack([v[40:n - news + t + 1, 0].mean(0) for t in range(news)])
+        assert ((out[:, 0] - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -9).all()
+    first = at.forward(q.to(at.dtype)[:news], *args(max(news, 40)))
+    at.status()
+    seen = min(40, news)
+    rows = first[:, 0] if news <= 40 else first[:40, 0]
+    assert torch.isnan(rows).all(), seen
+    assert torch.isfinite(first[:, 1:]).all()
