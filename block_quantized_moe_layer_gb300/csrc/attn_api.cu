@@ -116,6 +116,7 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
   if (!(d->rope_base >= 0.0) || d->rope_base > 1e30)
     return set_error(MOE_EINVAL, "moe_attn_create: rope_base must be finite and >= 0 (0: 10000)");
 
+  double f[128];  // angles a token (rot_dim <= 256), alive until the stream has copied them
   moe_attn* h = new (std::nothrow) moe_attn();
   if (!h) return set_error(MOE_ENOMEM, "moe_attn_create: host allocation");
   struct Guard {
@@ -144,14 +145,14 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
   CKA(cudaMemsetAsync(h->status, 0, 16, st), "zero status");
   if (h->rot) {
     const int half = h->rot / 2;
-    double f[128];  // rot_dim <= 256
     for (int i = 0; i < half; ++i) {
       f[i] = d->freq ? d->freq[i] : std::pow(d->rope_base > 0.0 ? d->rope_base : 10000.0, -2.0 * i / h->rot);
       if (!(std::fabs(f[i]) <= 1e30)) return set_error(MOE_EINVAL, "moe_attn_create: freq[%d] is not finite", i);
     }
     CKA(cudaMalloc(&h->freq, half * sizeof(double)), "alloc frequencies");
     CKA(cudaMalloc(&h->rope, (size_t)2 * h->len_max * h->rot * sizeof(float)), "alloc rotation table");
-    CKA(cudaMemcpy(h->freq, f, half * sizeof(double), cudaMemcpyHostToDevice), "copy frequencies");
+    // (on the table's own stream: the default stream's copies are not ordered with it)
+    CKA(cudaMemcpyAsync(h->freq, f, half * sizeof(double), cudaMemcpyHostToDevice, st), "copy frequencies");
     CKA(attn::rope_launch(h, st), "rotation table");
   }
   if (h->q_norm || h->k_norm) {

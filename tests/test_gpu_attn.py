@@ -632,3 +632,24 @@ def test_forward_scores_of_minus_infinity(D, act, news):
     rows = first[:, 0] if news <= 40 else first[:40, 0]
     assert torch.isnan(rows).all(), seen
     assert torch.isfinite(first[:, 1:]).all()
+
+
+def test_creation_on_a_side_stream_beside_a_busy_default_stream():
+    """The rotation table is made from the frequencies, whatever else is queued on other streams."""
+    D, T, far = 256, 64, 1 << 20
+    x = torch.randn(T, 3, D, device="cuda")
+    q, k, v = x.split([1, 1, 1], 1)
+    pos = torch.randint(far, (T,), dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    a = pkg.Attention(1, 1, D, 16, 4, T, 1, far, act=pkg.ACT_F32)
+    want = a.append(q, k, v, pos, slots, a.pages())
+    big = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _ in range(4):
+            big = big @ big * 1e-2
+        b = pkg.Attention(1, 1, D, 16, 4, T, 1, far, act=pkg.ACT_F32, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(b.append(q, k, v, pos, slots, b.pages()), want)
+        b.close()
