@@ -208,6 +208,16 @@ __device__ __forceinline__ void copy_angles(float* s, const AppendParams& p, int
   for (int i = 4 * (threadIdx.x & 31); i < p.rot; i += 128) copy16(s + i, r + i);
 }
 
+// A row whose mean square (with eps) v lies outside 2^-60 .. 2^100 is normalised
+// at another scale, a power of two, so that its squares neither overflow nor
+// vanish (|x| from 2^-149 to 2^128 at D <= 256).  Rare: without this a row above
+// 2^64 would become zeros, and without eps one below 2^-75 infinities.
+__device__ __forceinline__ bool norm_range(float v) {  // (not a NaN, nor 0)
+  constexpr uint32_t kLow = (127 - 60) << 23, kHigh = (127 + 100) << 23;
+  return __float_as_uint(v) - kLow <= kHigh - kLow;
+}
+__device__ __forceinline__ float norm_scale(float v) { return norm_range(v) ? 1.f : (v < 1.f ? 0x1p88f : 0x1p-70f); }
+
 // x_hi + x_lo: the sum of squares of a lane's channels, each step's rounding
 // error kept (two-sum; the square's own by an fma).
 __device__ __forceinline__ double square_sum(const float (&x)[16]) {
@@ -231,6 +241,22 @@ __device__ __forceinline__ float ring_channel(const uint4* slot, int thread, int
   else return piece[i % kPer];
 }
 
+// The scale of a thread's row by its mean square v, and the mean square at that
+// scale (the whole warp calls it).  A call, so that the rows of every day keep their registers.
+template <int G, typename In>
+__device__ __noinline__ float2 wide_norm(const uint4* slot, bool holds, float v, float inv_d, float eps) {
+  const float scale = norm_scale(v);
+  float ss = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const float x = holds ? ring_channel<In>(slot, threadIdx.x, i) * scale : 0.f;
+    ss = fmaf(x, x, ss);
+  }
+#pragma unroll
+  for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return make_float2(scale, fmaf(ss, inv_d, eps * scale * scale));
+}
+
 // Settles in fp64 what fp32 left open in a warp's key rows (the whole warp
 // calls it): the scales of lanes with `border`, then the codes of `unsure`.
 // One channel a turn, with its partner and the row's sum: a row with one
@@ -248,14 +274,24 @@ __device__ __noinline__ void settle_rows(const uint4* slot, bool holds, const fl
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = holds ? ring_channel<In>(slot, threadIdx.x, i) : 0.f;
-    double ss = square_sum(x);
+    auto mean_square = [&]() {
+      double ss = square_sum(x);
 #pragma unroll
-    for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      return ss * (1.0 / D);
+    };
+    double v = mean_square() + eps;
+    const float scale = norm_scale((float)v);
+    if (__any_sync(0xffffffffu, scale != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= scale;
+      v = mean_square() + eps * scale * scale;
+    }
     // a reciprocal square root by two Newton steps from the fp32 one (2^-22, 2^-43, 2^-53)
-    const double v = fma(ss, 1.0 / D, eps);
     inv = (double)rsqrtf((float)v);
 #pragma unroll
     for (int i = 0; i < 2; ++i) inv = fma(inv * 0.5, fma(-v * inv, inv, 1.0), inv);
+    inv *= scale;
   }
   // channel i of lane `who`, in fp64
   auto channel = [&](int who, int i) {
@@ -384,7 +420,7 @@ __device__ __forceinline__ void query_heads(const AppendParams& p, int D, int t,
       const uint4* s = mine + (slot * kPieces + i * (kPieces / NB)) * kAppendThreads;
       pairs8(s, x[i], (In*)nullptr);
       pairs8(s + kPieces / NB / 2 * kAppendThreads, x[i] + 4, (In*)nullptr);
-      if (!holds) {  // lanes past the channels add nothing to the sum
+      if (!holds || i >= rows) {  // lanes past the channels add nothing to the sum
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[i][k] = 0;
       }
@@ -412,10 +448,26 @@ __device__ __forceinline__ void query_heads(const AppendParams& p, int D, int t,
       for (int o = G / 2; o; o >>= 1)
 #pragma unroll
         for (int i = 0; i < NB; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+      bool wide = false;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        ss[i] = fmaf(ss[i], p.inv_d, p.eps);
+        wide |= !norm_range(ss[i]);
+      }
+      if (__any_sync(0xffffffffu, wide)) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const float2 r = wide_norm<G, In>(ring + (slot * kPieces + i * (kPieces / NB)) * kAppendThreads, holds && i < rows, ss[i],
+                                            p.inv_d, p.eps);
+          ss[i] = r.y;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i][k] = f2_mul(x[i][k], f2(r.x, r.x));
+        }
+      }
       uint64_t i2[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const float inv = rsqrtf(fmaf(ss[i], p.inv_d, p.eps));
+        const float inv = rsqrtf(ss[i]);
         i2[i] = f2(inv, inv);
       }
 #pragma unroll
@@ -555,7 +607,14 @@ __device__ __forceinline__ void cache_heads(const AppendParams& p, int D, int t,
         for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
         for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        float v = fmaf(ss, p.inv_d, p.eps);
+        if (__any_sync(0xffffffffu, key && !norm_range(v))) {
+          const float2 r = wide_norm<G, In>(ring + at * kPieces * kAppendThreads, holds, v, p.inv_d, p.eps);
+          v = r.y;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] *= r.x;
+        }
+        const float inv = rsqrtf(v);
         if (norm) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

@@ -653,3 +653,59 @@ def test_creation_on_a_side_stream_beside_a_busy_default_stream():
         torch.cuda.synchronize()
         assert torch.equal(b.append(q, k, v, pos, slots, b.pages()), want)
         b.close()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hk,D,rot", HEADS)
+def test_append_norm_of_very_large_and_very_small_rows(hq, hk, D, rot, interleaved):
+    """Rows whose squares leave the range of fp32 are normalised all the same."""
+    rng = np.random.default_rng(22)
+    T = 40
+    x = rng.normal(size=(T, hq + 2 * hk, D))
+    x[0::4] *= 1e22
+    x[1::4, ::2] *= 2.0 ** 120  # heads of a token differ
+    x[2::4] *= 3e37
+    x = np.clip(x, -3.3e38, 3.3e38)
+    for dtype, act in ((torch.bfloat16, pkg.ACT_BF16), (torch.float32, pkg.ACT_F32)):
+        _append_check(rng, hq, hk, D, rot, T, 32, dtype, act, interleaved=interleaved, x=x)
+    # without eps small rows have a norm too (fp32: down to 2^-149, where a channel has few bits)
+    x = rng.normal(size=(T, hq + 2 * hk, D))
+    x[0::4] *= 1e-22
+    x[1::4, ::2] *= 2.0 ** -110
+    x[2::4] *= 2.0 ** -124
+    f, pos = oa.frequencies(rot), rng.integers(0, 1000, T)
+    for dtype in (torch.bfloat16, torch.float32):
+        qw, kw = _norms(rng, D)
+        at = pkg.Attention(hq, hk, D, 16, 4, T, 1, 1000, act=pkg.ACT_F32, rot_dim=rot, interleaved=interleaved, q_norm=qw, k_norm=kw, eps=0.0)
+        t = torch.tensor(x, device="cuda").to(dtype)
+        q, k, v = t.split([hq, hk, hk], 1)
+        slots, pages = _slots(rng, 4, 16, T), at.pages()
+        out = at.append(q, k, v, torch.tensor(pos.astype(np.int32), device="cuda"), slots, pages)
+        at.status()
+        want = oa.prepared(_np(q), _np(qw), pos, rot, f, interleaved, eps=0.0)
+        m = np.abs(oa.prepared(_np(q), _np(qw), pos, 0, f, eps=0.0))
+        if rot:
+            i, j = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+            s = m[..., i] + m[..., j]
+            m[..., i], m[..., j] = s, s
+        assert (np.abs(_np(out) - want) <= 2.0 ** -19 * m + 2.0 ** -24 * np.abs(want)).all()
+        keys = at.read(slots, pages)[0]
+        want = oa.dequantise(*oa.quantise(oa.prepared(_np(k), _np(kw), pos, rot, f, interleaved, eps=0.0)))
+        assert np.array_equal(_np(keys), want)
+        at.close()
+
+
+def test_append_norm_of_rows_with_nothing_or_infinities():
+    """A zero row without eps is 0/0: NaN, stored as 0; an infinite channel makes NaN of itself and 0 of the others."""
+    hq, hk, D = 2, 1, 64
+    one = torch.ones(D, device="cuda")
+    at = pkg.Attention(hq, hk, D, 16, 1, 3, 1, 4, rot_dim=0, q_norm=one, k_norm=one, eps=0.0)
+    x = torch.randn(3, hq + 2 * hk, D, device="cuda").to(torch.bfloat16)
+    x[0] = 0
+    x[1, :, 5] = float("inf")
+    pages, slots = at.pages(), torch.arange(3, device="cuda")
+    out = at.append(x[:, :2], x[:, 2:3], x[:, 3:], slots.int(), slots, pages)
+    assert torch.isnan(out[0]).all() and torch.isnan(out[1, :, 5]).all() and torch.isfinite(out[2]).all()
+    assert (out[1][:, [i for i in range(D) if i != 5]] == 0).all()
+    keys = at.read(slots, pages)[0]
+    assert (keys[:2] == 0).all() and (keys[2] != 0).any()
