@@ -145,6 +145,17 @@ def _raw_stream(stream, t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _result(shape, dtype, device, stream):
+    """An uninitialised tensor in the memory of ``stream`` (None: the current
+    one), which is to write it: another stream's free block may still be in
+    use by what that stream has pending."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def quantized_bytes(fmt, rows, cols):
     return lib().moe_quantized_bytes(fmt, rows, cols)
 
@@ -442,6 +453,8 @@ class Attention:
     (default: all), in pairs (i, i + rot_dim/2) or, ``interleaved``, (2i,
     2i + 1), by ``freq`` (rot_dim/2 numbers) or rope_base^(-2i/rot_dim) a
     token; ``window``: how many tokens a query sees (0: all earlier ones).
+    Every call runs on ``stream`` (default: the current one), and its results
+    are allocated there.
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_tokens, n_pages, T_max, S_max, len_max, act=ACT_BF16,
@@ -524,7 +537,7 @@ class Attention:
                      "append: slots must be contiguous int64 [T] on the GPU")
             self._cache_error("append", pages)
         if q_out is None:
-            q_out = torch.empty((T, self.n_q_heads, D), dtype=self.dtype, device=q.device)
+            q_out = _result((T, self.n_q_heads, D), self.dtype, q.device, stream)
         else:
             _require(q_out.shape == q.shape and q_out.dtype is self.dtype and q_out.is_cuda and q_out.is_contiguous(),
                      "append: q_out must be contiguous [T, n_q_heads, head_dim] in the act dtype")
@@ -547,8 +560,8 @@ class Attention:
             self._cache_error("read", pages)
         n = slots.shape[0]
         shape = (n, self.n_kv_heads, self.head_dim)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+        k = _result(shape, torch.bfloat16, slots.device, stream)
+        v = _result(shape, torch.bfloat16, slots.device, stream)
         rc = self._lib.moe_attn_read(self.handle, pages.data_ptr(), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
                                      _raw_stream(stream, slots))
         if rc:
@@ -581,7 +594,7 @@ class Attention:
             _require(max_len <= table.shape[1] * self.page_tokens, "forward: the table holds fewer than max_len tokens")
             self._cache_error("forward", pages)
         if out is None:
-            out = torch.empty((T, self.n_q_heads, D), dtype=self.dtype, device=q.device)
+            out = _result((T, self.n_q_heads, D), self.dtype, q.device, stream)
         else:
             _require(out.shape == q.shape and out.dtype is q.dtype and out.is_cuda and out.is_contiguous(),
                      "forward: out must be contiguous, of q's shape and type")
@@ -629,11 +642,11 @@ def token_logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     if tokens is not None:
         _require(tokens.shape == (n,) and tokens.dtype is i32 and tokens.is_cuda and tokens.is_contiguous(),
                  "token_logprobs: tokens must be contiguous int32 [n] on the GPU")
-        lp = torch.empty(n, dtype=f32, device=dev)
+        lp = _result((n,), f32, dev, stream)
     if entropy:
-        en = torch.empty(n, dtype=f32, device=dev)
-    ids = torch.empty((n, n_top), dtype=i32, device=dev)
-    top = torch.empty((n, n_top), dtype=f32, device=dev)
+        en = _result((n,), f32, dev, stream)
+    ids = _result((n, n_top), i32, dev, stream)
+    top = _result((n, n_top), f32, dev, stream)
     rc = lib().moe_token_logprobs(logits.data_ptr(), ACT_F32 if dt is f32 else ACT_BF16, stride[0], n, V,
                                   None if tokens is None else tokens.data_ptr(), n_top,
                                   None if lp is None else lp.data_ptr(), None if en is None else en.data_ptr(),

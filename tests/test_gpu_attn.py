@@ -709,3 +709,32 @@ def test_append_norm_of_rows_with_nothing_or_infinities():
     assert (out[1][:, [i for i in range(D) if i != 5]] == 0).all()
     keys = at.read(slots, pages)[0]
     assert (keys[:2] == 0).all() and (keys[2] != 0).any()
+
+
+def test_results_of_a_given_stream_belong_to_it():
+    """Results are allocated on the stream that writes them, not on the current
+    one, whose own pending work may still use the memory."""
+    hq, hk, D, P, T = 8, 2, 64, 16, 64
+    at = pkg.Attention(hq, hk, D, P, 8, T, 1, 100, rot_dim=0)
+    x = torch.randn(T, hq + 2 * hk, D, device="cuda").to(torch.bfloat16)
+    q, k, v = x.split([hq, hk, hk], 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pos, slots, pages = torch.arange(T, **i32), torch.arange(T, device="cuda"), at.pages()
+    seq = (torch.tensor([0, T], **i32), torch.tensor([T], **i32), torch.arange(4, **i32)[None], T, T)
+    logits = torch.randn(64, 1000, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    calls = (lambda s: [at.append(q, k, v, pos, slots, pages, stream=s)], lambda s: list(at.read(slots, pages, stream=s)),
+             lambda s: [at.forward(q, pages, *seq, stream=s)],
+             lambda s: list(pkg.token_logprobs(logits, pos, 8, stream=s).values()))
+    for i, call in enumerate(calls):
+        want = call(None)
+        torch.cuda.synchronize()
+        keep = [t.clone() for t in want]
+        torch.cuda.synchronize()
+        freed = {t.data_ptr() for t in want}
+        del want  # blocks of the same sizes, free on the current stream
+        got = call(side)
+        side.synchronize()
+        assert not freed & {t.data_ptr() for t in got}, i
+        assert all(torch.equal(a, b) for a, b in zip(got, keep))
