@@ -33,6 +33,7 @@ using namespace moe;
 namespace {
 
 int cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();  // reported here: the next launch of the process is not to find it
   return set_error(e == cudaErrorMemoryAllocation ? MOE_ENOMEM : MOE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 #define CKA(call, what)                              \

@@ -394,7 +394,10 @@ extern "C" int moe_token_logprobs(const void* logits, int32_t dtype, int64_t row
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return set_error(MOE_ECUDA, "%s: %s", who, cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // reported here: the next launch of the process is not to find it
+    return set_error(MOE_ECUDA, "%s: %s", who, cudaGetErrorString(e));
+  }
   LpParams p{logits, row_stride, n, V, n_top, 1, tokens, logprob, entropy, top_ids, top_logprobs};
   // blocks a row: more while they stay within 5/4 of the multiprocessors and a
   // block keeps 1024 logits (33 rows of 151936 bf16 logits: 15.3, 10.9, 8.7 and
@@ -403,6 +406,9 @@ extern "C" int moe_token_logprobs(const void* logits, int32_t dtype, int64_t row
   while (p.C < kLpMaxCluster && 2LL * n * p.C <= 5LL * sms / 4 && V / (2 * p.C) >= 1024) p.C *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = dtype == MOE_ACT_F32 ? logprob_launch<float>(p, st) : logprob_launch<__nv_bfloat16>(p, st);
-  if (e != cudaSuccess) return set_error(MOE_ECUDA, "%s launch: %s", who, cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return set_error(MOE_ECUDA, "%s launch: %s", who, cudaGetErrorString(e));
+  }
   return MOE_OK;
 }

@@ -738,3 +738,13 @@ def test_results_of_a_given_stream_belong_to_it():
         side.synchronize()
         assert not freed & {t.data_ptr() for t in got}, i
         assert all(torch.equal(a, b) for a, b in zip(got, keep))
+
+
+def test_a_refused_creation_leaves_no_error_behind():
+    """A workspace that no GPU holds is refused with MOE_ENOMEM; what is launched next does not see the error."""
+    with pytest.raises(pkg.MoEError) as e:
+        pkg.Attention(64, 64, 256, 16, 4, 1 << 20, 1, 1 << 27, rot_dim=0)  # (some 9 TB of operand images)
+    assert e.value.code == pkg.MOE_ENOMEM
+    assert int(torch.arange(5, device="cuda").sum()) == 10
+    at = pkg.Attention(4, 2, 64, 16, 4, 4, 1, 64)
+    at.status()
