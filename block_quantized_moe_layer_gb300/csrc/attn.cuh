@@ -75,15 +75,16 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
 // outside the pool; in two steps where the load is to be on its way meanwhile
 // (kNoPage: nothing to look at).
 constexpr int kNoPage = -0x7fffffff;
-__device__ __forceinline__ int page_entry(const AttnParams& p, int b, int i) { return p.table[(int64_t)b * p.table_stride + i]; }
+__device__ __forceinline__ int page_entry(const AttnParams& p, int b, int i) {
+  return max(p.table[(int64_t)b * p.table_stride + i], -1);  // (no entry is kNoPage)
+}
 __device__ __forceinline__ int checked_page(const AttnParams& p, int pg) {
   if (pg >= 0 && pg < p.n_pages) return pg;
   if (pg != kNoPage) atomicOr(p.status, kBadPage);
   return -1;
 }
 __device__ __forceinline__ int load_page(const AttnParams& p, int b, int i) {
-  const int pg = page_entry(p, b, i);
-  return checked_page(p, pg == kNoPage ? -1 : pg);
+  return checked_page(p, page_entry(p, b, i));
 }
 
 // Keys visible to a query at position pos: [key_lo(pos), pos].

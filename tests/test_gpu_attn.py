@@ -748,3 +748,33 @@ def test_a_refused_creation_leaves_no_error_behind():
     assert int(torch.arange(5, device="cuda").sum()) == 10
     at = pkg.Attention(4, 2, 64, 16, 4, 4, 1, 64)
     at.status()
+
+
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("news", [1, 8, 100])  # 4 rows each: the small, the verify and the prompt kernel
+def test_forward_bad_table_entries_mask_their_tokens_in_every_kernel(D, news):
+    rng = np.random.default_rng(24 + D)
+    hq, hk, P, n = 8, 2, 16, 150
+    pages, table, keys, values, n_pages = _cache(rng, [n], hk, D, P, spare=0)
+    at = pkg.Attention(hq, hk, D, P, n_pages, news, 1, n, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(news, hq, D, device="cuda").to(torch.bfloat16)
+    for bad in (-1, n_pages, 1 << 30, -(1 << 31), 1 - (1 << 31), 2 ** 31 - 1):
+        t2 = table.clone()
+        t2[0, 1] = t2[0, 9] = bad  # tokens 16..31 and 144..149
+        lse = torch.empty(news, hq, device="cuda")
+        out = _np(at.forward(q, pages, torch.tensor([0, news], **i32), torch.tensor([n], **i32), t2, news, n, lse=lse))
+        with pytest.raises(pkg.MoEError, match="block-table"):
+            at.status()
+        for t in range(news):
+            pos = n - news + t
+            here = np.array([j for j in range(pos + 1) if j // 16 not in (1, 9)])
+            want, wl, mag = oa.attention(_np(q[t:t + 1]), keys[0][here], values[0][here], 1)
+            assert (np.abs(out[t] - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -9 * mag[0]).all(), (bad, t)
+            assert (np.abs(_np(lse[t]) - wl[0]) <= 2.0 ** -9).all()
+    # every page absent: no key
+    t2 = torch.full_like(table, -1)
+    out = at.forward(q, pages, torch.tensor([0, news], **i32), torch.tensor([n], **i32), t2, news, n, lse=lse)
+    with pytest.raises(pkg.MoEError, match="block-table"):
+        at.status()
+    assert (out == 0).all() and torch.isneginf(lse).all()
