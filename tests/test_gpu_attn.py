@@ -778,3 +778,46 @@ def test_forward_bad_table_entries_mask_their_tokens_in_every_kernel(D, news):
     with pytest.raises(pkg.MoEError, match="block-table"):
         at.status()
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("act", [pkg.ACT_F32, pkg.ACT_BF16])
+@pytest.mark.parametrize("news", [1, 8, 100])
+def test_forward_lengths_and_starts_beyond_the_call_in_every_kernel(news, act):
+    """They are clamped to what the call said, reported, and nothing outside is read or written."""
+    rng = np.random.default_rng(25)
+    hq, hk, D, P, n = 8, 2, 64, 16, 150
+    pages, table, keys, values, n_pages = _cache(rng, [n], hk, D, P, spare=0)
+    at = pkg.Attention(hq, hk, D, P, n_pages, news + 6, 1, n, act=act, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(news + 6, hq, D, device="cuda").to(at.dtype)
+    for starts, length, rows, want_len in (([3, news + 3], 1 << 30, (3, news), n), ([3, news + 3], -5, (3, news), 0),
+                                           ([-2, news], n, (0, news), n), ([5, 2], n, (0, 0), n),
+                                           ([6, 1 << 30], n, (6, news), n), ([1 << 30, 1 << 30], n, (0, 0), n)):
+        out = torch.full_like(q, 7.0)
+        at.forward(q, pages, torch.tensor(starts, **i32), torch.tensor([length], **i32), table, news, n, out=out)
+        with pytest.raises(pkg.MoEError, match="lengths"):
+            at.status()
+        a, t = rows
+        assert (out[:a] == 7).all() and (out[a + t:] == 7).all()
+        if t:
+            want, _, mag = oa.attention(_np(q[a:a + t]), keys[0][:want_len], values[0][:want_len], t) if want_len else (0.0, 0, 0.0)
+            assert (np.abs(_np(out[a:a + t]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag).all(), starts
+
+
+def test_forward_prompts_in_groups_that_share_the_images():
+    """More sequences than the operand images hold at once run group by group, whole and with split row tiles."""
+    rng = np.random.default_rng(26)
+    hq, hk, D, n = 16, 16, 256, 2000
+    tiles = -(-n // 128)
+    assert (256 << 20) // (4 * 128 * D) // (hk * tiles) < 9  # the sequences that go at once
+    _forward_check(rng, hq, hk, D, [2000, 1, 700, 1999, 300, 1300, 0, 257, 2000], [300, 1, 257, 280, 300, 260, 3, 257, 12], 128)
+    # one key/value head: the row tiles of a group do not fill the GPU, so their keys are split
+    _forward_check(rng, 4, 1, 256, [9000] + [200] * 9, [65] + [66] * 9, 64, extra=150_000)
+
+
+@pytest.mark.parametrize("hq,hk,D", [(16, 16, 64), (16, 16, 128)])
+def test_forward_prompt_walks_past_its_ring(hq, hk, D):
+    """Row tiles that go whole, over more key tiles than the ring of images has stages."""
+    rng = np.random.default_rng(27)
+    # 16 heads x 5 row tiles of 256 rows = 80 pairs: 76 whole ones, the others split
+    _forward_check(rng, hq, hk, D, [2500], [1280], 64)
