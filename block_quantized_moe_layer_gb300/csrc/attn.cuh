@@ -72,20 +72,16 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
 }
 
 // The page of the tokens [i P, (i + 1) P) of sequence b, or -1 for an entry
-// outside the pool; in two steps where the load is to be on its way meanwhile
-// (kNoPage: nothing to look at).
-constexpr int kNoPage = -0x7fffffff;
-__device__ __forceinline__ int page_entry(const AttnParams& p, int b, int i) {
-  return max(p.table[(int64_t)b * p.table_stride + i], -1);  // (no entry is kNoPage)
-}
-__device__ __forceinline__ int checked_page(const AttnParams& p, int pg) {
+// outside the pool, which is reported; in two steps where the load is to be on
+// its way meanwhile (its result is not touched before the second one; seen:
+// the entry was loaded, else pg is -1).
+__device__ __forceinline__ int page_entry(const AttnParams& p, int b, int i) { return p.table[(int64_t)b * p.table_stride + i]; }
+__device__ __forceinline__ int checked_page(const AttnParams& p, int pg, bool seen) {
   if (pg >= 0 && pg < p.n_pages) return pg;
-  if (pg != kNoPage) atomicOr(p.status, kBadPage);
+  if (seen) atomicOr(p.status, kBadPage);
   return -1;
 }
-__device__ __forceinline__ int load_page(const AttnParams& p, int b, int i) {
-  return checked_page(p, page_entry(p, b, i));
-}
+__device__ __forceinline__ int load_page(const AttnParams& p, int b, int i) { return checked_page(p, page_entry(p, b, i), true); }
 
 // Keys visible to a query at position pos: [key_lo(pos), pos].
 __device__ __forceinline__ int key_lo(const AttnParams& p, int pos) {

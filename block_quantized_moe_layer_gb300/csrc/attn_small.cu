@@ -104,23 +104,26 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   // Warp 0 issues the copies too (a fifth warp would cost the compute warps a
   // third of their registers): lane i takes page i of a tile.
   const uint64_t pol = l2_evict_first_policy();
-  auto page_of = [&](int i) {  // kNoPage where nothing of the page is seen
-    const int pi = (tile_a + i) * ppt + lane, j0 = pi << p.pshift;
-    return lane < ppt && i < n_tiles && j0 < hi && j0 + p.P > lo ? page_entry(p, b, pi) : kNoPage;
+  auto page_seen = [&](int i) {  // something of this lane's page is seen
+    const int j0 = ((tile_a + i) * ppt + lane) << p.pshift;
+    return lane < ppt && i < n_tiles && j0 < hi && j0 + p.P > lo;
   };
+  auto page_of = [&](int i) { return page_seen(i) ? page_entry(p, b, (tile_a + i) * ppt + lane) : -1; };
   auto issue = [&](int i, int entry) {
-    const int st = i % L::kStages, pg = checked_page(p, entry);
-    const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0);
+    const int st = i % L::kStages;
+    const bool has = entry >= 0 && entry < p.n_pages;
+    const uint32_t mask = __ballot_sync(0xffffffffu, has);
+    if (mask != (1u << ppt) - 1u) checked_page(p, entry, page_seen(i));
     if (lane == 0) {
       pmask[st] = mask;
       mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * head_bytes));
     }
     __syncwarp();
-    if (pg >= 0)
-      bulk_g2s_hint(smem + st * L::kStage + lane * head_bytes, p.pages + pg * p.page_bytes + (int64_t)kvh * head_bytes,
+    if (has)
+      bulk_g2s_hint(smem + st * L::kStage + lane * head_bytes, p.pages + entry * p.page_bytes + (int64_t)kvh * head_bytes,
                     (uint32_t)head_bytes, &full[st], pol);
   };
-  int issued = 0, next_pg = kNoPage;
+  int issued = 0, next_pg = -1;
   if (warp == 0) {
     int pg[L::kStages - 1];
 #pragma unroll

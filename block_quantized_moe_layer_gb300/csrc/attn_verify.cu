@@ -181,13 +181,14 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     // a whole tile ahead, was slower: 24.6 against 23 us at 32765 keys)
     uint4 code[kUnits];
     uint32_t scale[kUnits];
-    int page = kNoPage;
-    auto look_up = [&](int j) {  // (a page that no row here sees is not looked at: it may have been given back)
+    int page = -1;
+    auto page_seen = [&](int j) {  // (a page that no row here sees is not looked at: it may have been given back)
       const int key = (tile_a + j) * KT + kKeys * dw;
-      page = j < n_tiles && key < hi && (key | (p.P - 1)) >= lo ? page_entry(p, b, key >> p.pshift) : kNoPage;
+      return j < n_tiles && key < hi && (key | (p.P - 1)) >= lo;
     };
+    auto look_up = [&](int j) { page = page_seen(j) ? page_entry(p, b, ((tile_a + j) * KT + kKeys * dw) >> p.pshift) : -1; };
     auto fetch = [&](int j) {  // this lane's codes and scales of tile j: 0 for a key past the end or on an absent page
-      const int key = (tile_a + j) * KT + kKeys * dw, at = (key & (p.P - 1)) + kk, pg = checked_page(p, page);
+      const int key = (tile_a + j) * KT + kKeys * dw, at = (key & (p.P - 1)) + kk, pg = checked_page(p, page, page_seen(j));
       const uint8_t* src = p.pages + pg * p.page_bytes + (int64_t)kvh * p.head_bytes + (values ? p.head_bytes / 2 : 0);
       const bool has = pg >= 0 && key + kk < s.len;
       const uint8_t* sc = src + at * (D / 2) + 16 * piece;
