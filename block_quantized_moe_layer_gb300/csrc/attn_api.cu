@@ -170,8 +170,11 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
     const int64_t most_rows = (int64_t)h->T_max * (h->hq / h->hk);
     if (most_rows > kSmallCallRows) CKA(attn::verify_configure(h->D), "configure the verify kernel");
     if (most_rows > verify_call_rows(h->D)) {
-      // dequantised tiles of one longest sequence at least, of more while they stay within 256 MB
-      const int64_t one = (int64_t)h->hk * ((h->len_max + attn::kTileTokens - 1) / attn::kTileTokens);
+      // dequantised tiles of one longest sequence at least (of what its window
+      // and a call's queries reach), of more while they stay within 256 MB
+      int64_t reach = h->len_max;
+      if (h->window > 0) reach = std::min<int64_t>(reach, (int64_t)h->window + h->T_max + 2 * attn::kTileTokens);
+      const int64_t one = h->hk * ((reach + attn::kTileTokens - 1) / attn::kTileTokens);
       const int64_t room = (256LL << 20) / (4LL * attn::kTileTokens * h->D);
       const int64_t cap = one * std::max<int64_t>(1, std::min<int64_t>(h->S_max, room / one));
       if (cap > (1 << 28)) return set_error(MOE_EINVAL, "moe_attn_create: len_max=%d with %d heads is too long", h->len_max, h->hk);

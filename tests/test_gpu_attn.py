@@ -821,3 +821,16 @@ def test_forward_prompt_walks_past_its_ring(hq, hk, D):
     rng = np.random.default_rng(27)
     # 16 heads x 5 row tiles of 256 rows = 80 pairs: 76 whole ones, the others split
     _forward_check(rng, hq, hk, D, [2500], [1280], 64)
+
+
+def test_workspace_of_a_windowed_handle():
+    """A prompt's operand images take what its window and chunk can reach, not the longest sequence."""
+    kw = dict(n_q_heads=16, n_kv_heads=4, head_dim=192, page_tokens=64, n_pages=8, T_max=256, S_max=1, len_max=131072, rot_dim=0)
+    whole = pkg.Attention(**kw).workspace_bytes
+    part = pkg.Attention(**kw, window=512).workspace_bytes
+    tile = 4 * 2 * 128 * 192 * 2  # 128 tokens of all heads
+    assert whole >= 1024 * tile and part <= whole - 1000 * tile
+    # and they hold all that a call needs: chunks of T_max tokens far into a sequence, several sequences
+    rng = np.random.default_rng(28)
+    _forward_check(rng, 8, 2, 64, [3000, 200, 129, 2100], [300, 200, 100, 1], 64, window=100, extra=30_000)
+    _forward_check(rng, 16, 2, 256, [2000, 130], [128, 20], 128, window=1, extra=30_000)
