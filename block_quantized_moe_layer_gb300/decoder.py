@@ -21,7 +21,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import ACT_BF16, Attention, Layer, LmHead, token_logprobs, verify_accept
+from . import ACT_BF16, MOE_EINVAL, Attention, Layer, LmHead, MoEError, token_logprobs, verify_accept
 
 
 def rmsnorm(h, eps=1e-6):
@@ -70,6 +70,10 @@ class Decoder:
         """Appends `tokens` (a host list) to the sequence; the block's output rows."""
         at, dev = self.block.attention, self.embed.device
         P, n, first = at.page_tokens, len(tokens), seq.length
+        if first + n > self.max_len:
+            raise MoEError(MOE_EINVAL, f"{first} + {n} tokens: the longest sequence has {self.max_len}")
+        if first + n > (len(seq.pages) + len(self.free)) * P:
+            raise MoEError(MOE_EINVAL, f"{first} + {n} tokens: {len(self.free)} pages of {P} are left")
         while len(seq.pages) * P < first + n:
             seq.pages.append(self.free.pop())
         pos = torch.arange(first, first + n, dtype=torch.int32)

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_quantized_moe_layer_gb300 import decoder, synth
+from block_quantized_moe_layer_gb300 import MoEError, decoder, synth
 from oracle import accept as oacc
 from oracle import attn as oa
 
@@ -85,3 +85,20 @@ def test_rejected_drafts_leave_no_trace():
     model._run(fresh, [9])
     again = model.verify(fresh, best, [7])["logits"]
     assert torch.allclose(once, again, rtol=0, atol=3 * 2.0 ** -8 * float(once.abs().max()))
+
+
+def test_a_step_that_does_not_fit_is_refused_before_anything_changes():
+    model = _model()
+    seq = model.new_sequence()
+    model.prefill(seq, list(range(100)))
+    pages, free = list(seq.pages), list(model.free)
+    with pytest.raises(MoEError, match="longest"):
+        model._run(seq, [1] * (model.max_len - 100 + 1))
+    assert seq.length == 100 and seq.pages == pages and model.free == free
+    model.free = model.free[:2]
+    with pytest.raises(MoEError, match="pages"):
+        model._run(seq, [1] * 60)
+    assert seq.length == 100 and seq.pages == pages and len(model.free) == 2
+    model._run(seq, [1] * 20)  # what fits still runs
+    assert seq.length == 120
+    model.block.attention.status()
