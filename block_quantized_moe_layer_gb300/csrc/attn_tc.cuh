@@ -41,15 +41,9 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[N]) 
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-  } else if constexpr (N == 16) {
-    tc::st_32x32b_x16(taddr, v);
   } else {
-    static_assert(N == 32, "8, 16 or 32 columns");
-    uint32_t a[16], b[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a[i] = v[i], b[i] = v[16 + i];
-    tc::st_32x32b_x16(taddr, a);
-    tc::st_32x32b_x16(taddr + 16, b);
+    static_assert(N == 16, "8 or 16 columns");
+    tc::st_32x32b_x16(taddr, v);
   }
 }
 
