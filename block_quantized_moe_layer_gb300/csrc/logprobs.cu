@@ -15,6 +15,11 @@
 // their elements are read again (from L2) by whole warps, and those that
 // reach the bound are inserted into a sorted list kept across the lanes.
 // Ties go to the lower token id: the lists order 64-bit keys (value, ~id).
+//   Where many logits are equal (a mask leaves a few, or few values occur) all
+// of them reach the bound.  They are looked at in the order of their ids, and
+// once the list is full only a lower id than its last one's gets in, so a warp
+// inserts a few dozen: 64 rows of 151936 fp32, top 20, take 22 us, with 3
+// logits left of each 42, all equal 17 (offered one by one: 940).
 //
 // Rows are read with 16-byte loads, four in flight a thread, and bound by HBM;
 // where there are few rows a cluster of up to 8 blocks shares one and joins
@@ -244,11 +249,28 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     }
     if (tid == 0) bound = tmax[0][p.n_top - 1];
     __syncthreads();
+    // A candidate is above thr, or equal to it with an id below tie.  Both follow
+    // the n_top-th of this warp's list once there is one: of many equal logits
+    // (masked ones among them) only those with low enough ids are looked at.
     float thr = bound;
+    int tie = 0x7fffffff;
     uint64_t best = 0;  // lane r: the r-th best key of this warp so far, 0 for none
-    // candidates: bit e of a lane's mask stands for its v[e], of id + e
+    int found = 0;      // keys that were put into it
+    auto fits = [&](const float (&v)[N], int id, uint32_t mask) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) m |= v[e] >= thr ? 1u << e : 0u;
+      if (found >= p.n_top) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) m &= v[e] == thr && id + e >= tie ? ~(1u << e) : ~0u;
+      }
+      return m & mask;
+    };
+    // the elements of `mask`: bit e of a lane's stands for its v[e], of id + e
     auto offer = [&](const float (&v)[N], int id, uint32_t mask) {
-      for (uint32_t set; (set = __ballot_sync(0xffffffffu, mask != 0)) != 0;) {
+      mask = fits(v, id, mask);
+      uint32_t set = __ballot_sync(0xffffffffu, mask != 0);
+      while (set) {
         const int from = __ffs(set) - 1, e = __ffs(mask) - 1;
         float x = v[0];
 #pragma unroll
@@ -258,35 +280,40 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
         const int at = __popc(__ballot_sync(0xffffffffu, best > c));
         const uint64_t up = __shfl_up_sync(0xffffffffu, best, 1);
         best = lane < at ? best : (lane == at ? c : up);
+        set = __ballot_sync(0xffffffffu, mask != 0);
+        if (++found < p.n_top || (set && found % 8)) continue;
+        const uint64_t kth = __shfl_sync(0xffffffffu, best, p.n_top - 1);
+        if (key_value(kth) >= thr) {
+          thr = key_value(kth);
+          tie = (int)~(uint32_t)kth;
+          mask = fits(v, id, mask);
+          set = __ballot_sync(0xffffffffu, mask != 0);
+        }
       }
-      const uint64_t kth = __shfl_sync(0xffffffffu, best, p.n_top - 1);
-      if (kth) thr = fmaxf(thr, key_value(kth));
     };
     // the vectors of the warp's threads that reach the bound, spread over its
-    // lanes: all of them are on their way at once
+    // lanes in the order of their ids
     const bool mine_too = my_max >= thr;
     const uint32_t reach = __ballot_sync(0xffffffffu, mine_too);
+    const float most = warp_max(my_max);
     if (mine_too) reachers[warp][__popc(reach & ((1u << lane) - 1))] = lane;
     __syncwarp();
     if (reach) {  // (the same in all lanes)
       float v[N] = {};
       if (has_head) v[0] = Vec<In>::one(x + tid);
-      offer(v, tid, has_head && mine_too && v[0] >= thr ? 1u : 0u);
+      offer(v, tid, has_head && mine_too ? 1u : 0u);
       if (has_tail) v[0] = Vec<In>::one(x + tail0 + tid);
-      offer(v, tail0 + tid, has_tail && mine_too && v[0] >= thr ? 1u : 0u);
+      offer(v, tail0 + tid, has_tail && mine_too ? 1u : 0u);
     }
-    const int n_u = (v1 - v0 + kLpThreads - 1) / kLpThreads, items = __popc(reach) * n_u;
+    const int n_r = max(__popc(reach), 1), items = __popc(reach) * ((v1 - v0 + kLpThreads - 1) / kLpThreads);
+    auto vector_of = [&](int i) { return v0 + warp * 32 + reachers[warp][i % n_r] + i / n_r * kLpThreads; };
     for (int i0 = 0; i0 < items; i0 += 32) {
-      const int i = i0 + lane, r = i / max(n_u, 1);
-      const int u = i < items ? v0 + warp * 32 + reachers[warp][r] + (i - r * n_u) * kLpThreads : v1;
+      // (equal logits alone, and their ids too high: nothing of what is left fits)
+      if (most <= thr && head + vector_of(i0) * N >= tie) break;
+      const int i = i0 + lane, u = i < items ? vector_of(i) : v1;
       float v[N] = {};
-      uint32_t mask = 0;
-      if (u < v1) {
-        Vec<In>::load(xv + (int64_t)u * N, v);
-#pragma unroll
-        for (int e = 0; e < N; ++e) mask |= v[e] >= thr ? 1u << e : 0u;
-      }
-      offer(v, head + u * N, mask);
+      if (u < v1) Vec<In>::load(xv + (int64_t)u * N, v);
+      offer(v, head + u * N, u < v1 ? (1u << N) - 1u : 0u);
     }
     lists[warp][lane] = best;
     __syncthreads();

@@ -123,3 +123,48 @@ def test_optional_outputs_streams_and_refusals():
               lambda: pkg.token_logprobs(x.cpu(), tok)):
         with pytest.raises(pkg.MoEError):
             f()
+
+
+def _time_us(x, n_top):
+    for _ in range(3):
+        pkg.token_logprobs(x, None, n_top)
+    e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    torch.cuda.synchronize()
+    e[0].record()
+    for _ in range(10):
+        pkg.token_logprobs(x, None, n_top)
+    e[1].record()
+    e[1].synchronize()
+    return e[0].elapsed_time(e[1]) * 100
+
+
+@pytest.mark.parametrize("n,V", [(64, 151_936), (2, 151_936), (300, 32_768)])
+def test_masked_and_equal_logits_cost_no_more_than_twice_ordinary_rows(n, V):
+    """Rows with few logits left, or of few different values: every element
+    ties with the bound of the best, but few can be among them."""
+    x = torch.randn(n, V, device="cuda")
+    usual = _time_us(x, 20)
+    few = torch.full((n, V), float("-inf"), device="cuda")
+    few[:, torch.randint(V, (3,)).tolist()] = 1.0
+    part = x.clone()
+    part[:, V // 3:] = float("-inf")
+    for y in (few, part, torch.zeros(n, V, device="cuda"), x.round(), few.to(torch.bfloat16)):
+        us = _time_us(y, 20)
+        assert us <= 2 * usual + 20, (us, usual)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,V", [(1, 151_936), (3, 40_000), (200, 3001), (2, 33)])
+def test_masked_and_equal_logits_in_any_place(n, V, dtype):
+    rng = np.random.default_rng(V)
+    for left in (0, 1, 3, 19, 40):
+        x = torch.full((n, V), float("-inf"))
+        for i in range(n):
+            at = rng.choice(V, min(left, V), replace=False)
+            x[i, at] = torch.tensor(rng.integers(-2, 3, len(at)).astype(np.float32))
+        _check(x.to(dtype), rng.integers(0, V, n).tolist(), min(V, 20))
+    stretch = torch.full((n, V), float("-inf"))
+    stretch[:, V // 2:V // 2 + 25] = torch.randn(n, min(25, V - V // 2))
+    _check(stretch.to(dtype), [V // 2] * n, min(V, 32))
+    _check(torch.full((n, V), 2.0).to(dtype), [0] * n, min(V, 32))
+    _check((torch.randn(n, V) * 0.6).round().to(dtype), [1] * n, min(V, 32))
