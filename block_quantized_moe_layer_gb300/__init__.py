@@ -26,7 +26,7 @@ EXPORTS = (
     "moe_layer_timeline", "moe_layer_inject_timeout", "moe_lm_head_status", "moe_forward_f32",
     "mtp_round_hidden", "moe_forward_resnorm", "moe_attn_page_bytes", "moe_attn_create", "moe_attn_append",
     "moe_attn_read", "moe_attn_forward", "moe_attn_status", "moe_attn_workspace_bytes", "moe_attn_destroy",
-    "moe_token_logprobs",
+    "moe_token_logprobs", "moe_attn_inject_timeout",
 )
 
 # event names of moe_layer_timeline, in order
@@ -107,6 +107,7 @@ def lib():
             "moe_attn_read": (_c.c_int, [vp, vp, vp, i32, vp, vp, vp]),
             "moe_attn_forward": (_c.c_int, [vp, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
             "moe_attn_status": (_c.c_int, [vp, vp]),
+            "moe_attn_inject_timeout": (_c.c_int, [vp, i32]),
             "moe_attn_workspace_bytes": (sz, [vp]),
             "moe_attn_destroy": (None, [vp]),
             "moe_token_logprobs": (_c.c_int, [vp, i32, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
@@ -613,6 +614,10 @@ class Attention:
         """Raises MoEError if an earlier call met a slot, position, table
         entry or length out of range, or a bounded wait gave up."""
         _check(lib().moe_attn_status(self.handle, _stream(stream)))
+
+    def inject_timeout(self, wait_limit_us=1000):
+        """Test hook: the next forward's waits run out (``moe_attn_inject_timeout``)."""
+        _check(lib().moe_attn_inject_timeout(self.handle, wait_limit_us))
 
     def close(self):
         if getattr(self, "handle", None):

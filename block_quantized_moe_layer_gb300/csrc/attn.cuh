@@ -53,6 +53,7 @@ struct AttnParams {
   float2* part_ml;     // [tile][split][rows]: running maximum (log2 units) and sum
   int* status;
   uint64_t timeout_ns;
+  int miss;            // 1 under moe_attn_inject_timeout: an arrival that the barriers of the first operands wait for in vain
 };
 
 // One sequence of the call, clamped to what the call said (a value outside is
@@ -103,6 +104,7 @@ struct moe_attn {
   int hq = 0, hk = 0, D = 0, P = 0, n_pages = 0, rot = 0, interleaved = 0, window = 0, act = 0;
   int T_max = 0, S_max = 0, len_max = 0;
   float eps = 0.f, scale = 0.f;
+  int inject_us = 0;           // one-shot wait-timeout test hook (moe_attn_inject_timeout)
   float* rope = nullptr;       // [2: rounded, rest][len_max][2: cos, sin][rot/2]
   double* freq = nullptr;      // [rot/2]
   float* norm_w = nullptr;     // [2][D]: query and key weights (ones where there are none)

@@ -267,6 +267,11 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
     CKA(attn::check_launch(p, st), "moe_attn_forward launch (fp32)");
     return MOE_OK;
   }
+  if (h->inject_us > 0) {  // one launch
+    p.timeout_ns = 1000ull * h->inject_us;
+    p.miss = 1;
+    h->inject_us = 0;
+  }
   p.part_o = reinterpret_cast<float*>(h->ws);
   p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
   const int64_t rows = (int64_t)max_q * p.g;
@@ -293,6 +298,15 @@ int moe_attn_status(moe_attn* h, void* stream) {
                    w[0] & attn::kBadPosition ? " a position outside 0..len_max-1;" : "",
                    w[0] & attn::kBadPage ? " a block-table entry outside the pages;" : "",
                    w[0] & attn::kBadLength ? " lengths or query starts outside the call's T, max_q or max_len;" : "");
+}
+
+int moe_attn_inject_timeout(moe_attn* h, int32_t wait_limit_us) {
+  if (!h) return set_error(MOE_EINVAL, "moe_attn_inject_timeout: NULL handle");
+  if (h->act == MOE_ACT_F32) return set_error(MOE_EINVAL, "moe_attn_inject_timeout: the fp32 kernel has no waits");
+  if (wait_limit_us < 1 || wait_limit_us > 1000000)
+    return set_error(MOE_EINVAL, "moe_attn_inject_timeout: wait_limit_us=%d outside 1..10^6", wait_limit_us);
+  h->inject_us = wait_limit_us;
+  return MOE_OK;
 }
 
 size_t moe_attn_workspace_bytes(const moe_attn* h) { return h ? h->ws_bytes : 0; }

@@ -357,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2 * kMaxRing; ++i) {
-      mbar_init(&full[i], first_block ? 2 : 1);  // (the first block's: its own copy, and word of the other's)
+      mbar_init(&full[i], (first_block ? 2 : 1) + p.miss);  // (the first block's: its own copy, and word of the other's)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {

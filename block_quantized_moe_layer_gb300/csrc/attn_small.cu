@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   griddep_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + p.miss);
       mbar_init(&empty[s], kSmallWarps);
     }
     *abort = 0;

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kfull[i], 8);
+      mbar_init(&kfull[i], 8 + p.miss);
       mbar_init(&sfull[i], 1);
       mbar_init(&pvfull[i], 16);
       mbar_init(&odone[i], 1);

@@ -477,6 +477,13 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
  * where a bounded device-side wait gave up, MOE_OK otherwise.  The word is
  * then cleared. */
 int moe_attn_status(moe_attn* h, void* stream);
+
+/* Test hook: the handle's next (bf16) moe_attn_forward waits for keys that
+ * never count as arrived.  Its waits run out after wait_limit_us (1..10^6),
+ * copies and MMAs in flight are drained, and moe_attn_status then returns
+ * MOE_ETIMEOUT.  The output of that call is undefined, later calls are
+ * unaffected. */
+int moe_attn_inject_timeout(moe_attn* h, int32_t wait_limit_us);
 size_t moe_attn_workspace_bytes(const moe_attn* h);
 void moe_attn_destroy(moe_attn* h);
 

@@ -40,3 +40,8 @@ def test_attention_entry_points_reject_bad_arguments_on_host(lib):
         dtype, stride, n, V, top = args
         assert lib.moe_token_logprobs(None, dtype, stride, n, V, None, top, None, None, None, None, None) == pkg.MOE_EINVAL
     assert lib.moe_token_logprobs(None, 1, 10, 0, 10, None, 0, None, None, None, None, None) == pkg.MOE_OK
+
+
+def test_timeout_hook_rejects_a_missing_handle(lib):
+    assert lib.moe_attn_inject_timeout(None, 1000) == pkg.MOE_EINVAL
+    assert b"moe_attn_inject_timeout" in lib.moe_last_error()

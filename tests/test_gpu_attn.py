@@ -834,3 +834,31 @@ def test_workspace_of_a_windowed_handle():
     rng = np.random.default_rng(28)
     _forward_check(rng, 8, 2, 64, [3000, 200, 129, 2100], [300, 200, 100, 1], 64, window=100, extra=30_000)
     _forward_check(rng, 16, 2, 256, [2000, 130], [128, 20], 128, window=1, extra=30_000)
+
+
+@pytest.mark.parametrize("news", [1, 4, 70])  # 16 rows each: the small, the verify and the prompt kernel
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_forward_waits_run_out_and_the_handle_recovers(D, news):
+    """An operand that never arrives ends the launch with MOE_ETIMEOUT; the next one is as before."""
+    import time
+    rng = np.random.default_rng(29)
+    hq, hk, P, lens = 16, 1, 64, [4000, 130]
+    pages, table, keys, values, n_pages = _cache(rng, lens, hk, D, P)
+    at = pkg.Attention(hq, hk, D, P, n_pages, 2 * news, 2, 4000, rot_dim=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(2 * news, hq, D, device="cuda").to(torch.bfloat16)
+    args = (q, pages, torch.tensor([0, news, 2 * news], **i32), torch.tensor(lens, **i32), table, news, 4000)
+    want = at.forward(*args)
+    at.status()
+    at.inject_timeout(1000)
+    t0 = time.perf_counter()
+    at.forward(*args)
+    with pytest.raises(pkg.MoEError, match="timed out") as e:
+        at.status()
+    assert e.value.code == pkg.MOE_ETIMEOUT and time.perf_counter() - t0 < 5
+    at.status()  # cleared
+    for _ in range(2):
+        assert torch.equal(at.forward(*args), want)
+        at.status()
+    with pytest.raises(pkg.MoEError):
+        at.inject_timeout(0)
