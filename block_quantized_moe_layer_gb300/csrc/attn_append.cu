@@ -20,16 +20,21 @@
 // fp64: far positions lose nothing).
 //
 // Codes are those of the exact result.  fp32 leaves each y' within
-// 2^-19 (|y_a cos| + |y_b sin|) of it (a sum of squares in at most 13
-// additions, its scaling, a reciprocal square root within 2 units, four
-// products and a sum); a row in which that error could change a scale or a
-// code (about one in 500) has just those channels computed again in fp64.
+// 2^-19 (|y_a cos| + |y_b sin|) of it, 32 units of 2^-24: the sum of squares
+// is off by 20 of them (16 products added in turn, 4 shuffles), its mean with
+// eps by 2 more, of which the root halves all; the reciprocal root by 4; the
+// weight's, the row's and the angle's product, the angle itself and the sum by
+// one each: 20.  A row in which that error could change a scale or a code (about
+// one in 500) has just those channels computed again in fp64.
 // Values are exact already: their codes are decided by exact fp32 residuals.
 //
-// Measured: 4096 tokens of 64/4 heads of 192 in 66 us, 3.5 TB/s of 6.8 (issue
-// slots 60% busy, 20 warps a multiprocessor: the chains of a row's sum, its
-// rotation and the search for its scale are what is waited for); 4 tokens in
-// 4.2 us, of which a launch alone is 2.
+// Measured: 4096 tokens of 64/4 heads of 192 in 59.8 us, and read back in 6.6
+// (issue slots 60% busy, 20 warps a multiprocessor: the chains of a row's sum,
+// its rotation and the search for its scale are what is waited for, and at 192
+// channels 4 of a query row's 16 lanes hold none); 4 tokens in 2.7 us, of which
+// a launch is 2, and read back in 1.7.  A row at a border adds its chain of
+// fp64: 128 tokens of 32/8 heads of 128, which nearly always have one, take 5.7
+// us (without norms and rotation, where there is none, 3.1), 4 tokens with one 5.4.
 #include "attn.cuh"
 
 namespace moe {

@@ -28,7 +28,7 @@
 // the output in tensor memory rare; l and O stay consistent with m either way.
 //   TMEM columns: S at 0 and 128, O at 256, P from 256 + D on.
 // Bound: MMA issue and execution; 1024 query tokens of 64/4 heads of 192 behind
-// 7168 keys take 243 us (1.59 PFLOP/s, 0.82 of the cuBLAS rate measured): the
+// 7168 keys take 243 to 247 us (1.59 PFLOP/s, 0.82 of the cuBLAS rate measured): the
 // tensor pipe is active 77% of prompt_kernel; the rest are the blocks' starts
 // and ends (some 12000 cycles of 120000) and the last wave.
 //

@@ -25,9 +25,11 @@
 // memory first (another 54 KB) and single images, whatever the order of the
 // roles; values transposed by hand into cores 144 bytes apart made O += P V
 // 1850 instead of 800.  Now 4 tokens of 64/4 heads of 192 over 32765 keys take
-// 21.5 us with the join (6.7 times the MMAs' time at their peak rate, 5.1 times
-// the cache's): 7 tiles a block, some 3300 cycles each, and its start, end and
-// join; the tensor pipe is active 26%; the warps wait for page loads, then for each other.
+// 21.7 us with the join where L2 holds the cache (28 MB; 6.7 times the MMAs'
+// time at their peak rate, 5.1 times the cache's from HBM), 26.3 where it does
+// not: 7 tiles a block, some 3300 cycles each, about half of it, and its start,
+// end and join; the tensor pipe is active 26%; the warps wait for page loads,
+// then for each other.
 #include "attn_tc.cuh"
 
 namespace moe {

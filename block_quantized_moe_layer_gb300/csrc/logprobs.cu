@@ -27,7 +27,7 @@
 // Measured: 1023 rows of 32768 fp32 in 28.4 us, 4.7 TB/s of 6.8 (a row is a
 // block of 256 threads, so its join and its best tokens are not covered by its
 // own loads, only by the other blocks'); 33 rows of 151936 bf16, top 20, in
-// 12.5 us; 4 rows of 32768 in 7.3 us.
+// 12.8 us; 4 rows of 32768 in 7.4 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -394,7 +394,7 @@ typedef struct {
   int32_t n_pages;     /* pages in the caller's buffer */
   int32_t rot_dim;     /* channels rotated (the first ones): 0..head_dim, multiple of 16 */
   int32_t interleaved; /* rotated pairs: 0 = (i, i + rot_dim/2), 1 = (2i, 2i + 1) */
-  int32_t window;      /* 0 = all earlier tokens, else each query sees its last `window` tokens (itself among them) */
+  int32_t window;      /* each query sees its last `window` tokens (itself among them); 0, or len_max and more: all */
   int32_t act_dtype;   /* moe_act: type of queries and outputs of moe_attn_forward and of moe_attn_append's q_out.
                           MOE_ACT_F32 is the check mode: fp32 throughout, slower */
   int32_t T_max;       /* most query tokens of a call, 1..2^20 */
@@ -435,7 +435,8 @@ int moe_attn_create(const moe_attn_desc* desc, void* stream, moe_attn** out);
  * stores nothing (padding).  A slot beyond the pages, or a position outside
  * 0..len_max-1, stores nothing and is reported by moe_attn_status; the
  * queries of such a position are 0.  Tokens of one call with the same slot
- * leave either's rows there.  Asynchronous, no allocation. */
+ * leave a mixture of their rows there (valid codes and scales, of either).
+ * Asynchronous, no allocation. */
 int moe_attn_append(moe_attn* h, const void* q, const void* k, const void* v, int32_t in_dtype, const int64_t* strides,
                     const int32_t* positions, const int64_t* slots, int32_t T, void* pages, void* q_out, void* stream);
 
@@ -466,6 +467,8 @@ int moe_attn_read(moe_attn* h, const void* pages, const int64_t* slots, int32_t 
  * Pages' contents past lens[b] are not used, whatever they hold.
  *   bf16: scores from exact products in fp32; the softmax's weights are
  * rounded to fp16 for their product with the values, sums are fp32.
+ *   Nothing is launched where T, n_seqs or max_q is 0.  table may be NULL where
+ * max_len is 0.
  *   Calls on one handle must not run concurrently (they share its
  * workspace).  Asynchronous, no allocation. */
 int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
@@ -491,9 +494,9 @@ void moe_attn_destroy(moe_attn* h);
  *   logprob[i] = log softmax(row i)[tokens[i]], entropy[i] = -sum p ln p,
  *   top_ids / top_logprobs [n][n_top]: the n_top most probable tokens,
  *   descending, ties to the lower id.
- * fp32 outputs, natural logarithms.  0 <= n_top <= min(32, V); logprob and
- * entropy may be NULL (tokens too, without logprob).  A token outside
- * 0..V-1 has logprob NaN.  Logits of -inf have probability 0; a row without
+ * fp32 sums and outputs, natural logarithms.  0 <= n_top <= min(32, V);
+ * logprob and entropy may be NULL (tokens too, without logprob).  A token
+ * outside 0..V-1 has logprob NaN.  Logits of -inf have probability 0; a row without
  * any logit above -inf has entropy 0 and log probabilities -inf.  A NaN or
  * +inf logit makes the row's sums NaN; NaN logits are never among the top
  * (missing ids are -1).  Asynchronous, no allocation, no workspace. */
