@@ -23,7 +23,8 @@ its children are tried in order, r = p at first.  Drafts drawn from q without
 replacement: child x is accepted if u < r(x) / q(x), else r = (r - q)+ and q
 loses x, both normalised again.  Drafts chosen without chance: accepted if
 u < r(x), else r loses x.  Where no child is left the next token is drawn: the
-first whose cumulative r passes the root's number.
+first whose cumulative r passes the root's number.  At a temperature of 0 drafts
+count as chosen: the child that is the largest logit's token is accepted.
 
 The cache.  A page holds P tokens.  For each key/value head it holds four
 arrays in turn: key codes [P][D/2], key scales [P][D/16], value codes and value
@@ -400,14 +401,13 @@ def _verify(s):
             x = tokens[b, c][:, None]
             total = r.sum(1, keepdim=True)
             mine = r.gather(1, x)
+            wins = uniforms[b, c][:, None] * total < mine
+            rest = r.scatter(1, x, 0.0)
             if drawn:
                 qx = q.gather(1, x)
-                wins = uniforms[b, c][:, None] * total * qx < mine * left
-                rest = (r - q * (total / left)).clamp(min=0)
-                left = torch.where((tries[:, None]) & ~wins, left - qx, left)
-            else:
-                wins = uniforms[b, c][:, None] * total < mine
-                rest = r.scatter(1, x, 0.0)
+                wins = torch.where(greedy, wins, uniforms[b, c][:, None] * total * qx < mine * left)
+                rest = torch.where(greedy, rest, (r - q * (total / left)).clamp(min=0))
+                left = torch.where(tries[:, None] & ~wins, left - qx, left)
             wins = wins[:, 0] & tries
             r = torch.where((tries & ~wins)[:, None], rest, r)
             if level + 1 < m:
@@ -513,7 +513,7 @@ def _exact_verify(s):
         line, at = [0], 0
         while at is not None:
             r = softmax(s["logits"][a + at])
-            q = softmax(s["draft_logits"][a + at]) if "draft_logits" in s else None
+            q = softmax(s["draft_logits"][a + at]) if "draft_logits" in s and temperature[b] > 0 else None
             here, at = at, None
             for c in range(here + 1, e - a):
                 if parents[c] != here:
@@ -529,7 +529,8 @@ def _exact_verify(s):
                     r = (r - q).clamp(min=0)
                     q[x] = 0
                     q = q / q.sum()
-                r = r / r.sum()
+                if float(r.sum()) > 0:
+                    r = r / r.sum()
         mass = r.cumsum(0)
         nexts.append(int(torch.searchsorted(mass, uniforms[a] * mass[-1:], right=True)[0].clamp(max=len(r) - 1)))
         paths.append(line + [-1] * (s["max_nodes"] - len(line)))
