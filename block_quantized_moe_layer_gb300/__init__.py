@@ -27,6 +27,7 @@ EXPORTS = (
     "mtp_round_hidden", "moe_forward_resnorm", "moe_attn_page_bytes", "moe_attn_create", "moe_attn_append",
     "moe_attn_read", "moe_attn_forward", "moe_attn_status", "moe_attn_workspace_bytes", "moe_attn_destroy",
     "moe_token_logprobs", "moe_attn_inject_timeout",
+    "moe_attn_forward_tree", "moe_attn_commit", "mtp_verify_sample",
 )
 
 # event names of moe_layer_timeline, in order
@@ -106,6 +107,10 @@ def lib():
             "moe_attn_append": (_c.c_int, [vp, vp, vp, vp, i32, _c.POINTER(i64), vp, vp, i32, vp, vp, vp]),
             "moe_attn_read": (_c.c_int, [vp, vp, vp, i32, vp, vp, vp]),
             "moe_attn_forward": (_c.c_int, [vp, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
+            "moe_attn_forward_tree": (_c.c_int, [vp, vp, i64, i64, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp, vp]),
+            "moe_attn_commit": (_c.c_int, [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp]),
+            "mtp_verify_sample": (_c.c_int, [vp, i32, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, vp,
+                                             vp]),
             "moe_attn_status": (_c.c_int, [vp, vp]),
             "moe_attn_inject_timeout": (_c.c_int, [vp, i32]),
             "moe_attn_workspace_bytes": (sz, [vp]),
@@ -343,6 +348,62 @@ def verify_accept_noalloc(draft_ids, logits, out=None, stream=None):
     return out
 
 
+def verify_sample(logits, tokens, parents, starts, uniforms, max_nodes, draft_logits=None, temperature=None,
+                  replacement=False, stream=None):
+    """Verification of trees of drafted tokens against the target's
+    probabilities, and the draw of each sequence's next token
+    (``mtp_verify_sample``; the rule is in ``moe_layer.h``).
+
+    logits [N, V] fp32 or bf16 (rows contiguous): row i is the distribution
+    after node i.  Sequence b's nodes are starts[b]..starts[b+1]-1 (int32), its
+    root, the last certain token, first; tokens int32 [N]; parents int32 [N]:
+    indices within the sequence, or None for chains; uniforms fp32 [N] in
+    [0, 1): a draft's decides about it, the root's draws the next token.
+    ``draft_logits`` (logits' shape and type): the distributions that the
+    drafts were drawn from, without replacement among a node's children, or
+    with ``replacement`` independently; None: drafts chosen without chance.
+    ``temperature`` fp32 [sequences] (0: the largest logit), or None for 1.
+    Returns a dict of device tensors: path int32 [sequences, max_nodes] (the
+    root and the accepted nodes, -1 behind), n_accepted and next, int32
+    [sequences].  max_nodes (a host integer, at most 64) bounds a sequence's
+    nodes."""
+    import torch
+    f32, i32, dt = torch.float32, torch.int32, logits.dtype
+    _require(logits.dim() == 2 and logits.is_cuda and (dt is f32 or dt is torch.bfloat16),
+             "verify_sample: logits must be fp32 or bf16 [N, V] on the GPU")
+    N, V = logits.shape
+    stride, dev = logits.stride(), logits.device
+    _require(stride[1] == 1 or V == 1, "verify_sample: each row of logits must be contiguous")
+    dstride = (0, 1)
+    if draft_logits is not None:
+        dstride = draft_logits.stride()
+        _require(draft_logits.shape == (N, V) and draft_logits.dtype is dt and draft_logits.is_cuda
+                 and (dstride[1] == 1 or V == 1), "verify_sample: draft_logits must have logits' shape and type")
+    for name, t, want, n in (("tokens", tokens, i32, N), ("parents", parents, i32, N), ("uniforms", uniforms, f32, N)):
+        _require((t is None and name == "parents")
+                 or (t.shape == (n,) and t.dtype is want and t.is_cuda and t.is_contiguous()),
+                 f"verify_sample: {name} must be contiguous {want} [N] on the GPU")
+    _require(starts.dim() == 1 and starts.shape[0] >= 1 and starts.dtype is i32 and starts.is_cuda and starts.is_contiguous(),
+             "verify_sample: starts must be contiguous int32 [sequences + 1] on the GPU")
+    n = starts.shape[0] - 1
+    _require(temperature is None or (temperature.shape == (n,) and temperature.dtype is f32 and temperature.is_cuda
+                                     and temperature.is_contiguous()),
+             "verify_sample: temperature must be contiguous fp32 [sequences] on the GPU")
+    _require(1 <= max_nodes <= 64, "verify_sample: max_nodes outside 1..64")
+    path = _result((n, max_nodes), i32, dev, stream)
+    acc = _result((n,), i32, dev, stream)
+    nxt = _result((n,), i32, dev, stream)
+    rc = lib().mtp_verify_sample(
+        logits.data_ptr(), ACT_F32 if dt is f32 else ACT_BF16, stride[0],
+        None if draft_logits is None else draft_logits.data_ptr(), dstride[0], V, tokens.data_ptr(),
+        None if parents is None else parents.data_ptr(), starts.data_ptr(), n, N, max_nodes, uniforms.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), int(replacement), path.data_ptr(), acc.data_ptr(),
+        nxt.data_ptr(), _raw_stream(stream, logits))
+    if rc:
+        _check(rc)
+    return dict(path=path, n_accepted=acc, next=nxt)
+
+
 class LmHead:
     """Output norm + Q8_0 LM head [V, H] on the current CUDA device; ``w`` is
     the serialised Q8_0 byte tensor (host or device)."""
@@ -569,12 +630,17 @@ class Attention:
             _check(rc)
         return k, v
 
-    def forward(self, q, pages, starts, lens, table, max_q, max_len, out=None, lse=None, stream=None):
+    def forward(self, q, pages, starts, lens, table, max_q, max_len, out=None, lse=None, stream=None, parents=None):
         """Causal attention of each sequence's last tokens over the cache
         (``moe_attn_forward``): q [T, n_q_heads, head_dim] in the act dtype,
         sequence b's query tokens starts[b]..starts[b+1]-1, its cached tokens
         lens[b] in the pages table[b].  max_q and max_len (host integers) bound
-        the query tokens and lengths.  ``lse``: optional fp32 [T, n_q_heads]."""
+        the query tokens and lengths.  ``lse``: optional fp32 [T, n_q_heads].
+
+        ``parents`` (int32 [T]): a sequence's query tokens are the nodes of a
+        tree, at most 64, each behind its parent (an index within the sequence;
+        -1: behind the tokens before the tree), and see their own line alone
+        (``moe_attn_forward_tree``)."""
         import torch
         i32, D = torch.int32, self.head_dim
         qs, ts = q.stride(), table.stride()
@@ -602,13 +668,58 @@ class Attention:
         if lse is not None:
             _require(lse.shape == (T, self.n_q_heads) and lse.dtype is torch.float32 and lse.is_cuda
                      and lse.is_contiguous(), "forward: lse must be contiguous fp32 [T, n_q_heads] on the GPU")
-        rc = self._lib.moe_attn_forward(
-            self.handle, q.data_ptr(), qs[0], qs[1], pages.data_ptr(), starts.data_ptr(), lens.data_ptr(),
-            table.data_ptr(), ts[0] if n > 1 else table.shape[1], n, T, max_q, max_len, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), _raw_stream(stream, q))
+        if parents is None:
+            rc = self._lib.moe_attn_forward(
+                self.handle, q.data_ptr(), qs[0], qs[1], pages.data_ptr(), starts.data_ptr(), lens.data_ptr(),
+                table.data_ptr(), ts[0] if n > 1 else table.shape[1], n, T, max_q, max_len, out.data_ptr(),
+                None if lse is None else lse.data_ptr(), _raw_stream(stream, q))
+        else:
+            _require(parents.shape == (T,) and parents.dtype is i32 and parents.is_cuda and parents.is_contiguous(),
+                     "forward: parents must be contiguous int32 [T] on the GPU")
+            rc = self._lib.moe_attn_forward_tree(
+                self.handle, q.data_ptr(), qs[0], qs[1], pages.data_ptr(), starts.data_ptr(), lens.data_ptr(),
+                table.data_ptr(), ts[0] if n > 1 else table.shape[1], parents.data_ptr(), n, T, max_q, max_len,
+                out.data_ptr(), None if lse is None else lse.data_ptr(), _raw_stream(stream, q))
         if rc:
             _check(rc)
         return out
+
+    def commit(self, pages, starts, lens, table, path, max_len, new_lens=None, stream=None):
+        """Keeps the accepted nodes ``path`` (int32 [sequences, width], node
+        indices, -1 behind; :func:`verify_sample`'s) of the trees that
+        ``forward`` saw with these starts, lens and table: their cache rows
+        move behind the tokens before the tree (``moe_attn_commit``).  Returns
+        the new lengths, int32 [sequences]; call it for each layer's pages."""
+        import torch
+        i32 = torch.int32
+        n, ts = table.shape[0], table.stride()
+        if not (len(ts) == 2 and ts[1] == 1 and table.dtype is i32 and table.is_cuda
+                and starts.shape == (n + 1,) and starts.dtype is i32 and starts.is_cuda and starts.is_contiguous()
+                and lens.shape == (n,) and lens.dtype is i32 and lens.is_cuda and lens.is_contiguous()
+                and path.dim() == 2 and path.shape[0] == n and path.dtype is i32 and path.is_cuda and path.is_contiguous()
+                and max_len <= table.shape[1] * self.page_tokens and self._cache_ok(pages)):
+            _require(table.dim() == 2 and table.dtype is i32 and table.is_cuda and ts[1] == 1,
+                     "commit: table must be int32 [sequences, pages] on the GPU")
+            _require(starts.dtype is i32 and starts.is_cuda and starts.is_contiguous() and starts.shape == (n + 1,),
+                     "commit: starts must be contiguous int32 [sequences + 1] on the GPU")
+            _require(lens.dtype is i32 and lens.is_cuda and lens.is_contiguous() and lens.shape == (n,),
+                     "commit: lens must be contiguous int32 [sequences] on the GPU")
+            _require(path.dim() == 2 and path.shape[0] == n and path.dtype is i32 and path.is_cuda and path.is_contiguous(),
+                     "commit: path must be contiguous int32 [sequences, width] on the GPU")
+            _require(max_len <= table.shape[1] * self.page_tokens, "commit: the table holds fewer than max_len tokens")
+            self._cache_error("commit", pages)
+        if new_lens is None:
+            new_lens = _result((n,), i32, lens.device, stream)
+        else:
+            _require(new_lens.shape == (n,) and new_lens.dtype is i32 and new_lens.is_cuda and new_lens.is_contiguous(),
+                     "commit: new_lens must be contiguous int32 [sequences] on the GPU")
+        rc = self._lib.moe_attn_commit(
+            self.handle, pages.data_ptr(), starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
+            ts[0] if n > 1 else table.shape[1], path.data_ptr(), path.shape[1], n, max_len, new_lens.data_ptr(),
+            _raw_stream(stream, lens))
+        if rc:
+            _check(rc)
+        return new_lens
 
     def status(self, stream=None):
         """Raises MoEError if an earlier call met a slot, position, table

@@ -31,7 +31,11 @@ enum : int {
   kBadPage = 4,      // a block-table entry outside the page pool
   kBadLength = 8,    // sequence lengths or query starts outside what the call said
   kTimeout = 16,     // a bounded wait gave up
+  kBadParent = 32,   // a tree node's parent that is no earlier node of its sequence
+  kBadPath = 64,     // an accepted path that is no ascending list of the sequence's nodes
 };
+
+constexpr int kTreeNodes = 64;  // most nodes of a sequence's tree: a node's ancestors are the bits of one word
 
 // Dequantised key/value tiles of one pass of the prompt path.
 constexpr int kTileTokens = 128;
@@ -47,6 +51,7 @@ struct AttnParams {
   const uint8_t* pages;
   int64_t head_bytes, page_bytes;
   const int32_t *starts, *lens, *table;
+  const int32_t* parents;  // [T] of a tree call, else null
   void* out;           // [T][hq][D]
   float* lse;          // [T][hq] or null
   float* part_o;       // [tile][split][rows][D]
@@ -54,6 +59,15 @@ struct AttnParams {
   int* status;
   uint64_t timeout_ns;
   int miss;            // 1 under moe_attn_inject_timeout: an arrival that the barriers of the first operands wait for in vain
+};
+
+struct CommitParams {
+  uint8_t* pages;
+  const int32_t *starts, *lens, *table, *path;
+  int32_t* new_lens;
+  int table_stride, width, max_len, hk, D, P, pshift, n_pages;
+  int64_t head_bytes, page_bytes;
+  int* status;
 };
 
 // One sequence of the call, clamped to what the call said (a value outside is
@@ -87,6 +101,72 @@ __device__ __forceinline__ int load_page(const AttnParams& p, int b, int i) { re
 // Keys visible to a query at position pos: [key_lo(pos), pos].
 __device__ __forceinline__ int key_lo(const AttnParams& p, int pos) {
   return p.window > 0 ? max(0, pos - p.window + 1) : 0;
+}
+
+// The ancestors of a sequence's tree nodes, themselves among them: bit a of a
+// node's word stands for node a.  One warp; lane i takes the nodes i and
+// i + 32.  Each round doubles how far up a word reaches, so a chain of 64 nodes
+// takes 6 rounds, the usual tree 2 or 3.  A parent that is no earlier node is
+// reported and taken as -1 (the node follows the prefix).
+struct TreeWords {
+  uint64_t word[2];
+};
+__device__ __forceinline__ TreeWords tree_words(const AttnParams& p, const Seq& s) {
+  const int lane = threadIdx.x & 31;
+  int up[2];
+  TreeWords t;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = lane + 32 * k;
+    up[k] = -1;
+    t.word[k] = 0;
+    if (i < s.nq) {
+      const int u = p.parents[s.start + i];
+      up[k] = u >= 0 && u < i ? u : -1;
+      bad |= u != up[k];
+      t.word[k] = 1ull << i;
+    }
+  }
+  if (bad) atomicOr(p.status, kBadParent);
+#pragma unroll 1
+  for (int round = 0; round < 6; ++round) {
+    if (!__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) break;
+    uint64_t w[2];
+    int n[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int from = up[k] & 31;
+      const uint64_t w0 = __shfl_sync(0xffffffffu, t.word[0], from), w1 = __shfl_sync(0xffffffffu, t.word[1], from);
+      const int n0 = __shfl_sync(0xffffffffu, up[0], from), n1 = __shfl_sync(0xffffffffu, up[1], from);
+      w[k] = up[k] < 0 ? 0 : (up[k] < 32 ? w0 : w1);
+      n[k] = up[k] < 0 ? -1 : (up[k] < 32 ? n0 : n1);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      t.word[k] |= w[k];
+      up[k] = n[k];
+    }
+  }
+  return t;
+}
+// What a tree node sees: the tokens [lo, p0) before the tree and the nodes of
+// `word`.  A node stands at position p0 + its depth; within a window it sees
+// the nearest of its ancestors, which are the highest bits.
+struct TreeRow {
+  uint64_t word;
+  int lo;
+};
+__device__ __forceinline__ TreeRow tree_row(const AttnParams& p, int p0, uint64_t word) {
+  const int n = __popcll(word);
+  TreeRow r{word, key_lo(p, p0 + n - 1)};
+  if (p.window > 0)
+    for (int k = p.window; k < n; ++k) r.word &= r.word - 1;
+  return r;
+}
+__device__ __forceinline__ bool tree_sees(const TreeRow& r, int p0, int j) {
+  const int a = j - p0;
+  return a < 0 ? j >= r.lo : a < kTreeNodes && ((r.word >> a) & 1);
 }
 
 // A row's softmax reference once it has seen a key, whatever the key's score:

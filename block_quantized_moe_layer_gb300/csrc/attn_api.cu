@@ -25,6 +25,7 @@ cudaError_t verify_launch(const AttnParams& p, int num_sms, size_t part_rows, cu
 size_t prompt_ws_bytes(int D, int tile_cap);
 cudaError_t prompt_configure();
 cudaError_t prompt_launch(const AttnParams& p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st);
+cudaError_t commit_launch(const CommitParams& p, int n_seqs, cudaStream_t st);
 }  // namespace attn
 }  // namespace moe
 
@@ -77,6 +78,64 @@ int check_rows(const char* who, const char* name, const void* p, int64_t tok, in
                      (long long)tok, (long long)head);
   if (heads > 1 && head < D)
     return set_error(MOE_EINVAL, "%s: %s's head stride %lld is below the head's %d channels", who, name, (long long)head, D);
+  return MOE_OK;
+}
+
+// moe_attn_forward, and with parents moe_attn_forward_tree.
+int forward(const char* who, moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
+            const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride, const int32_t* parents,
+            int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out, float* lse, void* stream) {
+  if (!h) return set_error(MOE_EINVAL, "%s: NULL handle", who);
+  if (T < 0 || T > h->T_max) return set_error(MOE_EINVAL, "%s: T=%d outside 0..%d", who, T, h->T_max);
+  if (n_seqs < 0 || n_seqs > h->S_max) return set_error(MOE_EINVAL, "%s: n_seqs=%d outside 0..%d", who, n_seqs, h->S_max);
+  if (max_q < 0 || max_q > T) return set_error(MOE_EINVAL, "%s: max_q=%d outside 0..T=%d", who, max_q, T);
+  if (max_len < 0 || max_len > h->len_max)
+    return set_error(MOE_EINVAL, "%s: max_len=%d outside 0..%d", who, max_len, h->len_max);
+  if (T == 0 || n_seqs == 0 || max_q == 0) return MOE_OK;
+  if (!pages || !starts || !lens || (!table && max_len > 0) || !out) return set_error(MOE_EINVAL, "%s: NULL argument", who);
+  if ((int64_t)table_stride * h->P < max_len)
+    return set_error(MOE_EINVAL, "%s: %d table entries a sequence hold %lld tokens, max_len is %d", who, table_stride,
+                     (long long)table_stride * h->P, max_len);
+  const size_t esz = h->act == MOE_ACT_BF16 ? 2 : 4;
+  int rc;
+  if ((rc = check_rows(who, "q", q, q_token_stride, q_head_stride, h->D, h->hq, esz))) return rc;
+  if ((addr(pages) | addr(out)) & 15) return set_error(MOE_EINVAL, "%s: pages and out must be 16-byte aligned", who);
+  if ((addr(starts) | addr(lens) | addr(table) | addr(lse) | addr(parents)) & 3)
+    return set_error(MOE_EINVAL, "%s: starts, lens, table, parents and lse must be 4-byte aligned", who);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  attn::AttnParams p{};
+  p.hq = h->hq; p.hk = h->hk; p.g = h->hq / h->hk; p.D = h->D; p.P = h->P;
+  p.pshift = 31 - __builtin_clz((unsigned)h->P);
+  p.n_pages = h->n_pages; p.window = h->window;
+  p.T = T; p.n_seqs = n_seqs; p.max_q = max_q; p.max_len = max_len; p.table_stride = table_stride;
+  p.n_split = 1;
+  p.scale_log2 = h->scale * 1.44269504088896341f;
+  p.q = q; p.q_tok = q_token_stride; p.q_head = q_head_stride;
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.head_bytes = h->head_bytes; p.page_bytes = h->page_bytes;
+  p.starts = starts; p.lens = lens; p.table = table; p.parents = parents;
+  p.out = out; p.lse = lse;
+  p.status = h->status;
+  p.timeout_ns = 2000000000ull;
+  if (h->act == MOE_ACT_F32) {
+    CKA(attn::check_launch(p, st), "attention launch (fp32)");
+    return MOE_OK;
+  }
+  if (h->inject_us > 0) {  // one launch
+    p.timeout_ns = 1000ull * h->inject_us;
+    p.miss = 1;
+    h->inject_us = 0;
+  }
+  p.part_o = reinterpret_cast<float*>(h->ws);
+  p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
+  const int64_t rows = (int64_t)max_q * p.g;
+  if (rows <= kSmallCallRows)
+    CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "attention launch");
+  else if (rows <= verify_call_rows(h->D))
+    CKA(attn::verify_launch(p, h->num_sms, h->part_rows, st), "attention launch (verify)");
+  else
+    CKA(attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st),
+        "attention launch (prompt)");
   return MOE_OK;
 }
 
@@ -230,58 +289,52 @@ int moe_attn_read(moe_attn* h, const void* pages, const int64_t* slots, int32_t 
 int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
                      const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride,
                      int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out, float* lse, void* stream) {
-  const char* who = "moe_attn_forward";
+  return forward("moe_attn_forward", h, q, q_token_stride, q_head_stride, pages, starts, lens, table, table_stride, nullptr, n_seqs,
+                 T, max_q, max_len, out, lse, stream);
+}
+
+int moe_attn_forward_tree(moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
+                          const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride,
+                          const int32_t* parents, int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out,
+                          float* lse, void* stream) {
+  const char* who = "moe_attn_forward_tree";
+  if (max_q > attn::kTreeNodes)
+    return set_error(MOE_EINVAL, "%s: max_q=%d, a tree has at most %d nodes", who, max_q, attn::kTreeNodes);
+  if (!parents && T > 0) return set_error(MOE_EINVAL, "%s: NULL parents", who);
+  return forward(who, h, q, q_token_stride, q_head_stride, pages, starts, lens, table, table_stride, parents, n_seqs, T, max_q,
+                 max_len, out, lse, stream);
+}
+
+int moe_attn_commit(moe_attn* h, void* pages, const int32_t* starts, const int32_t* lens, const int32_t* table,
+                    int32_t table_stride, const int32_t* path, int32_t path_width, int32_t n_seqs, int32_t max_len,
+                    int32_t* new_lens, void* stream) {
+  const char* who = "moe_attn_commit";
   if (!h) return set_error(MOE_EINVAL, "%s: NULL handle", who);
-  if (T < 0 || T > h->T_max) return set_error(MOE_EINVAL, "%s: T=%d outside 0..%d", who, T, h->T_max);
   if (n_seqs < 0 || n_seqs > h->S_max) return set_error(MOE_EINVAL, "%s: n_seqs=%d outside 0..%d", who, n_seqs, h->S_max);
-  if (max_q < 0 || max_q > T) return set_error(MOE_EINVAL, "%s: max_q=%d outside 0..T=%d", who, max_q, T);
+  if (path_width < 0 || path_width > attn::kTreeNodes)
+    return set_error(MOE_EINVAL, "%s: path_width=%d outside 0..%d", who, path_width, attn::kTreeNodes);
   if (max_len < 0 || max_len > h->len_max)
     return set_error(MOE_EINVAL, "%s: max_len=%d outside 0..%d", who, max_len, h->len_max);
-  if (T == 0 || n_seqs == 0 || max_q == 0) return MOE_OK;
-  if (!pages || !starts || !lens || (!table && max_len > 0) || !out) return set_error(MOE_EINVAL, "%s: NULL argument", who);
+  if (n_seqs == 0) return MOE_OK;
+  if (!pages || !starts || !lens || (!table && max_len > 0) || (!path && path_width > 0) || !new_lens)
+    return set_error(MOE_EINVAL, "%s: NULL argument", who);
   if ((int64_t)table_stride * h->P < max_len)
     return set_error(MOE_EINVAL, "%s: %d table entries a sequence hold %lld tokens, max_len is %d", who, table_stride,
                      (long long)table_stride * h->P, max_len);
-  const size_t esz = h->act == MOE_ACT_BF16 ? 2 : 4;
-  int rc;
-  if ((rc = check_rows(who, "q", q, q_token_stride, q_head_stride, h->D, h->hq, esz))) return rc;
-  if ((addr(pages) | addr(out)) & 15) return set_error(MOE_EINVAL, "%s: pages and out must be 16-byte aligned", who);
-  if ((addr(starts) | addr(lens) | addr(table) | addr(lse)) & 3)
-    return set_error(MOE_EINVAL, "%s: starts, lens, table and lse must be 4-byte aligned", who);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  attn::AttnParams p{};
-  p.hq = h->hq; p.hk = h->hk; p.g = h->hq / h->hk; p.D = h->D; p.P = h->P;
-  p.pshift = 31 - __builtin_clz((unsigned)h->P);
-  p.n_pages = h->n_pages; p.window = h->window;
-  p.T = T; p.n_seqs = n_seqs; p.max_q = max_q; p.max_len = max_len; p.table_stride = table_stride;
-  p.n_split = 1;
-  p.scale_log2 = h->scale * 1.44269504088896341f;
-  p.q = q; p.q_tok = q_token_stride; p.q_head = q_head_stride;
-  p.pages = static_cast<const uint8_t*>(pages);
-  p.head_bytes = h->head_bytes; p.page_bytes = h->page_bytes;
-  p.starts = starts; p.lens = lens; p.table = table;
-  p.out = out; p.lse = lse;
+  if (addr(pages) & 15) return set_error(MOE_EINVAL, "%s: pages must be 16-byte aligned", who);
+  if ((addr(starts) | addr(lens) | addr(table) | addr(path) | addr(new_lens)) & 3)
+    return set_error(MOE_EINVAL, "%s: starts, lens, table, path and new_lens must be 4-byte aligned", who);
+  // (lens is read by other blocks than the one that writes a sequence's new length)
+  if (addr(new_lens) < addr(lens) + 4 * (size_t)n_seqs && addr(lens) < addr(new_lens) + 4 * (size_t)n_seqs)
+    return set_error(MOE_EINVAL, "%s: new_lens must not overlap lens", who);
+  attn::CommitParams p{};
+  p.pages = static_cast<uint8_t*>(pages);
+  p.starts = starts; p.lens = lens; p.table = table; p.path = path; p.new_lens = new_lens;
+  p.table_stride = table_stride; p.width = path_width; p.max_len = max_len;
+  p.hk = h->hk; p.D = h->D; p.P = h->P; p.pshift = 31 - __builtin_clz((unsigned)h->P);
+  p.n_pages = h->n_pages; p.head_bytes = h->head_bytes; p.page_bytes = h->page_bytes;
   p.status = h->status;
-  p.timeout_ns = 2000000000ull;
-  if (h->act == MOE_ACT_F32) {
-    CKA(attn::check_launch(p, st), "moe_attn_forward launch (fp32)");
-    return MOE_OK;
-  }
-  if (h->inject_us > 0) {  // one launch
-    p.timeout_ns = 1000ull * h->inject_us;
-    p.miss = 1;
-    h->inject_us = 0;
-  }
-  p.part_o = reinterpret_cast<float*>(h->ws);
-  p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
-  const int64_t rows = (int64_t)max_q * p.g;
-  if (rows <= kSmallCallRows)
-    CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch");
-  else if (rows <= verify_call_rows(h->D))
-    CKA(attn::verify_launch(p, h->num_sms, h->part_rows, st), "moe_attn_forward launch (verify)");
-  else
-    CKA(attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st),
-        "moe_attn_forward launch (prompt)");
+  CKA(attn::commit_launch(p, n_seqs, static_cast<cudaStream_t>(stream)), "moe_attn_commit launch");
   return MOE_OK;
 }
 
@@ -294,10 +347,12 @@ int moe_attn_status(moe_attn* h, void* stream) {
   CKA(cudaMemset(h->status, 0, 16), "status reset");
   CKA(cudaDeviceSynchronize(), "status reset sync");
   if (w[0] & attn::kTimeout) return set_error(MOE_ETIMEOUT, "a device-side wait timed out (site %d)", w[1]);
-  return set_error(MOE_EINVAL, "an earlier call met%s%s%s%s", w[0] & attn::kBadSlot ? " a slot outside the pages;" : "",
+  return set_error(MOE_EINVAL, "an earlier call met%s%s%s%s%s%s", w[0] & attn::kBadSlot ? " a slot outside the pages;" : "",
                    w[0] & attn::kBadPosition ? " a position outside 0..len_max-1;" : "",
                    w[0] & attn::kBadPage ? " a block-table entry outside the pages;" : "",
-                   w[0] & attn::kBadLength ? " lengths or query starts outside the call's T, max_q or max_len;" : "");
+                   w[0] & attn::kBadLength ? " lengths or query starts outside the call's T, max_q or max_len;" : "",
+                   w[0] & attn::kBadParent ? " a tree node's parent that is no earlier node;" : "",
+                   w[0] & attn::kBadPath ? " a path that is no ascending list of a sequence's nodes;" : "");
 }
 
 int moe_attn_inject_timeout(moe_attn* h, int32_t wait_limit_us) {

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kCheckWarps = 8;
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kWords = D / 8;  // words of a row: lanes that own channels
   constexpr int kPar = kWords <= 16 ? 32 / kWords : 1, kBatch = 8;
@@ -40,15 +40,21 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
   for (int i = threadIdx.x; i < D; i += blockDim.x)
     sq[i] = static_cast<const float*>(p.q)[tok * p.q_tok + h * p.q_head + i] * p.scale_log2;
   __syncthreads();
-  const int pos = s.len - s.nq + t;
-  const int lo = key_lo(p, pos);
+  const int p0 = s.len - s.nq, pos = p0 + t;  // its place in the cache: the last key that it may see
+  TreeRow tree{0, 0};
+  if constexpr (TREE) {
+    const TreeWords w = tree_words(p, s);
+    const uint64_t w0 = __shfl_sync(0xffffffffu, w.word[0], t & 31), w1 = __shfl_sync(0xffffffffu, w.word[1], t & 31);
+    tree = tree_row(p, p0, t < 32 ? w0 : w1);
+  }
+  const int lo = TREE ? tree.lo : key_lo(p, pos);
   const int kvh = h / p.g;
   const int word = kPar > 1 ? lane % kWords : lane, sub = kPar > 1 ? lane / kWords : 0;
   float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   // chunks of 32 keys, aligned so that a chunk lies in at most two pages (16-token pages)
   for (int c = (lo & ~31) + 32 * warp; c <= pos; c += 32 * kCheckWarps) {
     const int j = c + lane;
-    const bool in = j >= lo && j <= pos;
+    const bool in = TREE ? j <= pos && tree_sees(tree, p0, j) : j >= lo && j <= pos;
     const int pg = in ? load_page(p, b, j >> p.pshift) : -1;
     const uint8_t* base = pg < 0 ? nullptr : p.pages + pg * p.page_bytes + kvh * p.head_bytes;
     const int at = j & (p.P - 1);
@@ -136,14 +142,18 @@ __global__ void __launch_bounds__(kCheckWarps * 32) check_kernel(const __grid_co
 
 }  // namespace
 
-cudaError_t check_launch(const AttnParams& p, cudaStream_t st) {
+template <bool TREE>
+static cudaError_t check_launch_any(const AttnParams& p, cudaStream_t st) {
   const dim3 grid((unsigned)(p.max_q * p.hq), p.n_seqs);
   switch (p.D) {
-    case 64: return launch_pdl(check_kernel<64>, grid, kCheckWarps * 32, 0, st, p);
-    case 128: return launch_pdl(check_kernel<128>, grid, kCheckWarps * 32, 0, st, p);
-    case 192: return launch_pdl(check_kernel<192>, grid, kCheckWarps * 32, 0, st, p);
-    default: return launch_pdl(check_kernel<256>, grid, kCheckWarps * 32, 0, st, p);
+    case 64: return launch_pdl(check_kernel<64, TREE>, grid, kCheckWarps * 32, 0, st, p);
+    case 128: return launch_pdl(check_kernel<128, TREE>, grid, kCheckWarps * 32, 0, st, p);
+    case 192: return launch_pdl(check_kernel<192, TREE>, grid, kCheckWarps * 32, 0, st, p);
+    default: return launch_pdl(check_kernel<256, TREE>, grid, kCheckWarps * 32, 0, st, p);
   }
+}
+cudaError_t check_launch(const AttnParams& p, cudaStream_t st) {
+  return p.parents ? check_launch_any<true>(p, st) : check_launch_any<false>(p, st);
 }
 
 }  // namespace attn

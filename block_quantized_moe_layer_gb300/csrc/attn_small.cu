@@ -62,12 +62,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8x8 fragment
   return y;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
     small_kernel(const __grid_constant__ AttnParams p, int n_rt, int chunk) {
   using L = SmallPlan<D, NT>;
   constexpr int kJ = D / 64, kRows = L::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t tree[TREE ? kTreeNodes : 1];  // the nodes' words of ancestors
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + kSmallMaxStages;
   volatile uint32_t* pmask = reinterpret_cast<uint32_t*>(empty + kSmallMaxStages);  // pages present of a stage
@@ -94,8 +95,9 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   if (n_rows <= 0) return;  // (the whole block; every thread has passed its dependency wait)
   // keys that some row sees, and this block's tiles of them
   const int p0 = s.len - s.nq;  // position of the first query
-  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + n_rows - 1) / p.g;
-  const int lo = key_lo(p, pos_min), hi = pos_max + 1;
+  // (of a tree all rows see what lies before it, and a node's place in the cache bounds its position)
+  const int pos_min = TREE ? p0 - 1 : p0 + row0 / p.g, pos_max = p0 + (row0 + n_rows - 1) / p.g;
+  const int lo = key_lo(p, TREE ? p0 : pos_min), hi = pos_max + 1;
   const int tile_a = lo / kSmallTile + split * chunk;
   const int tile_b = min(tile_a + chunk, (max(hi, 0) + kSmallTile - 1) / kSmallTile);
   const int n_tiles = hi > lo ? max(0, tile_b - tile_a) : 0;
@@ -135,13 +137,21 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       if (i < n_tiles) issue(i, pg[i]), ++issued;
   }
 
+  if constexpr (TREE) {
+    if (warp == 1) {
+      const TreeWords w = tree_words(p, s);
+      tree[lane] = w.word[0];
+      tree[lane + 32] = w.word[1];
+    }
+    __syncthreads();
+  }
   const int n = lane >> 2, t = lane & 3;
   const int key_n = (n & 1) ? 4 + (((n >> 1) + 2) & 3) : n >> 1;  // kKey(n)
   const int key_e = t, key_o = 4 + ((t + 2) & 3);                  // kKey(2t), kKey(2t + 1)
   // query rows 8 i + n as B operands (channels 64 j + 16 t .. + 15), and what
   // the rows 8 i + 2t, 8 i + 2t + 1 of the accumulators see
   uint32_t bq[NT][8 * kJ];
-  int hi_r[2 * NT], lo_r[2 * NT];
+  int hi_r[2 * NT], lo_r[2 * NT];  // (of a tree hi_r is the row's node, -1: no row)
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int r = 8 * i + n, tq = (row0 + r) / p.g, h = kvh * p.g + (row0 + r) % p.g;
@@ -159,8 +169,13 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = 8 * i + 2 * t + e, pos = p0 + (row0 + rr) / p.g;
-      hi_r[2 * i + e] = rr < n_rows ? pos + 1 : 0;
-      lo_r[2 * i + e] = key_lo(p, pos);
+      if constexpr (TREE) {
+        hi_r[2 * i + e] = rr < n_rows ? pos - p0 : -1;
+        lo_r[2 * i + e] = rr < n_rows ? key_lo(p, p0 + __popcll(tree[pos - p0]) - 1) : 0;
+      } else {
+        hi_r[2 * i + e] = rr < n_rows ? pos + 1 : 0;
+        lo_r[2 * i + e] = key_lo(p, pos);
+      }
     }
   }
   const int lo_max = key_lo(p, pos_max);
@@ -250,6 +265,11 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
         __syncwarp();
+        TreeRow tr[2 * NT];
+        if constexpr (TREE) {
+#pragma unroll
+          for (int r = 0; r < 2 * NT; ++r) tr[r] = hi_r[r] < 0 ? TreeRow{0, p0} : tree_row(p, p0, tree[hi_r[r]]);
+        }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
           const bool page = (mask >> ((warp * 32 + 16 * a) >> p.pshift)) & 1;
@@ -258,8 +278,14 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
           for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const bool s0 = page && j0 < hi_r[2 * u + e] && j0 >= lo_r[2 * u + e];
-              const bool s1 = page && j1 < hi_r[2 * u + e] && j1 >= lo_r[2 * u + e];
+              bool s0, s1;
+              if constexpr (TREE) {
+                s0 = page && tree_sees(tr[2 * u + e], p0, j0);
+                s1 = page && tree_sees(tr[2 * u + e], p0, j1);
+              } else {
+                s0 = page && j0 < hi_r[2 * u + e] && j0 >= lo_r[2 * u + e];
+                s1 = page && j1 < hi_r[2 * u + e] && j1 >= lo_r[2 * u + e];
+              }
               if (!s0) sc[u][a][e] = -INFINITY;
               if (!s1) sc[u][a][2 + e] = -INFINITY;
               seen |= s0 || s1 ? 1u << (2 * u + e) : 0u;
@@ -584,17 +610,23 @@ cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStre
   const int64_t fit = std::min<int64_t>(kMaxSplit, std::max<int64_t>(1, (int64_t)(part_rows / L::kRows) / base));
   chunk = std::max<int>(chunk, (int)((tiles + fit - 1) / fit));
   p.n_split = (tiles + chunk - 1) / chunk;
-  cudaError_t e = launch_pdl(small_kernel<D, NT>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads, L::kTotal,
-                             st, p, n_rt, chunk);
+  cudaError_t e = launch_pdl(p.parents ? small_kernel<D, NT, true> : small_kernel<D, NT, false>,
+                             dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads, L::kTotal, st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
   return join_launch(p, L::kRows, n_rt, -1, st);
 }
 
+template <int D, int NT>
+cudaError_t small_configure_nt() {
+  constexpr int bytes = SmallPlan<D, NT>::kTotal;
+  cudaError_t e = cudaFuncSetAttribute(small_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(small_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e;
+}
 template <int D>
 cudaError_t small_configure_d() {
-  cudaError_t e = cudaFuncSetAttribute(small_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<D, 1>::kTotal);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(small_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallPlan<D, 2>::kTotal);
+  const cudaError_t e = small_configure_nt<D, 1>();
+  return e != cudaSuccess ? e : small_configure_nt<D, 2>();
 }
 
 template <int D>

@@ -158,5 +158,13 @@ __device__ __forceinline__ KeyBits<QC> key_bits(int k0, int lo, int hi) {
   return v;
 }
 
+// The same of a tree node's row: prefix keys [lo, p0), then the nodes of `word`.
+template <int QC>
+__device__ __forceinline__ KeyBits<QC> tree_bits(int k0, int lo, int p0, uint64_t word) {
+  const int a = k0 - p0;  // node of the first key
+  const uint64_t nodes = a >= 0 ? (a < 64 ? word >> a : 0) : (a > -QC ? word << -a : 0);
+  return key_bits<QC>(k0, lo, p0) | (KeyBits<QC>)nodes;
+}
+
 }  // namespace attn
 }  // namespace moe

@@ -65,7 +65,7 @@ struct VerifyPlan {
   static_assert(kRowsV * kPitch <= kMax, "the output fits the images' room");
 };
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_constant__ AttnParams p, int n_rt, int chunk) {
   using L = VerifyPlan<D>;
   constexpr int KT = L::KT, QC = KT / 4;  // keys of a softmax thread
@@ -108,8 +108,9 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   const Seq s = load_seq(p, b);
   const int row0 = rt * kRowsV, n_rows = max(0, min(kRowsV, s.nq * p.g - row0));
   const int p0 = s.len - s.nq;
-  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + max(n_rows, 1) - 1) / p.g;
-  const int lo = key_lo(p, max(0, pos_min)), hi = pos_max + 1, lo_max = key_lo(p, pos_max);
+  // (of a tree all rows see what lies before it, and a node's place in the cache bounds its position)
+  const int pos_min = TREE ? p0 - 1 : p0 + row0 / p.g, pos_max = p0 + (row0 + max(n_rows, 1) - 1) / p.g;
+  const int lo = key_lo(p, max(0, TREE ? p0 : pos_min)), hi = pos_max + 1, lo_max = key_lo(p, pos_max);
   const int tile_a = lo / KT + split * chunk;
   const int n_tiles = hi > lo && n_rows > 0 ? max(0, min(tile_a + chunk, (hi + KT - 1) / KT) - tile_a) : 0;
 
@@ -120,8 +121,20 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   if (has_row) {
     tq = (row0 + row) / p.g;
     hq = kvh * p.g + (row0 + row) % p.g;
-    hi_r = p0 + tq + 1;
+    hi_r = TREE ? p0 : p0 + tq + 1;
     lo_r = key_lo(p, p0 + tq);
+  }
+  uint64_t word = 0;  // a tree row's nodes
+  if constexpr (TREE) {
+    if (soft && n_rows > 0) {
+      const TreeWords w = tree_words(p, s);
+      const uint64_t w0 = __shfl_sync(0xffffffffu, w.word[0], tq & 31), w1 = __shfl_sync(0xffffffffu, w.word[1], tq & 31);
+      if (has_row) {
+        const TreeRow r = tree_row(p, p0, tq < 32 ? w0 : w1);
+        word = r.word;
+        lo_r = r.lo;
+      }
+    }
   }
 
   float m = -INFINITY, l = 0.f;
@@ -267,7 +280,9 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
         seen = true;
         return false;
       }
-      bits = key_bits<QC>(c0 + QC * quarter, lo_r, hi_r) & (mask * 0xFFu);  // (bytes of 1 to bytes of 0xFF)
+      if constexpr (TREE) bits = tree_bits<QC>(c0 + QC * quarter, lo_r, hi_r, word);
+      else bits = key_bits<QC>(c0 + QC * quarter, lo_r, hi_r);
+      bits &= mask * 0xFFu;  // (bytes of 1 to bytes of 0xFF)
       seen |= bits != 0;
       return true;
     });
@@ -331,21 +346,28 @@ cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStr
   want = std::min<int64_t>(std::min<int64_t>(want, kMaxSplit), std::max<int64_t>(1, (int64_t)(part_rows / kRowsV) / base));
   const int chunk = (int)std::max<int64_t>(std::min(tiles, 2), (tiles + want - 1) / want);
   p.n_split = (tiles + chunk - 1) / chunk;
-  cudaError_t e = launch_pdl(verify_kernel<D>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
+  cudaError_t e = launch_pdl(p.parents ? verify_kernel<D, true> : verify_kernel<D, false>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
                              VerifyPlan<D>::kTotal, st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
   return join_launch(p, kRowsV, n_rt, -1, st);
 }
 
+template <int D>
+cudaError_t verify_configure_d() {
+  cudaError_t e = cudaFuncSetAttribute(verify_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, VerifyPlan<D>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(verify_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, VerifyPlan<D>::kTotal);
+  return e;
+}
+
 }  // namespace
 
 cudaError_t verify_configure(int D) {
-  const auto set = [](const void* f, int bytes) { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); };
   switch (D) {
-    case 64: return set((const void*)verify_kernel<64>, VerifyPlan<64>::kTotal);
-    case 128: return set((const void*)verify_kernel<128>, VerifyPlan<128>::kTotal);
-    case 192: return set((const void*)verify_kernel<192>, VerifyPlan<192>::kTotal);
-    default: return set((const void*)verify_kernel<256>, VerifyPlan<256>::kTotal);
+    case 64: return verify_configure_d<64>();
+    case 128: return verify_configure_d<128>();
+    case 192: return verify_configure_d<192>();
+    default: return verify_configure_d<256>();
   }
 }
 

@@ -297,6 +297,54 @@ int mtp_verify_accept(const int32_t* draft_ids, int32_t k, const float* logits, 
 int mtp_verify_accept_noalloc(const int32_t* draft_ids, int32_t k, const float* logits, int32_t V,
                               int32_t* out_n_accepted, int32_t* out_next_token, void* stream);
 
+/* Verification of drafted tokens, a tree of them for each of n_seqs sequences,
+ * against the target's probabilities from given random numbers, and the draw
+ * of the next token: the accepted tokens and the next one are distributed as
+ * if each had been drawn from the target.
+ *   Sequence b's nodes are starts[b]..starts[b+1]-1.  The first is the root:
+ * the last token that is certain (its own token is not looked at); the others
+ * are drafts: tokens[i] after the line of nodes up to parents[i], an index
+ * within the sequence of an earlier node.  parents NULL: a chain, each node
+ * after the one before.  Row i of logits, and of draft_logits where the drafts
+ * were drawn, belongs to node i: the distribution of the tokens after it.
+ *   p = softmax(logits[i] / T), T = temperature[b] (NULL: 1).  From the root on,
+ * the children of a node are tried in their order, with r = p at first and u
+ * the child's uniforms[i], 0 <= u < 1:
+ *   draft_logits NULL (drafts chosen without chance): a child with token x is
+ *     accepted if u sum(r) < r(x); else r(x) = 0;
+ *   else, q = softmax(draft_logits[i] / T): accepted if u sum(r) q(x) < r(x);
+ *     else r = max(r / sum(r) - q, 0).  With replacement = 0 the children of a
+ *     node were drawn without replacement: a rejected token leaves q, which is
+ *     normalised again; with 1 they are independent draws from q.
+ * The walk goes on from the first child accepted; where none is, the next
+ * token is the first whose cumulative r passes the root's uniforms times
+ * sum(r).  (If rounding leaves nothing of r, it is drawn from p.)
+ *   T = 0 (below 1e-6): p is the largest logit alone (ties to the lowest id),
+ * and drafts count as chosen.  T outside 0..1e6, or NaN: as a row without a
+ * distribution.
+ *   A token outside 0..V-1 (an absent draft, -1), a parent that is no earlier
+ * node, and, unless the draws are independent, a token that an earlier sibling
+ * has, are passed over.  A row of draft_logits without a distribution (below):
+ * its node's children are passed over.
+ *   path int32 [n_seqs][max_nodes]: the accepted nodes' indices within the
+ * sequence, the root first, -1 behind them; out_n_accepted int32 [n_seqs]: the
+ * drafts among them; out_next_token int32 [n_seqs]: -1 where the row has no
+ * distribution (a NaN or +inf logit, or none above -inf).  A sequence without
+ * nodes, or whose starts are outside 0..n_nodes, has a path of -1, n_accepted
+ * -1 and next token -1.  Nodes from max_nodes on are left out; 1 <= max_nodes
+ * <= 64.
+ *   logits, draft_logits: [n_nodes][V] of dtype (moe_act), rows contiguous,
+ * strides in elements; only the rows of the nodes on the path are read.
+ *   Weights below 2^-100 of a row's largest count as 0.  Weights are right to
+ * 2^-32, their sums in more bits: a number closer than that to a border
+ * between two outcomes may fall on either side.  The same inputs give the same
+ * outputs.  Asynchronous, no allocation, no workspace. */
+int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_stride, const void* draft_logits,
+                      int64_t draft_stride, int32_t V, const int32_t* tokens, const int32_t* parents,
+                      const int32_t* starts, int32_t n_seqs, int32_t n_nodes, int32_t max_nodes,
+                      const float* uniforms, const float* temperature, int32_t replacement, int32_t* path,
+                      int32_t* out_n_accepted, int32_t* out_next_token, void* stream);
+
 /* ------------------------------------------------------------------------
  * Output head and one MTP draft/verify round.
  * ------------------------------------------------------------------------ */
@@ -475,8 +523,47 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
                      const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride,
                      int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out, float* lse, void* stream);
 
+/* moe_attn_forward for trees of drafted tokens: the query tokens of a sequence
+ * are the nodes of a tree (or of several), in any order in which a parent comes
+ * before its children.  parents int32 [T] (device): each one's parent as an
+ * index within its sequence, -1 where it follows the tokens before the tree.
+ * Node i, the row lens[b] - m + i of the cache (m = starts[b+1] - starts[b]
+ * nodes), sees those tokens, its ancestors and itself:
+ *   position(i) = lens[b] - m + (number of i's ancestors).
+ * With a window it sees its last `window` tokens along that line.  The keys are
+ * appended with those positions, at the nodes' own slots.
+ *   A parent that is no earlier node (below -1, or the node itself or a later
+ * one) counts as -1 and is reported by moe_attn_status.  max_q is at most 64.
+ * Where lens[b] < m the first nodes are not in the cache: they see nothing (0,
+ * lse -inf), and nobody sees them.
+ *   Everything else is as in moe_attn_forward; a chain (parents -1, 0, 1, ...)
+ * gives its results. */
+int moe_attn_forward_tree(moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
+                          const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride,
+                          const int32_t* parents, int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out,
+                          float* lse, void* stream);
+
+/* Keeps a tree's accepted nodes (mtp_verify_sample's path) in the cache: the
+ * rows of sequence b's nodes path[b][0], path[b][1], ... move, bytes as they
+ * are, to the places behind the tokens before the tree,
+ *   row p0 + k <- row p0 + path[b][k]  for all k at once, p0 = lens[b] - m,
+ * and new_lens[b] = p0 + (number of nodes kept).  The rows behind are left as
+ * they were.
+ *   path int32 [n_seqs][path_width] (device): ascending node indices, -1 behind
+ * the last; 0 <= path_width <= 64.  The first entry that is neither an
+ * ascending node index nor -1 ends the path and is reported by moe_attn_status.
+ * A move from or to a page outside the pool is left out and reported.  A
+ * sequence with lens[b] outside 0..max_len, or with fewer tokens than nodes, or
+ * more than 64 nodes, stays as it is (new_lens[b] = lens[b]) and is reported.
+ * Sequences must not share the pages that hold their nodes.
+ *   new_lens int32 [n_seqs], not overlapping lens: a model calls this for each
+ * layer's pages with the same lens.  Asynchronous, no allocation, no workspace. */
+int moe_attn_commit(moe_attn* h, void* pages, const int32_t* starts, const int32_t* lens, const int32_t* table,
+                    int32_t table_stride, const int32_t* path, int32_t path_width, int32_t n_seqs, int32_t max_len,
+                    int32_t* new_lens, void* stream);
+
 /* Synchronises `stream` and reports what earlier calls met: MOE_EINVAL with
- * the kinds of bad slots, positions, table entries or lengths, MOE_ETIMEOUT
+ * the kinds of bad slots, positions, table entries, lengths, parents or paths, MOE_ETIMEOUT
  * where a bounded device-side wait gave up, MOE_OK otherwise.  The word is
  * then cleared. */
 int moe_attn_status(moe_attn* h, void* stream);
