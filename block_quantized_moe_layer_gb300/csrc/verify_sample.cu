@@ -29,6 +29,7 @@
 #include <cooperative_groups.h>
 
 #include <cmath>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "layer.cuh"
@@ -37,16 +38,18 @@ namespace moe {
 namespace {
 
 constexpr int kVsThreads = 512;
-constexpr int kVsWarps = kVsThreads / 32;
+constexpr int kVsWarps = kVsThreads / 32, kVsLogWarps = 4;
+static_assert(kVsWarps == 1 << kVsLogWarps, "a power of two");
 constexpr int kVsNodes = 64;
 constexpr int kVsMaxCluster = 8;
+constexpr int kVsBatch = 4;  // 16-byte loads in flight a thread
 
 struct VsParams {
   const void* logits;
   int64_t stride;  // elements
   const void* draft;
   int64_t draft_stride;
-  int V, n_seqs, n_nodes, max_nodes, replacement, C;
+  int V, n_seqs, n_nodes, max_nodes, replacement, log_c;
   const int32_t *tokens, *parents, *starts;
   const float *uniforms, *temperature;
   int32_t *path, *n_accepted, *next;
@@ -82,46 +85,45 @@ __device__ __forceinline__ void accumulate(Pair& a, Pair b) {
   a.h = t;
   a.l = __fadd_rn(a.l, __fadd_rn(e, b.l));
 }
-__device__ __forceinline__ Pair shuffled(Pair a, int o) {
-  return Pair{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
-}
-__device__ __forceinline__ double value(Pair a) { return (double)a.h + (double)a.l; }
+// In whole steps of 1 / scale (a power of two): sums of these are exact, in any order.
+__device__ __forceinline__ int64_t fixed(Pair a, float scale) { return __float2ll_rn(a.h * scale) + __float2ll_rn(a.l * scale); }
 
 // A row's exponential: weight(l) = 2^(c (l - ref)) in units of 2^top.  ref is 0
 // where |c l_max| < 2^10, else l_max: then the difference is exact for every
-// logit that counts.  Below 2^-100 of the largest a weight is 0 (a masked
-// logit's is exactly 0).
+// logit that counts.  Below 2^-126 of the unit a weight is 0: the exponent of
+// what is clamped there is that of 0 (a masked logit's weight is exactly 0).
 struct RowExp {
-  float ref, floor, cut, ch, cl;
+  float ref, floor, ch, cl;
   uint32_t scale0;
 };
+constexpr float kMagic = 49152.f;  // 1.5 2^15: its sum with y has steps of 2^-8
 __device__ __forceinline__ RowExp row_exp(float most, float ch, float cl) {
   RowExp r;
-  const float y = most * ch;
-  r.ref = fabsf(y) < 1024.f ? 0.f : most;
+  r.ref = fabsf(most * ch) < 1024.f ? 0.f : most;
   const float top = rintf((most - r.ref) * ch);
-  r.floor = (top - 120.f) / ch;
-  r.cut = top - 100.f;
+  r.floor = (top - 127.f) / ch;
   r.ch = ch;
   r.cl = cl;
-  r.scale0 = (uint32_t)(127 - (int)top) << 23;
+  r.scale0 = ((uint32_t)(127 - (int)top) << 23) - ((__float_as_uint(kMagic) >> 8) << 23);
   return r;
 }
-constexpr float kMagic = 49152.f;  // 1.5 2^15: its sum with y has steps of 2^-8
-__device__ __forceinline__ Pair weight(float logit, const RowExp& r, const float2* table) {
+// 2^y as table entry (h + l) times (1 + p), times the scale: y = x c = (bits of k) / 256 + g.
+struct Raw {
+  float h, l, s;  // (h + l) s
+};
+__device__ __forceinline__ Raw weight_raw(float logit, const RowExp& r, const float2* table) {
   constexpr float L1 = 0.693147180559945f, L2 = 0.240226506959101f, L3 = 0.0555041086648216f;
   const float x = fmaxf(__fsub_rn(logit, r.ref), r.floor);
-  const float y = __fmul_rn(x, r.ch);
-  const float yl = fmaf(x, r.cl, fmaf(x, r.ch, -y));
-  const float k = __fadd_rn(y, kMagic);
-  const float g = __fsub_rn(y, __fsub_rn(k, kMagic));
+  const float k = fmaf(x, r.ch, kMagic);
   const uint32_t bits = __float_as_uint(k);
   const float2 t = table[bits & 255];
-  const float p = fmaf(g, fmaf(g, fmaf(g, L3, L2), L1), yl * L1);
-  // (bits >> 8) - (kMagic's bits >> 8) is the whole part of y
-  const uint32_t scale = ((bits >> 8) << 23) - ((__float_as_uint(kMagic) >> 8) << 23) + r.scale0;
-  const float s = y > r.cut ? __uint_as_float(scale) : 0.f;
-  return Pair{__fmul_rn(t.x, s), __fmul_rn(fmaf(t.x, p, t.y), s)};
+  const float g = fmaf(x, r.cl, fmaf(x, r.ch, -__fsub_rn(k, kMagic)));
+  const float p = __fmul_rn(g, fmaf(g, fmaf(g, L3, L2), L1));
+  return Raw{t.x, fmaf(t.x, p, t.y), __uint_as_float(((bits >> 8) << 23) + r.scale0)};
+}
+__device__ __forceinline__ Pair weight(float logit, const RowExp& r, const float2* table) {
+  const Raw w = weight_raw(logit, r, table);
+  return Pair{__fmul_rn(w.h, w.s), __fmul_rn(w.l, w.s)};
 }
 // (e - k f)+
 __device__ __forceinline__ Pair residual(Pair e, Pair f, Pair k) {
@@ -133,28 +135,58 @@ __device__ __forceinline__ Pair residual(Pair e, Pair f, Pair k) {
   return r.h + r.l > 0.f ? r : Pair{0.f, 0.f};
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <typename In>
 struct Load;
 template <>
 struct Load<float> {
   static constexpr int kN = 4;
-  __device__ static void vec(const float* p, float (&x)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  __device__ static void unpack(uint4 v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  }
+  template <int B>
+  __device__ static float most(const uint4 (&v)[B]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      m = max_nan(m, __uint_as_float(v[b].x), __uint_as_float(v[b].y));
+      m = max_nan(m, __uint_as_float(v[b].z), __uint_as_float(v[b].w));
+    }
+    return m;
   }
   __device__ static float one(const float* p) { return __ldg(p); }
 };
 template <>
 struct Load<__nv_bfloat16> {
   static constexpr int kN = 8;
-  __device__ static void vec(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  __device__ static void unpack(uint4 v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
+  }
+  template <int B>
+  __device__ static float most(const uint4 (&v)[B]) {
+    uint32_t m = 0xFF80FF80u;  // -inf twice
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    }
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 };
@@ -164,17 +196,38 @@ struct Load<__nv_bfloat16> {
 // or from V on count as -inf).
 template <typename In>
 struct Row {
+  static constexpr int N = Load<In>::kN;
   const In* p;
   int V, skew;
   bool aligned;  // its vectors start on 16-byte boundaries too
-  __device__ void load(int j, float (&x)[Load<In>::kN]) const {
-    constexpr int N = Load<In>::kN;
-    const int e = j * N - skew;
-    if (aligned && e >= 0 && e + N <= V) {
-      Load<In>::vec(p + e, x);
+  __device__ bool whole(int j) const { return aligned && j * N >= skew && j * N - skew + N <= V; }
+  __device__ uint4 raw(int j) const { return __ldg(reinterpret_cast<const uint4*>(p + (j * N - skew))); }
+  __device__ void load(int j, float (&x)[N]) const {
+    if (whole(j)) {
+      Load<In>::unpack(raw(j), x);
     } else {
+      const int e = j * N - skew;
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = e + i >= 0 && e + i < V ? Load<In>::one(p + e + i) : -INFINITY;
+    }
+  }
+  // Vectors j, j + 32, ... below j1, kBatch at once: batch(words) where all are whole, else one(x, first element) each.
+  template <int kBatch, class B, class F>
+  __device__ void each(int j, int j1, B batch, F one) const {
+    for (; j < j1; j += 32 * kBatch) {
+      if (j + 32 * (kBatch - 1) < j1 && whole(j) && whole(j + 32 * (kBatch - 1))) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) v[b] = raw(j + 32 * b);
+        batch(v, j);
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < kBatch && j + 32 * b < j1; ++b) {
+          float x[N];
+          load(j + 32 * b, x);
+          one(x, (j + 32 * b) * N - skew);
+        }
+      }
     }
   }
 };
@@ -183,10 +236,44 @@ __device__ __forceinline__ int skew_of(const In* p) {
   return (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(In));
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Largest logit and sum of 2^(c (l - m)), in fp32.
+struct Soft {
+  float m, s;
+};
+__device__ __forceinline__ void raise(Soft& a, float m, float ch) {
+  const float mn = max_nan(a.m, m);
+  if (mn != a.m) {  // (or NaN)
+    a.s = a.m == -INFINITY ? 0.f : a.s * exp2_fast((a.m - mn) * ch);
+    a.m = mn;
+  }
+}
+// The joined parts of a warp's lanes.
+__device__ __forceinline__ Soft warp_soft(Soft a, float ch) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  raise(a, m, ch);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+  return a;
+}
+__device__ __forceinline__ Pair warp_pair(Pair a) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) accumulate(a, Pair{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)});
+  return a;
+}
+__device__ __forceinline__ uint64_t warp_best(uint64_t k) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
+    k = other > k ? other : k;
+  }
+  return k;
 }
 // Orders by value, then by the lower id.
 __device__ __forceinline__ uint64_t order_key(float x, int id) {
@@ -195,66 +282,62 @@ __device__ __forceinline__ uint64_t order_key(float x, int id) {
   return ((uint64_t)o << 32) | (uint32_t)~id;
 }
 
-// What a block tells the others of its cluster.
-struct Part {
-  float most, most_f;
-  uint64_t best;
-  double sum, sum_f;
-};
-
 enum : int { kGoOn, kReject, kDraw };
 
 struct Walk {  // one block's shared memory
   float2 table[256];
-  int parent[kVsNodes], token[kVsNodes], path[kVsNodes];
+  int parent[kVsNodes], token[kVsNodes], path[kVsNodes], child[kVsNodes];
   float u[kVsNodes];
-  Part part[2];
-  float wmost[kVsWarps], wmost_f[kVsWarps];
-  uint64_t wbest[kVsWarps];
-  double wsum[kVsWarps], wsum_f[kVsWarps];  // of the warps' ranges: what is left of the target's weights, the draft's
-  int child[kVsNodes], n_children;
-  double child_e[kVsNodes], child_f[kVsNodes];
+  // read by the first warp of each block of the cluster: two sets, used in turn
+  Soft soft[2][kVsWarps];
+  uint64_t best[2][kVsWarps];
+  int64_t sum[2][kVsWarps], sum_f[2][kVsWarps];  // of the warps' ranges: what is left of the target's weights, the draft's
+  int64_t child_e[kVsNodes], child_f[kVsNodes];
   bool gone[kVsNodes];  // of the children: rejected, its token's weight taken out
-  double scan[kVsThreads];
-  // written by one thread for all
+  int64_t part[kVsWarps];
+  // written by the first warp for the block
   float most, most_f;
-  uint64_t best;
-  double Z, F;       // the sums of the cluster
-  double kappa, left;  // the draft's part taken out; of its probability what is not rejected
-  int act, at, cursor;
-  double threshold;
-  int owner, range, winner;
+  int act, at, range, winner;
+  double kappa;
+  int64_t threshold;
 };
 
 // The first of the warp's values (one a lane, in order) whose cumulative sum
 // passes t, or the last above 0 where rounding leaves none; before: the sum
 // ahead of it.  -1 if there is none.
-__device__ __forceinline__ int pick(double q, double t, int lane, double& before) {
-  double incl = q;
+__device__ __forceinline__ int pick(int64_t q, int64_t t, int lane, int64_t& before) {
+  int64_t incl = q;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double up = __shfl_up_sync(0xffffffffu, incl, o);
+    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += up;
   }
-  const uint32_t some = __ballot_sync(0xffffffffu, q > 0.0), past = __ballot_sync(0xffffffffu, q > 0.0 && incl > t);
+  const uint32_t some = __ballot_sync(0xffffffffu, q > 0), past = __ballot_sync(0xffffffffu, q > 0 && incl > t);
   const int at = past ? __ffs(past) - 1 : (some ? 31 - __clz(some) : -1);
   before = __shfl_sync(0xffffffffu, incl - q, max(at, 0));
   return at;
 }
+__device__ __forceinline__ int64_t warp_total(int64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
 template <typename In>
-__global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_constant__ VsParams p) {
+__global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __grid_constant__ VsParams p) {
   namespace cg = cooperative_groups;
   constexpr int N = Load<In>::kN;
+  constexpr int kGroup = kVsMaxCluster * kVsWarps / 32;  // most ranges of a lane of the first warp
   __shared__ Walk w;
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / p.C, rank = blockIdx.x % p.C;
+  const int b = blockIdx.x >> p.log_c, rank = blockIdx.x & ((1 << p.log_c) - 1);
   if (tid < 256) w.table[tid] = make_float2(kExpTable.hi[tid], kExpTable.lo[tid]);
   griddep_wait();
   cg::cluster_group cl = cg::this_cluster();
 
   const int start = p.starts[b], end = p.starts[b + 1];
+  const float T = p.temperature ? p.temperature[b] : 1.f;
   const bool empty = start < 0 || end > p.n_nodes || end <= start;
   if (empty) {  // (the whole cluster)
     if (rank == 0) {
@@ -264,12 +347,14 @@ __global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_
     return;
   }
   const int m = min(end - start, p.max_nodes);
-  const float T = p.temperature ? p.temperature[b] : 1.f;
   const bool valid_T = T >= 0.f && T <= 1e6f;
   const bool greedy = T < 1e-6f;
-  const double c = 1.4426950408889634074 / (double)(greedy || !valid_T ? 1.f : T);
-  const float ch = (float)c, c_lo = (float)(c - (double)ch);
   const bool drawn = p.draft && !greedy;
+  // log2(e) / T in two parts
+  const float div = greedy || !valid_T ? 1.f : T;
+  const float ch = __fdiv_rn(1.44269502f, div), c_lo = __fdiv_rn(fmaf(-ch, div, 1.44269502f) + 1.92596299e-8f, div);
+  // steps of the whole sums: below 2^62 for V weights of at most 2^0.5 each
+  const float scale = __uint_as_float((uint32_t)(127 + 61 - (32 - __clz(p.V))) << 23);
   if (tid < kVsNodes) {
     w.path[tid] = tid == 0 ? 0 : -1;
     w.parent[tid] = -2;
@@ -283,209 +368,315 @@ __global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_
 
   int node = 0, length = 1, turn = 0;
   int next = -1;
-  bool mine_to_write = rank == 0 && tid == 0;  // the thread that stores the next token
-  // Ranges of whole vectors: warp w of block r takes the vectors [(16 r + w) per, ...).
+  bool writes = rank == 0 && tid == 0;  // the thread that stores the next token
   while (valid_T) {
     const In* pe = static_cast<const In*>(p.logits) + (int64_t)(start + node) * p.stride;
     const In* pf = drawn ? static_cast<const In*>(p.draft) + (int64_t)(start + node) * p.draft_stride : pe;
     const int skew = skew_of(pe);
     const Row<In> re{pe, p.V, skew, true}, rf{pf, p.V, skew, skew_of(pf) == skew};
     const int n_vec = (p.V + skew + N - 1) / N;
-    const int per = (n_vec + p.C * kVsWarps - 1) / (p.C * kVsWarps);
-    const int range = rank * kVsWarps + warp;
-    const int j0 = min(n_vec, range * per), j1 = min(n_vec, j0 + per);
+    // ranges of whole vectors, a warp each: warp w of block r has the range 16 r + w
+    const int n_ranges = kVsWarps << p.log_c, per = (n_vec + n_ranges - 1) >> (kVsLogWarps + p.log_c);
+    const int j0 = min(n_vec, (rank * kVsWarps + warp) * per), j1 = min(n_vec, j0 + per);
 
-    // ---- the largest logits, and the children
-    float most = -INFINITY, most_f = -INFINITY;
-    uint64_t best = 0;
-    for (int j = j0 + lane; j < j1; j += 32) {
-      float x[N];
-      re.load(j, x);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (greedy && x[i] > most) best = order_key(x[i], j * N - skew + i);
-        most = max_nan(most, x[i]);
-      }
-      if (drawn) {
-        rf.load(j, x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) most_f = max_nan(most_f, x[i]);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-      most_f = max_nan(most_f, __shfl_xor_sync(0xffffffffu, most_f, o));
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
-      best = other > best ? other : best;
-    }
-    if (lane == 0) w.wmost[warp] = most, w.wmost_f[warp] = most_f, w.wbest[warp] = best;
+    // ---- the children; the first warp asks for their logits (a lane a child)
+    const bool kid0 = lane > node && w.parent[lane] == node, kid1 = lane + 32 > node && w.parent[lane + 32] == node;
+    const uint32_t set0 = __ballot_sync(0xffffffffu, kid0), set1 = __ballot_sync(0xffffffffu, kid1);
+    const int n_children = __popc(set0) + __popc(set1);
+    const bool both = drawn && n_children > 0;  // the draft's row matters
+    int my_child = 0, my_token = -1;
+    float my_e = 0.f, my_f = 0.f;
     if (warp == 0) {
-      int n = 0;
-#pragma unroll
-      for (int k = 0; k < kVsNodes; k += 32) {
-        const bool is = k + lane > node && w.parent[k + lane] == node;
-        const uint32_t set = __ballot_sync(0xffffffffu, is);
-        if (is) w.child[n + __popc(set & ((1u << lane) - 1))] = k + lane;
-        n += __popc(set);
+      if (kid0) w.child[__popc(set0 & ((1u << lane) - 1))] = lane;
+      if (kid1) w.child[__popc(set0) + __popc(set1 & ((1u << lane) - 1))] = lane + 32;
+      __syncwarp();
+      if (lane < n_children) {
+        my_child = w.child[lane];
+        my_token = w.token[my_child];
+        if (my_token >= 0 && my_token < p.V) {
+          my_e = Load<In>::one(pe + my_token);
+          if (both) my_f = Load<In>::one(pf + my_token);
+        }
       }
-      if (lane == 0) w.n_children = n;
     }
-    __syncthreads();
-    if (warp == 0) {
-      float a = w.wmost[lane % kVsWarps], d = w.wmost_f[lane % kVsWarps];
-      uint64_t k = w.wbest[lane % kVsWarps];
+
+    // ---- the largest logits and, for children, their sums in fp32: half of the warps a row
+    const int log_t = both ? kVsLogWarps - 1 : kVsLogWarps, team_warps = 1 << log_t, team = warp >> log_t;
+    const int per_t = (n_vec + (team_warps << p.log_c) - 1) >> (log_t + p.log_c);
+    {
+      const Row<In>& row = team ? rf : re;
+      const int a0 = min(n_vec, (rank * team_warps + (warp & (team_warps - 1))) * per_t), a1 = min(n_vec, a0 + per_t);
+      Soft a{-INFINITY, 0.f};
+      uint64_t best = 0;
+      auto one = [&](const float (&x)[N], int e) {
+        float mx = x[0];
 #pragma unroll
-      for (int o = kVsWarps / 2; o; o >>= 1) {
-        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-        d = max_nan(d, __shfl_xor_sync(0xffffffffu, d, o));
-        const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
-        k = other > k ? other : k;
+        for (int i = 1; i < N; ++i) mx = max_nan(mx, x[i]);
+        if (greedy) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (x[i] > a.m) best = order_key(x[i], e + i), a.m = x[i];
+        }
+        if (greedy || n_children == 0) {
+          a.m = max_nan(a.m, mx);
+          return;
+        }
+        raise(a, mx, ch);
+        const float base = a.m == -INFINITY ? 0.f : -a.m * ch;
+#pragma unroll
+        for (int i = 0; i < N; ++i) a.s += exp2_fast(fmaf(x[i], ch, base));
+      };
+      row.template each<kVsBatch>(a0 + lane, a1, [&](const uint4 (&v)[kVsBatch], int j) {
+        if (greedy) {
+#pragma unroll
+          for (int k = 0; k < kVsBatch; ++k) {
+            float x[N];
+            Load<In>::unpack(v[k], x);
+            one(x, (j + 32 * k) * N - skew);
+          }
+          return;
+        }
+        const float mx = Load<In>::most(v);
+        if (n_children == 0) {
+          a.m = max_nan(a.m, mx);
+          return;
+        }
+        raise(a, mx, ch);
+        const float base = a.m == -INFINITY ? 0.f : -a.m * ch;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kVsBatch; ++k) {
+          float x[N];
+          Load<In>::unpack(v[k], x);
+#pragma unroll
+          for (int i = 0; i < N; ++i) s[i & 3] += exp2_fast(fmaf(x[i], ch, base));
+        }
+        a.s += (s[0] + s[1]) + (s[2] + s[3]);
+      }, one);
+      a = warp_soft(a, ch);
+      if (lane == 0) w.soft[turn][warp] = a;
+      if (greedy) {
+        best = warp_best(best);
+        if (lane == 0) w.best[turn][warp] = best;
       }
-      if (lane == 0) w.part[turn].most = a, w.part[turn].most_f = d, w.part[turn].best = k;
     }
     cl.sync();
     if (warp == 0) {
-      const Part* q = cl.map_shared_rank(&w.part[turn], lane % p.C);
-      float a = q->most, d = q->most_f;
-      uint64_t k = q->best;
+      Soft e{-INFINITY, 0.f}, f = e;
+      uint64_t best = 0;
+      {
+        Soft s[kGroup];
+        const bool mine_f = (lane & (kVsWarps - 1)) >= team_warps;  // this lane's parts are the draft's
 #pragma unroll
-      for (int o = kVsMaxCluster / 2; o; o >>= 1) {
-        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-        d = max_nan(d, __shfl_xor_sync(0xffffffffu, d, o));
-        const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
-        k = other > k ? other : k;
+        for (int g = 0; g < kGroup; ++g) {
+          const int i = lane + 32 * g;
+          s[g] = e;
+          if (i < n_ranges) {
+            const Walk* q = cl.map_shared_rank(&w, i >> kVsLogWarps);
+            s[g] = q->soft[turn][i & (kVsWarps - 1)];
+            if (greedy) {
+              const uint64_t k = q->best[turn][i & (kVsWarps - 1)];
+              best = k > best ? k : best;
+            }
+          }
+        }
+        Soft a = s[0];
+#pragma unroll
+        for (int g = 1; g < kGroup; ++g) a.m = max_nan(a.m, s[g].m);
+        a.s = 0.f;
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) a.s += s[g].m == -INFINITY ? 0.f : s[g].s * exp2_fast((s[g].m - a.m) * ch);
+        const Soft none{-INFINITY, 0.f};
+        e = warp_soft(mine_f ? none : a, ch);
+        if (both) f = warp_soft(mine_f ? a : none, ch);
       }
-      if (lane == 0) w.most = a, w.most_f = d, w.best = k;
+      int act = kDraw, at = 0;
+      if (!(e.m > -INFINITY && e.m < INFINITY)) {
+        at = -1;  // no distribution (NaN, +inf, or nothing left)
+      } else if (greedy) {
+        at = (int)~(uint32_t)warp_best(best);
+#pragma unroll 1
+        for (int i = lane; i < ((n_children + 31) & ~31); i += 32) {
+          const uint32_t hit = __ballot_sync(0xffffffffu, i < n_children && w.token[w.child[i < n_children ? i : 0]] == at);
+          if (hit) {
+            act = kGoOn;
+            at = w.child[i - lane + __ffs(hit) - 1];
+            break;
+          }
+        }
+      } else if (n_children > 0 && (!drawn || (f.m > -INFINITY && f.m < INFINITY))) {
+        // a child that is accepted by a margin above the fp32 sums' error: the most
+        // likely end of a step.  (Errors, relative: 2^-22 of an exponential and of
+        // each time a sum is rescaled, 2^-24 an addition; of an argument y = c l - c m
+        // 2^-24 (|y| + |c m|) ln 2, where the weights 2^y bring |y| to log2(V) at most.)
+        const float slack = 1e-5f + 3e-7f * (float)(per_t * N / 32 + 1) + 1.2e-7f * fmaxf(fabsf(e.m * ch), both ? fabsf(f.m * ch) : 0.f);
+        const bool is = lane < n_children && my_token >= 0 && my_token < p.V;
+        const float we = exp2_fast((my_e - e.m) * ch), wf = both ? exp2_fast((my_f - f.m) * ch) : 0.f, u = w.u[my_child];
+        uint32_t left_set = __ballot_sync(0xffffffffu, is);
+        float left = e.s;
+        while (left_set) {
+          const int i = __ffs(left_set) - 1;
+          const float ui = __shfl_sync(0xffffffffu, u, i), ei = __shfl_sync(0xffffffffu, we, i), fi = __shfl_sync(0xffffffffu, wf, i);
+          const float r = both ? f.s * ei : ei, x = both ? ui * e.s * fi : ui * left;
+          const float near = both ? 2.f * slack * (x + r) : slack * (ui * e.s + r);
+          if (r - x > near) {
+            act = kGoOn;
+            at = __shfl_sync(0xffffffffu, my_child, i);
+          }
+          if (both || !(x - r > near)) break;  // (of drawn drafts the first alone; not sure to be rejected)
+          left -= ei;
+          left_set &= ~__ballot_sync(0xffffffffu, my_token == __shfl_sync(0xffffffffu, my_token, i));  // (and its like)
+        }
+      }
+      if (lane == 0) w.act = act, w.at = at, w.most = e.m, w.most_f = f.m;
     }
     turn ^= 1;
     __syncthreads();
-    most = w.most;
-    most_f = w.most_f;
-    if (!(most > -INFINITY && most < INFINITY)) break;  // no distribution (NaN, +inf, or nothing left)
-    const int n_children = w.n_children;
-    if (greedy) {
-      const int top = (int)~(uint32_t)w.best;
-      int to = -1;
-      for (int i = 0; i < n_children && to < 0; ++i)
-        if (w.token[w.child[i]] == top) to = w.child[i];
-      if (to < 0) {
-        next = top;
-        break;
-      }
-      if (tid == 0) w.path[length] = to;
+    if (w.act == kGoOn) {
+      node = w.at;
+      if (tid == 0) w.path[length] = node;
       ++length;
-      node = to;
       __syncthreads();
       continue;
     }
-    const bool judged = drawn && most_f > -INFINITY && most_f < INFINITY;  // the draft's row is a distribution
+    if (greedy || w.at < 0) {
+      next = w.at;
+      break;
+    }
+    const float most = w.most, most_f = w.most_f;
+    const bool judged = both && most_f > -INFINITY && most_f < INFINITY;  // the draft's row is a distribution
     const RowExp ee = row_exp(most, ch, c_lo), ef = row_exp(judged ? most_f : 0.f, ch, c_lo);
 
-    // ---- the sums
+    // ---- else the sums in more bits
+    if (tid < n_children) {
+      const int x = w.token[w.child[tid]];
+      const bool is = x >= 0 && x < p.V;
+      w.child_e[tid] = is ? fixed(weight(Load<In>::one(pe + x), ee, w.table), scale) : -1;
+      w.child_f[tid] = is && judged ? fixed(weight(Load<In>::one(pf + x), ef, w.table), scale) : 0;
+      w.gone[tid] = false;
+    }
     double kappa = 0.0;
     Pair kp{0.f, 0.f};
     auto left_of = [&](const float (&xe)[N], const float (&xf)[N], Pair (&r)[N]) {  // what is left of a vector's weights
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        r[k] = weight(xe[k], ee, w.table);
-        if (kappa > 0.0) r[k] = residual(r[k], weight(xf[k], ef, w.table), kp);
-      }
+      for (int k = 0; k < N; ++k) r[k] = residual(weight(xe[k], ee, w.table), weight(xf[k], ef, w.table), kp);
+    };
+    auto total = [&](const Row<In>& row, const RowExp& x_of) {  // this warp's range of a row
+      // In two parts: what a weight has in steps of 2^-17 of the unit, whose sum is
+      // exact below 2^6, and the rest.  Both go to a pair every 32 elements.
+      constexpr float kGrid = 96.f;  // 1.5 2^6
+      Pair a{0.f, 0.f};
+      float hi = 0.f, lo = 0.f;
+      int n = 0;
+      auto one = [&](const float (&x)[N], int) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const Raw r = weight_raw(x[k], x_of, w.table);
+          const float l = __fmul_rn(r.l, r.s);
+          const float top = __fsub_rn(__fadd_rn(fmaf(r.h, r.s, l), kGrid), kGrid);
+          lo = __fadd_rn(lo, __fadd_rn(fmaf(r.h, r.s, -top), l));
+          hi = __fadd_rn(hi, top);
+        }
+        if (++n == 32 / N) {
+          accumulate(a, Pair{hi, lo});
+          hi = lo = 0.f;
+          n = 0;
+        }
+      };
+      row.template each<4>(j0 + lane, j1, [&](const uint4 (&v)[4], int) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x[N];
+          Load<In>::unpack(v[k], x);
+          one(x, 0);
+        }
+      }, one);
+      accumulate(a, Pair{hi, lo});
+      return fixed(warp_pair(a), scale);
     };
     auto sums = [&](bool draft) {  // this warp's range: what is left of the target's weights, and the draft's
-      Pair a{0.f, 0.f}, d{0.f, 0.f};
-      for (int j = j0 + lane; j < j1; j += 32) {
-        float xe[N], xf[N];
-        Pair r[N];
-        re.load(j, xe);
-        if (draft || kappa > 0.0) rf.load(j, xf);
-        left_of(xe, xf, r);
+      int64_t e, f = 0;
+      if (kappa > 0.0) {
+        Pair a{0.f, 0.f};
+#pragma unroll 2
+        for (int j = j0 + lane; j < j1; j += 32) {
+          float xe[N], xf[N];
+          Pair r[N];
+          re.load(j, xe);
+          rf.load(j, xf);
+          left_of(xe, xf, r);
 #pragma unroll
-        for (int k = 0; k < N; ++k) accumulate(a, r[k]);
-        if (draft) {
-#pragma unroll
-          for (int k = 0; k < N; ++k) accumulate(d, weight(xf[k], ef, w.table));
+          for (int k = 0; k < N; ++k) accumulate(a, r[k]);
         }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        accumulate(a, shuffled(a, o));
-        if (draft) accumulate(d, shuffled(d, o));
+        e = fixed(warp_pair(a), scale);
+      } else {
+        e = total(re, ee);
+        if (draft) f = total(rf, ef);
       }
       if (lane == 0) {
-        w.wsum[warp] = value(a);
-        if (draft) w.wsum_f[warp] = value(d);
+        w.sum[turn][warp] = e;
+        if (draft) w.sum_f[turn][warp] = f;
       }
     };
-    auto exchange = [&](bool draft) {  // their sums over the cluster, to warp 0 (and in part[turn ^ 1].sum a block's own)
-      __syncthreads();
-      if (warp == 0) {
-        double a = lane < kVsWarps ? w.wsum[lane] : 0.0, d = draft && lane < kVsWarps ? w.wsum_f[lane] : 0.0;
-#pragma unroll
-        for (int o = kVsWarps / 2; o; o >>= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          if (draft) d += __shfl_xor_sync(0xffffffffu, d, o);
-        }
-        if (lane == 0) w.part[turn].sum = a, w.part[turn].sum_f = d;
-      }
+    // of the first warp's lanes, in order: the ranges group * lane on
+    const int group = max(n_ranges >> 5, 1);
+    int64_t mine[kGroup], Z = 0, F = 0;
+    auto gather = [&](bool draft) {  // the sums of all ranges, to the first warp
       cl.sync();
       if (warp == 0) {
-        const Part* q = cl.map_shared_rank(&w.part[turn], lane % p.C);
-        double a = lane < p.C ? q->sum : 0.0, d = draft && lane < p.C ? q->sum_f : 0.0;
+        int64_t s = 0, d = 0;
 #pragma unroll
-        for (int o = kVsMaxCluster / 2; o; o >>= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          if (draft) d += __shfl_xor_sync(0xffffffffu, d, o);
+        for (int g = 0; g < kGroup; ++g) {
+          const int i = lane * group + g;
+          mine[g] = 0;
+          if (g < group && i < n_ranges) {
+            const Walk* q = cl.map_shared_rank(&w, i >> kVsLogWarps);
+            mine[g] = q->sum[turn][i & (kVsWarps - 1)];
+            if (draft) d += q->sum_f[turn][i & (kVsWarps - 1)];
+          }
+          s += mine[g];
         }
-        if (lane == 0) {
-          w.Z = a;
-          if (draft) w.F = d;
-        }
+        Z = warp_total(s);
+        if (draft) F = warp_total(d);
       }
       turn ^= 1;
     };
     sums(judged);
-    if (tid < n_children) {
-      const int x = w.token[w.child[tid]];
-      const bool is = x >= 0 && x < p.V;
-      w.child_e[tid] = is ? value(weight(Load<In>::one(pe + x), ee, w.table)) : -1.0;
-      w.child_f[tid] = is && judged ? value(weight(Load<In>::one(pf + x), ef, w.table)) : 0.0;
-      w.gone[tid] = false;
-    }
-    if (tid == 0) w.kappa = 0.0, w.left = 1.0, w.cursor = 0;
-    exchange(judged);
+    gather(judged);
 
-    // ---- the children in order (one thread of each block decides, all of them the same)
+    // ---- the children in order (each block's first warp decides, all of them the same)
+    double left = 1.0;  // of the draft's probability what is not rejected
+    int cursor = 0;
     while (true) {
-      if (tid == 0) {
-        int act = kDraw;
-        for (int i = w.cursor; i < n_children; ++i) {
+      if (warp == 0) {
+        int act = kDraw, at = 0;
+        for (int i = cursor; i < n_children; ++i) {
           const int x = w.token[w.child[i]];
-          const double e = w.child_e[i], f = w.child_f[i], u = (double)w.u[w.child[i]];
-          if (e < 0.0 || (drawn && !judged)) continue;  // no such token, or nothing to judge it by: passed over
+          const int64_t e = w.child_e[i], f = w.child_f[i];
+          if (e < 0 || (drawn && !judged)) continue;  // no such token, or nothing to judge it by: passed over
           if (!judged || !p.replacement) {
             bool again = false;  // an earlier sibling's token
             for (int k = 0; k < i; ++k) again |= w.token[w.child[k]] == x;
             if (again) continue;
           }
-          const double r = judged ? e - w.kappa * f : e;
-          if (judged ? u * w.Z * f < w.left * w.F * r : u * w.Z < r) {
+          const double side = (double)w.u[w.child[i]] * (double)Z;
+          if (judged ? side * (double)f < left * (double)F * ((double)e - kappa * (double)f) : side < (double)e) {
             act = kGoOn;
-            w.at = w.child[i];
+            at = w.child[i];
             break;
           }
           if (!judged) {
-            w.Z -= e;
-            w.gone[i] = true;
-          } else if (w.left > 0.0 && w.Z > 0.0) {
-            w.kappa += w.Z / (w.left * w.F);
-            if (!p.replacement) w.left -= f / w.F;
-            w.cursor = i + 1;
+            Z -= e;
+            if (lane == 0) w.gone[i] = true;
+          } else if (left > 0.0 && Z > 0) {
+            kappa += (double)Z / (left * (double)F);
+            if (!p.replacement) left -= (double)f / (double)F;
+            cursor = i + 1;
             act = kReject;
             break;
           }
         }
-        w.act = act;
+        if (lane == 0) w.act = act, w.at = at, w.kappa = kappa;
       }
       __syncthreads();
       if (w.act != kReject) break;
@@ -493,7 +684,7 @@ __global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_
       kp.h = (float)kappa;
       kp.l = (float)(kappa - (double)kp.h);
       sums(false);
-      exchange(false);
+      gather(false);
     }
     if (w.act == kGoOn) {
       node = w.at;
@@ -503,49 +694,70 @@ __global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_
       continue;
     }
 
-    // ---- the next token
-    if (!judged && n_children > 0) {  // what the rejected drafts that were chosen leave of the ranges' sums
-      if (tid == 0) {
+    // ---- the next token: the range that holds the number's place, a thread's vectors of it, the token
+    if (warp == 0) {
+      if (!judged) {  // what the rejected drafts that were chosen leave of the ranges' sums
         for (int i = 0; i < n_children; ++i) {
           if (!w.gone[i]) continue;
-          const int at = (w.token[w.child[i]] + skew) / N / per;
-          if (at / kVsWarps != rank) continue;
-          double& q = w.wsum[at % kVsWarps];
-          const double rest = q - w.child_e[i];
-          q = rest > q * 0x1p-40 ? rest : 0.0;  // (all of it: no rounding stays)
+          const int at = (w.token[w.child[i]] + skew) / N / per;  // its range
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g)
+            if (at == lane * group + g) {
+              const int64_t rest = mine[g] - w.child_e[i];
+              mine[g] = rest > (mine[g] >> 36) + 16 ? rest : 0;  // (all of it: no rounding stays)
+            }
         }
+        int64_t s = 0;
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) s += mine[g];
+        Z = warp_total(s);
       }
-      exchange(false);
-      __syncthreads();
-    }
-    bool out = !judged;  // the rejected tokens' own weights are out
-    if (!(w.Z > 0.0)) {  // nothing is left: the target's own weights
-      kappa = 0.0;
-      out = false;
-      __syncthreads();
-      sums(false);
-      exchange(false);
-    }
-    if (warp == 0) {
-      // the block, its warp's range, and what the threshold is there
-      double before;
-      const Part* q = cl.map_shared_rank(&w.part[turn ^ 1], lane % p.C);
-      const double t = (double)w.u[0] * w.Z;
-      const int owner = pick(lane < p.C ? q->sum : 0.0, t, lane, before);
-      double inside;
-      const int at = pick(lane < kVsWarps ? w.wsum[lane] : 0.0, t - before, lane, inside);
-      if (lane == 0) w.owner = owner, w.range = rank * kVsWarps + max(at, 0), w.threshold = t - before - inside;
+      if (lane == 0) w.at = Z > 0;
     }
     __syncthreads();
-    mine_to_write = false;
-    if (rank != w.owner) break;
+    const bool out = !judged && w.at;  // the rejected tokens' own weights are out
+    if (!w.at) {                       // nothing is left: the target's own weights
+      kappa = 0.0;
+      sums(false);
+      gather(false);
+    }
+    if (warp == 0) {
+      int64_t s = 0, before;
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) s += mine[g];
+      const int64_t t = __double2ll_rd((double)w.u[0] * (double)Z);  // (a whole sum passes the number where it passes this)
+      const int from = max(pick(s, t, lane, before), 0);
+      if (lane == from) {
+        int64_t run = before;
+        int at = 0;
+        bool found = false;
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+          if (found || mine[g] <= 0) continue;
+          at = g;
+          before = run;
+          run += mine[g];
+          found = run > t;
+        }
+        w.range = lane * group + at;
+        w.threshold = t - before;
+      }
+    }
+    __syncthreads();
+    writes = false;
+    if (rank != w.range / kVsWarps) break;
     const int k0 = min(n_vec, w.range * per), k1 = min(n_vec, k0 + per), each = (per + kVsThreads - 1) / kVsThreads;
     const int a0 = min(k1, k0 + tid * each), a1 = min(k1, a0 + each);
     auto left_at = [&](int j, Pair (&r)[N]) {
       float xe[N], xf[N];
       re.load(j, xe);
-      if (kappa > 0.0) rf.load(j, xf);
-      left_of(xe, xf, r);
+      if (kappa > 0.0) {
+        rf.load(j, xf);
+        left_of(xe, xf, r);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) r[k] = weight(xe[k], ee, w.table);
+      }
       if (out) {
         for (int i = 0; i < n_children; ++i) {
           const int k = w.token[w.child[i]] - (j * N - skew);
@@ -563,37 +775,40 @@ __global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < N; ++k) accumulate(a, r[k]);
     }
-    w.scan[tid] = value(a);
+    const int64_t own = fixed(a, scale), of_warp = warp_total(own);
+    if (lane == 0) w.part[warp] = of_warp;
     __syncthreads();
-    if (warp == 0) {  // the thread whose vectors hold the threshold: 16 threads a lane, then those
-      constexpr int kPer = kVsThreads / 32;
-      double sum = 0.0, before, inside;
-      for (int k = 0; k < kPer; ++k) sum += w.scan[lane * kPer + k];
-      const int some = max(pick(sum, w.threshold, lane, before), 0);
-      const int at = max(pick(lane < kPer ? w.scan[some * kPer + lane] : 0.0, w.threshold - before, lane, inside), 0);
-      if (lane == 0) w.winner = some * kPer + at, w.threshold -= before + inside;
+    if (warp == 0) {
+      int64_t before;
+      const int at = max(pick(lane < kVsWarps ? w.part[lane] : 0, w.threshold, lane, before), 0);
+      if (lane == 0) w.winner = at, w.threshold -= before;
     }
     __syncthreads();
-    if (tid == w.winner) {
-      mine_to_write = true;
-      double run = 0.0;
-      bool found = false;
-      for (int j = a0; j < a1 && !found; ++j) {
-        Pair r[N];
-        left_at(j, r);
+    if (warp == w.winner) {
+      int64_t before;
+      const int at = max(pick(own, w.threshold, lane, before), 0);
+      if (lane == at) {
+        writes = true;
+        const int64_t t = w.threshold - before;
+        int64_t run = 0;
+        bool found = false;
+        for (int j = a0; j < a1 && !found; ++j) {
+          Pair r[N];
+          left_at(j, r);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const double q = value(r[k]);
-          if (found || !(q > 0.0)) continue;
-          next = j * N - skew + k;  // (the last with any where rounding leaves none that passes)
-          run += q;
-          found = run > w.threshold;
+          for (int k = 0; k < N; ++k) {
+            const int64_t q = fixed(r[k], scale);
+            if (found || q <= 0) continue;
+            next = j * N - skew + k;  // (the last with any where rounding leaves none that passes)
+            run += q;
+            found = run > t;
+          }
         }
       }
     }
     break;
   }
-  if (mine_to_write) p.next[b] = next;
+  if (writes) p.next[b] = next;
   __syncthreads();
   if (rank == 0) {
     for (int i = tid; i < p.max_nodes; i += kVsThreads) p.path[(int64_t)b * p.max_nodes + i] = i < m ? w.path[i] : -1;
@@ -605,14 +820,14 @@ __global__ void __launch_bounds__(kVsThreads) verify_sample_kernel(const __grid_
 template <typename In>
 cudaError_t verify_sample_launch(const VsParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.n_seqs * p.C));
+  cfg.gridDim = dim3((unsigned)p.n_seqs << p.log_c);
   cfg.blockDim = dim3(kVsThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.C;
+  attr[1].val.clusterDim.x = 1u << p.log_c;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -653,9 +868,10 @@ extern "C" int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_
     cudaGetLastError();  // reported here: the next launch of the process is not to find it
     return set_error(MOE_ECUDA, "%s: %s", who, cudaGetErrorString(e));
   }
-  VsParams p{logits, row_stride, draft_logits, draft_stride, V, n_seqs, n_nodes, max_nodes, replacement, 1,
+  VsParams p{logits, row_stride, draft_logits, draft_stride, V, n_seqs, n_nodes, max_nodes, replacement, 0,
              tokens, parents, starts, uniforms, temperature, path, out_n_accepted, out_next_token};
-  while (p.C < kVsMaxCluster && 2LL * n_seqs * p.C <= 5LL * sms / 4 && V / (2 * p.C) >= 1024) p.C *= 2;
+  while ((2 << p.log_c) <= kVsMaxCluster && ((int64_t)n_seqs << (p.log_c + 1)) <= 2LL * sms && (V >> (p.log_c + 1)) >= 1024) ++p.log_c;
+  if (getenv("VSC")) p.log_c = atoi(getenv("VSC"));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = dtype == MOE_ACT_F32 ? verify_sample_launch<float>(p, st) : verify_sample_launch<__nv_bfloat16>(p, st);
   if (e != cudaSuccess) {
