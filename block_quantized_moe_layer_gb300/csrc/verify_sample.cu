@@ -29,7 +29,6 @@
 #include <cooperative_groups.h>
 
 #include <cmath>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "layer.cuh"
@@ -42,6 +41,7 @@ constexpr int kVsWarps = kVsThreads / 32, kVsLogWarps = 4;
 static_assert(kVsWarps == 1 << kVsLogWarps, "a power of two");
 constexpr int kVsNodes = 64;
 constexpr int kVsMaxCluster = 8;
+constexpr int kVsRanges = kVsMaxCluster * kVsWarps;  // most ranges of a row
 constexpr int kVsBatch = 4;  // 16-byte loads in flight a thread
 
 struct VsParams {
@@ -86,14 +86,16 @@ __device__ __forceinline__ void accumulate(Pair& a, Pair b) {
   a.l = __fadd_rn(a.l, __fadd_rn(e, b.l));
 }
 // In whole steps of 1 / scale (a power of two): sums of these are exact, in any order.
-__device__ __forceinline__ int64_t fixed(Pair a, float scale) { return __float2ll_rn(a.h * scale) + __float2ll_rn(a.l * scale); }
+__device__ __forceinline__ int64_t fixed(float h, float l, float scale) { return __float2ll_rn(h * scale) + __float2ll_rn(l * scale); }
 
-// A row's exponential: weight(l) = 2^(c (l - ref)) in units of 2^top.  ref is 0
-// where |c l_max| < 2^10, else l_max: then the difference is exact for every
-// logit that counts.  Below 2^-126 of the unit a weight is 0: the exponent of
-// what is clamped there is that of 0 (a masked logit's weight is exactly 0).
+// A row's exponential: weight(l) = k 2^(c (l - ref)) in units of 2^top, k = 1
+// unless scaled() says more.  ref is 0 where |c l_max| < 2^10, else l_max: then
+// the difference is exact for every logit that counts.  Below 2^-126 of the unit
+// a weight is 0: the exponent of what is clamped there is that of 0 (a masked
+// logit's weight is exactly 0).
 struct RowExp {
-  float ref, floor, ch, cl;
+  float ref, floor, ceil, top, ch, cl;
+  float magic, rest;  // log2(k) in steps of 2^-8, and what is left of it
   uint32_t scale0;
 };
 constexpr float kMagic = 49152.f;  // 1.5 2^15: its sum with y has steps of 2^-8
@@ -101,38 +103,68 @@ __device__ __forceinline__ RowExp row_exp(float most, float ch, float cl) {
   RowExp r;
   r.ref = fabsf(most * ch) < 1024.f ? 0.f : most;
   const float top = rintf((most - r.ref) * ch);
+  r.top = top;
   r.floor = (top - 127.f) / ch;
+  r.ceil = INFINITY;
   r.ch = ch;
   r.cl = cl;
+  r.magic = kMagic;
+  r.rest = 0.f;
   r.scale0 = ((uint32_t)(127 - (int)top) << 23) - ((__float_as_uint(kMagic) >> 8) << 23);
   return r;
 }
-// 2^y as table entry (h + l) times (1 + p), times the scale: y = x c = (bits of k) / 256 + g.
+// The same times k > 0 (both weights of a logit are compared); held below 8
+// units, which is above every weight of the other row.  log2(k) = e + i/256 +
+// log2(1 + d), 1 + d what the table leaves of k's mantissa, by its series.
+__device__ __forceinline__ RowExp scaled(RowExp r, double k, const float2* table) {
+  const int high = __double2hiint(k);
+  int e = ((high >> 20) & 0x7FF) - 1023;
+  const double m = __hiloint2double((high & 0xFFFFF) | 0x3FF00000, __double2loint(k));  // 1..2
+  float mh = (float)m, ml = (float)(m - (double)mh);
+  int i = __float2int_rn(256.f * __log2f(mh));
+  if (i > 255) i = 0, ++e, mh *= 0.5f, ml *= 0.5f;
+  const float2 t = table[max(i, 0)];
+  const float d = __fdiv_rn((mh - t.x) + (ml - t.y), t.x);
+  const float steps = (float)e + (float)max(i, 0) * 0.00390625f;
+  r.magic = kMagic + steps;
+  r.rest = d * fmaf(d, fmaf(d, 0.48089835f, -0.72134752f), 1.44269504f);
+  r.floor = (r.top - steps - 127.f) / r.ch;
+  r.ceil = (r.top - steps + 3.f) / r.ch;
+  return r;
+}
+// 2^y = (h + l) s: y = c x = (steps of 2^-8: table entry and s) + g.
 struct Raw {
-  float h, l, s;  // (h + l) s
+  float h, l, s;
 };
+template <bool SCALED = false>
 __device__ __forceinline__ Raw weight_raw(float logit, const RowExp& r, const float2* table) {
   constexpr float L1 = 0.693147180559945f, L2 = 0.240226506959101f, L3 = 0.0555041086648216f;
-  const float x = fmaxf(__fsub_rn(logit, r.ref), r.floor);
-  const float k = fmaf(x, r.ch, kMagic);
+  float x = fmaxf(__fsub_rn(logit, r.ref), r.floor);
+  if (SCALED) x = fminf(x, r.ceil);
+  const float k = fmaf(x, r.ch, r.magic);
   const uint32_t bits = __float_as_uint(k);
   const float2 t = table[bits & 255];
-  const float g = fmaf(x, r.cl, fmaf(x, r.ch, -__fsub_rn(k, kMagic)));
+  float g = fmaf(x, r.cl, fmaf(x, r.ch, -__fsub_rn(k, r.magic)));
+  if (SCALED) g += r.rest;
   const float p = __fmul_rn(g, fmaf(g, fmaf(g, L3, L2), L1));
   return Raw{t.x, fmaf(t.x, p, t.y), __uint_as_float(((bits >> 8) << 23) + r.scale0)};
 }
-__device__ __forceinline__ Pair weight(float logit, const RowExp& r, const float2* table) {
-  const Raw w = weight_raw(logit, r, table);
-  return Pair{__fmul_rn(w.h, w.s), __fmul_rn(w.l, w.s)};
+// A weight in two parts: what it has in steps of 2^-17 of the unit, so that a sum
+// of them is exact below 2^6, and the rest.
+struct Parts {
+  float hi, lo;
+};
+__device__ __forceinline__ Parts parts(const Raw& r) {
+  constexpr float kGrid = 96.f;  // 1.5 2^6
+  const float l = __fmul_rn(r.l, r.s);
+  const float top = __fsub_rn(__fadd_rn(fmaf(r.h, r.s, l), kGrid), kGrid);
+  return Parts{top, __fadd_rn(fmaf(r.h, r.s, -top), l)};
 }
-// (e - k f)+
-__device__ __forceinline__ Pair residual(Pair e, Pair f, Pair k) {
-  const float t = __fmul_rn(k.h, f.h);
-  const float tl = fmaf(k.h, f.l, fmaf(k.l, f.h, fmaf(k.h, f.h, -t)));
-  const float d = __fsub_rn(e.h, t), z = __fsub_rn(d, e.h);
-  const float err = __fsub_rn(__fsub_rn(e.h, __fsub_rn(d, z)), __fadd_rn(t, z));
-  const Pair r{d, __fadd_rn(err, __fsub_rn(e.l, tl))};
-  return r.h + r.l > 0.f ? r : Pair{0.f, 0.f};
+// (e - k f)+, f's exponential scaled by k
+__device__ __forceinline__ Parts residual(const Raw& e, const Raw& f) {
+  const Parts a = parts(e), b = parts(f);
+  const Parts r{__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)};
+  return __fadd_rn(r.hi, r.lo) > 0.f ? r : Parts{0.f, 0.f};
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
@@ -202,6 +234,10 @@ struct Row {
   bool aligned;  // its vectors start on 16-byte boundaries too
   __device__ bool whole(int j) const { return aligned && j * N >= skew && j * N - skew + N <= V; }
   __device__ uint4 raw(int j) const { return __ldg(reinterpret_cast<const uint4*>(p + (j * N - skew))); }
+  __device__ uint4 raw_or_none(int j, int j1) const {
+    const uint32_t none = sizeof(In) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+    return j < j1 ? raw(j) : make_uint4(none, none, none, none);
+  }
   __device__ void load(int j, float (&x)[N]) const {
     if (whole(j)) {
       Load<In>::unpack(raw(j), x);
@@ -211,14 +247,15 @@ struct Row {
       for (int i = 0; i < N; ++i) x[i] = e + i >= 0 && e + i < V ? Load<In>::one(p + e + i) : -INFINITY;
     }
   }
-  // Vectors j, j + 32, ... below j1, kBatch at once: batch(words) where all are whole, else one(x, first element) each.
+  // Vectors j, j + 32, ... below j1, kBatch at once: batch(words, j) where those
+  // below j1 are whole (-inf past them), else one(x, first element) each.
   template <int kBatch, class B, class F>
   __device__ void each(int j, int j1, B batch, F one) const {
     for (; j < j1; j += 32 * kBatch) {
-      if (j + 32 * (kBatch - 1) < j1 && whole(j) && whole(j + 32 * (kBatch - 1))) {
+      if (whole(j) && whole(min(j + 32 * (kBatch - 1), j + ((j1 - 1 - j) & ~31)))) {
         uint4 v[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) v[b] = raw(j + 32 * b);
+        for (int b = 0; b < kBatch; ++b) v[b] = raw_or_none(j + 32 * b, j1);
         batch(v, j);
       } else {
 #pragma unroll 1
@@ -252,14 +289,16 @@ __device__ __forceinline__ void raise(Soft& a, float m, float ch) {
     a.m = mn;
   }
 }
-// The joined parts of a warp's lanes.
-__device__ __forceinline__ Soft warp_soft(Soft a, float ch) {
+// The joined parts of a warp's lanes, or of each half's.
+__device__ __forceinline__ Soft warp_soft(Soft a, float ch, bool halves = false) {
   float m = a.m;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!halves) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
   raise(a, m, ch);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+  for (int o = 8; o; o >>= 1) a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+  if (!halves) a.s += __shfl_xor_sync(0xffffffffu, a.s, 16);
   return a;
 }
 __device__ __forceinline__ Pair warp_pair(Pair a) {
@@ -288,17 +327,22 @@ struct Walk {  // one block's shared memory
   float2 table[256];
   int parent[kVsNodes], token[kVsNodes], path[kVsNodes], child[kVsNodes];
   float u[kVsNodes];
-  // read by the first warp of each block of the cluster: two sets, used in turn
-  Soft soft[2][kVsWarps];
-  uint64_t best[2][kVsWarps];
-  int64_t sum[2][kVsWarps], sum_f[2][kVsWarps];  // of the warps' ranges: what is left of the target's weights, the draft's
+  // all warps of the cluster write theirs to every block; two sets, used in turn
+  Soft soft[2][kVsRanges];
+  union {
+    uint64_t best[2][kVsRanges];
+    int64_t sum[2][kVsRanges];  // of the ranges: what is left of the target's weights
+  };
+  int64_t sum_f[2][kVsRanges];  // the draft's
   int64_t child_e[kVsNodes], child_f[kVsNodes];
+  int child_at[kVsNodes];  // their ranges
   bool gone[kVsNodes];  // of the children: rejected, its token's weight taken out
   int64_t part[kVsWarps];
   // written by the first warp for the block
   float most, most_f;
   int act, at, range, winner;
   double kappa;
+  RowExp kf;
   int64_t threshold;
 };
 
@@ -333,13 +377,15 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x >> p.log_c, rank = blockIdx.x & ((1 << p.log_c) - 1);
   if (tid < 256) w.table[tid] = make_float2(kExpTable.hi[tid], kExpTable.lo[tid]);
-  griddep_wait();
   cg::cluster_group cl = cg::this_cluster();
+  cl.barrier_arrive();  // (waited for before the first write to another block's memory)
+  griddep_wait();
 
   const int start = p.starts[b], end = p.starts[b + 1];
   const float T = p.temperature ? p.temperature[b] : 1.f;
   const bool empty = start < 0 || end > p.n_nodes || end <= start;
   if (empty) {  // (the whole cluster)
+    cl.barrier_wait();
     if (rank == 0) {
       for (int i = tid; i < p.max_nodes; i += kVsThreads) p.path[(int64_t)b * p.max_nodes + i] = -1;
       if (tid == 0) p.n_accepted[b] = -1, p.next[b] = -1;
@@ -364,6 +410,7 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
       w.u[tid] = p.uniforms[start + tid];
     }
   }
+  cl.barrier_wait();
   __syncthreads();
 
   int node = 0, length = 1, turn = 0;
@@ -384,18 +431,17 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
     const uint32_t set0 = __ballot_sync(0xffffffffu, kid0), set1 = __ballot_sync(0xffffffffu, kid1);
     const int n_children = __popc(set0) + __popc(set1);
     const bool both = drawn && n_children > 0;  // the draft's row matters
-    int my_child = 0, my_token = -1;
-    float my_e = 0.f, my_f = 0.f;
+    const bool kid[2] = {kid0, kid1};
+    int my_token[2] = {-1, -1};
+    float my_x[2] = {0.f, 0.f}, my_y[2] = {0.f, 0.f};
     if (warp == 0) {
-      if (kid0) w.child[__popc(set0 & ((1u << lane) - 1))] = lane;
-      if (kid1) w.child[__popc(set0) + __popc(set1 & ((1u << lane) - 1))] = lane + 32;
-      __syncwarp();
-      if (lane < n_children) {
-        my_child = w.child[lane];
-        my_token = w.token[my_child];
-        if (my_token >= 0 && my_token < p.V) {
-          my_e = Load<In>::one(pe + my_token);
-          if (both) my_f = Load<In>::one(pf + my_token);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (!kid[k]) continue;
+        my_token[k] = w.token[lane + 32 * k];
+        if (my_token[k] >= 0 && my_token[k] < p.V) {
+          my_x[k] = Load<In>::one(pe + my_token[k]);
+          if (both) my_y[k] = Load<In>::one(pf + my_token[k]);
         }
       }
     }
@@ -454,81 +500,74 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
         a.s += (s[0] + s[1]) + (s[2] + s[3]);
       }, one);
       a = warp_soft(a, ch);
-      if (lane == 0) w.soft[turn][warp] = a;
-      if (greedy) {
-        best = warp_best(best);
-        if (lane == 0) w.best[turn][warp] = best;
+      if (greedy) best = warp_best(best);
+      if (lane < 1 << p.log_c) {  // a lane a block
+        Walk* q = cl.map_shared_rank(&w, lane);
+        const int at = ((team * team_warps) << p.log_c) + rank * team_warps + (warp & (team_warps - 1));
+        q->soft[turn][at] = a;
+        if (greedy) q->best[turn][at] = best;
       }
     }
     cl.sync();
     if (warp == 0) {
-      Soft e{-INFINITY, 0.f}, f = e;
+      // a lane's parts; where the draft's row is read, half a warp a row
+      Soft s[kGroup], a{-INFINITY, 0.f};
       uint64_t best = 0;
-      {
-        Soft s[kGroup];
-        const bool mine_f = (lane & (kVsWarps - 1)) >= team_warps;  // this lane's parts are the draft's
+      const int parts = both ? n_ranges >> 1 : n_ranges, step = both ? 16 : 32, first = lane & (step - 1);
+      const int row_at = both && lane >= 16 ? parts : 0;
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-          const int i = lane + 32 * g;
-          s[g] = e;
-          if (i < n_ranges) {
-            const Walk* q = cl.map_shared_rank(&w, i >> kVsLogWarps);
-            s[g] = q->soft[turn][i & (kVsWarps - 1)];
-            if (greedy) {
-              const uint64_t k = q->best[turn][i & (kVsWarps - 1)];
-              best = k > best ? k : best;
-            }
-          }
+      for (int g = 0; g < kGroup; ++g) {
+        const int i = first + step * g;
+        s[g] = Soft{-INFINITY, 0.f};
+        if (i < parts) {
+          s[g] = w.soft[turn][row_at + i];
+          if (greedy) best = w.best[turn][i] > best ? w.best[turn][i] : best;
         }
-        Soft a = s[0];
-#pragma unroll
-        for (int g = 1; g < kGroup; ++g) a.m = max_nan(a.m, s[g].m);
-        a.s = 0.f;
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) a.s += s[g].m == -INFINITY ? 0.f : s[g].s * exp2_fast((s[g].m - a.m) * ch);
-        const Soft none{-INFINITY, 0.f};
-        e = warp_soft(mine_f ? none : a, ch);
-        if (both) f = warp_soft(mine_f ? a : none, ch);
+        a.m = max_nan(a.m, s[g].m);
       }
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) a.s += s[g].m == -INFINITY ? 0.f : s[g].s * exp2_fast((s[g].m - a.m) * ch);
+      a = warp_soft(a, ch, both);
+      const Soft e{__shfl_sync(0xffffffffu, a.m, 0), __shfl_sync(0xffffffffu, a.s, 0)};
+      const Soft f{__shfl_sync(0xffffffffu, a.m, 16), __shfl_sync(0xffffffffu, a.s, 16)};
       int act = kDraw, at = 0;
       if (!(e.m > -INFINITY && e.m < INFINITY)) {
         at = -1;  // no distribution (NaN, +inf, or nothing left)
       } else if (greedy) {
         at = (int)~(uint32_t)warp_best(best);
-#pragma unroll 1
-        for (int i = lane; i < ((n_children + 31) & ~31); i += 32) {
-          const uint32_t hit = __ballot_sync(0xffffffffu, i < n_children && w.token[w.child[i < n_children ? i : 0]] == at);
-          if (hit) {
-            act = kGoOn;
-            at = w.child[i - lane + __ffs(hit) - 1];
-            break;
-          }
-        }
+        const uint32_t hit0 = __ballot_sync(0xffffffffu, my_token[0] == at), hit1 = __ballot_sync(0xffffffffu, my_token[1] == at);
+        if (hit0 | hit1) act = kGoOn, at = hit0 ? __ffs(hit0) - 1 : 31 + __ffs(hit1);
       } else if (n_children > 0 && (!drawn || (f.m > -INFINITY && f.m < INFINITY))) {
         // a child that is accepted by a margin above the fp32 sums' error: the most
         // likely end of a step.  (Errors, relative: 2^-22 of an exponential and of
         // each time a sum is rescaled, 2^-24 an addition; of an argument y = c l - c m
         // 2^-24 (|y| + |c m|) ln 2, where the weights 2^y bring |y| to log2(V) at most.)
         const float slack = 1e-5f + 3e-7f * (float)(per_t * N / 32 + 1) + 1.2e-7f * fmaxf(fabsf(e.m * ch), both ? fabsf(f.m * ch) : 0.f);
-        const bool is = lane < n_children && my_token >= 0 && my_token < p.V;
-        const float we = exp2_fast((my_e - e.m) * ch), wf = both ? exp2_fast((my_f - f.m) * ch) : 0.f, u = w.u[my_child];
-        uint32_t left_set = __ballot_sync(0xffffffffu, is);
         float left = e.s;
-        while (left_set) {
-          const int i = __ffs(left_set) - 1;
-          const float ui = __shfl_sync(0xffffffffu, u, i), ei = __shfl_sync(0xffffffffu, we, i), fi = __shfl_sync(0xffffffffu, wf, i);
-          const float r = both ? f.s * ei : ei, x = both ? ui * e.s * fi : ui * left;
-          const float near = both ? 2.f * slack * (x + r) : slack * (ui * e.s + r);
-          if (r - x > near) {
-            act = kGoOn;
-            at = __shfl_sync(0xffffffffu, my_child, i);
+        bool sure = true;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool is = kid[k] && my_token[k] >= 0 && my_token[k] < p.V;
+          const float we = exp2_fast((my_x[k] - e.m) * ch), wf = both ? exp2_fast((my_y[k] - f.m) * ch) : 0.f, u = w.u[lane + 32 * k];
+          uint32_t set = __ballot_sync(0xffffffffu, is);
+          if (k == 1 && set && !both) {  // (without those whose token an earlier child had)
+            uint32_t again = 0;
+            for (uint32_t s = set0; s; s &= s - 1) again |= __ballot_sync(0xffffffffu, my_token[1] == __shfl_sync(0xffffffffu, my_token[0], __ffs(s) - 1));
+            set &= ~again;
           }
-          if (both || !(x - r > near)) break;  // (of drawn drafts the first alone; not sure to be rejected)
-          left -= ei;
-          left_set &= ~__ballot_sync(0xffffffffu, my_token == __shfl_sync(0xffffffffu, my_token, i));  // (and its like)
+          while (set && sure) {
+            const int i = __ffs(set) - 1;
+            const float ui = __shfl_sync(0xffffffffu, u, i), ei = __shfl_sync(0xffffffffu, we, i), fi = __shfl_sync(0xffffffffu, wf, i);
+            const float r = both ? f.s * ei : ei, x = both ? ui * e.s * fi : ui * left;
+            const float near = both ? 2.f * slack * (x + r) : slack * (ui * e.s + r);
+            if (r - x > near) act = kGoOn, at = i + 32 * k;
+            sure = !both && x - r > near;  // (of drawn drafts the first alone; not sure to be rejected)
+            left -= ei;
+            set &= ~__ballot_sync(0xffffffffu, my_token[k] == __shfl_sync(0xffffffffu, my_token[k], i));  // (and its like)
+          }
         }
       }
-      if (lane == 0) w.act = act, w.at = at, w.most = e.m, w.most_f = f.m;
+      if (lane == 0) w.act = act, w.at = at, w.most = e.m, w.most_f = both ? f.m : -INFINITY;
     }
     turn ^= 1;
     __syncthreads();
@@ -546,76 +585,80 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
     const float most = w.most, most_f = w.most_f;
     const bool judged = both && most_f > -INFINITY && most_f < INFINITY;  // the draft's row is a distribution
     const RowExp ee = row_exp(most, ch, c_lo), ef = row_exp(judged ? most_f : 0.f, ch, c_lo);
+    RowExp kf = ef;  // the draft's times kappa
 
     // ---- else the sums in more bits
-    if (tid < n_children) {
-      const int x = w.token[w.child[tid]];
-      const bool is = x >= 0 && x < p.V;
-      w.child_e[tid] = is ? fixed(weight(Load<In>::one(pe + x), ee, w.table), scale) : -1;
-      w.child_f[tid] = is && judged ? fixed(weight(Load<In>::one(pf + x), ef, w.table), scale) : 0;
-      w.gone[tid] = false;
+    if (warp == 0) {  // the children in order, and their weights
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (!kid[k]) continue;
+        const int i = (k ? __popc(set0) : 0) + __popc((k ? set1 : set0) & ((1u << lane) - 1));
+        const bool is = my_token[k] >= 0 && my_token[k] < p.V;
+        auto whole_weight = [&](float x, const RowExp& x_of) {
+          const Raw r = weight_raw(x, x_of, w.table);
+          return fixed(__fmul_rn(r.h, r.s), __fmul_rn(r.l, r.s), scale);
+        };
+        w.child[i] = lane + 32 * k;
+        w.child_e[i] = is ? whole_weight(my_x[k], ee) : -1;
+        w.child_f[i] = is && judged ? whole_weight(my_y[k], ef) : 0;
+        w.child_at[i] = is ? (my_token[k] + skew) / N / per : 0;
+        w.gone[i] = false;
+      }
     }
     double kappa = 0.0;
-    Pair kp{0.f, 0.f};
-    auto left_of = [&](const float (&xe)[N], const float (&xf)[N], Pair (&r)[N]) {  // what is left of a vector's weights
-#pragma unroll
-      for (int k = 0; k < N; ++k) r[k] = residual(weight(xe[k], ee, w.table), weight(xf[k], ef, w.table), kp);
-    };
-    auto total = [&](const Row<In>& row, const RowExp& x_of) {  // this warp's range of a row
-      // In two parts: what a weight has in steps of 2^-17 of the unit, whose sum is
-      // exact below 2^6, and the rest.  Both go to a pair every 32 elements.
-      constexpr float kGrid = 96.f;  // 1.5 2^6
+    // Sums of parts: to a pair every 32 elements, while the high ones' sum is exact.
+    struct Sum {
       Pair a{0.f, 0.f};
       float hi = 0.f, lo = 0.f;
-      int n = 0;
+      __device__ void add(const Parts& r) {
+        hi = __fadd_rn(hi, r.hi);
+        lo = __fadd_rn(lo, r.lo);
+      }
+      __device__ void flush() {
+        accumulate(a, Pair{hi, lo});
+        hi = lo = 0.f;
+      }
+    };
+    auto total = [&](const Row<In>& row, const RowExp& x_of) {  // this warp's range of a row
+      Sum sum;
       auto one = [&](const float (&x)[N], int) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const Raw r = weight_raw(x[k], x_of, w.table);
-          const float l = __fmul_rn(r.l, r.s);
-          const float top = __fsub_rn(__fadd_rn(fmaf(r.h, r.s, l), kGrid), kGrid);
-          lo = __fadd_rn(lo, __fadd_rn(fmaf(r.h, r.s, -top), l));
-          hi = __fadd_rn(hi, top);
-        }
-        if (++n == 32 / N) {
-          accumulate(a, Pair{hi, lo});
-          hi = lo = 0.f;
-          n = 0;
-        }
+        for (int k = 0; k < N; ++k) sum.add(parts(weight_raw(x[k], x_of, w.table)));
+        sum.flush();
       };
       row.template each<4>(j0 + lane, j1, [&](const uint4 (&v)[4], int) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float x[N];
           Load<In>::unpack(v[k], x);
-          one(x, 0);
-        }
-      }, one);
-      accumulate(a, Pair{hi, lo});
-      return fixed(warp_pair(a), scale);
-    };
-    auto sums = [&](bool draft) {  // this warp's range: what is left of the target's weights, and the draft's
-      int64_t e, f = 0;
-      if (kappa > 0.0) {
-        Pair a{0.f, 0.f};
-#pragma unroll 2
-        for (int j = j0 + lane; j < j1; j += 32) {
-          float xe[N], xf[N];
-          Pair r[N];
-          re.load(j, xe);
-          rf.load(j, xf);
-          left_of(xe, xf, r);
 #pragma unroll
-          for (int k = 0; k < N; ++k) accumulate(a, r[k]);
+          for (int i = 0; i < N; ++i) sum.add(parts(weight_raw(x[i], x_of, w.table)));
         }
-        e = fixed(warp_pair(a), scale);
-      } else {
-        e = total(re, ee);
-        if (draft) f = total(rf, ef);
+        sum.flush();
+      }, one);
+      const Pair a = warp_pair(sum.a);
+      return fixed(a.h, a.l, scale);
+    };
+    auto total_left = [&]() {  // of what is left, with the draft's part taken out
+      Sum sum;
+#pragma unroll 1
+      for (int j = j0 + lane; j < j1; j += 32) {
+        float xe[N], xf[N];
+        re.load(j, xe);
+        rf.load(j, xf);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum.add(residual(weight_raw(xe[i], ee, w.table), weight_raw<true>(xf[i], kf, w.table)));
+        sum.flush();
       }
-      if (lane == 0) {
-        w.sum[turn][warp] = e;
-        if (draft) w.sum_f[turn][warp] = f;
+      const Pair a = warp_pair(sum.a);
+      return fixed(a.h, a.l, scale);
+    };
+    auto sums = [&](bool draft) {  // this warp's range: what is left of the target's weights, and the draft's, to all blocks
+      const int64_t e = kappa > 0.0 ? total_left() : total(re, ee), f = draft ? total(rf, ef) : 0;
+      if (lane < 1 << p.log_c) {
+        Walk* q = cl.map_shared_rank(&w, lane);
+        q->sum[turn][rank * kVsWarps + warp] = e;
+        if (draft) q->sum_f[turn][rank * kVsWarps + warp] = f;
       }
     };
     // of the first warp's lanes, in order: the ranges group * lane on
@@ -630,9 +673,8 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
           const int i = lane * group + g;
           mine[g] = 0;
           if (g < group && i < n_ranges) {
-            const Walk* q = cl.map_shared_rank(&w, i >> kVsLogWarps);
-            mine[g] = q->sum[turn][i & (kVsWarps - 1)];
-            if (draft) d += q->sum_f[turn][i & (kVsWarps - 1)];
+            mine[g] = w.sum[turn][i];
+            if (draft) d += w.sum_f[turn][i];
           }
           s += mine[g];
         }
@@ -676,13 +718,13 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
             break;
           }
         }
-        if (lane == 0) w.act = act, w.at = at, w.kappa = kappa;
+        if (act == kReject) kf = scaled(ef, kappa, w.table);
+        if (lane == 0) w.act = act, w.at = at, w.kappa = kappa, w.kf = kf;
       }
       __syncthreads();
       if (w.act != kReject) break;
       kappa = w.kappa;
-      kp.h = (float)kappa;
-      kp.l = (float)(kappa - (double)kp.h);
+      kf = w.kf;
       sums(false);
       gather(false);
     }
@@ -699,7 +741,7 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
       if (!judged) {  // what the rejected drafts that were chosen leave of the ranges' sums
         for (int i = 0; i < n_children; ++i) {
           if (!w.gone[i]) continue;
-          const int at = (w.token[w.child[i]] + skew) / N / per;  // its range
+          const int at = w.child_at[i];
 #pragma unroll
           for (int g = 0; g < kGroup; ++g)
             if (at == lane * group + g) {
@@ -748,15 +790,15 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
     if (rank != w.range / kVsWarps) break;
     const int k0 = min(n_vec, w.range * per), k1 = min(n_vec, k0 + per), each = (per + kVsThreads - 1) / kVsThreads;
     const int a0 = min(k1, k0 + tid * each), a1 = min(k1, a0 + each);
-    auto left_at = [&](int j, Pair (&r)[N]) {
+    auto left_at = [&](int j, int64_t (&r)[N]) {  // what is left of vector j's weights
       float xe[N], xf[N];
       re.load(j, xe);
-      if (kappa > 0.0) {
-        rf.load(j, xf);
-        left_of(xe, xf, r);
-      } else {
+      if (kappa > 0.0) rf.load(j, xf);
 #pragma unroll
-        for (int k = 0; k < N; ++k) r[k] = weight(xe[k], ee, w.table);
+      for (int k = 0; k < N; ++k) {
+        const Raw e = weight_raw(xe[k], ee, w.table);
+        const Parts a = kappa > 0.0 ? residual(e, weight_raw<true>(xf[k], kf, w.table)) : parts(e);
+        r[k] = fixed(a.hi, a.lo, scale);
       }
       if (out) {
         for (int i = 0; i < n_children; ++i) {
@@ -764,18 +806,17 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
           if (!w.gone[i] || k < 0 || k >= N) continue;
 #pragma unroll
           for (int e = 0; e < N; ++e)
-            if (e == k) r[e] = Pair{0.f, 0.f};
+            if (e == k) r[e] = 0;
         }
       }
     };
-    Pair a{0.f, 0.f};
+    int64_t r[N], own = 0;
     for (int j = a0; j < a1; ++j) {
-      Pair r[N];
       left_at(j, r);
 #pragma unroll
-      for (int k = 0; k < N; ++k) accumulate(a, r[k]);
+      for (int k = 0; k < N; ++k) own += r[k];
     }
-    const int64_t own = fixed(a, scale), of_warp = warp_total(own);
+    const int64_t of_warp = warp_total(own);
     if (lane == 0) w.part[warp] = of_warp;
     __syncthreads();
     if (warp == 0) {
@@ -793,14 +834,12 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
         int64_t run = 0;
         bool found = false;
         for (int j = a0; j < a1 && !found; ++j) {
-          Pair r[N];
-          left_at(j, r);
+          if (each > 1) left_at(j, r);  // (one vector is still there)
 #pragma unroll
           for (int k = 0; k < N; ++k) {
-            const int64_t q = fixed(r[k], scale);
-            if (found || q <= 0) continue;
+            if (found || r[k] <= 0) continue;
             next = j * N - skew + k;  // (the last with any where rounding leaves none that passes)
-            run += q;
+            run += r[k];
             found = run > t;
           }
         }
@@ -814,7 +853,7 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
     for (int i = tid; i < p.max_nodes; i += kVsThreads) p.path[(int64_t)b * p.max_nodes + i] = i < m ? w.path[i] : -1;
     if (tid == 0) p.n_accepted[b] = length - 1;
   }
-  cl.sync();  // nobody reads a block's shared memory after its end
+  // (nothing is written to another block's memory after the last exchange)
 }
 
 template <typename In>
@@ -871,7 +910,6 @@ extern "C" int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_
   VsParams p{logits, row_stride, draft_logits, draft_stride, V, n_seqs, n_nodes, max_nodes, replacement, 0,
              tokens, parents, starts, uniforms, temperature, path, out_n_accepted, out_next_token};
   while ((2 << p.log_c) <= kVsMaxCluster && ((int64_t)n_seqs << (p.log_c + 1)) <= 2LL * sms && (V >> (p.log_c + 1)) >= 1024) ++p.log_c;
-  if (getenv("VSC")) p.log_c = atoi(getenv("VSC"));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = dtype == MOE_ACT_F32 ? verify_sample_launch<float>(p, st) : verify_sample_launch<__nv_bfloat16>(p, st);
   if (e != cudaSuccess) {
