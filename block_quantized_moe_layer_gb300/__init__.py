@@ -369,35 +369,46 @@ def verify_sample(logits, tokens, parents, starts, uniforms, max_nodes, draft_lo
     nodes."""
     import torch
     f32, i32, dt = torch.float32, torch.int32, logits.dtype
-    _require(logits.dim() == 2 and logits.is_cuda and (dt is f32 or dt is torch.bfloat16),
-             "verify_sample: logits must be fp32 or bf16 [N, V] on the GPU")
-    N, V = logits.shape
-    stride, dev = logits.stride(), logits.device
-    _require(stride[1] == 1 or V == 1, "verify_sample: each row of logits must be contiguous")
-    dstride = (0, 1)
-    if draft_logits is not None:
-        dstride = draft_logits.stride()
-        _require(draft_logits.shape == (N, V) and draft_logits.dtype is dt and draft_logits.is_cuda
-                 and (dstride[1] == 1 or V == 1), "verify_sample: draft_logits must have logits' shape and type")
-    for name, t, want, n in (("tokens", tokens, i32, N), ("parents", parents, i32, N), ("uniforms", uniforms, f32, N)):
-        _require((t is None and name == "parents")
-                 or (t.shape == (n,) and t.dtype is want and t.is_cuda and t.is_contiguous()),
-                 f"verify_sample: {name} must be contiguous {want} [N] on the GPU")
-    _require(starts.dim() == 1 and starts.shape[0] >= 1 and starts.dtype is i32 and starts.is_cuda and starts.is_contiguous(),
-             "verify_sample: starts must be contiguous int32 [sequences + 1] on the GPU")
-    n = starts.shape[0] - 1
-    _require(temperature is None or (temperature.shape == (n,) and temperature.dtype is f32 and temperature.is_cuda
-                                     and temperature.is_contiguous()),
-             "verify_sample: temperature must be contiguous fp32 [sequences] on the GPU")
-    _require(1 <= max_nodes <= 64, "verify_sample: max_nodes outside 1..64")
+    shape, stride, n = logits.shape, logits.stride(), starts.numel() - 1
+    if len(shape) != 2:
+        raise MoEError(MOE_EINVAL, "verify_sample: logits must be fp32 or bf16 [N, V] on the GPU")
+    N, V = shape
+    rows = (N,)
+    dstride = stride if draft_logits is None else draft_logits.stride()
+    # (on a decode step's critical path: one test, spelled out only on failure)
+    if not ((dt is f32 or dt is torch.bfloat16) and logits.is_cuda and (stride[1] == 1 or V == 1)
+            and (draft_logits is None or (draft_logits.shape == shape and draft_logits.dtype is dt and draft_logits.is_cuda
+                                          and (dstride[1] == 1 or V == 1)))
+            and tokens.shape == rows and tokens.dtype is i32 and tokens.is_cuda and tokens.is_contiguous()
+            and (parents is None or (parents.shape == rows and parents.dtype is i32 and parents.is_cuda and parents.is_contiguous()))
+            and uniforms.shape == rows and uniforms.dtype is f32 and uniforms.is_cuda and uniforms.is_contiguous()
+            and n >= 0 and starts.dim() == 1 and starts.dtype is i32 and starts.is_cuda and starts.is_contiguous()
+            and (temperature is None or (temperature.shape == (n,) and temperature.dtype is f32 and temperature.is_cuda
+                                         and temperature.is_contiguous()))
+            and 1 <= max_nodes <= 64):
+        _require(logits.is_cuda and (dt is f32 or dt is torch.bfloat16), "verify_sample: logits must be fp32 or bf16 [N, V] on the GPU")
+        _require(stride[1] == 1 or V == 1, "verify_sample: each row of logits must be contiguous")
+        _require(draft_logits is None or (draft_logits.shape == shape and draft_logits.dtype is dt and draft_logits.is_cuda
+                                          and (dstride[1] == 1 or V == 1)), "verify_sample: draft_logits must have logits' shape and type")
+        for name, t, want in (("tokens", tokens, i32), ("parents", parents, i32), ("uniforms", uniforms, f32)):
+            _require((t is None and name == "parents") or (t.shape == rows and t.dtype is want and t.is_cuda and t.is_contiguous()),
+                     f"verify_sample: {name} must be contiguous {want} [N] on the GPU")
+        _require(n >= 0 and starts.dim() == 1 and starts.dtype is i32 and starts.is_cuda and starts.is_contiguous(),
+                 "verify_sample: starts must be contiguous int32 [sequences + 1] on the GPU")
+        _require(temperature is None or (temperature.shape == (n,) and temperature.dtype is f32 and temperature.is_cuda
+                                         and temperature.is_contiguous()),
+                 "verify_sample: temperature must be contiguous fp32 [sequences] on the GPU")
+        _require(False, "verify_sample: max_nodes outside 1..64")
+    # (three blocks: a view costs the host more than a block)
+    dev = logits.device
     path = _result((n, max_nodes), i32, dev, stream)
     acc = _result((n,), i32, dev, stream)
     nxt = _result((n,), i32, dev, stream)
-    rc = lib().mtp_verify_sample(
+    rc = (_lib or lib()).mtp_verify_sample(
         logits.data_ptr(), ACT_F32 if dt is f32 else ACT_BF16, stride[0],
         None if draft_logits is None else draft_logits.data_ptr(), dstride[0], V, tokens.data_ptr(),
         None if parents is None else parents.data_ptr(), starts.data_ptr(), n, N, max_nodes, uniforms.data_ptr(),
-        None if temperature is None else temperature.data_ptr(), int(replacement), path.data_ptr(), acc.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), 1 if replacement else 0, path.data_ptr(), acc.data_ptr(),
         nxt.data_ptr(), _raw_stream(stream, logits))
     if rc:
         _check(rc)

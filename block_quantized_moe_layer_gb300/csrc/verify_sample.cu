@@ -19,13 +19,24 @@
 // the parts are exchanged through distributed shared memory, and every block
 // comes to the same decisions from the same numbers.  One launch, no workspace.
 //
-// Precision.  A draw that falls within d of a border of two tokens can go
-// either way, and with 150000 tokens there are that many borders: fp32 sums
-// (2^-22) would miss the right token in several draws of a hundred.  So weights
-// are pairs of fp32 numbers, right to some 2^-33, and their sums carry the
-// rounding errors along (two-sum).  2^y of y = round(256 y) / 256 + g: a table
-// of 256 entries, and 1 + g (L + g (L^2/2 + g L^3/6)), L = ln 2, of its series
-// (|g| <= 2^-9).
+// A step is decided by fp32 sums (exp2 of the hardware, one pass over the rows)
+// where a child is accepted by more than their error, as it mostly is.  Only the
+// last row of a walk, and the few steps that are close, need more bits:
+// a draw that falls within d of a border of two tokens can go either way, and
+// with 150000 tokens there are that many borders; fp32 sums would miss the right
+// token in several draws of a hundred.  There a weight is a pair of fp32 numbers,
+// right to some 2^-33, sums carry their rounding errors along, and the ranges'
+// sums are whole numbers, exact in any order.  2^y of y = round(256 y) / 256 + g:
+// a table and a short series (Tang's table-driven exponential), 1 + g (L + g
+// (L^2/2 + g L^3/6)), L = ln 2, |g| <= 2^-9.
+//
+// Measured: a chain of 4 nodes, 32768 fp32 logits, 13.4 us (3 us a step: a pass,
+// a cluster barrier, the decision; 4 for the last one); 4 trees of 64 nodes 14.8;
+// 64 chains of 4 with drawn drafts, 151936 bf16 logits, 76 us (the rows read
+// take 20: a step 9 us; a rejected drawn draft, whose two rows are summed in more
+// bits and then looked at twice again, 50); 32 trees of 12 nodes, 151936 fp32,
+// 31 us.  16, 8 and 4 blocks a sequence take 31, 34 and 39 us there; 512 threads
+// a block and two blocks a multiprocessor 36, 1024 threads 43.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -36,11 +47,11 @@
 namespace moe {
 namespace {
 
-constexpr int kVsThreads = 512;
-constexpr int kVsWarps = kVsThreads / 32, kVsLogWarps = 4;
+constexpr int kVsThreads = 256;
+constexpr int kVsWarps = kVsThreads / 32, kVsLogWarps = 3;
 static_assert(kVsWarps == 1 << kVsLogWarps, "a power of two");
 constexpr int kVsNodes = 64;
-constexpr int kVsMaxCluster = 8;
+constexpr int kVsMaxCluster = 16, kVsBlocks = 2;  // blocks a sequence at most; a multiprocessor
 constexpr int kVsRanges = kVsMaxCluster * kVsWarps;  // most ranges of a row
 constexpr int kVsBatch = 4;  // 16-byte loads in flight a thread
 
@@ -55,7 +66,7 @@ struct VsParams {
   int32_t *path, *n_accepted, *next;
 };
 
-// 2^(i/256) as two fp32 numbers, from its series.
+// 2^(i/256) / (1 + i/256) as two fp32 numbers, from its series.
 struct ExpTable {
   float hi[256], lo[256];
 };
@@ -68,12 +79,40 @@ constexpr ExpTable make_exp_table() {
       term *= x / k;
       sum += term;
     }
+    sum /= 1.0 + i / 256.0;
     t.hi[i] = (float)sum;
     t.lo[i] = (float)(sum - (double)t.hi[i]);
   }
   return t;
 }
 __device__ constexpr ExpTable kExpTable = make_exp_table();
+
+// Two fp32 numbers in a register pair, an instruction for both.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ float f2_lo(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float f2_hi(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 struct Pair {  // h + l
   float h, l;
@@ -110,7 +149,7 @@ __device__ __forceinline__ RowExp row_exp(float most, float ch, float cl) {
   r.cl = cl;
   r.magic = kMagic;
   r.rest = 0.f;
-  r.scale0 = ((uint32_t)(127 - (int)top) << 23) - ((__float_as_uint(kMagic) >> 8) << 23);
+  r.scale0 = ((uint32_t)(127 - (int)top) << 23) - (__float_as_uint(kMagic) << 15);
   return r;
 }
 // The same times k > 0 (both weights of a logit are compared); held below 8
@@ -124,7 +163,8 @@ __device__ __forceinline__ RowExp scaled(RowExp r, double k, const float2* table
   int i = __float2int_rn(256.f * __log2f(mh));
   if (i > 255) i = 0, ++e, mh *= 0.5f, ml *= 0.5f;
   const float2 t = table[max(i, 0)];
-  const float d = __fdiv_rn((mh - t.x) + (ml - t.y), t.x);
+  const float step = 1.f + (float)max(i, 0) * 0.00390625f;
+  const float d = __fdiv_rn(fmaf(-t.x, step, mh) + fmaf(-t.y, step, ml), t.x * step);
   const float steps = (float)e + (float)max(i, 0) * 0.00390625f;
   r.magic = kMagic + steps;
   r.rest = d * fmaf(d, fmaf(d, 0.48089835f, -0.72134752f), 1.44269504f);
@@ -132,39 +172,51 @@ __device__ __forceinline__ RowExp scaled(RowExp r, double k, const float2* table
   r.ceil = (r.top - steps + 3.f) / r.ch;
   return r;
 }
-// 2^y = (h + l) s: y = c x = (steps of 2^-8: table entry and s) + g.
+// 2^y = (h + l) s of two logits: y = c x = (steps of 2^-8) + g; the steps' bits are
+// the exponent of s and the eight first ones of its mantissa, by whose value the
+// table's entries are divided.
 struct Raw {
-  float h, l, s;
+  uint64_t h, l, s;
 };
 template <bool SCALED = false>
-__device__ __forceinline__ Raw weight_raw(float logit, const RowExp& r, const float2* table) {
+__device__ __forceinline__ Raw weight(float x0, float x1, const RowExp& r, const float2* table) {
   constexpr float L1 = 0.693147180559945f, L2 = 0.240226506959101f, L3 = 0.0555041086648216f;
-  float x = fmaxf(__fsub_rn(logit, r.ref), r.floor);
-  if (SCALED) x = fminf(x, r.ceil);
-  const float k = fmaf(x, r.ch, r.magic);
-  const uint32_t bits = __float_as_uint(k);
-  const float2 t = table[bits & 255];
-  float g = fmaf(x, r.cl, fmaf(x, r.ch, -__fsub_rn(k, r.magic)));
-  if (SCALED) g += r.rest;
-  const float p = __fmul_rn(g, fmaf(g, fmaf(g, L3, L2), L1));
-  return Raw{t.x, fmaf(t.x, p, t.y), __uint_as_float(((bits >> 8) << 23) + r.scale0)};
+  const uint64_t ch = f2(r.ch, r.ch), magic = f2(r.magic, r.magic);
+  uint64_t x = f2_sub(f2(x0, x1), f2(r.ref, r.ref));
+  x0 = fmaxf(f2_lo(x), r.floor);
+  x1 = fmaxf(f2_hi(x), r.floor);
+  if (SCALED) x0 = fminf(x0, r.ceil), x1 = fminf(x1, r.ceil);
+  x = f2(x0, x1);
+  const uint64_t k = f2_fma(x, ch, magic);
+  const uint32_t k0 = (uint32_t)k, k1 = (uint32_t)(k >> 32);
+  const float2 t0 = table[k0 & 255], t1 = table[k1 & 255];
+  uint64_t g = f2_fma(x, f2(r.cl, r.cl), f2_fma(x, ch, f2_sub(magic, k)));
+  if (SCALED) g = f2_add(g, f2(r.rest, r.rest));
+  const uint64_t p = f2_mul(g, f2_fma(g, f2_fma(g, f2(L3, L3), f2(L2, L2)), f2(L1, L1)));
+  Raw w;
+  w.h = f2(t0.x, t1.x);
+  w.l = f2_fma(w.h, p, f2(t0.y, t1.y));
+  w.s = (uint64_t)((k0 << 15) + r.scale0) | ((uint64_t)((k1 << 15) + r.scale0) << 32);
+  return w;
 }
-// A weight in two parts: what it has in steps of 2^-17 of the unit, so that a sum
-// of them is exact below 2^6, and the rest.
+// Two weights, each in two parts: what it has in steps of 2^-17 of the unit, so
+// that a sum of them is exact below 2^6, and the rest.
 struct Parts {
-  float hi, lo;
+  uint64_t hi, lo;
 };
 __device__ __forceinline__ Parts parts(const Raw& r) {
-  constexpr float kGrid = 96.f;  // 1.5 2^6
-  const float l = __fmul_rn(r.l, r.s);
-  const float top = __fsub_rn(__fadd_rn(fmaf(r.h, r.s, l), kGrid), kGrid);
-  return Parts{top, __fadd_rn(fmaf(r.h, r.s, -top), l)};
+  const uint64_t grid = f2(96.f, 96.f);  // 1.5 2^6
+  const uint64_t l = f2_mul(r.l, r.s), top = f2_sub(f2_add(f2_fma(r.h, r.s, l), grid), grid);
+  return Parts{top, f2_add(f2_fma(r.h, r.s, f2_sub(0, top)), l)};
 }
 // (e - k f)+, f's exponential scaled by k
 __device__ __forceinline__ Parts residual(const Raw& e, const Raw& f) {
   const Parts a = parts(e), b = parts(f);
-  const Parts r{__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)};
-  return __fadd_rn(r.hi, r.lo) > 0.f ? r : Parts{0.f, 0.f};
+  Parts r{f2_sub(a.hi, b.hi), f2_sub(a.lo, b.lo)};
+  const uint64_t sum = f2_add(r.hi, r.lo);
+  if (!(f2_lo(sum) > 0.f)) r.hi &= 0xFFFFFFFF00000000ull, r.lo &= 0xFFFFFFFF00000000ull;
+  if (!(f2_hi(sum) > 0.f)) r.hi &= 0xFFFFFFFFull, r.lo &= 0xFFFFFFFFull;
+  return r;
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
@@ -247,24 +299,33 @@ struct Row {
       for (int i = 0; i < N; ++i) x[i] = e + i >= 0 && e + i < V ? Load<In>::one(p + e + i) : -INFINITY;
     }
   }
-  // Vectors j, j + 32, ... below j1, kBatch at once: batch(words, j) where those
-  // below j1 are whole (-inf past them), else one(x, first element) each.
+  // A warp's vectors [j0, j1), a lane every 32nd, kBatch at once and the next ones
+  // on their way: batch(words, n, vector) of n rounds where those of all lanes
+  // are whole (-inf past j1), else one(x, first element) each.
   template <int kBatch, class B, class F>
-  __device__ void each(int j, int j1, B batch, F one) const {
-    for (; j < j1; j += 32 * kBatch) {
-      if (whole(j) && whole(min(j + 32 * (kBatch - 1), j + ((j1 - 1 - j) & ~31)))) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) v[b] = raw_or_none(j + 32 * b, j1);
-        batch(v, j);
-      } else {
+  __device__ void each(int j0, int j1, B batch, F one) const {
+    const int lane = threadIdx.x & 31;
+    const bool all = j0 < j1 && whole(j0) && whole(j1 - 1);
+    if (!all) {
 #pragma unroll 1
-        for (int b = 0; b < kBatch && j + 32 * b < j1; ++b) {
-          float x[N];
-          load(j + 32 * b, x);
-          one(x, (j + 32 * b) * N - skew);
-        }
+      for (int j = j0 + lane; j < j1; j += 32) {
+        float x[N];
+        load(j, x);
+        one(x, j * N - skew);
       }
+      return;
+    }
+    uint4 v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) v[b] = raw_or_none(j0 + lane + 32 * b, j1);
+#pragma unroll 1
+    for (int j = j0; j < j1; j += 32 * kBatch) {
+      uint4 u[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) u[b] = v[b];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) v[b] = raw_or_none(j + lane + 32 * (kBatch + b), j1);
+      batch(u, min(kBatch, (j1 - j + 31) >> 5), j + lane);
     }
   }
 };
@@ -368,7 +429,7 @@ __device__ __forceinline__ int64_t warp_total(int64_t v) {
 }
 
 template <typename In>
-__global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __grid_constant__ VsParams p) {
+__global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(const __grid_constant__ VsParams p) {
   namespace cg = cooperative_groups;
   constexpr int N = Load<In>::kN;
   constexpr int kGroup = kVsMaxCluster * kVsWarps / 32;  // most ranges of a lane of the first warp
@@ -472,32 +533,38 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
 #pragma unroll
         for (int i = 0; i < N; ++i) a.s += exp2_fast(fmaf(x[i], ch, base));
       };
-      row.template each<kVsBatch>(a0 + lane, a1, [&](const uint4 (&v)[kVsBatch], int j) {
-        if (greedy) {
+      row.template each<kVsBatch>(a0, a1, [&](const uint4 (&v)[kVsBatch], int n, int j) {
+        const float mx = Load<In>::most(v);
+        if (greedy && mx > a.m) {
 #pragma unroll
           for (int k = 0; k < kVsBatch; ++k) {
             float x[N];
             Load<In>::unpack(v[k], x);
-            one(x, (j + 32 * k) * N - skew);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (x[i] > a.m) best = order_key(x[i], (j + 32 * k) * N - skew + i), a.m = x[i];
           }
-          return;
         }
-        const float mx = Load<In>::most(v);
-        if (n_children == 0) {
+        if (greedy || n_children == 0) {
           a.m = max_nan(a.m, mx);
           return;
         }
         raise(a, mx, ch);
         const float base = a.m == -INFINITY ? 0.f : -a.m * ch;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t s[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < kVsBatch; ++k) {
+          if (k >= n) break;
           float x[N];
           Load<In>::unpack(v[k], x);
 #pragma unroll
-          for (int i = 0; i < N; ++i) s[i & 3] += exp2_fast(fmaf(x[i], ch, base));
+          for (int i = 0; i < N; i += 2) {
+            const uint64_t y = f2_fma(f2(x[i], x[i + 1]), f2(ch, ch), f2(base, base));
+            s[(i >> 1) & 1] = f2_add(s[(i >> 1) & 1], f2(exp2_fast(f2_lo(y)), exp2_fast(f2_hi(y))));
+          }
         }
-        a.s += (s[0] + s[1]) + (s[2] + s[3]);
+        s[0] = f2_add(s[0], s[1]);
+        a.s += f2_lo(s[0]) + f2_hi(s[0]);
       }, one);
       a = warp_soft(a, ch);
       if (greedy) best = warp_best(best);
@@ -595,8 +662,8 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
         const int i = (k ? __popc(set0) : 0) + __popc((k ? set1 : set0) & ((1u << lane) - 1));
         const bool is = my_token[k] >= 0 && my_token[k] < p.V;
         auto whole_weight = [&](float x, const RowExp& x_of) {
-          const Raw r = weight_raw(x, x_of, w.table);
-          return fixed(__fmul_rn(r.h, r.s), __fmul_rn(r.l, r.s), scale);
+          const Parts r = parts(weight(x, x, x_of, w.table));
+          return fixed(f2_lo(r.hi), f2_lo(r.lo), scale);
         };
         w.child[i] = lane + 32 * k;
         w.child_e[i] = is ? whole_weight(my_x[k], ee) : -1;
@@ -609,30 +676,31 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
     // Sums of parts: to a pair every 32 elements, while the high ones' sum is exact.
     struct Sum {
       Pair a{0.f, 0.f};
-      float hi = 0.f, lo = 0.f;
+      uint64_t hi = 0, lo = 0;
       __device__ void add(const Parts& r) {
-        hi = __fadd_rn(hi, r.hi);
-        lo = __fadd_rn(lo, r.lo);
+        hi = f2_add(hi, r.hi);
+        lo = f2_add(lo, r.lo);
       }
       __device__ void flush() {
-        accumulate(a, Pair{hi, lo});
-        hi = lo = 0.f;
+        accumulate(a, Pair{__fadd_rn(f2_lo(hi), f2_hi(hi)), __fadd_rn(f2_lo(lo), f2_hi(lo))});
+        hi = lo = 0;
       }
     };
     auto total = [&](const Row<In>& row, const RowExp& x_of) {  // this warp's range of a row
       Sum sum;
       auto one = [&](const float (&x)[N], int) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) sum.add(parts(weight_raw(x[k], x_of, w.table)));
+        for (int k = 0; k < N; k += 2) sum.add(parts(weight(x[k], x[k + 1], x_of, w.table)));
         sum.flush();
       };
-      row.template each<4>(j0 + lane, j1, [&](const uint4 (&v)[4], int) {
+      row.template each<kVsBatch>(j0, j1, [&](const uint4 (&v)[kVsBatch], int n, int) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kVsBatch; ++k) {
+          if (k >= n) break;
           float x[N];
           Load<In>::unpack(v[k], x);
 #pragma unroll
-          for (int i = 0; i < N; ++i) sum.add(parts(weight_raw(x[i], x_of, w.table)));
+          for (int i = 0; i < N; i += 2) sum.add(parts(weight(x[i], x[i + 1], x_of, w.table)));
         }
         sum.flush();
       }, one);
@@ -641,14 +709,31 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
     };
     auto total_left = [&]() {  // of what is left, with the draft's part taken out
       Sum sum;
-#pragma unroll 1
-      for (int j = j0 + lane; j < j1; j += 32) {
-        float xe[N], xf[N];
-        re.load(j, xe);
-        rf.load(j, xf);
+      auto add = [&](const float (&xe)[N], const float (&xf)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum.add(residual(weight_raw(xe[i], ee, w.table), weight_raw<true>(xf[i], kf, w.table)));
+        for (int i = 0; i < N; i += 2)
+          sum.add(residual(weight(xe[i], xe[i + 1], ee, w.table), weight<true>(xf[i], xf[i + 1], kf, w.table)));
         sum.flush();
+      };
+      if (j0 < j1 && re.whole(j0) && re.whole(j1 - 1) && rf.aligned) {
+        uint4 ve = re.raw_or_none(j0 + lane, j1), vf = rf.raw_or_none(j0 + lane, j1);
+#pragma unroll 1
+        for (int j = j0 + lane; j < j1; j += 32) {
+          float xe[N], xf[N];
+          Load<In>::unpack(ve, xe);
+          Load<In>::unpack(vf, xf);
+          ve = re.raw_or_none(j + 32, j1);
+          vf = rf.raw_or_none(j + 32, j1);
+          add(xe, xf);
+        }
+      } else {
+#pragma unroll 1
+        for (int j = j0 + lane; j < j1; j += 32) {
+          float xe[N], xf[N];
+          re.load(j, xe);
+          rf.load(j, xf);
+          add(xe, xf);
+        }
       }
       const Pair a = warp_pair(sum.a);
       return fixed(a.h, a.l, scale);
@@ -795,10 +880,11 @@ __global__ void __launch_bounds__(kVsThreads, 2) verify_sample_kernel(const __gr
       re.load(j, xe);
       if (kappa > 0.0) rf.load(j, xf);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const Raw e = weight_raw(xe[k], ee, w.table);
-        const Parts a = kappa > 0.0 ? residual(e, weight_raw<true>(xf[k], kf, w.table)) : parts(e);
-        r[k] = fixed(a.hi, a.lo, scale);
+      for (int k = 0; k < N; k += 2) {
+        const Raw e = weight(xe[k], xe[k + 1], ee, w.table);
+        const Parts a = kappa > 0.0 ? residual(e, weight<true>(xf[k], xf[k + 1], kf, w.table)) : parts(e);
+        r[k] = fixed(f2_lo(a.hi), f2_lo(a.lo), scale);
+        r[k + 1] = fixed(f2_hi(a.hi), f2_hi(a.lo), scale);
       }
       if (out) {
         for (int i = 0; i < n_children; ++i) {
@@ -871,6 +957,10 @@ cudaError_t verify_sample_launch(const VsParams& p, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if (p.log_c > 3) {  // above the portable size
+    const cudaError_t e = cudaFuncSetAttribute(verify_sample_kernel<In>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&cfg, verify_sample_kernel<In>, p);
 }
 
@@ -909,7 +999,7 @@ extern "C" int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_
   }
   VsParams p{logits, row_stride, draft_logits, draft_stride, V, n_seqs, n_nodes, max_nodes, replacement, 0,
              tokens, parents, starts, uniforms, temperature, path, out_n_accepted, out_next_token};
-  while ((2 << p.log_c) <= kVsMaxCluster && ((int64_t)n_seqs << (p.log_c + 1)) <= 2LL * sms && (V >> (p.log_c + 1)) >= 1024) ++p.log_c;
+  while ((2 << p.log_c) <= kVsMaxCluster && ((int64_t)n_seqs << (p.log_c + 1)) <= (int64_t)kVsBlocks * sms && (V >> (p.log_c + 1)) >= 1024) ++p.log_c;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = dtype == MOE_ACT_F32 ? verify_sample_launch<float>(p, st) : verify_sample_launch<__nv_bfloat16>(p, st);
   if (e != cudaSuccess) {
