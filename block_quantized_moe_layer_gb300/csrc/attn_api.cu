@@ -25,6 +25,8 @@ cudaError_t verify_launch(const AttnParams& p, int num_sms, size_t part_rows, cu
 size_t prompt_ws_bytes(int D, int tile_cap);
 cudaError_t prompt_configure();
 cudaError_t prompt_launch(const AttnParams& p, int num_sms, size_t part_rows, uint8_t* ws, int tile_cap, cudaStream_t st);
+cudaError_t tree_configure(int D);
+cudaError_t tree_launch(const AttnParams& p, int num_sms, size_t part_rows, cudaStream_t st);
 cudaError_t commit_launch(const CommitParams& p, int n_seqs, cudaStream_t st);
 }  // namespace attn
 }  // namespace moe
@@ -53,6 +55,14 @@ int cuda_fail(cudaError_t e, const char* what) {
 // sequences 200 and 219, 265 and 221.
 constexpr int kSmallCallRows = 16;
 constexpr int verify_call_rows(int D) { return D == 64 ? 192 : 256; }
+// The same of a tree, above which it runs on pairs of blocks that share their keys:
+// one sequence of 32000 tokens, heads of 192, 33 us (verify) and 34 (pairs) at 128
+// rows, 44 and 35 at 192, 56 and 37 at 256; 8 sequences of up to 8000 56 and 55, 90
+// and 56, 90 and 57; heads of 128 72 and 79, 97 and 79, 116 and 79; heads of 64 68
+// and 73, 90 and 73, 106 and 73.  Heads of 256, whose products are the most beside
+// the dequantisation, 36 and 49 at 64 rows, 53 and 41 at 96.  (Expanded in memory
+// first, as a prompt's, 1024 rows of 8 sequences of 8000 tokens took 171, pairs 152.)
+constexpr int tree_verify_rows(int D) { return D == 256 ? 64 : 128; }
 
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 bool page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
@@ -131,6 +141,8 @@ int forward(const char* who, moe_attn* h, const void* q, int64_t q_token_stride,
   const int64_t rows = (int64_t)max_q * p.g;
   if (rows <= kSmallCallRows)
     CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "attention launch");
+  else if (parents && rows > tree_verify_rows(h->D))
+    CKA(attn::tree_launch(p, h->num_sms, h->part_rows, st), "attention launch (tree)");
   else if (rows <= verify_call_rows(h->D))
     CKA(attn::verify_launch(p, h->num_sms, h->part_rows, st), "attention launch (verify)");
   else
@@ -228,6 +240,7 @@ int moe_attn_create(const moe_attn_desc* d, void* stream, moe_attn** out) {
     h->ws_bytes = h->part_rows * (h->D * sizeof(float) + sizeof(float2));
     const int64_t most_rows = (int64_t)h->T_max * (h->hq / h->hk);
     if (most_rows > kSmallCallRows) CKA(attn::verify_configure(h->D), "configure the verify kernel");
+    if (most_rows > tree_verify_rows(h->D)) CKA(attn::tree_configure(h->D), "configure the tree kernel");
     if (most_rows > verify_call_rows(h->D)) {
       // dequantised tiles of one longest sequence at least (of what its window
       // and a call's queries reach), of more while they stay within 256 MB

@@ -169,53 +169,6 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
   }
 }
 
-// ---- pairs of blocks (clusters of two)
-__device__ __forceinline__ void pair_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void pair_alloc(uint32_t* slot) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(slot)) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
-}
-// Both blocks' rows times both halves of B, into each block's tensor memory.
-__device__ __forceinline__ void pair_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void pair_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrives at the barrier of each block in `blocks` (a bit each) once the MMAs issued so far are complete.
-__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t blocks) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                   smem_u32(bar)),
-               "h"(blocks)
-               : "memory");
-}
-// Arrives at the first block's barrier.  No memory that the other block reads
-// or writes by loads and stores stands behind such an arrival: weights in
-// tensor memory are complete (wait::st), images have landed, and only MMAs read
-// either.  So no cluster-wide release, which waits some 1600 cycles for the
-// thread's own loads and stores (382 against 268 us).
-__device__ __forceinline__ void arrive_first(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
 // The softmax of one group's tiles: thread (turn, row) takes all 128 scores of
 // its row in the tiles turn, turn + 2, ...: two tiles are worked on at once, so
 // that one group's waits fall into the other's arithmetic.  The reference m
@@ -334,12 +287,11 @@ __device__ __forceinline__ void softmax_turns(const AttnParams& p, int n_tiles, 
   product(n_tiles - 1, 34);
 }
 
-template <int D, bool TREE>
+template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Images im, int n_rt, int whole, int chunk) {
   using L = PromptPlan<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ uint64_t tree[TREE ? kTreeNodes : 1];  // the nodes' words of ancestors
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   float* smax = reinterpret_cast<float*>(sm + L::kMax);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);  // ring of keys, ring of values: copy landed
@@ -387,9 +339,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
   const int p0 = s.len - s.nq;
   // positions of the pair's keys, and those that all of the block's rows see
   const int pair_min = p0 + pair_row0 / p.g, pair_max = p0 + (pair_row0 + pair_rows - 1) / p.g;
-  // (of a tree all rows see what lies before it, and a node's place in the cache bounds its position)
-  const int pos_min = TREE ? p0 - 1 : p0 + row0 / p.g, pos_max = p0 + (row0 + max(n_rows, 1) - 1) / p.g;
-  const int lo = key_lo(p, max(0, TREE ? p0 : pair_min)), hi = pair_max + 1, lo_max = key_lo(p, pos_max);
+  const int pos_min = p0 + row0 / p.g, pos_max = p0 + (row0 + max(n_rows, 1) - 1) / p.g;
+  const int lo = key_lo(p, max(0, pair_min)), hi = pair_max + 1, lo_max = key_lo(p, pos_max);
   int seq_first, seq_last;
   seq_tiles(p, s, seq_first, seq_last);
   const int tile_a = lo / kTileTokens + split * chunk;
@@ -398,13 +349,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
   const uint4* valid = im.valid + (int64_t)b * im.tiles + (tile_a - seq_first);
 
   if (warp == kMmaWarp) pair_alloc(tslot);
-  if constexpr (TREE) {
-    if (warp == kCopyWarp) {
-      const TreeWords w = tree_words(p, s);
-      tree[lane] = w.word[0];
-      tree[lane + 32] = w.word[1];
-    }
-  }
   const int turn = warp >> 2, row = (warp & 3) * 32 + lane;  // of the softmax threads
   int tq = 0, hq = 0, hi_r = 0, lo_r = 0;
   const bool has_row = warp < kSoftWarps && row < n_rows;
@@ -551,14 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
           seen = true;
           return false;
         }
-        if constexpr (TREE) {  // (few tiles come here: a row's nodes and window are looked up each time)
-          const TreeRow r = has_row ? tree_row(p, p0, tree[tq]) : TreeRow{0, p0};
-          bits[0] = tree_bits<64>(c0, r.lo, p0, r.word) & e0;
-          bits[1] = tree_bits<64>(c0 + 64, r.lo, p0, r.word) & e1;
-        } else {
-          bits[0] = key_bits<64>(c0, lo_r, hi_r) & e0;
-          bits[1] = key_bits<64>(c0 + 64, lo_r, hi_r) & e1;
-        }
+        bits[0] = key_bits<64>(c0, lo_r, hi_r) & e0;
+        bits[1] = key_bits<64>(c0 + 64, lo_r, hi_r) & e1;
         seen |= (bits[0] | bits[1]) != 0;
         return true;
       });
@@ -668,8 +606,8 @@ cudaError_t prompt_launch_d(AttnParams p, int num_sms, size_t part_rows, uint8_t
     }
     cudaError_t e = launch_pdl(expand_kernel, dim3(4 * im.tiles, p.hk, g.n_seqs), 256, 0, st, g, im);
     if (e == cudaSuccess)
-      e = launch_pdl(p.parents ? prompt_kernel<D, true> : prompt_kernel<D, false>, dim3((unsigned)(2 * (whole + rest * g.n_split))),
-                     kPromptThreads, PromptPlan<D>::kTotal, st, g, im, n_rt, (int)whole, chunk);
+      e = launch_pdl(prompt_kernel<D>, dim3((unsigned)(2 * (whole + rest * g.n_split))), kPromptThreads, PromptPlan<D>::kTotal, st, g, im,
+                     n_rt, (int)whole, chunk);
     if (e == cudaSuccess && g.n_split > 1) e = join_launch(g, kPairRows, n_rt, (int)whole, st);
     if (e != cudaSuccess) return e;
   }
@@ -682,18 +620,14 @@ size_t prompt_ws_bytes(int D, int tile_cap) {
   return (size_t)tile_cap * ((size_t)2 * kTileTokens * D * 2 + sizeof(uint4));
 }
 
-template <int D>
-static cudaError_t prompt_configure_d() {
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<D>::kTotal);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(prompt_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<D>::kTotal);
-  return e;
-}
 cudaError_t prompt_configure() {
-  cudaError_t e = prompt_configure_d<64>();
-  if (e == cudaSuccess) e = prompt_configure_d<128>();
-  if (e == cudaSuccess) e = prompt_configure_d<192>();
-  if (e == cudaSuccess) e = prompt_configure_d<256>();
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<64>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<128>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prompt_kernel<192>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<192>::kTotal);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prompt_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptPlan<256>::kTotal);
   return e;
 }
 

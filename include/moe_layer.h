@@ -537,7 +537,7 @@ int moe_attn_forward(moe_attn* h, const void* q, int64_t q_token_stride, int64_t
  * Where lens[b] < m the first nodes are not in the cache: they see nothing (0,
  * lse -inf), and nobody sees them.
  *   Everything else is as in moe_attn_forward; a chain (parents -1, 0, 1, ...)
- * gives its results. */
+ * gives its results, up to roundings. */
 int moe_attn_forward_tree(moe_attn* h, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pages,
                           const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t table_stride,
                           const int32_t* parents, int32_t n_seqs, int32_t T, int32_t max_q, int32_t max_len, void* out,

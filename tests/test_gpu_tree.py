@@ -135,9 +135,9 @@ def test_tree_long_and_split():
 
 
 def test_tree_chain_is_causal():
-    """A chain gives the causal call's bits."""
+    """A chain gives the causal call's bits up to 64 rows, where the same kernel runs."""
     rng = np.random.default_rng(7)
-    for hq, hk, D, m, window in ((16, 2, 128, 2, 0), (16, 2, 128, 30, 0), (16, 1, 192, 64, 0), (4, 1, 64, 4, 7), (16, 1, 256, 60, 90)):
+    for hq, hk, D, m, window in ((16, 2, 128, 2, 0), (16, 2, 128, 8, 0), (16, 1, 192, 4, 0), (4, 1, 64, 4, 7), (2, 2, 256, 60, 90)):
         pages, table, _, _, n_pages = _cache(rng, [500, m], hk, D, 16)
         at = pkg.Attention(hq, hk, D, 16, n_pages, 2 * m, 2, 500, rot_dim=0, window=window)
         q = torch.tensor(rng.normal(size=(2 * m, hq, D)), device="cuda").to(torch.bfloat16)
@@ -208,6 +208,34 @@ def test_tree_captured():
     assert new.tolist() == [691]
     assert torch.equal(out, at.forward(q, before, *args[1:], m, 700, parents=_i32(other)))
     at.close()
+
+
+@pytest.mark.parametrize("hq,m", [(2, 4), (16, 3), (16, 40)])
+def test_tree_waits_run_out(hq, m):
+    """Each kernel's bounded waits: reported, and later calls are unaffected."""
+    rng = np.random.default_rng(12)
+    pages, table, _, _, n_pages = _cache(rng, [500], 1, 128, 16)
+    at = pkg.Attention(hq, 1, 128, 16, n_pages, m, 1, 500, rot_dim=0)
+    q = torch.tensor(rng.normal(size=(m, hq, 128)), device="cuda").to(torch.bfloat16)
+    args = (q, pages, _i32([0, m]), _i32([500]), table, m, 500)
+    parents = _i32(_tree(rng, m))
+    want = at.forward(*args, parents=parents)
+    at.inject_timeout(1000)
+    at.forward(*args, parents=parents)
+    with pytest.raises(pkg.MoEError) as e:
+        at.status()
+    assert e.value.code == pkg.MOE_ETIMEOUT
+    assert torch.equal(at.forward(*args, parents=parents), want)
+    at.status()
+    at.close()
+
+
+def test_tree_around_the_row_limits():
+    """The most rows of the verify kernel and one node more, with several row tiles of pairs."""
+    rng = np.random.default_rng(13)
+    for hq, hk, D, nodes in ((4, 1, 64, 32), (8, 2, 128, 32), (16, 1, 192, 8), (8, 1, 256, 8), (16, 2, 64, 16), (16, 1, 192, 33)):
+        for m in (nodes, nodes + 1):
+            _check(rng, hq, hk, D, [m + 300, m, 129 + m], [m, m, 1], 16)
 
 
 # ------------------------------------------------------------------ commit
