@@ -222,8 +222,20 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     look_up(0);
     fetch(0);
     look_up(1);
+    // Heads of 128 leave the registers to ask for the next tile before this one is
+    // written: 32 trees of 48 rows over up to 8192 keys 134 us and 126 so (64: 66.8
+    // and 67.6; of 192 a second set of registers was slower).
+    constexpr bool kAhead = D == 128;
     for (int j = 0; j < n_tiles; ++j) {
       const int i = j & 1;
+      uint4 code_j[kUnits];
+      uint32_t scale_j[kUnits];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) code_j[u] = code[u], scale_j[u] = scale[u];
+      if constexpr (kAhead) {
+        fetch(j + 1);
+        look_up(j + 2);
+      }
       bool ok = true;
       if (j > 1) ok = wait_bar(&image_free[i], (uint32_t)((j >> 1) - 1) & 1, abort, p.status, p.timeout_ns, 28);
       ok = __all_sync(0xffffffffu, ok);
@@ -231,10 +243,10 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       uint4* o = reinterpret_cast<uint4*>(image + i * L::kImage) + 4 * piece * KT + kKeys * dw + kk;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const uint32_t w[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+        const uint32_t w[4] = {code_j[u].x, code_j[u].y, code_j[u].z, code_j[u].w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t sb = __byte_perm(scale[u], 0, h ? 0x4141 : 0x4040);
+          const uint32_t sb = __byte_perm(scale_j[u], 0, h ? 0x4141 : 0x4040);
           uint32_t x[8];
           if (values) {
             const ValueScale d = value_scale(sb);
@@ -252,8 +264,10 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&image_full[i]);
-      fetch(j + 1);
-      look_up(j + 2);
+      if constexpr (!kAhead) {
+        fetch(j + 1);
+        look_up(j + 2);
+      }
     }
   } else if (soft && n_tiles > 0) {
     // ------------------------------------------------------------ softmax

@@ -53,6 +53,7 @@ static_assert(kVsWarps == 1 << kVsLogWarps, "a power of two");
 constexpr int kVsNodes = 64;
 constexpr int kVsMaxCluster = 16, kVsBlocks = 2;  // blocks a sequence at most; a multiprocessor
 constexpr int kVsRanges = kVsMaxCluster * kVsWarps;  // most ranges of a row
+constexpr int kVsBands = 4;
 constexpr int kVsBatch = 4;  // 16-byte loads in flight a thread
 
 struct VsParams {
@@ -209,9 +210,8 @@ __device__ __forceinline__ Parts parts(const Raw& r) {
   const uint64_t l = f2_mul(r.l, r.s), top = f2_sub(f2_add(f2_fma(r.h, r.s, l), grid), grid);
   return Parts{top, f2_add(f2_fma(r.h, r.s, f2_sub(0, top)), l)};
 }
-// (e - k f)+, f's exponential scaled by k
-__device__ __forceinline__ Parts residual(const Raw& e, const Raw& f) {
-  const Parts a = parts(e), b = parts(f);
+// (a - b)+
+__device__ __forceinline__ Parts residual(const Parts& a, const Parts& b) {
   Parts r{f2_sub(a.hi, b.hi), f2_sub(a.lo, b.lo)};
   const uint64_t sum = f2_add(r.hi, r.lo);
   if (!(f2_lo(sum) > 0.f)) r.hi &= 0xFFFFFFFF00000000ull, r.lo &= 0xFFFFFFFF00000000ull;
@@ -375,6 +375,13 @@ __device__ __forceinline__ uint64_t warp_best(uint64_t k) {
   }
   return k;
 }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The relative widths 2^-13, 2^-15, 2^-17, 2^-19.
+__device__ __forceinline__ constexpr float band(int k) { return k == 0 ? 0x1p-13f : k == 1 ? 0x1p-15f : k == 2 ? 0x1p-17f : 0x1p-19f; }
 // Orders by value, then by the lower id.
 __device__ __forceinline__ uint64_t order_key(float x, int id) {
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 and 0 are equal
@@ -382,7 +389,7 @@ __device__ __forceinline__ uint64_t order_key(float x, int id) {
   return ((uint64_t)o << 32) | (uint32_t)~id;
 }
 
-enum : int { kGoOn, kReject, kDraw };
+enum : int { kGoOn, kReject, kDraw, kSureReject };
 
 struct Walk {  // one block's shared memory
   float2 table[256];
@@ -395,6 +402,8 @@ struct Walk {  // one block's shared memory
     int64_t sum[2][kVsRanges];  // of the ranges: what is left of the target's weights
   };
   int64_t sum_f[2][kVsRanges];  // the draft's
+  int64_t whole_e[kVsRanges], whole_f[kVsRanges];  // the same of both rows, beside what is left of one
+  float near[kVsBands][kVsRanges];
   int64_t child_e[kVsNodes], child_f[kVsNodes];
   int child_at[kVsNodes];  // their ranges
   bool gone[kVsNodes];  // of the children: rejected, its token's weight taken out
@@ -628,11 +637,19 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
             const float r = both ? f.s * ei : ei, x = both ? ui * e.s * fi : ui * left;
             const float near = both ? 2.f * slack * (x + r) : slack * (ui * e.s + r);
             if (r - x > near) act = kGoOn, at = i + 32 * k;
+            if (both && x - r > near) act = kSureReject, at = i + 32 * k;
             sure = !both && x - r > near;  // (of drawn drafts the first alone; not sure to be rejected)
             left -= ei;
             set &= ~__ballot_sync(0xffffffffu, my_token[k] == __shfl_sync(0xffffffffu, my_token[k], i));  // (and its like)
           }
         }
+      }
+      if (act == kSureReject) {
+        // k as it is about (units: see row_exp); above 4 the draft's weights would leave theirs
+        const RowExp x = row_exp(e.m, ch, c_lo), y = row_exp(f.m, ch, c_lo);
+        const float k0 = e.s * exp2_fast((e.m - x.ref) * ch - x.top) / (f.s * exp2_fast((f.m - y.ref) * ch - y.top));
+        if (!(k0 <= 4.f)) act = kDraw;
+        if (lane == 0) w.kf = scaled(y, (double)k0, w.table), w.kappa = (double)k0;
       }
       if (lane == 0) w.act = act, w.at = at, w.most = e.m, w.most_f = both ? f.m : -INFINITY;
     }
@@ -707,14 +724,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       const Pair a = warp_pair(sum.a);
       return fixed(a.h, a.l, scale);
     };
-    auto total_left = [&]() {  // of what is left, with the draft's part taken out
-      Sum sum;
-      auto add = [&](const float (&xe)[N], const float (&xf)[N]) {
-#pragma unroll
-        for (int i = 0; i < N; i += 2)
-          sum.add(residual(weight(xe[i], xe[i + 1], ee, w.table), weight<true>(xf[i], xf[i + 1], kf, w.table)));
-        sum.flush();
-      };
+    auto for_both = [&](auto add) {  // this warp's range of both rows, the next vectors on their way
       if (j0 < j1 && re.whole(j0) && re.whole(j1 - 1) && rf.aligned) {
         uint4 ve = re.raw_or_none(j0 + lane, j1), vf = rf.raw_or_none(j0 + lane, j1);
 #pragma unroll 1
@@ -735,6 +745,15 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
           add(xe, xf);
         }
       }
+    };
+    auto total_left = [&]() {  // of what is left, with the draft's part taken out
+      Sum sum;
+      for_both([&](const float (&xe)[N], const float (&xf)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+          sum.add(residual(parts(weight(xe[i], xe[i + 1], ee, w.table)), parts(weight<true>(xf[i], xf[i + 1], kf, w.table))));
+        sum.flush();
+      });
       const Pair a = warp_pair(sum.a);
       return fixed(a.h, a.l, scale);
     };
@@ -768,12 +787,115 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       }
       turn ^= 1;
     };
-    sums(judged);
-    gather(judged);
-
-    // ---- the children in order (each block's first warp decides, all of them the same)
     double left = 1.0;  // of the draft's probability what is not rejected
     int cursor = 0;
+    if (w.act != kSureReject) {
+      sums(judged);
+      gather(judged);
+    } else {
+      // The first draft is surely rejected.  Both rows' sums and what is left in one
+      // pass, with k as the fp32 sums have it, k0: of what is left R(k0) = sum over
+      // {e > k0 f} of e - k0 f, R(k0 (1 + d)) = R(k0) - d sum over the same of k0 f,
+      // but for the tokens that change sides, which have |e - k0 f| <= d k0 f and
+      // change it by d of their k0 f at most.  So the k0 f of those within 2^-13, 2^-15,
+      // 2^-17 and 2^-19 are summed too: d, which is known afterwards, is mostly 2^-20.
+      const double k0 = w.kappa;
+      const int first_child = w.at;
+      kf = w.kf;
+      Sum all_e, all_f, rest, taken;
+      float near[kVsBands] = {};
+      auto note = [&](float d, float b) {
+        if (fabsf(d) > 0x1p-13f * b) return;
+#pragma unroll
+        for (int k = 0; k < kVsBands; ++k)
+          if (fabsf(d) <= band(k) * b) near[k] += b;
+      };
+      auto add = [&](const float (&xe)[N], const float (&xf)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const Parts a = parts(weight(xe[i], xe[i + 1], ee, w.table)), b = parts(weight<true>(xf[i], xf[i + 1], kf, w.table));
+          Parts r{f2_sub(a.hi, b.hi), f2_sub(a.lo, b.lo)}, c = b;
+          const uint64_t d = f2_add(r.hi, r.lo);
+          if (!(f2_lo(d) > 0.f)) r.hi &= 0xFFFFFFFF00000000ull, r.lo &= 0xFFFFFFFF00000000ull, c.hi &= 0xFFFFFFFF00000000ull, c.lo &= 0xFFFFFFFF00000000ull;
+          if (!(f2_hi(d) > 0.f)) r.hi &= 0xFFFFFFFFull, r.lo &= 0xFFFFFFFFull, c.hi &= 0xFFFFFFFFull, c.lo &= 0xFFFFFFFFull;
+          const uint64_t b1 = f2_add(b.hi, b.lo);
+          note(f2_lo(d), f2_lo(b1));
+          note(f2_hi(d), f2_hi(b1));
+          all_e.add(a);
+          all_f.add(b);
+          rest.add(r);
+          taken.add(c);
+        }
+        all_e.flush();
+        all_f.flush();
+        rest.flush();
+        taken.flush();
+      };
+      for_both(add);
+      auto fixed_of = [&](const Sum& s) {
+        const Pair a = warp_pair(s.a);
+        return fixed(a.h, a.l, scale);
+      };
+      const int64_t v[4] = {fixed_of(rest), fixed_of(taken), fixed_of(all_e), fixed_of(all_f)};
+#pragma unroll
+      for (int k = 0; k < kVsBands; ++k) near[k] = warp_sum(near[k]);
+      if (lane < 1 << p.log_c) {
+        Walk* q = cl.map_shared_rank(&w, lane);
+        const int i = rank * kVsWarps + warp;
+        q->sum[turn][i] = v[0];
+        q->sum_f[turn][i] = v[1];
+        q->whole_e[i] = v[2];
+        q->whole_f[i] = v[3];
+#pragma unroll
+        for (int k = 0; k < kVsBands; ++k) q->near[k][i] = near[k];
+      }
+      gather(true);
+      if (warp == 0) {
+        int64_t te = 0, tf = 0;
+        for (int i = lane; i < n_ranges; i += 32) te += w.whole_e[i], tf += w.whole_f[i];
+        te = warp_total(te);
+        tf = warp_total(tf);
+        const double d = (double)te / (double)tf - 1.0;
+        const int64_t f_all = __double2ll_rn((double)tf / k0);
+        int within = -1;  // the narrowest band that holds all that change sides
+#pragma unroll
+        for (int k = 0; k < kVsBands; ++k)
+          if (fabs(d) < 0.9 * (double)band(k)) within = k;
+        float tn = 0.f;
+        if (within >= 0)
+          for (int i = lane; i < n_ranges; i += 32) tn += w.near[within][i];
+        tn = warp_sum(tn);
+        const bool good = within >= 0 && fabs(d) * (double)tn * (double)scale <= 0x1p-33 * (double)Z;
+        if (good) {
+          int64_t s = 0;
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g) {
+            const int i = lane * group + g;
+            if (g < group && i < n_ranges) mine[g] -= __double2ll_rn(d * (double)w.sum_f[turn ^ 1][i]);
+            if (mine[g] < 0) mine[g] = 0;
+            s += mine[g];
+          }
+          Z = warp_total(s);
+          kappa = k0 * (1.0 + d);
+          kf = scaled(ef, kappa, w.table);
+          for (int i = 0; i < n_children; ++i)
+            if (w.child[i] == first_child) {
+              cursor = i + 1;
+              if (!p.replacement) left = 1.0 - (double)w.child_f[i] / (double)f_all;
+            }
+        } else {
+          Z = te;
+        }
+        F = f_all;
+        if (lane == 0) w.kappa = good ? kappa : 0.0, w.kf = kf;
+      }
+      __syncthreads();
+      kappa = w.kappa;
+      kf = w.kf;
+      __syncthreads();
+    }
+
+    // ---- the children in order (each block's first warp decides, all of them the same)
     while (true) {
       if (warp == 0) {
         int act = kDraw, at = 0;
@@ -882,7 +1004,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
 #pragma unroll
       for (int k = 0; k < N; k += 2) {
         const Raw e = weight(xe[k], xe[k + 1], ee, w.table);
-        const Parts a = kappa > 0.0 ? residual(e, weight<true>(xf[k], xf[k + 1], kf, w.table)) : parts(e);
+        const Parts a = kappa > 0.0 ? residual(parts(e), parts(weight<true>(xf[k], xf[k + 1], kf, w.table))) : parts(e);
         r[k] = fixed(f2_lo(a.hi), f2_lo(a.lo), scale);
         r[k + 1] = fixed(f2_hi(a.hi), f2_hi(a.lo), scale);
       }

@@ -213,6 +213,26 @@ def test_numbers_at_the_ends():
         assert int(r["next"]) == V - 1
 
 
+def test_drafts_nearly_the_target():
+    """Draft distributions that are the target's but for a few tokens, and scaled or far ones: what is left of the target
+    is a few tokens, or nearly all."""
+    rng = np.random.default_rng(31)
+    for V in (300, 20000):
+        x = _peaked(rng, 60, V)
+        swapped = x.copy()
+        order = np.argsort(-x, 1)
+        rows = np.arange(60)
+        for a, b in ((0, 3), (1, 40), (2, 100)):
+            swapped[rows, order[:, a]], swapped[rows, order[:, b]] = x[rows, order[:, b]], x[rows, order[:, a]]
+        for y in (swapped, x + 5.0, x + 1e-4 * rng.normal(size=x.shape), 0.3 * x, 3 * x, rng.normal(size=x.shape), np.roll(x, 1, 1)):
+            for top in (3, 40):  # drafts that the draft head likes, or the target hardly
+                best = np.argsort(-y, 1)[:, :top]
+                tokens = np.array([best[5 * (i // 5) + max(0, i % 5 - 1), (i % 5 * 7) % top] for i in range(60)])
+                for replacement in (False, True):
+                    _case(rng, V, [5] * 12, True, torch.float32, logits=x, draft=y, tokens=tokens, replacement=replacement,
+                          trees=[[-1, 0, 0, 1, 2]] * 6 + [[-1, 0, 1, 2, 3]] * 6)
+
+
 def test_more_nodes_than_said():
     rng = np.random.default_rng(29)
     _case(rng, 200, [10, 3, 8], True, torch.float32, max_nodes=5)
