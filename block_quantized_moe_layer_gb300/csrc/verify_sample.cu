@@ -30,13 +30,19 @@
 // a table and a short series (Tang's table-driven exponential), 1 + g (L + g
 // (L^2/2 + g L^3/6)), L = ln 2, |g| <= 2^-9.
 //
-// Measured: a chain of 4 nodes, 32768 fp32 logits, 13.4 us (3 us a step: a pass,
-// a cluster barrier, the decision; 4 for the last one); 4 trees of 64 nodes 14.8;
-// 64 chains of 4 with drawn drafts, 151936 bf16 logits, 76 us (the rows read
-// take 20: a step 9 us; a rejected drawn draft, whose two rows are summed in more
-// bits and then looked at twice again, 50); 32 trees of 12 nodes, 151936 fp32,
-// 31 us.  16, 8 and 4 blocks a sequence take 31, 34 and 39 us there; 512 threads
-// a block and two blocks a multiprocessor 36, 1024 threads 43.
+//   A drawn draft that is surely rejected takes one pass over both rows for their
+// sums and for what is left, at the k that the fp32 sums give, and a correction
+// (see there); the others, and a node's second rejection, a pass each.
+//
+// Measured (three calls' inputs in turn): a chain of 4 nodes, 32768 fp32 logits,
+// 12.3 us (3 us a step: a pass, a cluster barrier, the decision; 4 for the last
+// one); 4 trees of 64 nodes 14.7; 64 chains of 4 with drawn drafts, 151936 bf16
+// logits, 67 us (the rows read take 20: a step 8 us, the last row of a walk 15, a
+// rejected drawn draft 40, all of it instructions); 32 trees of 12 nodes, 151936
+// fp32, 39 us (the longest walk's five rows).  16, 8 and 4 blocks a sequence take
+// 34, 39 and 42 us there with 256 threads a block (inputs in L2: 31), 512 threads
+// 36, 1024 threads 43; 4, 2 and 1 loads in flight a thread 34, 37 and 40.  Asking
+// L2 for the next row ahead of the walk cost 1 us, and 7 of the 67.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
     const int skew = skew_of(pe);
     const Row<In> re{pe, p.V, skew, true}, rf{pf, p.V, skew, skew_of(pf) == skew};
     const int n_vec = (p.V + skew + N - 1) / N;
-    // ranges of whole vectors, a warp each: warp w of block r has the range 16 r + w
+    // ranges of whole vectors, a warp each: warp w of block r has the range 8 r + w
     const int n_ranges = kVsWarps << p.log_c, per = (n_vec + n_ranges - 1) >> (kVsLogWarps + p.log_c);
     const int j0 = min(n_vec, (rank * kVsWarps + warp) * per), j1 = min(n_vec, j0 + per);
 

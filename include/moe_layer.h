@@ -335,9 +335,10 @@ int mtp_verify_accept_noalloc(const int32_t* draft_ids, int32_t k, const float* 
  * <= 64.
  *   logits, draft_logits: [n_nodes][V] of dtype (moe_act), rows contiguous,
  * strides in elements; only the rows of the nodes on the path are read.
- *   Weights below 2^-100 of a row's largest count as 0.  Weights are right to
- * 2^-32, their sums in more bits: a number closer than that to a border
- * between two outcomes may fall on either side.  The same inputs give the same
+ *   Probabilities and their sums are right to 2^-32 of a row's sum: a number
+ * closer than that to a border between two outcomes may fall on either side
+ * (for a rejected drawn draft, in units of what is left).  A token below 2^-36
+ * of a row's largest probability is not drawn.  The same inputs give the same
  * outputs.  Asynchronous, no allocation, no workspace. */
 int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_stride, const void* draft_logits,
                       int64_t draft_stride, int32_t V, const int32_t* tokens, const int32_t* parents,
@@ -568,7 +569,7 @@ int moe_attn_commit(moe_attn* h, void* pages, const int32_t* starts, const int32
  * then cleared. */
 int moe_attn_status(moe_attn* h, void* stream);
 
-/* Test hook: the handle's next (bf16) moe_attn_forward waits for keys that
+/* Test hook: the handle's next (bf16) moe_attn_forward or _tree waits for keys that
  * never count as arrived.  Its waits run out after wait_limit_us (1..10^6),
  * copies and MMAs in flight are drained, and moe_attn_status then returns
  * MOE_ETIMEOUT.  The output of that call is undefined, later calls are
