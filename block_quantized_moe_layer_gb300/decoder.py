@@ -133,6 +133,7 @@ class Decoder:
             raise MoEError(MOE_EINVAL, f"{len(drafts)} drafts with parents {list(parents)}: an earlier node each, at most 63")
         first = seq.length
         h = self._run(seq, [last] + list(drafts), tree)
+        seq.length = first  # (until the nodes that stay are known: a call that is refused on the way leaves none)
         logits = self._logits(h)
         i32 = dict(dtype=torch.int32, device=dev)
         nodes, lens = torch.tensor([0, n], **i32), torch.tensor([first + n], **i32)

@@ -101,3 +101,18 @@ def test_bad_trees_are_refused_before_anything_changes():
     with pytest.raises(MoEError, match="longest"):
         seq.length = model.max_len - 1
         model.verify_tree(seq, 3, [1, 2], [0, 0])
+
+
+def test_a_refused_step_keeps_no_node():
+    """Numbers or draft rows of the wrong size: the sequence is as it was, and the next step gives what it would have given."""
+    a, b = _model(), _model()
+    sa, sb = a.new_sequence(), b.new_sequence()
+    a.prefill(sa, list(range(50)))
+    b.prefill(sb, list(range(50)))
+    with pytest.raises(MoEError, match="uniforms"):
+        a.verify_tree(sa, 3, [1, 2], [0, 0], uniforms=[0.5, 0.5])
+    with pytest.raises(MoEError, match="draft_logits"):
+        a.verify_tree(sa, 3, [1, 2], [0, 0], draft_logits=torch.zeros(2, 1000, device="cuda"))
+    assert sa.length == 50
+    x, y = (m.verify_tree(s, 3, [1, 2], [0, 0], uniforms=[0.3, 0.4, 0.5], temperature=0.7) for m, s in ((a, sa), (b, sb)))
+    assert torch.equal(x["logits"], y["logits"]) and x["accept"] == y["accept"] and sa.length == sb.length
