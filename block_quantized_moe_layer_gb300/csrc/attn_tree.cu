@@ -31,7 +31,8 @@
 // exponentials 1000, weights to tensor memory 250, the next scores 300), beside
 // dequantising warps that are busy two thirds of the time.  Not better: two groups
 // of softmax warps in turn, which read the scores twice (3100), four threads a row
-// (3300), weights beside the output so that the next scores come sooner (2950).
+// (3300), weights beside the output so that the next scores come sooner (2950),
+// a quarter of the weights while the row's maximum is exchanged (3150: registers).
 #include "attn_tc.cuh"
 
 namespace moe {

@@ -30,6 +30,10 @@
 // not: 7 tiles a block, some 3300 cycles each, about half of it, and its start,
 // end and join; the tensor pipe is active 26%; the warps wait for page loads,
 // then for each other.
+//   For trees of drafted tokens (TREE) a row sees the tokens before the tree and
+// the nodes of one word (attn.cuh), by which the last tiles are masked.  32 trees
+// of 12 nodes (48 rows) over up to 8192 keys, 32/8 heads of 128: 125 us, issue
+// slots 73% busy, 256 blocks on 152 multiprocessors.
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -224,8 +228,9 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
     look_up(1);
     // Heads of 128 leave the registers to ask for the next tile before this one is
     // written: 32 trees of 48 rows over up to 8192 keys 134 us and 126 so (64: 66.8
-    // and 67.6; of 192 a second set of registers was slower).
-    constexpr bool kAhead = D == 128;
+    // and 67.6; of 192 a second set of registers was slower).  Not for the shorter
+    // tails of chains: 8 sequences of 32 rows over 8000 keys 48.5 us, and 49.3 so.
+    constexpr bool kAhead = TREE && D == 128;
     for (int j = 0; j < n_tiles; ++j) {
       const int i = j & 1;
       uint4 code_j[kUnits];
