@@ -52,6 +52,7 @@ struct AttnParams {
   int64_t head_bytes, page_bytes;
   const int32_t *starts, *lens, *table;
   const int32_t* parents;  // [T] of a tree call, else null
+  int by_length;       // 1: a tree call's blocks take the longest sequences first
   void* out;           // [T][hq][D]
   float* lse;          // [T][hq] or null
   float* part_o;       // [tile][split][rows][D]
@@ -84,6 +85,27 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   s.len = min(max(n, 0), p.max_len);
   if ((s.start != a || s.start + s.nq != e || s.len != n) && threadIdx.x == 0) atomicOr(p.status, kBadLength);
   return s;
+}
+
+// The sequence with the i-th most cached tokens (the lower one first of two
+// equal ones), for a block of all its threads.  Where a call has more blocks than
+// the GPU holds at once, those that start last are then the shortest, and end with
+// the others.  A length is compared with all others, so a call has few sequences.
+constexpr int kSortedSeqs = 128;
+__device__ __forceinline__ int seq_by_length(const AttnParams& p, int i) {
+  __shared__ int found;
+  for (int t = threadIdx.x; t < p.n_seqs; t += blockDim.x) {
+    const int n = p.lens[t];
+    int before = 0;
+#pragma unroll 8
+    for (int u = 0; u < p.n_seqs; ++u) {
+      const int o = p.lens[u];
+      before += o > n || (o == n && u < t);
+    }
+    if (before == i) found = t;
+  }
+  __syncthreads();
+  return found;
 }
 
 // The page of the tokens [i P, (i + 1) P) of sequence b, or -1 for an entry

@@ -218,7 +218,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
   const bool split_tile = pair >= whole;
   const int tile_i = split_tile ? whole + (pair - whole) / p.n_split : pair;
   const int split = split_tile ? (pair - whole) % p.n_split : 0;
-  const int rt = n_rt - 1 - tile_i / (p.hk * p.n_seqs), b = tile_i % (p.hk * p.n_seqs) / p.hk, kvh = tile_i % p.hk;
+  const int rt = n_rt - 1 - tile_i / (p.hk * p.n_seqs), bi = tile_i % (p.hk * p.n_seqs) / p.hk, kvh = tile_i % p.hk;
+  const int b = p.by_length ? seq_by_length(p, bi) : bi;
   const bool parts = split_tile && p.n_split > 1;
   const Seq s = load_seq(p, b);
   const int pair_row0 = rt * kPairRowsT, pair_rows = min(kPairRowsT, s.nq * p.g - pair_row0);
@@ -504,6 +505,8 @@ cudaError_t tree_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStrea
     const int64_t cost = (rest * n + places - 1) / places * (c + 4) + (n > 1 ? 4 : 0);
     if (n == 1 || cost < best) best = cost, chunk = c, p.n_split = (tiles + c - 1) / c;
   }
+  // (the join of split parts knows their sequences by the call's order)
+  p.by_length = p.n_split == 1 && total > places && p.n_seqs <= kSortedSeqs && p.window == 0;
   cudaError_t e = launch_pdl(tree_kernel<D>, dim3((unsigned)(2 * (whole + rest * p.n_split))), kThreadsT, TreePlan<D>::kTotal, st, p, n_rt,
                              (int)whole, chunk);
   if (e == cudaSuccess && p.n_split > 1) e = join_launch(p, kPairRowsT, n_rt, (int)whole, st);

@@ -32,8 +32,9 @@
 // then for each other.
 //   For trees of drafted tokens (TREE) a row sees the tokens before the tree and
 // the nodes of one word (attn.cuh), by which the last tiles are masked.  32 trees
-// of 12 nodes (48 rows) over up to 8192 keys, 32/8 heads of 128: 125 us, issue
-// slots 73% busy, 256 blocks on 152 multiprocessors.
+// of 12 nodes (48 rows) over up to 8192 keys, 32/8 heads of 128: 107 us, 256
+// blocks, the longest sequences first; a tile takes some 1900 cycles, of which
+// shared memory is busy 1400 and the tensor pipe 840.
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   const uint32_t tbase = *tslot;
   griddep_wait();
 
-  const int split = blockIdx.x, b = blockIdx.z;
+  const int split = blockIdx.x, b = TREE && p.by_length ? seq_by_length(p, blockIdx.z) : blockIdx.z;
   const int kvh = blockIdx.y / n_rt, rt = blockIdx.y % n_rt;
   const Seq s = load_seq(p, b);
   const int row0 = rt * kRowsV, n_rows = max(0, min(kRowsV, s.nq * p.g - row0));
@@ -365,6 +366,8 @@ cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStr
   want = std::min<int64_t>(std::min<int64_t>(want, kMaxSplit), std::max<int64_t>(1, (int64_t)(part_rows / kRowsV) / base));
   const int chunk = (int)std::max<int64_t>(std::min(tiles, 2), (tiles + want - 1) / want);
   p.n_split = (tiles + chunk - 1) / chunk;
+  // (measured for trees alone, of which 32 of 12 nodes over 4096..8192 tokens take 107 us so, 125 in their order)
+  p.by_length = p.parents && base > num_sms && p.n_seqs <= kSortedSeqs && p.window == 0;
   cudaError_t e = launch_pdl(p.parents ? verify_kernel<D, true> : verify_kernel<D, false>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
                              VerifyPlan<D>::kTotal, st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;

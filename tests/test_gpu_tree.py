@@ -238,6 +238,17 @@ def test_tree_around_the_row_limits():
             _check(rng, hq, hk, D, [m + 300, m, 129 + m], [m, m, 1], 16)
 
 
+@pytest.mark.parametrize("seqs,m,window", [(40, 9, 0), (12, 64, 0), (130, 5, 0), (130, 33, 0), (40, 9, 50)])
+def test_tree_more_blocks_than_the_gpu_holds(seqs, m, window):
+    """Calls that take the longest sequences first: lengths up and down, equal ones, sequences without nodes or tokens."""
+    rng = np.random.default_rng(seqs + m)
+    news = [int(x) for x in rng.integers(1, m + 1, seqs)]
+    news[0], news[3], news[5] = m, 0, 0
+    lens = [n + int(rng.choice([0, 7, 7, 64, 200, 330])) for n in news]
+    lens[5] = 0
+    _check(rng, 32, 8, 64, lens, news, 32, window=window)
+
+
 # ------------------------------------------------------------------ commit
 
 
