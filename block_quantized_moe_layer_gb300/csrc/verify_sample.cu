@@ -35,11 +35,12 @@
 // (see there); the others, and a node's second rejection, a pass each.
 //
 // Measured (three calls' inputs in turn): a chain of 4 nodes, 32768 fp32 logits,
-// 12.3 us (3 us a step: a pass, a cluster barrier, the decision; 4 for the last
-// one); 4 trees of 64 nodes 14.7; 64 chains of 4 with drawn drafts, 151936 bf16
-// logits, 67 us (the rows read take 20: a step 8 us, the last row of a walk 15, a
-// rejected drawn draft 40, all of it instructions); 32 trees of 12 nodes, 151936
-// fp32, 39 us (the longest walk's five rows).  16, 8 and 4 blocks a sequence take
+// 12.2 us (2.4 us a step: the pass 0.7, a cluster barrier 0.9, the decision 0.8);
+// 4 trees of 64 nodes 14.9; 64 chains of 4 with drawn drafts, 151936 bf16 logits,
+// 62 us (the rows read take 20: a step 9 us, 5.7 of them HBM's while all walk; a
+// rejected drawn draft 20 to 30, all of it instructions, and 2 for the decision;
+// the next token's place in its range 5); 32 trees of 12 nodes, 151936 fp32, 38 us
+// (the longest walk's five rows: 5 us a step, the last 4, then the place).  16, 8 and 4 blocks a sequence take
 // 34, 39 and 42 us there with 256 threads a block (inputs in L2: 31), 512 threads
 // 36, 1024 threads 43; 4, 2 and 1 loads in flight a thread 34, 37 and 40.  Asking
 // L2 for the next row ahead of the walk cost 1 us, and 7 of the 67.
@@ -133,6 +134,12 @@ __device__ __forceinline__ void accumulate(Pair& a, Pair b) {
 }
 // In whole steps of 1 / scale (a power of two): sums of these are exact, in any order.
 __device__ __forceinline__ int64_t fixed(float h, float l, float scale) { return __float2ll_rn(h * scale) + __float2ll_rn(l * scale); }
+
+// 1 / x to some 2^-46 (a division in fp64 takes a step of its own here).
+__device__ __forceinline__ double reciprocal(double x) {
+  const double y = (double)__frcp_rn((float)x);
+  return fma(y, fma(-x, y, 1.0), y);
+}
 
 // A row's exponential: weight(l) = k 2^(c (l - ref)) in units of 2^top, k = 1
 // unless scaled() says more.  ref is 0 where |c l_max| < 2^10, else l_max: then
@@ -730,7 +737,10 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       const Pair a = warp_pair(sum.a);
       return fixed(a.h, a.l, scale);
     };
-    auto for_both = [&](auto add) {  // this warp's range of both rows, the next vectors on their way
+    // This warp's range of both rows, the next vectors on their way; flush() behind
+    // every 32 tokens of a lane (16 of each half of the sums: below 2^7, exact).
+    auto for_both = [&](auto add, auto flush) {
+      int round = 0;
       if (j0 < j1 && re.whole(j0) && re.whole(j1 - 1) && rf.aligned) {
         uint4 ve = re.raw_or_none(j0 + lane, j1), vf = rf.raw_or_none(j0 + lane, j1);
 #pragma unroll 1
@@ -741,6 +751,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
           ve = re.raw_or_none(j + 32, j1);
           vf = rf.raw_or_none(j + 32, j1);
           add(xe, xf);
+          if ((++round & (32 / N - 1)) == 0) flush();
         }
       } else {
 #pragma unroll 1
@@ -749,8 +760,10 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
           re.load(j, xe);
           rf.load(j, xf);
           add(xe, xf);
+          if ((++round & (32 / N - 1)) == 0) flush();
         }
       }
+      flush();
     };
     auto total_left = [&]() {  // of what is left, with the draft's part taken out
       Sum sum;
@@ -758,8 +771,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
 #pragma unroll
         for (int i = 0; i < N; i += 2)
           sum.add(residual(parts(weight(xe[i], xe[i + 1], ee, w.table)), parts(weight<true>(xf[i], xf[i + 1], kf, w.table))));
-        sum.flush();
-      });
+      }, [&]() { sum.flush(); });
       const Pair a = warp_pair(sum.a);
       return fixed(a.h, a.l, scale);
     };
@@ -811,12 +823,14 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       Sum all_e, all_f, rest, taken;
       float near[kVsBands] = {};
       auto note = [&](float d, float b) {
-        if (fabsf(d) > 0x1p-13f * b) return;
 #pragma unroll
         for (int k = 0; k < kVsBands; ++k)
           if (fabsf(d) <= band(k) * b) near[k] += b;
       };
+      // (few tokens are near, so they are told by one branch for all of a vector's)
       auto add = [&](const float (&xe)[N], const float (&xf)[N]) {
+        float d1[N], b1[N];
+        bool close = false;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
           const Parts a = parts(weight(xe[i], xe[i + 1], ee, w.table)), b = parts(weight<true>(xf[i], xf[i + 1], kf, w.table));
@@ -824,20 +838,26 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
           const uint64_t d = f2_add(r.hi, r.lo);
           if (!(f2_lo(d) > 0.f)) r.hi &= 0xFFFFFFFF00000000ull, r.lo &= 0xFFFFFFFF00000000ull, c.hi &= 0xFFFFFFFF00000000ull, c.lo &= 0xFFFFFFFF00000000ull;
           if (!(f2_hi(d) > 0.f)) r.hi &= 0xFFFFFFFFull, r.lo &= 0xFFFFFFFFull, c.hi &= 0xFFFFFFFFull, c.lo &= 0xFFFFFFFFull;
-          const uint64_t b1 = f2_add(b.hi, b.lo);
-          note(f2_lo(d), f2_lo(b1));
-          note(f2_hi(d), f2_hi(b1));
+          const uint64_t whole = f2_add(b.hi, b.lo);
+          d1[i] = f2_lo(d), d1[i + 1] = f2_hi(d);
+          b1[i] = f2_lo(whole), b1[i + 1] = f2_hi(whole);
+          close |= (fabsf(d1[i]) <= band(0) * b1[i]) | (fabsf(d1[i + 1]) <= band(0) * b1[i + 1]);
           all_e.add(a);
           all_f.add(b);
           rest.add(r);
           taken.add(c);
         }
+        if (close) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) note(d1[i], b1[i]);
+        }
+      };
+      for_both(add, [&]() {
         all_e.flush();
         all_f.flush();
         rest.flush();
         taken.flush();
-      };
-      for_both(add);
+      });
       auto fixed_of = [&](const Sum& s) {
         const Pair a = warp_pair(s.a);
         return fixed(a.h, a.l, scale);
@@ -861,33 +881,33 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
         for (int i = lane; i < n_ranges; i += 32) te += w.whole_e[i], tf += w.whole_f[i];
         te = warp_total(te);
         tf = warp_total(tf);
-        const double d = (double)te / (double)tf - 1.0;
-        const int64_t f_all = __double2ll_rn((double)tf / k0);
+        const float d = __fdiv_rn((float)(te - tf), (float)tf);
+        const int64_t f_all = __double2ll_rn((double)tf * reciprocal(k0));
         int within = -1;  // the narrowest band that holds all that change sides
 #pragma unroll
         for (int k = 0; k < kVsBands; ++k)
-          if (fabs(d) < 0.9 * (double)band(k)) within = k;
+          if (fabsf(d) < 0.9f * band(k)) within = k;
         float tn = 0.f;
         if (within >= 0)
           for (int i = lane; i < n_ranges; i += 32) tn += w.near[within][i];
         tn = warp_sum(tn);
-        const bool good = within >= 0 && fabs(d) * (double)tn * (double)scale <= 0x1p-33 * (double)Z;
+        const bool good = within >= 0 && fabsf(d) * tn * scale <= 0x1p-33f * (float)Z;
         if (good) {
           int64_t s = 0;
 #pragma unroll
           for (int g = 0; g < kGroup; ++g) {
             const int i = lane * group + g;
-            if (g < group && i < n_ranges) mine[g] -= __double2ll_rn(d * (double)w.sum_f[turn ^ 1][i]);
+            if (g < group && i < n_ranges) mine[g] -= __float2ll_rn(d * (float)w.sum_f[turn ^ 1][i]);
             if (mine[g] < 0) mine[g] = 0;
             s += mine[g];
           }
           Z = warp_total(s);
-          kappa = k0 * (1.0 + d);
+          kappa = fma(k0, (double)d, k0);
           kf = scaled(ef, kappa, w.table);
           for (int i = 0; i < n_children; ++i)
             if (w.child[i] == first_child) {
               cursor = i + 1;
-              if (!p.replacement) left = 1.0 - (double)w.child_f[i] / (double)f_all;
+              if (!p.replacement) left = 1.0 - (double)w.child_f[i] * reciprocal((double)f_all);
             }
         } else {
           Z = te;
@@ -924,8 +944,8 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
             Z -= e;
             if (lane == 0) w.gone[i] = true;
           } else if (left > 0.0 && Z > 0) {
-            kappa += (double)Z / (left * (double)F);
-            if (!p.replacement) left -= (double)f / (double)F;
+            kappa += (double)Z * reciprocal(left * (double)F);
+            if (!p.replacement) left -= (double)f * reciprocal((double)F);
             cursor = i + 1;
             act = kReject;
             break;
@@ -1003,30 +1023,49 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
     if (rank != w.range / kVsWarps) break;
     const int k0 = min(n_vec, w.range * per), k1 = min(n_vec, k0 + per), each = (per + kVsThreads - 1) / kVsThreads;
     const int a0 = min(k1, k0 + tid * each), a1 = min(k1, a0 + each);
-    auto left_at = [&](int j, int64_t (&r)[N]) {  // what is left of vector j's weights
-      float xe[N], xf[N];
+    auto load = [&](int j, float (&xe)[N], float (&xf)[N]) {  // vector j, without the tokens that are out
       re.load(j, xe);
       if (kappa > 0.0) rf.load(j, xf);
-#pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        const Raw e = weight(xe[k], xe[k + 1], ee, w.table);
-        const Parts a = kappa > 0.0 ? residual(parts(e), parts(weight<true>(xf[k], xf[k + 1], kf, w.table))) : parts(e);
-        r[k] = fixed(f2_lo(a.hi), f2_lo(a.lo), scale);
-        r[k + 1] = fixed(f2_hi(a.hi), f2_hi(a.lo), scale);
-      }
       if (out) {
         for (int i = 0; i < n_children; ++i) {
           const int k = w.token[w.child[i]] - (j * N - skew);
           if (!w.gone[i] || k < 0 || k >= N) continue;
 #pragma unroll
           for (int e = 0; e < N; ++e)
-            if (e == k) r[e] = 0;
+            if (e == k) xe[e] = -INFINITY;
         }
       }
     };
-    int64_t r[N], own = 0;
-    for (int j = a0; j < a1; ++j) {
-      left_at(j, r);
+    auto left_of = [&](const float (&xe)[N], const float (&xf)[N], int k) {  // what is left of two weights
+      const Parts a = parts(weight(xe[k], xe[k + 1], ee, w.table));
+      return kappa > 0.0 ? residual(a, parts(weight<true>(xf[k], xf[k + 1], kf, w.table))) : a;
+    };
+    auto whole_left = [&](const float (&xe)[N], const float (&xf)[N], int64_t (&r)[N]) {
+#pragma unroll
+      for (int k = 0; k < N; k += 2) {
+        const Parts a = left_of(xe, xf, k);
+        r[k] = fixed(f2_lo(a.hi), f2_lo(a.lo), scale);
+        r[k + 1] = fixed(f2_hi(a.hi), f2_hi(a.lo), scale);
+      }
+    };
+    float xe[N], xf[N];
+    int64_t r[N], own = 0;  // (one vector a thread: the next step has its r still)
+    if (a0 < a1) load(a0, xe, xf);
+    if (each > 1) {
+      Sum sum;
+#pragma unroll 1
+      for (int j = a0; j < a1; ++j) {
+        float ye[N], yf[N];
+        if (j + 1 < a1) load(j + 1, ye, yf);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) sum.add(left_of(xe, xf, k));
+        sum.flush();
+#pragma unroll
+        for (int k = 0; k < N; ++k) xe[k] = ye[k], xf[k] = yf[k];
+      }
+      own = fixed(sum.a.h, sum.a.l, scale);
+    } else if (a0 < a1) {
+      whole_left(xe, xf, r);
 #pragma unroll
       for (int k = 0; k < N; ++k) own += r[k];
     }
@@ -1039,25 +1078,45 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       if (lane == 0) w.winner = at, w.threshold -= before;
     }
     __syncthreads();
-    if (warp == w.winner) {
+    if (warp == w.winner) {  // a lane a vector of the thread's that has the place
       int64_t before;
       const int at = max(pick(own, w.threshold, lane, before), 0);
-      if (lane == at) {
-        writes = true;
-        const int64_t t = w.threshold - before;
-        int64_t run = 0;
-        bool found = false;
-        for (int j = a0; j < a1 && !found; ++j) {
-          if (each > 1) left_at(j, r);  // (one vector is still there)
+      const int b0 = __shfl_sync(0xffffffffu, a0, at), b1 = __shfl_sync(0xffffffffu, a1, at);
+      int64_t t = w.threshold - before;
+      bool passed = false;
+#pragma unroll 1
+      for (int j0 = b0; j0 < b1 && !passed; j0 += 32) {
+        int j = a0, by = at;
+        int64_t all = 0;
+        before = 0;
+        if (each > 1) {
+          j = j0 + lane;
+          if (j < b1) {
+            load(j, xe, xf);
+            whole_left(xe, xf, r);
+#pragma unroll
+            for (int k = 0; k < N; ++k) all += r[k];
+          }
+          by = pick(all, t, lane, before);
+        }
+        int token = -1;
+        if (lane == by) {
+          int64_t run = before;
+          bool found = false;
 #pragma unroll
           for (int k = 0; k < N; ++k) {
             if (found || r[k] <= 0) continue;
-            next = j * N - skew + k;  // (the last with any where rounding leaves none that passes)
+            token = j * N - skew + k;  // (the last with any where rounding leaves none that passes)
             run += r[k];
             found = run > t;
           }
         }
+        token = __shfl_sync(0xffffffffu, token, max(by, 0));
+        if (token >= 0) next = token;
+        if (each > 1) t -= warp_total(all);
+        passed = t < 0;
       }
+      writes = lane == 0;
     }
     break;
   }

@@ -110,6 +110,17 @@ def test_cluster_sizes(V, n_seqs):
         _case(rng, V, [3] * n_seqs, drawn, torch.float32)
 
 
+@pytest.mark.parametrize("V,dtype", [(300001, torch.float32), (100003, torch.bfloat16), (20011, torch.float32)])
+def test_many_sequences_of_long_rows(V, dtype):
+    """One block a sequence, so that a thread has many vectors of the range that holds the next token (most sequences are empty here)."""
+    rng = np.random.default_rng(V)
+    sizes = [0] * 160
+    for b in range(0, 160, 20):
+        sizes[b] = 2 + b // 20 % 3
+    for drawn in (False, True):
+        _case(rng, V, sizes, drawn, dtype, temperature=np.linspace(0.5, 1.5, 160))
+
+
 def test_independent_draws():
     rng = np.random.default_rng(21)
     for V in (3, 50, 2000):
