@@ -32,7 +32,8 @@
 // dequantising warps that are busy two thirds of the time.  Not better: two groups
 // of softmax warps in turn, which read the scores twice (3100), four threads a row
 // (3300), weights beside the output so that the next scores come sooner (2950),
-// a quarter of the weights while the row's maximum is exchanged (3150: registers).
+// a quarter of the weights while the row's maximum is exchanged (3150), all of
+// them, made again where the reference moves (3080: registers, both).
 #include "attn_tc.cuh"
 
 namespace moe {
