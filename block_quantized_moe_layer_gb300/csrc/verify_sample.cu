@@ -37,7 +37,7 @@
 // Measured (three calls' inputs in turn): a chain of 4 nodes, 32768 fp32 logits,
 // 12.2 us (2.4 us a step: the pass 0.7, a cluster barrier 0.9, the decision 0.8);
 // 4 trees of 64 nodes 14.9; 64 chains of 4 with drawn drafts, 151936 bf16 logits,
-// 62 us (the rows read take 20: a step 9 us, 5.7 of them HBM's while all walk; a
+// 63 us (the rows read take 20: a step 9 us, 5.7 of them HBM's while all walk; a
 // rejected drawn draft 20 to 30, all of it instructions, and 2 for the decision;
 // the next token's place in its range 5); 32 trees of 12 nodes, 151936 fp32, 38 us
 // (the longest walk's five rows: 5 us a step, the last 4, then the place).  16, 8 and 4 blocks a sequence take
