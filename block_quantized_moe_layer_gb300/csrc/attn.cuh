@@ -53,6 +53,7 @@ struct AttnParams {
   const int32_t *starts, *lens, *table;
   const int32_t* parents;  // [T] of a tree call, else null
   int by_length;       // 1: a tree call's blocks take the longest sequences first
+  int clustered;       // 1: a tree call's parts of a row tile are a cluster, which joins them
   void* out;           // [T][hq][D]
   float* lse;          // [T][hq] or null
   float* part_o;       // [tile][split][rows][D]

@@ -28,9 +28,11 @@
 // of up to 8000 keys, 64/4 heads of 192 (16 rows), in 76.5 us (the bytes take 24).
 // One token over 257 keys takes 8.0 us: two launches and one chain of loads.
 // For trees of drafted tokens (TREE) a node's ancestors are one word (attn.cuh),
-// made by a warp beside the first copies: 4 nodes over 515 keys take 8.9 us.
+// made by a warp beside the first copies: 4 nodes over 515 keys take 7.8 us, their parts joined in a cluster.
 // Slot n of 8 keys is key kKey(n) = 0,6,1,7,2,4,3,5: then both access patterns
 // meet all banks at 192 and 64 channels.
+#include <cooperative_groups.h>
+
 #include "attn_mma.cuh"
 
 namespace moe {
@@ -41,6 +43,7 @@ constexpr int kSmallWarps = 4;
 constexpr int kSmallThreads = kSmallWarps * 32;
 constexpr int kSmallTile = 128;
 constexpr int kSmallMaxStages = 8;
+constexpr int kJoinFew = 8;  // parts that are joined with all loads at once, or by a cluster
 
 // NT: 8-row groups of a block.  Blocks a multiprocessor by the registers that
 // the accumulators and queries take (24 D NT / 64 of them); stages by what
@@ -71,6 +74,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
   constexpr int kJ = D / 64, kRows = L::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t tree[TREE ? kTreeNodes : 1];  // the nodes' words of ancestors
+  __shared__ float2 block_ml[TREE ? kRows : 1];     // for the other blocks of a cluster
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + kSmallMaxStages;
   volatile uint32_t* pmask = reinterpret_cast<uint32_t*>(empty + kSmallMaxStages);  // pages present of a stage
@@ -413,7 +417,10 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       x[2] = fmaf(v.z, f, x[2]);
       x[3] = fmaf(v.w, f, x[3]);
     }
-    if (p.n_split == 1) {
+    if (TREE && p.clustered) {  // (over the first warp's part, which this thread alone reads)
+      *reinterpret_cast<float4*>(ob + r * D + c) = make_float4(x[0], x[1], x[2], x[3]);
+      if (c == 0) block_ml[r] = make_float2(mx, lt);
+    } else if (p.n_split == 1) {
       const float inv = mx > -INFINITY ? kValueUnscale / lt : 0.f;
       const int row = row0 + r, tok = s.start + row / p.g, h = kvh * p.g + row % p.g;
       const __nv_bfloat162 u = __floats2bfloat162_rn(x[0] * inv, x[1] * inv), v = __floats2bfloat162_rn(x[2] * inv, x[3] * inv);
@@ -428,11 +435,42 @@ __global__ void __launch_bounds__(kSmallThreads, SmallPlan<D, NT>::kBlocks)
       *reinterpret_cast<float4*>(p.part_o + (part + r) * D + c) = make_float4(x[0], x[1], x[2], x[3]);
     }
   }
+  if constexpr (TREE) {
+    if (!p.clustered) return;
+    // join the blocks' parts, a share of the outputs each
+    auto cl = cooperative_groups::this_cluster();
+    cl.sync();
+    for (int i = split * kSmallThreads + tid; i < n_rows * (D / 4); i += p.n_split * kSmallThreads) {
+      const int r = i / (D / 4), c = 4 * (i % (D / 4));
+      float2 a[kJoinFew];
+      float4 v[kJoinFew];
+      float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinFew; ++k) {
+        const bool has = k < p.n_split;
+        a[k] = has ? *cl.map_shared_rank(&block_ml[r], k) : make_float2(-INFINITY, 0.f);
+        v[k] = has ? *cl.map_shared_rank(reinterpret_cast<float4*>(ob + r * D + c), k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        mx = fmaxf(mx, a[k].x);
+      }
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kJoinFew; ++k) {
+        const float f = a[k].x == -INFINITY ? 0.f : exp2_approx(a[k].x - mx);
+        lt = fmaf(a[k].y, f, lt);
+        x.x = fmaf(v[k].x, f, x.x);
+        x.y = fmaf(v[k].y, f, x.y);
+        x.z = fmaf(v[k].z, f, x.z);
+        x.w = fmaf(v[k].w, f, x.w);
+      }
+      const int row = row0 + r;
+      store_joined(p, (int64_t)(s.start + row / p.g) * p.hq + kvh * p.g + row % p.g, c / 4, D, x, lt, mx);
+    }
+    cl.sync();  // (a block stays until the others have read its part)
+  }
 }
 
 // Joins up to kJoinFew parts of a row's keys: a thread 4 channels of a row,
 // all its loads at once.
-constexpr int kJoinFew = 8;
 // The tile's place among the split ones (-1: it was not split).  whole < 0: all
 // were, in the order sequence, head, row tile; else the prompt kernel's order,
 // whose first `whole` went whole.
@@ -612,8 +650,13 @@ cudaError_t small_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStre
   const int64_t fit = std::min<int64_t>(kMaxSplit, std::max<int64_t>(1, (int64_t)(part_rows / L::kRows) / base));
   chunk = std::max<int>(chunk, (int)((tiles + fit - 1) / fit));
   p.n_split = (tiles + chunk - 1) / chunk;
-  cudaError_t e = launch_pdl(p.parents ? small_kernel<D, NT, true> : small_kernel<D, NT, false>,
-                             dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kSmallThreads, L::kTotal, st, p, n_rt, chunk);
+  const dim3 grid(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs);
+  // A tree's few parts are a cluster's blocks, where all are on the GPU at once: no
+  // second launch (4 nodes over 515 keys, 32/8 heads of 128, 8.9 us, and 7.8 so; 16 rows over 1020 keys 9.3 to 11.2, and 7.4 to 10)
+  p.clustered = p.parents && p.n_split > 1 && p.n_split <= kJoinFew && base * p.n_split <= (int64_t)L::kBlocks * num_sms / 2;
+  if (p.clustered) return launch_pdl_cluster(small_kernel<D, NT, true>, p.n_split, grid, kSmallThreads, L::kTotal, st, p, n_rt, chunk);
+  cudaError_t e = launch_pdl(p.parents ? small_kernel<D, NT, true> : small_kernel<D, NT, false>, grid, kSmallThreads, L::kTotal, st, p,
+                             n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;
   return join_launch(p, L::kRows, n_rt, -1, st);
 }
