@@ -35,6 +35,8 @@
 // of 12 nodes (48 rows) over up to 8192 keys, 32/8 heads of 128: 107 us, 256
 // blocks, the longest sequences first; a tile takes some 1900 cycles, of which
 // shared memory is busy 1400 and the tensor pipe 840.
+#include <cooperative_groups.h>
+
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -45,6 +47,7 @@ cudaError_t join_launch(const AttnParams& p, int rows_per_tile, int n_rt, int wh
 namespace {
 
 constexpr int kRowsV = 64;
+constexpr int kJoinV = 8;  // parts that a cluster joins at most
 constexpr int kWarpsV = 25;
 constexpr int kMmaWarp = 24;
 constexpr int kThreadsV = kWarpsV * 32;
@@ -333,6 +336,45 @@ __global__ void __launch_bounds__(kThreadsV, 1) verify_kernel(const __grid_const
   __syncthreads();
   tc::fence_after();
   if (warp == kMmaWarp) tc::dealloc_512(tbase);
+  if constexpr (TREE) {
+    if (p.clustered) {
+      // the blocks' parts, a share of the outputs each (a part without keys has no output)
+      __shared__ float2 block_ml[kRowsV];
+      if (tid < kRowsV) {
+        float mr = smax[4 * kRowsV + tid], lt = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mr = fmaxf(mr, smax[(4 + k) * kRowsV + tid]), lt += smax[k * kRowsV + tid];
+        block_ml[tid] = make_float2(mr, lt);
+      }
+      auto cl = cooperative_groups::this_cluster();
+      cl.sync();
+      for (int i = split * kThreadsV + tid; i < n_rows * (D / 4); i += p.n_split * kThreadsV) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        float2 a[kJoinV];
+        float mr = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int k = 0; k < kJoinV; ++k) {
+          a[k] = k < p.n_split ? *cl.map_shared_rank(&block_ml[r], k) : make_float2(-INFINITY, 0.f);
+          mr = fmaxf(mr, a[k].x);
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kJoinV; ++k) {
+          if (a[k].x == -INFINITY) continue;
+          const float4 v = *cl.map_shared_rank(reinterpret_cast<float4*>(sm + r * L::kPitch + c * 16), k);
+          const float f = exp2_approx(a[k].x - mr);
+          lt = fmaf(a[k].y, f, lt);
+          x.x = fmaf(v.x, f, x.x);
+          x.y = fmaf(v.y, f, x.y);
+          x.z = fmaf(v.z, f, x.z);
+          x.w = fmaf(v.w, f, x.w);
+        }
+        store_joined(p, (int64_t)(s.start + (row0 + r) / p.g) * p.hq + kvh * p.g + (row0 + r) % p.g, c, D, x, lt, mr);
+      }
+      cl.sync();  // (a block stays until the others have read its part)
+      return;
+    }
+  }
   const int64_t part0 = ((int64_t)(b * p.hk * n_rt + blockIdx.y) * p.n_split + split) * kRowsV;
   for (int i = tid; i < n_rows * (D / 4); i += kThreadsV) {
     const int r = i / (D / 4), c = i % (D / 4);
@@ -368,6 +410,14 @@ cudaError_t verify_launch_d(AttnParams p, int num_sms, size_t part_rows, cudaStr
   p.n_split = (tiles + chunk - 1) / chunk;
   // (measured for trees alone, of which 32 of 12 nodes over 4096..8192 tokens take 107 us so, 125 in their order)
   p.by_length = p.parents && base > num_sms && p.n_seqs <= kSortedSeqs && p.window == 0;
+  // A tree's few parts are a cluster's blocks where all fit the GPU at once (a block
+  // a multiprocessor, and a cluster's in one of its groups): no second
+  // launch (48 rows over 640 keys, 32/8 heads of 128, 11.0 us and 10.0 so; 4 sequences
+  // 12.8 and 10.2)
+  p.clustered = p.parents && p.n_split > 1 && p.n_split <= kJoinV && base * p.n_split <= num_sms * 2 / 3;
+  if (p.clustered)
+    return launch_pdl_cluster(verify_kernel<D, true>, p.n_split, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
+                              VerifyPlan<D>::kTotal, st, p, n_rt, chunk);
   cudaError_t e = launch_pdl(p.parents ? verify_kernel<D, true> : verify_kernel<D, false>, dim3(p.n_split, (unsigned)(p.hk * n_rt), p.n_seqs), kThreadsV,
                              VerifyPlan<D>::kTotal, st, p, n_rt, chunk);
   if (e != cudaSuccess || p.n_split == 1) return e;

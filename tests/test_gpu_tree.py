@@ -249,6 +249,18 @@ def test_tree_more_blocks_than_the_gpu_holds(seqs, m, window):
     _check(rng, 32, 8, 64, lens, news, 32, window=window)
 
 
+@pytest.mark.parametrize("hq,hk,D,m", [(32, 8, 64, 4), (8, 2, 128, 4), (16, 1, 192, 1), (16, 2, 256, 2),
+                                       (32, 8, 64, 12), (8, 2, 128, 32), (16, 1, 192, 8), (16, 2, 256, 8)])
+def test_tree_parts_of_short_contexts(hq, hk, D, m):
+    """Two to nine parts of a context, around the number that a cluster joins; sequences whose parts are mostly empty, or all."""
+    rng = np.random.default_rng(D + m)
+    for n in (129, 300, 513, 1024, 1030, 2049):
+        _check(rng, hq, hk, D, [n], [m], 64)
+        _check(rng, hq, hk, D, [n, m, m + 1, 0], [m, m, 1, 0], 64)
+        _check(rng, hq, hk, D, [n, n - 50], [m, max(m - 1, 1)], 32, window=200)
+    _check(rng, hq, hk, D, [600, 2], [m, m], 16)  # fewer cached tokens than nodes
+
+
 # ------------------------------------------------------------------ commit
 
 
