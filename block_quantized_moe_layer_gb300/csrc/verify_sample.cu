@@ -30,6 +30,13 @@
 // a table and a short series (Tang's table-driven exponential), 1 + g (L + g
 // (L^2/2 + g L^3/6)), L = ln 2, |g| <= 2^-9.
 //
+//   Drafts drawn without replacement are judged by shares of what the rejected ones
+// leave of f.  Where that is little it is no difference of sums (of a peaked draft
+// row nothing but rounding is left of one): it is summed again without them, in
+// units of the largest weight that is left, one more exchange and two passes over
+// the draft's row.  A sibling is never judged by a share of nothing: it is passed
+// over, which leaves the tokens' distribution as it is.
+//
 //   A drawn draft that is surely rejected takes one pass over both rows for their
 // sums and for what is left, at the k that the fp32 sums give, and a correction
 // (see there); the others, and a node's second rejection, a pass each.
@@ -152,10 +159,10 @@ struct RowExp {
   uint32_t scale0;
 };
 constexpr float kMagic = 49152.f;  // 1.5 2^15: its sum with y has steps of 2^-8
-__device__ __forceinline__ RowExp row_exp(float most, float ch, float cl) {
+__device__ __forceinline__ RowExp row_exp(float ref, float most, float ch, float cl) {  // of logits up to `most`
   RowExp r;
-  r.ref = fabsf(most * ch) < 1024.f ? 0.f : most;
-  const float top = rintf((most - r.ref) * ch);
+  r.ref = ref;
+  const float top = rintf((most - ref) * ch);
   r.top = top;
   r.floor = (top - 127.f) / ch;
   r.ceil = INFINITY;
@@ -165,6 +172,9 @@ __device__ __forceinline__ RowExp row_exp(float most, float ch, float cl) {
   r.rest = 0.f;
   r.scale0 = ((uint32_t)(127 - (int)top) << 23) - (__float_as_uint(kMagic) << 15);
   return r;
+}
+__device__ __forceinline__ RowExp row_exp(float most, float ch, float cl) {
+  return row_exp(fabsf(most * ch) < 1024.f ? 0.f : most, most, ch, cl);
 }
 // The same times k > 0 (both weights of a logit are compared); held below 8
 // units, which is above every weight of the other row.  log2(k) = e + i/256 +
@@ -402,7 +412,16 @@ __device__ __forceinline__ uint64_t order_key(float x, int id) {
   return ((uint64_t)o << 32) | (uint32_t)~id;
 }
 
-enum : int { kGoOn, kReject, kDraw, kSureReject };
+enum : int { kGoOn, kReject, kDraw, kSureReject, kRest };
+
+// Drafts drawn without replacement: less than this of the draft's probability is
+// left, and the sum of what is left is made anew (sum_again).  By subtraction it
+// is right to 2^-32 of the whole, so to 2^-30 of itself above this.
+constexpr double kFewLeft = 0.25;
+// The largest weight left is below 2^-this of the row's largest: nothing is left.
+// (Above it, differences from a reference of 2^10 / c are exact down to 2^-44 of the
+// largest that is left, half a step of the sums at most.)
+constexpr float kNothingLeft = 400.f;
 
 struct Walk {  // one block's shared memory
   float2 table[256];
@@ -419,7 +438,7 @@ struct Walk {  // one block's shared memory
   float near[kVsBands][kVsRanges];
   int64_t child_e[kVsNodes], child_f[kVsNodes];
   int child_at[kVsNodes];  // their ranges
-  bool gone[kVsNodes];  // of the children: rejected, its token's weight taken out
+  bool gone[kVsNodes];  // of the children: rejected, its token's weight taken out (drawn without replacement: out of the draft's)
   int64_t part[kVsWarps];
   // written by the first warp for the block
   float most, most_f;
@@ -450,7 +469,9 @@ __device__ __forceinline__ int64_t warp_total(int64_t v) {
   return v;
 }
 
-template <typename In>
+// DRAFT: the drafts may be drawn.  Calls without a draft's row have an instance of
+// their own, which is shorter (a chain of 4 chosen drafts 13.9 us in the common one, 12.6 in its own).
+template <typename In, bool DRAFT>
 __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(const __grid_constant__ VsParams p) {
   namespace cg = cooperative_groups;
   constexpr int N = Load<In>::kN;
@@ -478,7 +499,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
   const int m = min(end - start, p.max_nodes);
   const bool valid_T = T >= 0.f && T <= 1e6f;
   const bool greedy = T < 1e-6f;
-  const bool drawn = p.draft && !greedy;
+  const bool drawn = DRAFT && p.draft && !greedy;
   // log2(e) / T in two parts
   const float div = greedy || !valid_T ? 1.f : T;
   const float ch = __fdiv_rn(1.44269502f, div), c_lo = __fdiv_rn(fmaf(-ch, div, 1.44269502f) + 1.92596299e-8f, div);
@@ -681,20 +702,21 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
     }
     const float most = w.most, most_f = w.most_f;
     const bool judged = both && most_f > -INFINITY && most_f < INFINITY;  // the draft's row is a distribution
-    const RowExp ee = row_exp(most, ch, c_lo), ef = row_exp(judged ? most_f : 0.f, ch, c_lo);
+    const RowExp ee = row_exp(most, ch, c_lo);
+    RowExp ef = row_exp(judged ? most_f : 0.f, ch, c_lo);
     RowExp kf = ef;  // the draft's times kappa
 
     // ---- else the sums in more bits
+    auto whole_weight = [&](float x, const RowExp& x_of) {
+      const Parts r = parts(weight(x, x, x_of, w.table));
+      return fixed(f2_lo(r.hi), f2_lo(r.lo), scale);
+    };
     if (warp == 0) {  // the children in order, and their weights
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (!kid[k]) continue;
         const int i = (k ? __popc(set0) : 0) + __popc((k ? set1 : set0) & ((1u << lane) - 1));
         const bool is = my_token[k] >= 0 && my_token[k] < p.V;
-        auto whole_weight = [&](float x, const RowExp& x_of) {
-          const Parts r = parts(weight(x, x, x_of, w.table));
-          return fixed(f2_lo(r.hi), f2_lo(r.lo), scale);
-        };
         w.child[i] = lane + 32 * k;
         w.child_e[i] = is ? whole_weight(my_x[k], ee) : -1;
         w.child_f[i] = is && judged ? whole_weight(my_y[k], ef) : 0;
@@ -805,8 +827,77 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       }
       turn ^= 1;
     };
-    double left = 1.0;  // of the draft's probability what is not rejected
+    // (the first warp's)
+    double left = 1.0;   // of the draft's weights, F in all, what is not rejected
+    bool spent = false;  // nothing is
     int cursor = 0;
+    // vector j without the rejected tokens
+    auto drop = [&](int j, float (&x)[N]) {
+      for (int i = 0; i < n_children; ++i) {
+        const int k = w.token[w.child[i]] - (j * N - skew);
+        if (!w.gone[i] || k < 0 || k >= N) continue;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (e == k) x[e] = -INFINITY;
+      }
+    };
+    // What the rejected tokens leave of the draft's row: F its sum, and its weights,
+    // in units of the largest that is left.
+    auto sum_again = [&]() {
+      const int here = rank * kVsWarps + warp;
+      bool any = false;  // of the rejected tokens one lies in this warp's range
+      for (int i = 0; i < n_children; ++i) any |= w.gone[i] && w.child_at[i] == here;
+      auto each_left = [&](auto one) {
+#pragma unroll 1
+        for (int j = j0 + lane; j < j1; j += 32) {
+          float x[N];
+          rf.load(j, x);
+          if (any) drop(j, x);
+          one(x);
+        }
+      };
+      float m = -INFINITY;
+      each_left([&](const float (&x)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, x[i]);
+      });
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane < 1 << p.log_c) cl.map_shared_rank(&w, lane)->soft[turn][here] = Soft{m, 0.f};
+      cl.sync();
+      for (int i = lane; i < n_ranges; i += 32) m = fmaxf(m, w.soft[turn][i].m);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      turn ^= 1;
+      if (!((most_f - m) * ch <= kNothingLeft)) {  // (all threads of the cluster)
+        spent = true;
+        return;
+      }
+      // (the reference stays: differences from it are as exact as before)
+      const RowExp now = row_exp(ef.ref, m, ch, c_lo);
+      kappa *= __hiloint2double((1023 + (int)(now.top - ef.top)) << 20, 0);
+      ef = now;
+      Sum sum;
+      each_left([&](const float (&x)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) sum.add(parts(weight(x[i], x[i + 1], ef, w.table)));
+        sum.flush();
+      });
+      const Pair a = warp_pair(sum.a);
+      const int64_t f = fixed(a.h, a.l, scale);
+      if (lane < 1 << p.log_c) cl.map_shared_rank(&w, lane)->sum_f[turn][here] = f;
+      cl.sync();
+      if (warp == 0) {
+        int64_t d = 0;
+        for (int i = lane; i < n_ranges; i += 32) d += w.sum_f[turn][i];
+        F = warp_total(d);
+        left = 1.0;
+        for (int i = lane; i < n_children; i += 32)
+          if (w.child_e[i] >= 0 && !w.gone[i]) w.child_f[i] = whole_weight(Load<In>::one(pf + w.token[w.child[i]]), ef);
+        __syncwarp();
+      }
+      turn ^= 1;
+    };
     if (w.act != kSureReject) {
       sums(judged);
       gather(judged);
@@ -907,7 +998,10 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
           for (int i = 0; i < n_children; ++i)
             if (w.child[i] == first_child) {
               cursor = i + 1;
-              if (!p.replacement) left = 1.0 - (double)w.child_f[i] * reciprocal((double)f_all);
+              if (!p.replacement) {
+                left = 1.0 - (double)w.child_f[i] * reciprocal((double)f_all);
+                if (lane == 0) w.gone[i] = true;
+              }
             }
         } else {
           Z = te;
@@ -928,11 +1022,16 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
         for (int i = cursor; i < n_children; ++i) {
           const int x = w.token[w.child[i]];
           const int64_t e = w.child_e[i], f = w.child_f[i];
-          if (e < 0 || (drawn && !judged)) continue;  // no such token, or nothing to judge it by: passed over
+          if (e < 0 || (drawn && !judged) || spent) continue;  // no such token, or nothing to judge it by: passed over
           if (!judged || !p.replacement) {
             bool again = false;  // an earlier sibling's token
             for (int k = 0; k < i; ++k) again |= w.token[w.child[k]] == x;
             if (again) continue;
+          }
+          if (judged && left < kFewLeft) {
+            cursor = i;
+            act = kRest;
+            break;
           }
           const double side = (double)w.u[w.child[i]] * (double)Z;
           if (judged ? side * (double)f < left * (double)F * ((double)e - kappa * (double)f) : side < (double)e) {
@@ -943,9 +1042,12 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
           if (!judged) {
             Z -= e;
             if (lane == 0) w.gone[i] = true;
-          } else if (left > 0.0 && Z > 0) {
+          } else if (Z > 0) {
             kappa += (double)Z * reciprocal(left * (double)F);
-            if (!p.replacement) left -= (double)f * reciprocal((double)F);
+            if (!p.replacement) {
+              left -= (double)f * reciprocal((double)F);
+              if (lane == 0) w.gone[i] = true;
+            }
             cursor = i + 1;
             act = kReject;
             break;
@@ -955,6 +1057,12 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
         if (lane == 0) w.act = act, w.at = at, w.kappa = kappa, w.kf = kf;
       }
       __syncthreads();
+      if constexpr (DRAFT) {
+        if (w.act == kRest) {
+          sum_again();
+          continue;
+        }
+      }
       if (w.act != kReject) break;
       kappa = w.kappa;
       kf = w.kf;
@@ -1026,15 +1134,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
     auto load = [&](int j, float (&xe)[N], float (&xf)[N]) {  // vector j, without the tokens that are out
       re.load(j, xe);
       if (kappa > 0.0) rf.load(j, xf);
-      if (out) {
-        for (int i = 0; i < n_children; ++i) {
-          const int k = w.token[w.child[i]] - (j * N - skew);
-          if (!w.gone[i] || k < 0 || k >= N) continue;
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (e == k) xe[e] = -INFINITY;
-        }
-      }
+      if (out) drop(j, xe);
     };
     auto left_of = [&](const float (&xe)[N], const float (&xf)[N], int k) {  // what is left of two weights
       const Parts a = parts(weight(xe[k], xe[k + 1], ee, w.table));
@@ -1131,6 +1231,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
 
 template <typename In>
 cudaError_t verify_sample_launch(const VsParams& p, cudaStream_t st) {
+  const auto kernel = p.draft ? verify_sample_kernel<In, true> : verify_sample_kernel<In, false>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.n_seqs << p.log_c);
   cfg.blockDim = dim3(kVsThreads);
@@ -1145,10 +1246,10 @@ cudaError_t verify_sample_launch(const VsParams& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (p.log_c > 3) {  // above the portable size
-    const cudaError_t e = cudaFuncSetAttribute(verify_sample_kernel<In>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, verify_sample_kernel<In>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace

@@ -315,7 +315,9 @@ int mtp_verify_accept_noalloc(const int32_t* draft_ids, int32_t k, const float* 
  *   else, q = softmax(draft_logits[i] / T): accepted if u sum(r) q(x) < r(x);
  *     else r = max(r / sum(r) - q, 0).  With replacement = 0 the children of a
  *     node were drawn without replacement: a rejected token leaves q, which is
- *     normalised again; with 1 they are independent draws from q.
+ *     normalised again (where what is left has no probability above 2^-400 of
+ *     q's largest, the later children are passed over); with 1 they are
+ *     independent draws from q.
  * The walk goes on from the first child accepted; where none is, the next
  * token is the first whose cumulative r passes the root's uniforms times
  * sum(r).  (If rounding leaves nothing of r, it is drawn from p.)
@@ -336,8 +338,9 @@ int mtp_verify_accept_noalloc(const int32_t* draft_ids, int32_t k, const float* 
  *   logits, draft_logits: [n_nodes][V] of dtype (moe_act), rows contiguous,
  * strides in elements; only the rows of the nodes on the path are read.
  *   Probabilities and their sums are right to 2^-32 of a row's sum: a number
- * closer than that to a border between two outcomes may fall on either side
- * (for a rejected drawn draft, in units of what is left).  A token below 2^-36
+ * closer than that to a border between two outcomes may fall on either side.
+ * After rejected drafts: r to 2^-31 of the target row's sum for each, q to
+ * 2^-30 of what is left of it.  A token below 2^-36
  * of a row's largest probability is not drawn.  The same inputs give the same
  * outputs.  Asynchronous, no allocation, no workspace. */
 int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_stride, const void* draft_logits,

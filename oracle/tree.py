@@ -83,6 +83,8 @@ def verify(logits, tokens, parents, uniforms, draft_logits=None, temperature=1.0
             if q is None:
                 children = []
         r, had, taken = p.copy(), set(), None
+        if q is not None:
+            rest, whole = q.copy(), q.max()  # what is left of q, and its largest at first
         for i in children:
             x, u = int(tokens[i]), float(uniforms[i])
             if not 0 <= x < V or (x in had and not (q is not None and replacement)):
@@ -99,9 +101,10 @@ def verify(logits, tokens, parents, uniforms, draft_logits=None, temperature=1.0
             elif total > 0 and q.sum() > 0:
                 r = np.maximum(r / total - q, 0)
                 if not replacement:
-                    q[x] = 0
-                    if q.sum() > 0:
-                        q = q / q.sum()
+                    rest[x] = 0
+                    if not rest.max() > 2.0 ** -400 * whole:
+                        break  # nothing is left of q: the later siblings are passed over
+                    q = rest / rest.sum()
         if taken is not None:
             path.append(taken)
             continue
