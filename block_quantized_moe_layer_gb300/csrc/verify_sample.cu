@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
   }
   const int m = min(end - start, p.max_nodes);
   const bool valid_T = T >= 0.f && T <= 1e6f;
-  const bool greedy = T < 1e-6f;
+  const bool greedy = T <= 1e-6f;  // (the fp32 number 1e-6 is below 1e-6)
   const bool drawn = DRAFT && p.draft && !greedy;
   // log2(e) / T in two parts
   const float div = greedy || !valid_T ? 1.f : T;
