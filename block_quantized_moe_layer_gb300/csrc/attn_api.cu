@@ -39,6 +39,10 @@ int cuda_fail(cudaError_t e, const char* what) {
   cudaGetLastError();  // reported here: the next launch of the process is not to find it
   return set_error(e == cudaErrorMemoryAllocation ? MOE_ENOMEM : MOE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+int launch_fail(cudaError_t e, const char* who, const char* kernel) {
+  cudaGetLastError();
+  return set_error(MOE_ECUDA, "%s launch%s: %s", who, kernel, cudaGetErrorString(e));
+}
 #define CKA(call, what)                              \
   do {                                               \
     cudaError_t e_ = (call);                         \
@@ -128,8 +132,8 @@ int forward(const char* who, moe_attn* h, const void* q, int64_t q_token_stride,
   p.status = h->status;
   p.timeout_ns = 2000000000ull;
   if (h->act == MOE_ACT_F32) {
-    CKA(attn::check_launch(p, st), "attention launch (fp32)");
-    return MOE_OK;
+    const cudaError_t e = attn::check_launch(p, st);
+    return e == cudaSuccess ? MOE_OK : launch_fail(e, who, " (fp32)");
   }
   if (h->inject_us > 0) {  // one launch
     p.timeout_ns = 1000ull * h->inject_us;
@@ -139,16 +143,21 @@ int forward(const char* who, moe_attn* h, const void* q, int64_t q_token_stride,
   p.part_o = reinterpret_cast<float*>(h->ws);
   p.part_ml = reinterpret_cast<float2*>(h->ws + h->part_rows * h->D * sizeof(float));
   const int64_t rows = (int64_t)max_q * p.g;
-  if (rows <= kSmallCallRows)
-    CKA(attn::small_launch(p, h->num_sms, h->part_rows, st), "attention launch");
-  else if (parents && rows > tree_verify_rows(h->D))
-    CKA(attn::tree_launch(p, h->num_sms, h->part_rows, st), "attention launch (tree)");
-  else if (rows <= verify_call_rows(h->D))
-    CKA(attn::verify_launch(p, h->num_sms, h->part_rows, st), "attention launch (verify)");
-  else
-    CKA(attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st),
-        "attention launch (prompt)");
-  return MOE_OK;
+  const char* kernel = "";
+  cudaError_t e;
+  if (rows <= kSmallCallRows) {
+    e = attn::small_launch(p, h->num_sms, h->part_rows, st);
+  } else if (parents && rows > tree_verify_rows(h->D)) {
+    kernel = " (tree)";
+    e = attn::tree_launch(p, h->num_sms, h->part_rows, st);
+  } else if (rows <= verify_call_rows(h->D)) {
+    kernel = " (verify)";
+    e = attn::verify_launch(p, h->num_sms, h->part_rows, st);
+  } else {
+    kernel = " (prompt)";
+    e = attn::prompt_launch(p, h->num_sms, h->part_rows, h->ws + h->tile_off, h->tile_cap, st);
+  }
+  return e == cudaSuccess ? MOE_OK : launch_fail(e, who, kernel);
 }
 
 }  // namespace
