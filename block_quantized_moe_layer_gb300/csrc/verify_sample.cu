@@ -442,7 +442,7 @@ struct Walk {  // one block's shared memory
   int64_t part[kVsWarps];
   // written by the first warp for the block
   float most, most_f;
-  int act, at, range, winner;
+  int act, at, range, winner, up, found;
   double kappa;
   RowExp kf;
   int64_t threshold;
@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       if (lane == 0) w.at = Z > 0;
     }
     __syncthreads();
-    const bool out = !judged && w.at;  // the rejected tokens' own weights are out
+    bool out = !judged && w.at;        // the rejected tokens' own weights are out
     if (!w.at) {                       // nothing is left: the target's own weights
       kappa = 0.0;
       sums(false);
@@ -1111,19 +1111,27 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       const int64_t t = __double2ll_rd((double)w.u[0] * (double)Z);  // (a whole sum passes the number where it passes this)
       const int from = max(pick(s, t, lane, before), 0);
       if (lane == from) {
-        int64_t run = before;
+        int64_t run = before, mass = 1;
         int at = 0;
         bool found = false;
 #pragma unroll
         for (int g = 0; g < kGroup; ++g) {
           if (found || mine[g] <= 0) continue;
           at = g;
+          mass = mine[g];
           before = run;
-          run += mine[g];
+          run += mass;
           found = run > t;
         }
+        // In the range the steps are finer, its mass 2^49 of them at least: in a long
+        // row, or behind rejected drafts, a token may have less than one of the row's,
+        // and many roundings of half a step would add up.
+        const int up = max(__clzll(mass) - 14, 0);
         w.range = lane * group + at;
-        w.threshold = t - before;
+        w.up = up;
+        const int64_t place = t - before;
+        w.threshold = place < 0 ? -1 : (place < mass ? place : mass) << up;
+        w.found = -1;
       }
     }
     __syncthreads();
@@ -1140,12 +1148,21 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
       const Parts a = parts(weight(xe[k], xe[k + 1], ee, w.table));
       return kappa > 0.0 ? residual(a, parts(weight<true>(xf[k], xf[k + 1], kf, w.table))) : a;
     };
+    // in the finer steps; h and l may be large and of opposite signs beside their sum
+    // (held where the range's sum, corrected or short of a rejected draft, says less
+    // than its tokens have: sums of these stay below 2^63)
+    const float fine = scale * __uint_as_float((uint32_t)(127 + w.up) << 23), most_fine = w.up > 0 ? 0x1p51f : INFINITY;
+    auto finer = [&](float h, float l) {
+      const float t = __fadd_rn(h, l), z = __fsub_rn(t, h);
+      const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(l, z));
+      return __float2ll_rn(fminf(t * fine, most_fine)) + __float2ll_rn(e * fine);
+    };
     auto whole_left = [&](const float (&xe)[N], const float (&xf)[N], int64_t (&r)[N]) {
 #pragma unroll
       for (int k = 0; k < N; k += 2) {
         const Parts a = left_of(xe, xf, k);
-        r[k] = fixed(f2_lo(a.hi), f2_lo(a.lo), scale);
-        r[k + 1] = fixed(f2_hi(a.hi), f2_hi(a.lo), scale);
+        r[k] = finer(f2_lo(a.hi), f2_lo(a.lo));
+        r[k + 1] = finer(f2_hi(a.hi), f2_hi(a.lo));
       }
     };
     float xe[N], xf[N];
@@ -1163,7 +1180,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
 #pragma unroll
         for (int k = 0; k < N; ++k) xe[k] = ye[k], xf[k] = yf[k];
       }
-      own = fixed(sum.a.h, sum.a.l, scale);
+      own = finer(sum.a.h, sum.a.l);
     } else if (a0 < a1) {
       whole_left(xe, xf, r);
 #pragma unroll
@@ -1174,7 +1191,7 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
     __syncthreads();
     if (warp == 0) {
       int64_t before;
-      const int at = max(pick(lane < kVsWarps ? w.part[lane] : 0, w.threshold, lane, before), 0);
+      const int at = pick(lane < kVsWarps ? w.part[lane] : 0, w.threshold, lane, before);  // (-1: see below)
       if (lane == 0) w.winner = at, w.threshold -= before;
     }
     __syncthreads();
@@ -1217,6 +1234,41 @@ __global__ void __launch_bounds__(kVsThreads, kVsBlocks) verify_sample_kernel(co
         passed = t < 0;
       }
       writes = lane == 0;
+      if (writes) w.found = next;
+    }
+    __syncthreads();
+    if (w.found < 0) {
+      // Rounding alone had put the place into this range: the first token from its
+      // start on, and round the row's end, that has anything left; else that has any.
+      constexpr int kRound = 1 << 26;
+      const int from = k0 * N - skew;
+#pragma unroll 1
+      for (int all = 0; all < 2; ++all) {
+        if (all) kappa = 0.0, out = false;
+        if (tid == 0) w.at = 2 * kRound;
+        __syncthreads();
+        int first = 2 * kRound;
+#pragma unroll 1
+        for (int j = tid; j < n_vec; j += kVsThreads) {
+          load(j, xe, xf);
+#pragma unroll
+          for (int k = 0; k < N; k += 2) {
+            const Parts a = left_of(xe, xf, k);
+            const uint64_t any = f2_add(a.hi, a.lo);
+            const int id = j * N - skew + k - from;
+            if (f2_hi(any) > 0.f) first = min(first, id + 1 >= 0 ? id + 1 : id + 1 + kRound);
+            if (f2_lo(any) > 0.f) first = min(first, id >= 0 ? id : id + kRound);
+          }
+        }
+        atomicMin(&w.at, first);
+        __syncthreads();
+        first = w.at;
+        __syncthreads();
+        if (first == 2 * kRound) continue;
+        next = from + (first < kRound ? first : first - kRound);
+        break;
+      }
+      writes = tid == 0;
     }
     break;
   }

@@ -337,11 +337,11 @@ int mtp_verify_accept_noalloc(const int32_t* draft_ids, int32_t k, const float* 
  * <= 64.
  *   logits, draft_logits: [n_nodes][V] of dtype (moe_act), rows contiguous,
  * strides in elements; only the rows of the nodes on the path are read.
- *   Probabilities and their sums are right to 2^-32 of a row's sum: a number
- * closer than that to a border between two outcomes may fall on either side.
- * After rejected drafts: r to 2^-31 of the target row's sum for each, q to
- * 2^-30 of what is left of it.  A token below 2^-36
- * of a row's largest probability is not drawn.  The same inputs give the same
+ *   Probabilities and their sums are right to 2^-32 of a row's sum (2^-30 for V
+ * above 2^22): a number closer than that to a border between two outcomes may
+ * fall on either side.  After rejected drafts: r to 2^-31 of the target row's
+ * sum for each, q to 2^-30 of what is left of it.  The next token is one that
+ * has some of r, or of p where nothing is left.  The same inputs give the same
  * outputs.  Asynchronous, no allocation, no workspace. */
 int mtp_verify_sample(const void* logits, int32_t dtype, int64_t row_stride, const void* draft_logits,
                       int64_t draft_stride, int32_t V, const int32_t* tokens, const int32_t* parents,
