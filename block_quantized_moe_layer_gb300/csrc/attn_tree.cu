@@ -388,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
       bool ok = true;
       for (int j = 0; j < n_tiles && ok; ++j) {
         ok = wait_bar<64>(&full[j & 1], (uint32_t)((j >> 1) & 1), abort, p.status, p.timeout_ns, 46);
-        if (ok) arrive_first(&full[j & 1]);
+        if (ok) arrive_first_release(&full[j & 1]);
       }
     }
     if (n_tiles > 0 && first_block && elect_one()) {
