@@ -24,8 +24,8 @@
 // the window's.
 // TMEM columns: S at 0 and 128 (P over it), O at 256.
 //
-// Measured: 16 nodes of 64/4 heads of 192 over 32765 tokens (256 rows) 37 us with
-// the join, 0.69 PFLOP/s; 8 trees of 64 nodes over up to 8000 tokens 152 us, 0.90
+// Measured: 16 nodes of 64/4 heads of 192 over 32765 tokens (256 rows) 38 us with
+// the join, 0.68 PFLOP/s; 8 trees of 64 nodes over up to 8000 tokens 151 us, 0.90
 // PFLOP/s.  A tile takes 2900 cycles, of which the MMAs need 1540 and the memory
 // 130.  Bound: the softmax's chain (scores to registers 600, the row's maximum 500,
 // exponentials 1000, weights to tensor memory 250, the next scores 300), beside
@@ -33,7 +33,8 @@
 // of softmax warps in turn, which read the scores twice (3100), four threads a row
 // (3300), weights beside the output so that the next scores come sooner (2950),
 // a quarter of the weights while the row's maximum is exchanged (3150), all of
-// them, made again where the reference moves (3080: registers, both).
+// them, made again where the reference moves (3080: registers, both).  (18 warps
+// leave a thread 96 registers, 52 bytes of them spilled; 16 would leave 128.)
 #include "attn_tc.cuh"
 
 namespace moe {

@@ -33,8 +33,8 @@
 //   Drafts drawn without replacement are judged by shares of what the rejected ones
 // leave of f.  Where that is little it is no difference of sums (of a peaked draft
 // row nothing but rounding is left of one): it is summed again without them, in
-// units of the largest weight that is left, one more exchange and two passes over
-// the draft's row.  A sibling is never judged by a share of nothing: it is passed
+// units of the largest weight that is left: two passes over the draft's row, an
+// exchange each.  A sibling is never judged by a share of nothing: it is passed
 // over, which leaves the tokens' distribution as it is.
 //
 //   A drawn draft that is surely rejected takes one pass over both rows for their
@@ -42,15 +42,16 @@
 // (see there); the others, and a node's second rejection, a pass each.
 //
 // Measured (three calls' inputs in turn): a chain of 4 nodes, 32768 fp32 logits,
-// 12.2 us (2.4 us a step: the pass 0.7, a cluster barrier 0.9, the decision 0.8);
-// 4 trees of 64 nodes 14.9; 64 chains of 4 with drawn drafts, 151936 bf16 logits,
+// 11.8 us (2.4 us a step: the pass 0.7, a cluster barrier 0.9, the decision 0.8);
+// 4 trees of 64 nodes 15.3; 64 chains of 4 with drawn drafts, 151936 bf16 logits,
 // 63 us (the rows read take 20: a step 9 us, 5.7 of them HBM's while all walk; a
 // rejected drawn draft 20 to 30, all of it instructions, and 2 for the decision;
-// the next token's place in its range 5); 32 trees of 12 nodes, 151936 fp32, 38 us
-// (the longest walk's five rows: 5 us a step, the last 4, then the place).  16, 8 and 4 blocks a sequence take
-// 34, 39 and 42 us there with 256 threads a block (inputs in L2: 31), 512 threads
-// 36, 1024 threads 43; 4, 2 and 1 loads in flight a thread 34, 37 and 40.  Asking
-// L2 for the next row ahead of the walk cost 1 us, and 7 of the 67.
+// the next token's place in its range 5; 166 where the draft's rows are aligned
+// otherwise than the target's); 32 trees of 12 nodes, 151936 fp32, 37 us (inputs in
+// L2: 29; the longest walk's five rows: 5 us a step, the last 4, then the place).
+// Blocks a sequence: 4, 8 and 16 take 54, 37 and 49 us there, 63, 71 and 115 for the
+// 64 chains (two blocks a multiprocessor are on the GPU at once).  Asking L2 for the
+// next row ahead of the walk cost 1 us, and 7 of the 64 chains' 67 at the time.
 #include <cooperative_groups.h>
 
 #include <cmath>

@@ -336,7 +336,9 @@ int mtp_verify_accept_noalloc(const int32_t* draft_ids, int32_t k, const float* 
  * -1 and next token -1.  Nodes from max_nodes on are left out; 1 <= max_nodes
  * <= 64.
  *   logits, draft_logits: [n_nodes][V] of dtype (moe_act), rows contiguous,
- * strides in elements; only the rows of the nodes on the path are read.
+ * strides in elements; only the rows of the nodes on the path are read.  Rows
+ * of draft_logits should start at the same place within 16 bytes as those of
+ * logits: others are read element by element (2 to 3 times the time).
  *   Probabilities and their sums are right to 2^-32 of a row's sum (2^-30 for V
  * above 2^22): a number closer than that to a border between two outcomes may
  * fall on either side.  After rejected drafts: r to 2^-31 of the target row's
